@@ -62,7 +62,9 @@ typedef enum {
     KDA_ERR_CUDA = 3         /* a CUDA launch or runtime call failed         */
 } kda_status;
 
-typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
+/* KDA_F16 is taken by the latent attention and log-probability calls only; every
+ * recurrent-state call returns KDA_ERR_UNSUPPORTED for it. */
+typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_F16 = 2 } kda_dtype;
 
 #define KDA_GATE_LOG 1u
 #define KDA_BETA_ACT 2u
@@ -418,6 +420,145 @@ kda_status kda_slot_copy_noalloc(const kda_pool_desc* pools, int32_t n_pools,
                                  const int32_t* src_slots, const int32_t* dst_offsets,
                                  const int32_t* dst_slots, int32_t n_src, int32_t n_dst,
                                  int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: full attention whose keys and values come from one latent
+ * vector c (512) and one rope key kr (64) a token, shared by all heads -- the
+ * layers a hybrid model runs between its recurrent-state layers.  Per head the
+ * model's up-projections give k = [W_k c ; kr] (128 + 64) and v = W_v c (128).
+ *   expanded form (kda_latent_prefill): k and v of every head are given;
+ *     s_p = scale (q_nope . k_nope_p + q_rope . kr_p),  o = sum_p softmax(s)_p v_p.
+ *   absorbed form (kda_latent_decode): W_k is taken into the query and W_v out
+ *     of the output (two products of the engine's, as its other projections
+ *     are), and attention runs on the latent vectors themselves:
+ *     s_p = scale (q_latent . c_p + q_rope . kr_p),  o = sum_p softmax(s)_p c_p.
+ * lse is the natural log of sum_p exp(s_p): two results over disjoint keys
+ * merge as o = sum_i e^{lse_i - lse} o_i, lse = log sum_i e^{lse_i}.
+ * A row whose mask leaves no key gets a zero output and lse = -inf.
+ * Types: bf16 or fp16 (products on the tensor cores, fp32 accumulation, softmax
+ * in fp32; the weights are rounded once to the input type for the product with
+ * the values).  Masked positions are never read into a result, whatever bits
+ * lie there, with one exception: a key that another row of the same sequence
+ * may see has to be finite.
+ *
+ * The cache is paged: [P, page_size, 576], a row c then kr; page i starts at
+ * cache + i * page_stride elements.  page_size is a multiple of 8, page_stride a
+ * multiple of 8 and >= page_size * 576.
+ *
+ * kda_rows_desc (HOST struct) places rows of heads: row r, head h starts at
+ * base + r * row_stride + h * head_stride (in elements; base 16-byte aligned,
+ * strides multiples of 8), its channels contiguous. */
+typedef struct {
+    const void* base;
+    int64_t row_stride;
+    int64_t head_stride;
+} kda_rows_desc;
+
+/* flag of kda_latent_prefill: every query row sees every key of its sequence
+ * (an earlier context, merged through lse) instead of the causal mask */
+#define KDA_LATENT_FULL 64u
+
+/*
+ * kda_latent_append -- one token's latent vector and rope key into the cache.
+ *
+ *   kv     : [T, 576] of dtype, row t at kv + t * kv_stride elements (kv_stride
+ *            a multiple of 8, >= 576).
+ *   weight : [512] of dtype or NULL.  With it the latent part is normalised,
+ *            c / sqrt(mean(c^2) + eps) * weight, in fp32 and rounded once;
+ *            without it c is copied.  kr is copied.
+ *   slot   : [T] int32, the token's place page * page_size + offset; < 0: not
+ *            written; >= P * page_size: not written, KDA_DEV_BAD_SLOT.  Two
+ *            tokens of one call must not share a place (not checked).
+ * d_latent = 512 and d_rope = 64 (else KDA_ERR_UNSUPPORTED), here and below.
+ */
+kda_status kda_latent_append(const void* kv, int64_t kv_stride, const void* weight, float eps,
+                             kda_dtype dtype, int32_t T, int32_t d_latent, int32_t d_rope,
+                             const int32_t* slot, void* cache, int64_t P, int32_t page_size,
+                             int64_t page_stride, int32_t* dev_status, void* stream);
+
+/*
+ * kda_latent_decode -- absorbed latent attention of K query positions a request
+ * over the paged cache (K = 1: decode; K up to 16: a speculative verify, rows
+ * and q_len as for kda_spec_verify).
+ *
+ *   q_latent    : rows R*K (request r's position t is row r*K + t) of H heads of
+ *                 512 in_dtype;  q_rope: the same rows, 64 channels.
+ *   q_len       : [R] int32 in [0, K] or NULL (= K); outside: request skipped,
+ *                 KDA_DEV_BAD_ACCEPT.  Rows t >= q_len: zero output, lse -inf.
+ *   block_table : [R, max_pages] int32: token p of request r lies in page
+ *                 block_table[r][p / page_size].  Entries past the request's
+ *                 last token are never read.  An entry outside [0, P): its
+ *                 tokens count as masked, KDA_DEV_BAD_SLOT.
+ *   seq_len     : [R] int32, tokens in the cache, this step's own q_len
+ *                 included: position t sees tokens 0 .. seq_len - q_len + t.
+ *                 < 0 or > max_pages * page_size: request skipped (zero
+ *                 output), KDA_DEV_BAD_SEQLEN.
+ *   out         : rows R*K, heads H, 512 channels of out_dtype (any of the three).
+ *   lse         : [R*K, H] fp32 or NULL.
+ *   workspace   : >= kda_latent_decode_workspace_size(R, K, H) bytes, read only
+ *                 after this call wrote it.
+ * 1 <= H, 1 <= K <= 16, R * K * H < 2^31.
+ */
+kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,
+                             kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
+                             int32_t H, int32_t d_latent, int32_t d_rope, float scale,
+                             const void* cache, int64_t P, int32_t page_size,
+                             int64_t page_stride, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seq_len, const kda_rows_desc* out,
+                             kda_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                             int32_t* dev_status, void* stream);
+
+size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t H);
+
+/*
+ * kda_latent_prefill -- expanded latent attention of packed sequences.
+ *
+ *   q           : rows Tq, H heads, 192 channels (128 nope, 64 rope) of in_dtype
+ *   k_nope, v   : rows Tk, H heads, 128 channels each (two halves of one
+ *                 up-projection are two descriptors with its strides)
+ *   k_rope      : [Tk, 64], row t at k_rope + t * k_rope_stride elements
+ *                 (a multiple of 8): shared by the heads, not repeated
+ *   cu_q, cu_k  : [N+1] int32 (device): sequence n has query rows
+ *                 [cu_q[n], cu_q[n+1]) and keys [cu_k[n], cu_k[n+1]).  A
+ *                 sequence whose bounds decrease or pass Tq / Tk is skipped
+ *                 (its rows not written) with KDA_DEV_BAD_SEQLEN.
+ *   flags       : 0: query i of Lq sees keys 0 .. Lk - Lq + i (the last query
+ *                 sees the last key); KDA_LATENT_FULL: all Lk keys.
+ *   out         : rows Tq, H heads, 128 channels of out_dtype (any of the three)
+ *   lse         : [Tq, H] fp32 or NULL
+ */
+kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
+                              const void* k_rope, int64_t k_rope_stride, const kda_rows_desc* v,
+                              kda_dtype in_dtype, const int32_t* cu_q, const int32_t* cu_k,
+                              int32_t N, int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope,
+                              int32_t d_rope, int32_t dv, float scale, uint32_t flags,
+                              const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * kda_token_logprobs -- what a serving step answers with beside its tokens: the
+ * log probability of a given token of every row, the entropy of the row and its
+ * k most likely tokens, in one pass over the logits (verify positions, sampled
+ * tokens, a prompt's own tokens).
+ *   x = logits row;  lse = log sum_j e^{x_j};  logprob = x_token - lse;
+ *   entropy = -sum_j p_j log p_j,  p_j = e^{x_j - lse}   (fp32 sums).
+ *
+ *   logits       : [R, V] of dtype (any of the three), row r at
+ *                  logits + r * row_stride elements; any element alignment
+ *   tokens       : [R] int32.  < 0: logprob[r] = 0 (a padding row; the other
+ *                  outputs are still written); >= V: the same and KDA_DEV_BAD_SLOT
+ *   logprob      : [R] fp32;  entropy: [R] fp32 or NULL
+ *   top_ids      : [R, top] int32, top_logprobs: [R, top] fp32 (either may be
+ *                  NULL when top = 0): the largest logits in descending order,
+ *                  equal ones by ascending id.  0 <= top <= 32, top <= V.
+ * A logit of -inf has probability 0 and adds nothing to the entropy.  A row of
+ * only -inf, or with +inf or NaN in it, has NaN figures (as the formulas give);
+ * its top_ids are still distinct ids, NaN ordered below -inf.
+ */
+kda_status kda_token_logprobs(const void* logits, int64_t row_stride, kda_dtype dtype, int32_t R,
+                              int32_t V, const int32_t* tokens, float* logprob, float* entropy,
+                              int32_t top, int32_t* top_ids, float* top_logprobs,
+                              int32_t* dev_status, void* stream);
 
 /*
  * kda_selftest_bounded_wait -- diagnostic: runs the kernels' bounded mbarrier

@@ -8,7 +8,9 @@ libkda.so is missing the import of the library raises.
 Entry points (same names as the C ABI):
   kda_chunk_prefill, kda_recurrent_decode, kda_spec_verify, kda_spec_accept, kda_spec_commit,
   kda_spec_accept_commit, kda_conv_compact, kda_slot_copy, kda_slot_copy_noalloc,
-  kda_chunk_prefill_workspace_size, kda_slot_copy_workspace_size.
+  kda_chunk_prefill_workspace_size, kda_slot_copy_workspace_size,
+  kda_latent_append, kda_latent_decode, kda_latent_decode_workspace_size, kda_latent_prefill,
+  kda_token_logprobs.
 """
 from __future__ import annotations
 
@@ -19,20 +21,23 @@ import torch
 
 __all__ = [
     "KDA_BF16", "KDA_F32", "KDA_GATE_LOG", "KDA_BETA_ACT", "KDA_STATE_BF16", "KDA_STATE_F16",
-    "KDA_QK_L2NORM",
+    "KDA_QK_L2NORM", "KDA_F16", "KDA_LATENT_FULL",
     "KdaError", "lib",
     "kda_chunk_prefill", "kda_recurrent_decode", "kda_spec_verify", "kda_spec_accept",
     "kda_spec_commit", "kda_spec_accept_commit", "kda_conv_compact", "kda_slot_copy",
     "kda_slot_copy_noalloc", "kda_chunk_prefill_workspace_size",
     "kda_slot_copy_workspace_size",
     "kda_status_string", "kda_abi_version", "kda_selftest_bounded_wait", "PoolDesc",
-    "ConvDesc", "CommitExtras",
+    "ConvDesc", "CommitExtras", "RowsDesc",
+    "kda_latent_append", "kda_latent_decode", "kda_latent_decode_workspace_size",
+    "kda_latent_prefill", "kda_token_logprobs",
 ]
 
-KDA_BF16, KDA_F32 = 0, 1
+KDA_BF16, KDA_F32, KDA_F16 = 0, 1, 2
 KDA_GATE_LOG, KDA_BETA_ACT, KDA_PREFILL_RECURRENT = 1, 2, 4
 KDA_STATE_BF16, KDA_STATE_F16 = 8, 16
 KDA_QK_L2NORM = 32
+KDA_LATENT_FULL = 64
 KDA_DEV_BAD_SLOT, KDA_DEV_BAD_TRACK, KDA_DEV_BAD_ACCEPT = 1, 2, 4
 KDA_DEV_BAD_SEQLEN, KDA_DEV_OVERLAP, KDA_DEV_TIMEOUT = 8, 16, 32
 KDA_MAX_POOLS = 16
@@ -64,6 +69,11 @@ class CommitExtras(ctypes.Structure):
                 ("block_idx_out", ctypes.c_void_p), ("n_convs", ctypes.c_int32),
                 ("conv_keep", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class RowsDesc(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 def lib():
@@ -100,12 +110,27 @@ def lib():
         L.kda_chunk_prefill_workspace_size.restype = sz
         L.kda_slot_copy_workspace_size.argtypes = [i64]
         L.kda_slot_copy_workspace_size.restype = sz
+        rows = ctypes.POINTER(RowsDesc)
+        L.kda_latent_append.argtypes = [vp, i64, vp, f32, ctypes.c_int, i32, i32, i32, vp, vp, i64,
+                                        i32, i64, vp, vp]
+        L.kda_latent_decode.argtypes = [rows, rows, ctypes.c_int, i32, i32, vp, i32, i32, i32, f32,
+                                        vp, i64, i32, i64, vp, i32, vp, rows, ctypes.c_int, vp, vp,
+                                        sz, vp, vp]
+        L.kda_latent_decode_workspace_size.argtypes = [i32, i32, i32]
+        L.kda_latent_decode_workspace_size.restype = sz
+        L.kda_latent_prefill.argtypes = [rows, rows, vp, i64, rows, ctypes.c_int, vp, vp, i32, i32,
+                                         i32, i32, i32, i32, i32, f32, u32, rows, ctypes.c_int, vp,
+                                         vp, vp]
+        L.kda_token_logprobs.argtypes = [vp, i64, ctypes.c_int, i32, i32, vp, vp, vp, i32, vp, vp,
+                                         vp, vp]
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_abi_version.restype = i32
         for f in ("kda_chunk_prefill", "kda_recurrent_decode", "kda_spec_verify",
                   "kda_spec_accept", "kda_spec_commit", "kda_spec_accept_commit",
-                  "kda_conv_compact", "kda_slot_copy", "kda_selftest_bounded_wait"):
+                  "kda_conv_compact", "kda_slot_copy", "kda_selftest_bounded_wait",
+                  "kda_latent_append", "kda_latent_decode", "kda_latent_prefill",
+                  "kda_token_logprobs"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -383,3 +408,151 @@ def _slot_sets(pools, clear_slots, src_slots, dst_offsets, dst_slots):
     sets = (_idx(clear_slots, "clear_slots"), n_clear, _idx(src_slots, "src_slots"),
             _idx(dst_offsets, "dst_offsets"), _idx(dst_slots, "dst_slots"), n_src, n_dst)
     return descs, n, sets
+
+
+# --------------------------------------------------------------------------
+# latent attention and token log probabilities
+
+
+def _dt3(t) -> int:
+    """Element type of the latent attention and log-probability calls (bf16, fp16 or fp32)."""
+    return KDA_F16 if t.dtype == torch.float16 else _dt(t)
+
+
+def _rows(t, name):
+    """Descriptor of a CUDA tensor [rows, heads, channels] whose channels are contiguous; rows
+    and heads may be strided (a view of a wider tensor)."""
+    if t.dim() != 3 or (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [rows, heads, channels] with contiguous channels")
+    # a dimension of one element is never stepped along: torch may give it any stride
+    rs = t.stride(0) if t.shape[0] > 1 else 0
+    hs = t.stride(1) if t.shape[1] > 1 else 0
+    return ctypes.byref(RowsDesc(_p_any(t), rs, hs))
+
+
+def _same(name, t, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _cache_pages(cache):
+    """(pages, page size, page stride) of a paged cache [P, page_size, width]."""
+    if cache.dim() != 3 or cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
+        raise ValueError("cache must be [pages, page_size, width] with contiguous pages")
+    P, page, width = cache.shape
+    return P, page, cache.stride(0) if P > 1 else page * width
+
+
+def kda_latent_append(kv, cache, slot, *, weight=None, eps=1e-6, dev_status=None, stream=None):
+    """Latent vectors (normalised when weight is given) and rope keys of new tokens into the
+    paged cache (see include/kda.h).  kv: [T, 576], rows may be strided."""
+    T, width = kv.shape
+    P, page, stride = _cache_pages(cache)
+    _same("cache", cache, P, page, width)
+    _same("slot", slot, T)
+    if T and kv.stride(1) != 1:
+        raise ValueError("kv needs contiguous rows")
+    if weight is not None:
+        _same("weight", weight, width - 64)
+    dt = {t.dtype for t in (kv, cache, weight) if t is not None}
+    if len(dt) != 1:
+        raise ValueError(f"kv, cache and weight must share one dtype, got {sorted(map(str, dt))}")
+    st = lib().kda_latent_append(
+        _p_any(kv), kv.stride(0) if T > 1 else width, _p(weight), float(eps), _dt3(kv), T,
+        width - 64, 64, _idx(slot, "slot"), _p_any(cache), P, page, stride,
+        _idx(dev_status, "dev_status"), _stream(stream))
+    _check(st, "kda_latent_append")
+
+
+def kda_latent_decode_workspace_size(R, K, H) -> int:
+    return int(lib().kda_latent_decode_workspace_size(R, K, H))
+
+
+def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_len, out, workspace, *, K=1,
+                      q_len=None, scale=1.0, lse=None, dev_status=None, stream=None):
+    """Absorbed latent attention of K query positions a request over a paged cache (see
+    include/kda.h).  q_latent [R*K, H, 512], q_rope [R*K, H, 64] and out [R*K, H, 512] may be
+    strided over rows and heads."""
+    RK, H, dl = q_latent.shape
+    dr = q_rope.shape[2]
+    R = int(block_table.shape[0])
+    K = int(K)
+    if K < 0 or RK != R * K:
+        raise ValueError(f"q_latent has {RK} rows, not {R} requests x K = {K}")
+    _same("q_rope", q_rope, RK, H, dr)
+    _same("out", out, RK, H, dl)
+    _same("seq_len", seq_len, R)
+    if q_len is not None:
+        _same("q_len", q_len, R)
+    if lse is not None:
+        _same("lse", lse, RK, H)
+    P, page, stride = _cache_pages(cache)
+    _same("cache", cache, P, page, dl + dr)
+    dt = {t.dtype for t in (q_latent, q_rope, cache)}
+    if len(dt) != 1:
+        raise ValueError(f"queries and cache must share one dtype, got {sorted(map(str, dt))}")
+    st = lib().kda_latent_decode(
+        _rows(q_latent, "q_latent"), _rows(q_rope, "q_rope"), _dt3(q_latent), R, K,
+        _idx(q_len, "q_len"), H, dl, dr, float(scale), _p_any(cache), P, page, stride,
+        _idx(block_table, "block_table"), int(block_table.shape[1]), _idx(seq_len, "seq_len"),
+        _rows(out, "out"), _dt3(out), None if lse is None else _f32(lse, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _idx(dev_status, "dev_status"),
+        _stream(stream))
+    _check(st, "kda_latent_decode")
+
+
+def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, *, scale=1.0, flags=0, lse=None,
+                       dev_status=None, stream=None):
+    """Expanded latent attention of packed sequences (see include/kda.h).  q [Tq, H, 192],
+    k_nope and v [Tk, H, 128] and out [Tq, H, 128] may be strided over rows and heads;
+    k_rope [Tk, 64] over rows."""
+    Tq, H, dq = q.shape
+    Tk, _, dn = k_nope.shape
+    dr, dv = k_rope.shape[1], v.shape[2]
+    _same("q", q, Tq, H, dn + dr)
+    _same("k_nope", k_nope, Tk, H, dn)
+    _same("k_rope", k_rope, Tk, dr)
+    _same("v", v, Tk, H, dv)
+    _same("out", out, Tq, H, dv)
+    _same("cu_k", cu_k, *cu_q.shape)
+    if lse is not None:
+        _same("lse", lse, Tq, H)
+    if Tk and k_rope.stride(1) != 1:
+        raise ValueError("k_rope needs contiguous rows")
+    dt = {t.dtype for t in (q, k_nope, k_rope, v)}
+    if len(dt) != 1:
+        raise ValueError(f"queries, keys and values must share one dtype, got {sorted(map(str, dt))}")
+    st = lib().kda_latent_prefill(
+        _rows(q, "q"), _rows(k_nope, "k_nope"), _p_any(k_rope),
+        k_rope.stride(0) if Tk > 1 else dr, _rows(v, "v"), _dt3(q), _idx(cu_q, "cu_q"),
+        _idx(cu_k, "cu_k"), int(cu_q.shape[0]) - 1, Tq, Tk, H, dn, dr, dv, float(scale),
+        int(flags), _rows(out, "out"), _dt3(out), None if lse is None else _f32(lse, "lse"),
+        _idx(dev_status, "dev_status"), _stream(stream))
+    _check(st, "kda_latent_prefill")
+
+
+def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, top_logprobs=None,
+                       dev_status=None, stream=None):
+    """Log probability of given tokens, entropy and top alternatives of logits rows (see
+    include/kda.h).  logits [R, V] (rows may be strided), tokens [R]; top_ids and top_logprobs
+    [R, top]."""
+    R, V = logits.shape
+    _same("tokens", tokens, R)
+    _same("logprob", logprob, R)
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    top = 0 if top_ids is None else int(top_ids.shape[1])
+    if top_ids is not None:
+        _same("top_ids", top_ids, R, top)
+        _same("top_logprobs", top_logprobs, R, top)
+    if entropy is not None:
+        _same("entropy", entropy, R)
+    if R and logits.stride(1) != 1 and V > 1:
+        raise ValueError("logits needs contiguous rows")
+    st = lib().kda_token_logprobs(
+        _p_any(logits), logits.stride(0) if R > 1 else V, _dt3(logits), R, V,
+        _idx(tokens, "tokens"), _f32(logprob, "logprob"),
+        None if entropy is None else _f32(entropy, "entropy"), top, _idx(top_ids, "top_ids"),
+        None if top_logprobs is None else _f32(top_logprobs, "top_logprobs"),
+        _idx(dev_status, "dev_status"), _stream(stream))
+    _check(st, "kda_token_logprobs")

@@ -1,0 +1,64 @@
+// latent_common.cuh -- element types and shapes shared by the latent attention
+// and log-probability kernels.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+constexpr int kLatent = 512;                  // latent vector of a token
+constexpr int kRope = 64;                     // rope key of a token
+constexpr int kLatentRow = kLatent + kRope;   // one cache row
+constexpr int kNope = 128;                    // a head's expanded key, without the rope part
+constexpr int kHeadK = kNope + kRope;
+constexpr int kHeadV = 128;
+
+// Element types of these calls: bf16, fp16 and fp32, widened exactly on load and rounded once
+// (to nearest even) on store.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<KDA_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float get(T x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ T put(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ float2 get2(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) { return pack_bf16x2(a, b); }
+};
+template <>
+struct Elem<KDA_F16> {
+    using T = __half;
+    static __device__ __forceinline__ float get(T x) { return __half2float(x); }
+    static __device__ __forceinline__ T put(float x) { return __float2half_rn(x); }
+    static __device__ __forceinline__ float2 get2(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
+struct Elem<KDA_F32> {
+    using T = float;
+    static __device__ __forceinline__ float get(T x) { return x; }
+    static __device__ __forceinline__ T put(float x) { return x; }
+};
+
+__host__ __device__ constexpr int dtype_bytes(int dt) { return dt == KDA_F32 ? 4 : 2; }
+
+// Four consecutive fp32 results (index i % 4 == 0) rounded into an output of type dt.
+__device__ __forceinline__ void store4_as(void* p, int64_t i, float4 x, int dt) {
+    if (dt == KDA_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+    else if (dt == KDA_BF16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
+            make_uint2(Elem<KDA_BF16>::put2(x.x, x.y), Elem<KDA_BF16>::put2(x.z, x.w));
+    else
+        *reinterpret_cast<uint2*>(static_cast<__half*>(p) + i) =
+            make_uint2(Elem<KDA_F16>::put2(x.x, x.y), Elem<KDA_F16>::put2(x.z, x.w));
+}
+
+}  // namespace kda
