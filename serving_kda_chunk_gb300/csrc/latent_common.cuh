@@ -49,6 +49,23 @@ struct Elem<KDA_F32> {
 
 __host__ __device__ constexpr int dtype_bytes(int dt) { return dt == KDA_F32 ? 4 : 2; }
 
+// 2^x (relative error about 2^-22; -inf gives 0, results below the normal range 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One fp32 result rounded into an output of type dt.
+__device__ __forceinline__ void store1_as(void* p, int64_t i, float x, int dt) {
+    if (dt == KDA_F32)
+        static_cast<float*>(p)[i] = x;
+    else if (dt == KDA_BF16)
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+    else
+        static_cast<__half*>(p)[i] = __float2half_rn(x);
+}
+
 // Four consecutive fp32 results (index i % 4 == 0) rounded into an output of type dt.
 __device__ __forceinline__ void store4_as(void* p, int64_t i, float4 x, int dt) {
     if (dt == KDA_F32)

@@ -1,0 +1,690 @@
+// latent_decode.cu -- kda_latent_decode: absorbed latent attention over a paged cache.
+//
+// One latent row (1152 bytes) serves every head as key and, its first 1024 bytes, as value, so a
+// request's tokens are read once for up to 64 query rows (positions x heads).  Tokens come 64 at a
+// time; with Q the query rows [N, 576], C a tile [64, 576] and V its first 512 channels:
+//   S   = Q C^T          M = 128 (rows N.. of A are whatever follows Q; their lanes are not read), N = 64
+//   P   = 2^(c S - m)    c = scale log2 e, one thread a query row, m a running maximum
+//   O^T += V^T P^T       4 products M = 128 value channels, N rows, K = 64 tokens
+// O stays transposed in TMEM (lane = value channel): 512 fp32 channels of 128 rows would take all
+// 512 columns, transposed they take 4 N, and few query rows waste no tensor-core rows in this
+// product.  The tile is used as it lies in shared memory: K-major for S, MN-major for V^T.
+// m moves only when a row's maximum exceeds it by 8 (a factor of 256, far inside fp32 and fp16):
+// rescaling O is then rare, and exact up to fp32 rounding.
+//
+// Work: all (row tile, request, token tile) triples in one line, cut into equal ranges, one a CTA
+// and SM, so ragged and few long requests load every SM alike.  A CTA walks its range through
+// whole requests (written as results) and at most two partial ones (unnormalised O, m and l to the
+// workspace, joined by combine_kernel).
+//
+// Roles: warp 0 loads (TMA boxes of one page's rows, a ring of 128-channel pairs so that a part is
+// free for the next tile as soon as its product is done), warp 1 issues MMAs, whichever of S(i+1)
+// and O(i) is ready first, warps 4-7 do softmax, rescaling, queries and results.
+#include "kda_host.h"
+#include "latent_common.cuh"
+#include "latent_host.h"
+#include "umma.cuh"
+
+namespace kda {
+namespace {
+
+using namespace umma;
+
+constexpr int kTile = 64;                   // tokens a tile
+constexpr int kDecCtas = 152;               // one a SM
+constexpr int kDecThreads = 256;
+constexpr uint32_t kDecWait = 1u << 18;     // polls, about a second: loads and MMAs take microseconds
+constexpr uint32_t kPairBytes = 2 * kTile * 128;  // two 64-channel columns of a tile
+constexpr uint32_t kRopeBytes = kTile * 128;
+
+struct DecodeArgs {
+    LatentRows ql, qr;
+    int32_t R, K;
+    const int32_t* q_len;
+    int32_t H;
+    float c;        // |scale| log2 e
+    bool negate;    // scale < 0
+    int64_t P;
+    int32_t page_size, box;  // box: rows of one TMA box, a divisor of page_size and of kTile
+    const int32_t* table;
+    int32_t max_pages;
+    const int32_t* seq_len;
+    void* out;
+    int64_t out_rs, out_hs;
+    int32_t out_dt;
+    float* lse;
+    int32_t n_rt;   // row tiles of a request
+    int4* meta;     // [CTAs] the request whose first part this CTA holds: (r, row tile, last CTA, -) or r = -1
+    float2* ml;     // [2 CTAs][N] (m in log2 units, l)
+    float* part;    // [2 CTAs][N][512]
+    int32_t* dev_status;
+};
+
+template <int N>
+struct DecLayout {
+    static constexpr int PAIRS = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of channel pairs, 4 a tile
+    static constexpr int ROPES = N == 64 ? 2 : 3;
+    static constexpr uint32_t Q = 0;
+    static constexpr uint32_t PAIR = Q + N * kLatentRow * 2;
+    static constexpr uint32_t ROPE = PAIR + PAIRS * kPairBytes;
+    static constexpr uint32_t P = ROPE + ROPES * kRopeBytes;
+    static constexpr uint32_t MISC = P + N * 128;
+    // MISC: barriers, then per-row floats
+    static constexpr int B_FULL = 0, B_EMPTY = PAIRS, B_RFULL = 2 * PAIRS, B_REMPTY = B_RFULL + ROPES,
+                         B_S = B_REMPTY + ROPES, B_P = B_S + 2, B_PV = B_P + 1, B_Q = B_PV + 1, B_DRAIN = B_Q + 1,
+                         BARS = B_DRAIN + 1;
+    static constexpr uint32_t ROWF = MISC + 8 * 40;      // [N] row factors
+    static constexpr uint32_t BAD = ROWF + 4 * N;        // [ROPES] bad boxes of the tile in a rope slot
+    static constexpr uint32_t CTRL = BAD + 16;           // tmem address, dead flag, start of the range
+    static constexpr uint32_t SCAN = CTRL + 48;          // [8] warp sums
+    static constexpr uint32_t ROWO = SCAN + 64;          // [N] output offsets of the rows
+    static constexpr uint32_t SMEM = ROWO + 8 * N;
+    static constexpr int TMEM = N == 64 ? 512 : 256;
+    static constexpr uint32_t TM_S = 4 * N;
+    static_assert(BARS <= 40 && SMEM <= 232448, "shared memory plan");
+};
+
+// Length and query count of a request as the kernel uses them: an invalid one has none.
+__device__ __forceinline__ int request(const DecodeArgs& a, int r, int& ql, int& err) {
+    int len = a.seq_len[r];
+    ql = a.q_len ? a.q_len[r] : a.K;
+    err = 0;
+    if (len < 0 || len > (int64_t)a.max_pages * a.page_size) {
+        err = KDA_DEV_BAD_SEQLEN;
+        len = 0;
+    }
+    if (ql < 0 || ql > a.K) {
+        err |= KDA_DEV_BAD_ACCEPT;
+        ql = len = 0;
+    }
+    return len;
+}
+// token tiles of a request; one without tokens takes one (empty) tile, for its zero rows
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+
+// The walk over a CTA's range: next() gives the tiles [j0, j1) of request r, row tile rt.
+struct Walk {
+    int r, rt, j;
+    long long left;
+    int j0, j1, n, len, ql, err;
+    int cr, crt;
+    __device__ __forceinline__ bool next(const DecodeArgs& a) {
+        if (left <= 0) return false;
+        cr = r;
+        crt = rt;
+        len = request(a, r, ql, err);
+        n = tiles_of(len);
+        j0 = j;
+        j1 = (long long)(n - j) <= left ? n : j + (int)left;
+        left -= j1 - j0;
+        j = j1;
+        if (j == n) {
+            j = 0;
+            if (++r == a.R) {
+                r = 0;
+                ++rt;
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int N, int DT>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ DecodeArgs a) {
+    using L = DecLayout<N>;
+    using E = Elem<DT>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) { return sb + L::MISC + 8 * i; };
+    float* rowf = reinterpret_cast<float*>(sm + L::ROWF);
+    volatile int* bad_box = reinterpret_cast<int*>(sm + L::BAD);
+    volatile int* ctrl = reinterpret_cast<int*>(sm + L::CTRL);  // 0 tmem, 1 dead, 2 r, 3 rt, 4 j
+    int64_t* rowo = reinterpret_cast<int64_t*>(sm + L::ROWO);
+    long long* scan = reinterpret_cast<long long*>(sm + L::SCAN);
+    const float inf = __int_as_float(0x7f800000);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (int i = 0; i < L::BARS; ++i) mbar_init(bar(i), i == L::B_P || i == L::B_Q ? 4 : 1);
+        ctrl[1] = 0;
+        ctrl[2] = -1;
+    }
+    if (warp == 1) tmem_alloc(sb + L::CTRL, L::TMEM);
+
+    // ---- this CTA's range: tiles of all requests, then the request its start falls into
+    long long mine = 0;
+    for (int r = tid; r < a.R; r += kDecThreads) {
+        int ql, err;
+        mine += tiles_of(request(a, r, ql, err));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) scan[warp] = mine;
+    __syncthreads();
+    long long S = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) S += scan[w];
+    const long long T = S * a.n_rt;
+    const long long G = T < gridDim.x ? T : gridDim.x;  // CTAs with work: each has a tile at least
+    const bool work = blockIdx.x < G;
+    const long long g0 = work ? T * blockIdx.x / G : 0, g1 = work ? T * (blockIdx.x + 1) / G : 0;
+    const int rt0 = (int)(g0 / S);
+    const long long want = g0 - rt0 * S;
+    long long before = 0;
+    for (int base = 0; base < a.R; base += kDecThreads) {
+        __syncthreads();
+        int ql, err;
+        const int r = base + tid;
+        const long long n = r < a.R ? tiles_of(request(a, r, ql, err)) : 0;
+        long long x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        long long off = before;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) off += scan[w];
+            before += scan[w];
+        }
+        const long long lo = off + x - n;
+        if (n > 0 && want >= lo && want < lo + n) {
+            ctrl[2] = r;
+            ctrl[3] = rt0;
+            ctrl[4] = (int)(want - lo);
+        }
+        if (before > want) break;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctrl[0];
+    Walk w;
+    w.r = ctrl[2];
+    w.rt = ctrl[3];
+    w.j = ctrl[4];
+    w.left = w.r < 0 ? 0 : g1 - g0;
+    bool dead = false;
+    // a wait that gives up marks the CTA: every role leaves its loop at its next wait
+    auto wait = [&](int b, uint32_t parity) {
+        if (dead) return;
+        if (!mbar_wait(bar(b), parity, kDecWait)) {
+            dead = true;
+            ctrl[1] = 1;
+            report(a.dev_status, KDA_DEV_TIMEOUT);
+        }
+    };
+
+    if (warp == 0) {
+        // ================================================================ loads
+        const int per = kTile / a.box;
+        uint32_t slot = 0, sph = 1, rslot = 0, rph = 1;  // empty barriers: the first pass finds them free
+        uint32_t filled = 0, rfilled = 0;
+        while (!dead && w.next(a)) {
+            const int32_t* tab = a.table + (int64_t)w.cr * a.max_pages;
+            auto page_of = [&](int j) {
+                const int64_t t = (int64_t)j * kTile + lane * a.box;
+                return lane < per && t < w.len ? tab[t / a.page_size] : -1;
+            };
+            int next = page_of(w.j0);
+            for (int j = w.j0; j < w.j1 && !dead; ++j) {
+                const int page = next;
+                if (j + 1 < w.j1) next = page_of(j + 1);
+                const int y = (int)(((int64_t)j * kTile + lane * a.box) % a.page_size);
+                const bool has = lane < per && (int64_t)j * kTile + lane * a.box < w.len;
+                const bool ok = has && page >= 0 && page < a.P;
+                const uint32_t okm = __ballot_sync(~0u, ok);
+                const uint32_t badm = __ballot_sync(~0u, has && !ok);
+                const uint32_t bytes = (uint32_t)__popc(okm) * a.box * 128;
+                if (badm && lane == 0) report(a.dev_status, KDA_DEV_BAD_SLOT);
+                for (int p = 0; p < 4; ++p) {
+                    wait(L::B_EMPTY + slot, sph);
+                    dead = __any_sync(~0u, dead);
+                    if (dead) break;
+                    if (lane == 0) mbar_expect_tx(bar(L::B_FULL + slot), 2 * bytes);
+                    __syncwarp();
+                    if (ok) {
+                        const uint32_t dst = sb + L::PAIR + slot * kPairBytes + lane * a.box * 128;
+                        tma_load_3d(dst, &map, p * 128, y, page, bar(L::B_FULL + slot));
+                        tma_load_3d(dst + kTile * 128, &map, p * 128 + 64, y, page, bar(L::B_FULL + slot));
+                    }
+                    ++filled;
+                    if (++slot == L::PAIRS) slot = 0, sph ^= 1;
+                }
+                if (dead) break;
+                wait(L::B_REMPTY + rslot, rph);
+                dead = __any_sync(~0u, dead);
+                if (dead) break;
+                if (lane == 0) {
+                    bad_box[rslot] = (int)badm;
+                    mbar_expect_tx(bar(L::B_RFULL + rslot), bytes);
+                }
+                __syncwarp();
+                if (ok)
+                    tma_load_3d(sb + L::ROPE + rslot * kRopeBytes + lane * a.box * 128, &map, kLatent, y, page,
+                                bar(L::B_RFULL + rslot));
+                ++rfilled;
+                if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
+            }
+            if (ctrl[1]) dead = true;
+            dead = __any_sync(~0u, dead);
+        }
+        // nothing may be in flight when the CTA ends: every slot's last load has landed
+        dead = false;
+        for (int i = 0; i < L::PAIRS; ++i)
+            if ((uint32_t)i < filled) wait(L::B_FULL + i, ((filled - 1 - i) / L::PAIRS) & 1);
+        for (int i = 0; i < L::ROPES; ++i)
+            if ((uint32_t)i < rfilled) wait(L::B_RFULL + i, ((rfilled - 1 - i) / L::ROPES) & 1);
+    } else if (warp == 1) {
+        // ================================================================ MMAs
+        if (lane == 0) {
+            const uint32_t sb4 = sb >> 4;
+            const uint32_t ids = idesc_16(DT == KDA_F16, 128, kTile, false, false, a.negate);
+            const uint32_t idv = idesc_16(DT == KDA_F16, 128, N, true, false, false);
+            Walk ws = w;  // S runs up to one tile ahead of O, over its own copy of the walk
+            bool more_s = ws.next(a), more_v = w.next(a);
+            int js = ws.j0, jv = w.j0;
+            uint32_t s_it = 0, v_it = 0;                  // tiles issued
+            uint32_t s_slot = 0, s_ph = 0, v_slot = 0, r_slot = 0, r_ph = 0, vr_slot = 0, segs = 0;
+            uint32_t idle = 0;
+            while (more_v && !dead) {
+                bool did = false;
+                if (more_s && s_it <= v_it + 1) {
+                    bool ready = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
+                    if (ready && js == ws.j0) ready = mbar_test(bar(L::B_Q), segs & 1);
+                    if (ready) {
+                        if (js == ws.j0) ++segs;
+                        const uint32_t d = tmem + L::TM_S + (s_it & 1) * kTile;
+                        for (int p = 0; p < 4; ++p) {
+                            wait(L::B_FULL + s_slot, s_ph);
+                            fence_after();
+                            const uint32_t b4 = sb4 + (L::PAIR + s_slot * kPairBytes) / 16;
+#pragma unroll
+                            for (int s = 0; s < 8; ++s)
+                                mma(d, desc_k4(sb4 + L::Q / 16, N, 8 * p + s), desc_k4(b4, kTile, s), ids, p + s != 0);
+                            if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
+                        }
+                        const uint32_t b4 = sb4 + (L::ROPE + r_slot * kRopeBytes) / 16;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma(d, desc_k4(sb4 + L::Q / 16, N, 32 + s), desc_k4(b4, kTile, s), ids, 1);
+                        commit(bar(L::B_S + (s_it & 1)));
+                        if (++r_slot == L::ROPES) r_slot = 0, r_ph ^= 1;
+                        ++s_it;
+                        if (++js == ws.j1) {
+                            more_s = ws.next(a);
+                            js = ws.j0;
+                        }
+                        did = true;
+                    }
+                }
+                if (v_it < s_it && mbar_test(bar(L::B_P), v_it & 1)) {
+                    fence_after();
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t a4 = sb4 + (L::PAIR + v_slot * kPairBytes) / 16;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma(tmem + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(sb4 + L::P / 16, N, s), idv,
+                                jv != w.j0 || s != 0);
+                        commit(bar(L::B_EMPTY + v_slot));
+                        if (++v_slot == L::PAIRS) v_slot = 0;
+                    }
+                    // the rope slot goes back with the tile, not with S: the softmax of this tile has
+                    // read the slot's bad boxes and waited on its barrier by now
+                    commit(bar(L::B_REMPTY + vr_slot));
+                    if (++vr_slot == L::ROPES) vr_slot = 0;
+                    commit(bar(L::B_PV));
+                    ++v_it;
+                    if (++jv == w.j1) {
+                        more_v = w.next(a);
+                        jv = w.j0;
+                    }
+                    did = true;
+                }
+                if (did) {
+                    idle = 0;
+                } else if (++idle > (1u << 24) || ctrl[1]) {  // test_wait polls of some tens of cycles: about a second
+                    dead = true;
+                    ctrl[1] = 1;
+                    report(a.dev_status, KDA_DEV_TIMEOUT);
+                }
+            }
+            commit(bar(L::B_DRAIN));
+            dead = false;
+            wait(L::B_DRAIN, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================================================================ softmax, queries, results
+        const int q4 = warp - 4, t = tid - 128;
+        const uint32_t tq = tmem + ((uint32_t)(q4 * 32) << 16);
+        const bool has_rows = q4 * 32 < N;
+        const int row = t;  // of the row tile, when has_rows and row < N
+        auto load_q = [&](int r, int rt) {
+            // 16-byte words of the rows: 72 a row; rows past the end are zero
+            const int rows = min(N, a.K * a.H - rt * N);
+            for (int e = t; e < N * 72; e += 128) {
+                const int i = e / 72, x = e - i * 72;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (i < rows) {
+                    const int f = rt * N + i, tt = f / a.H, h = f - tt * a.H;
+                    const int64_t qrow = (int64_t)r * a.K + tt;
+                    const uint16_t* src = x < 64 ? a.ql.base + qrow * a.ql.rs + h * a.ql.hs + x * 8
+                                                 : a.qr.base + qrow * a.qr.rs + h * a.qr.hs + (x - 64) * 8;
+                    v = __ldg(reinterpret_cast<const uint4*>(src));
+                }
+                sts16(sb + L::Q + chunk_k(i, x * 8, N), v);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::B_Q));
+        };
+        if (t == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        uint32_t it = 0, rslot = 0, rph = 0;
+        bool more = w.next(a), quit = false;  // quit: agreed by the four warps, so that barriers stay matched
+        if (more) load_q(w.cr, w.crt);
+        while (more && !quit) {
+            const Walk g = w;  // this segment
+            if (t == 0 && g.j0 == 0 && g.crt == 0 && g.err) report(a.dev_status, g.err);
+            float m = -inf, l = 0.f;
+            int last = -1;  // last token this thread's row sees
+            const int f = g.crt * N + row;
+            if (has_rows && row < N && f < a.K * a.H) {
+                const int tt = f / a.H;
+                if (tt < g.ql) last = g.len - g.ql + tt;
+            }
+            for (int j = g.j0; j < g.j1; ++j, ++it) {
+                float s[kTile];
+                float f_old = 1.f;
+                bool need = false;
+                wait(L::B_S + (it & 1), (it >> 1) & 1);
+                wait(L::B_RFULL + rslot, rph);
+                fence_after();
+                const int t0 = j * kTile;
+                const uint32_t bad = (uint32_t)bad_box[rslot];
+                if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
+                const int valid = g.len - t0;  // tokens of this tile (may exceed it)
+                if (has_rows) {
+                    float x0[32];
+                    ld32(tq + L::TM_S + (it & 1) * kTile, x0);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = x0[i];
+                    ld32(tq + L::TM_S + (it & 1) * kTile + 32, x0);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[32 + i] = x0[i];
+                    if (bad) {
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            if ((bad >> (i / a.box)) & 1) s[i] = -inf;
+                    }
+                    const int lim = last - t0;  // columns 0 .. lim are seen
+                    if (lim < kTile - 1) {
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            if (i > lim) s[i] = -inf;
+                    }
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int i = 4; i < kTile; i += 4)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], s[i + q]);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (j == g.j0) {
+                        m = mt;
+                    } else if (mt > m && (m == -inf || (mt - m) * a.c > 8.f)) {
+                        f_old = ex2((m - mt) * a.c);
+                        m = mt;
+                        need = true;
+                        l *= f_old;
+                    }
+                    if (row < N) rowf[row] = f_old;
+                    const float mc = m == -inf ? 0.f : m * a.c;
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 2) {
+                        s[i] = ex2(fmaf(s[i], a.c, -mc));
+                        s[i + 1] = ex2(fmaf(s[i + 1], a.c, -mc));
+                        l0 += s[i];
+                        l1 += s[i + 1];
+                    }
+                    l += l0 + l1;
+                }
+                // every thread of the role: does any row move its maximum (or has a wait given up)?
+                const bool any = bar_named_or(1, 128, need || dead);
+                if (j > g.j0 || it > 0) wait(L::B_PV, (it - 1) & 1);  // O and P free of the previous tile's product
+                if (any) {
+                    quit = bar_named_or(1, 128, dead || ctrl[1]);
+                    if (quit) break;
+                    fence_after();
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int n0 = 0; n0 < N; n0 += 16) {
+                            float o[16];
+                            ld16(tq + c * N + n0, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= rowf[n0 + i];
+                            st16f(tq + c * N + n0, o);
+                        }
+                    wait_st();
+                    bar_named(1, 128);  // rowf has been read
+                }
+                if (has_rows && row < N) {
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 8)
+                        sts16(sb + L::P + chunk_k(row, i, N),
+                              make_uint4(E::put2(s[i], s[i + 1]), E::put2(s[i + 2], s[i + 3]),
+                                         E::put2(s[i + 4], s[i + 5]), E::put2(s[i + 6], s[i + 7])));
+                }
+                if (valid < kTile || bad) {
+                    // tokens that are not there: their weight is zero, and so has to be the value
+                    // (what lies in the buffer, or past the end of a page, may be anything)
+                    const uint32_t first = it * 4;
+                    for (int e = t; e < kTile * 64; e += 128) {
+                        const int k = e >> 6, x = e & 63;  // token, 16-byte word of 512 channels
+                        if (k >= valid || ((bad >> (k / a.box)) & 1)) {
+                            const uint32_t slot = (first + (x >> 4)) % L::PAIRS;
+                            sts16(sb + L::PAIR + slot * kPairBytes + (uint32_t)(((x >> 3) & 1) * kTile * 128 + k * 128 + (x & 7) * 16),
+                                  make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                }
+                fence_async_smem();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_P));
+            }
+            if (quit) break;
+            // the next segment's queries: every S of this one has been read
+            more = w.next(a);
+            if (more) load_q(w.cr, w.crt);
+            // results of this segment
+            const bool whole = g.j0 == 0 && g.j1 == g.n;
+            const int slot = 2 * (int)blockIdx.x + (g.j0 == 0);
+            const int rows = min(N, a.K * a.H - g.crt * N);
+            bar_named(1, 128);  // rowf of the last tile has been read
+            if (has_rows && row < N) {
+                rowf[row] = l > 0.f ? 1.f / l : 0.f;
+                rowo[row] = ((int64_t)g.cr * a.K + f / a.H) * a.out_rs + (f % a.H) * a.out_hs;
+                const float m2 = m == -inf ? -inf : m * a.c;
+                if (!whole) {
+                    a.ml[(int64_t)slot * N + row] = make_float2(m2, l);
+                } else if (a.lse != nullptr && row < rows) {
+                    const int tt = f / a.H, h = f - tt * a.H;
+                    a.lse[((int64_t)g.cr * a.K + tt) * a.H + h] = l > 0.f ? (m2 + log2f(l)) * 0.69314718055994531f : -inf;
+                }
+            }
+            if (t == 0 && !whole && g.j0 == 0) {
+                // the last CTA with a part of this request
+                const long long end = g1 + (g.n - g.j1);  // this part ends the range
+                long long last_cta = (end - 1) * G / T;
+                while (T * (last_cta + 1) / G < end) ++last_cta;
+                while (T * last_cta / G >= end) --last_cta;
+                a.meta[blockIdx.x] = make_int4(g.cr, g.crt, (int)last_cta, 0);
+            }
+            bar_named(1, 128);
+            wait(L::B_PV, (it - 1) & 1);
+            fence_after();
+            for (int c = 0; c < 4; ++c) {
+                const int ch = c * 128 + t;
+#pragma unroll
+                for (int n0 = 0; n0 < N; n0 += 16) {
+                    float o[16];
+                    ld16(tq + c * N + n0, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int rr = n0 + i;
+                        if (rr >= rows) continue;
+                        if (whole) {
+                            store1_as(a.out, rowo[rr] + ch, o[i] * rowf[rr], a.out_dt);
+                        } else {
+                            a.part[((int64_t)slot * N + rr) * kLatent + ch] = o[i];
+                        }
+                    }
+                }
+            }
+            fence_before();
+            bar_named(1, 128);  // rowf read by all before the next segment writes it
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) tmem_dealloc(tmem, L::TMEM);
+}
+
+// Joins the parts of a request that several CTAs hold: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i.
+// Block (g, y): rows 4y .. 4y + 3 of the request whose first part CTA g holds; a thread has 4 channels.
+template <int N>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int g = blockIdx.x, t = threadIdx.x;
+    const int4 me = a.meta[g];
+    if (me.x < 0) return;
+    const int rows = min(N, a.K * a.H - me.y * N);
+    const float inf = __int_as_float(0x7f800000);
+    for (int row = blockIdx.y * 4; row < min(rows, (int)blockIdx.y * 4 + 4); ++row) {
+        float m = -inf;
+        for (int i = g; i <= me.z; ++i) m = fmaxf(m, a.ml[(int64_t)(2 * i + (i == g)) * N + row].x);
+        const float mr = m == -inf ? 0.f : m;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = g; i <= me.z; ++i) {
+            const int64_t at = (int64_t)(2 * i + (i == g)) * N + row;
+            const float2 ml = a.ml[at];
+            const float4 x = *reinterpret_cast<const float4*>(a.part + at * kLatent + 4 * t);
+            const float f = ex2(ml.x - mr);
+            l = fmaf(f, ml.y, l);
+            o.x = fmaf(f, x.x, o.x);
+            o.y = fmaf(f, x.y, o.y);
+            o.z = fmaf(f, x.z, o.z);
+            o.w = fmaf(f, x.w, o.w);
+        }
+        const float il = l > 0.f ? 1.f / l : 0.f;
+        const int f = me.y * N + row, tt = f / a.H, h = f - tt * a.H;
+        const int64_t orow = (int64_t)me.x * a.K + tt;
+        store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il),
+                  a.out_dt);
+        if (t == 0 && a.lse != nullptr)
+            a.lse[orow * a.H + h] = l > 0.f ? (mr + log2f(l)) * 0.69314718055994531f : -inf;
+    }
+}
+
+int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
+
+template <int N, int DT>
+kda_status launch(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
+    using L = DecLayout<N>;
+    auto* f = decode_kernel<N, DT>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    // every (row tile, request) has at least one tile and at most max_tiles
+    const int64_t most = (int64_t)a.n_rt * a.R * max_tiles;
+    const unsigned grid = (unsigned)(most < kDecCtas ? most : kDecCtas);
+    f<<<grid, kDecThreads, L::SMEM, s>>>(map, a);
+    if (max_tiles <= 1) return launch_status();  // one tile a request: nothing is split
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, N / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<N>, a) != cudaSuccess) return KDA_ERR_CUDA;
+    return launch_status();
+}
+
+template <int DT>
+kda_status launch_n(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
+    const int n = tile_rows((int64_t)a.K * a.H);
+    if (n == 16) return launch<16, DT>(map, a, max_tiles, s);
+    if (n == 32) return launch<32, DT>(map, a, max_tiles, s);
+    return launch<64, DT>(map, a, max_tiles, s);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t H) {
+    if (R < 0 || K < 0 || H < 0) return 16;
+    const size_t n = (size_t)tile_rows((int64_t)K * H);
+    return align16(kDecCtas * sizeof(int4)) + 2 * kDecCtas * n * (sizeof(float2) + kLatent * sizeof(float));
+}
+
+extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,
+                                        kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
+                                        int32_t H, int32_t d_latent, int32_t d_rope, float scale,
+                                        const void* cache, int64_t P, int32_t page_size,
+                                        int64_t page_stride, const int32_t* block_table,
+                                        int32_t max_pages, const int32_t* seq_len,
+                                        const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
+                                        void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                        void* stream) {
+    KDA_REQUIRE(R >= 0 && K >= 0 && H > 0 && P >= 0 && page_size > 0 && max_pages >= 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(d_latent == kLatent && d_rope == kRope && K <= 16, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(page_size % 8 == 0 && (int64_t)R * K * H < (1ll << 31), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE((int64_t)max_pages * page_size < (1ll << 31) - kTile && P < (1ll << 31), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
+    if (R == 0 || K == 0) return KDA_OK;
+    KDA_REQUIRE(rows_ok(q_latent) && rows_ok(q_rope) && rows_ok(out), KDA_ERR_INVALID_ARG);
+    const void* ptrs[] = {cache, block_table, seq_len, workspace};
+    for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(aligned16(q_len) && aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(ws_bytes >= kda_latent_decode_workspace_size(R, K, H), KDA_ERR_INVALID_ARG);
+    const int box = lowbit_box(page_size, kTile);
+    CUtensorMap map;
+    // the cache as pages of rows: one box is `box` rows of one page, 64 channels (a 128-byte swizzle row)
+    const cuuint64_t dims[3] = {kLatentRow, (cuuint64_t)page_size, (cuuint64_t)(P > 0 ? P : 1)};
+    const cuuint64_t strides[2] = {kLatentRow * 2, (cuuint64_t)page_stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
+    KDA_REQUIRE(encode_16bit(&map, in_dtype, 3, cache, dims, strides, boxes), KDA_ERR_CUDA);
+    const int n = tile_rows((int64_t)K * H);
+    DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
+                 block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
+                 out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, nullptr, nullptr, dev_status};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.meta = reinterpret_cast<int4*>(ws);
+    ws += align16(kDecCtas * sizeof(int4));
+    a.part = reinterpret_cast<float*>(ws);
+    ws += (size_t)2 * kDecCtas * n * kLatent * sizeof(float);
+    a.ml = reinterpret_cast<float2*>(ws);
+    const int64_t max_tiles = ((int64_t)max_pages * page_size + kTile - 1) / kTile;
+    cudaStream_t s = as_stream(stream);
+    if (in_dtype == KDA_BF16) return launch_n<KDA_BF16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
+    return launch_n<KDA_F16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
+}

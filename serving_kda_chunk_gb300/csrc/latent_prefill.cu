@@ -1,42 +1,18 @@
-// latent_attn.cu -- kda_latent_decode and kda_latent_prefill: absorbed and expanded latent
-// attention, in their plain blocked form on the CUDA cores.
+// latent_prefill.cu -- kda_latent_prefill: expanded latent attention, in its plain blocked form
+// on the CUDA cores.
 //
 // A block owns 32 query rows (8 a warp) and walks its keys 32 at a time through shared memory
 // with the running maximum and sum of a softmax: o = sum_p e^{s_p - m} v_p, l = sum_p e^{s_p - m}
 // in registers, rescaled by e^{m - m'} when the maximum moves.
 #include "kda_host.h"
 #include "latent_common.cuh"
+#include "latent_host.h"
 
 namespace kda {
 namespace {
 
-struct Rows {
-    const uint16_t* base;
-    int64_t rs, hs;
-};
-
-struct DecodeArgs {
-    Rows ql, qr;
-    int32_t R, K;
-    const int32_t* q_len;
-    int32_t H;
-    float scale;
-    const uint16_t* cache;
-    int64_t P;
-    int32_t page_size;
-    int64_t page_stride;
-    const int32_t* table;
-    int32_t max_pages;
-    const int32_t* seq_len;
-    void* out;
-    int64_t out_rs, out_hs;
-    int32_t out_dt;
-    float* lse;
-    int32_t* dev_status;
-};
-
 struct PrefillArgs {
-    Rows q, k, v;
+    LatentRows q, k, v;
     const uint16_t* kr;
     int64_t kr_stride;
     const int32_t* cu_q;
@@ -125,52 +101,6 @@ __device__ __forceinline__ void put(void* out, int64_t i, float x, int dt) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(128) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    extern __shared__ float sm[];
-    using E = Elem<DT>;
-    auto ld = [](const uint16_t* p) { return E::get(*reinterpret_cast<const typename E::T*>(p)); };
-    const int r = blockIdx.x, row0 = blockIdx.y * kRowsB, rows = min(kRowsB, a.K * a.H - row0);
-    int len = a.seq_len[r], ql = a.q_len ? a.q_len[r] : a.K;
-    if (len < 0 || len > (int64_t)a.max_pages * a.page_size) {
-        if (threadIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
-        len = 0;
-    }
-    if (ql < 0 || ql > a.K) {
-        if (threadIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_ACCEPT);
-        ql = len = 0;
-    }
-    const int32_t* tab = a.table + (int64_t)r * a.max_pages;
-    auto ok = [&](int p) {
-        const int pg = tab[p / a.page_size];
-        if (pg < 0 || pg >= a.P) {
-            report(a.dev_status, KDA_DEV_BAD_SLOT);
-            return false;
-        }
-        return true;
-    };
-    auto key = [&](int p, int d) {
-        return ld(a.cache + tab[p / a.page_size] * a.page_stride + (int64_t)(p % a.page_size) * kLatentRow + d);
-    };
-    auto q = [&](int i, int d) {
-        const int t = (row0 + i) / a.H, h = (row0 + i) % a.H;
-        const int64_t row = (int64_t)r * a.K + t;
-        return d < kLatent ? ld(a.ql.base + row * a.ql.rs + h * a.ql.hs + d)
-                           : ld(a.qr.base + row * a.qr.rs + h * a.qr.hs + d - kLatent);
-    };
-    auto last = [&](int i) {
-        const int t = (row0 + i) / a.H;
-        return t < ql ? len - ql + t : -1;
-    };
-    auto store = [&](int i, int d, float x) {
-        const int t = (row0 + i) / a.H, h = (row0 + i) % a.H;
-        const int64_t row = (int64_t)r * a.K + t;
-        if (d >= 0) put(a.out, row * a.out_rs + h * a.out_hs + d, x, a.out_dt);
-        else if (a.lse) a.lse[row * a.H + h] = x;
-    };
-    attend<kLatentRow, kLatent>(sm, rows, len, a.scale, q, key, key, ok, last, store);
-}
-
-template <int DT>
 __global__ void __launch_bounds__(128) prefill_kernel(const __grid_constant__ PrefillArgs a) {
     extern __shared__ float sm[];
     using E = Elem<DT>;
@@ -207,53 +137,10 @@ __global__ void __launch_bounds__(128) prefill_kernel(const __grid_constant__ Pr
 
 constexpr int smem_of(int dk, int dv) { return (kRowsB * dk + kKeysB * (dk + 1) + kKeysB * dv) * 4; }
 
-bool rows_ok(const kda_rows_desc* d) {
-    return d != nullptr && d->base != nullptr && aligned16(d->base) && d->row_stride % 8 == 0 && d->head_stride % 8 == 0;
-}
-Rows as_rows(const kda_rows_desc* d) { return {static_cast<const uint16_t*>(d->base), d->row_stride, d->head_stride}; }
-bool out_dtype_ok(kda_dtype d) { return d == KDA_BF16 || d == KDA_F16 || d == KDA_F32; }
-
 }  // namespace
 }  // namespace kda
 
 using namespace kda;
-
-extern "C" size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t H) {
-    (void)R; (void)K; (void)H;
-    return 16;
-}
-
-extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,
-                                        kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
-                                        int32_t H, int32_t d_latent, int32_t d_rope, float scale,
-                                        const void* cache, int64_t P, int32_t page_size,
-                                        int64_t page_stride, const int32_t* block_table,
-                                        int32_t max_pages, const int32_t* seq_len,
-                                        const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
-                                        void* workspace, size_t ws_bytes, int32_t* dev_status,
-                                        void* stream) {
-    KDA_REQUIRE(R >= 0 && K >= 0 && H > 0 && P >= 0 && page_size > 0 && max_pages >= 0, KDA_ERR_INVALID_ARG);
-    KDA_REQUIRE(d_latent == kLatent && d_rope == kRope && K <= 16, KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && out_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE(page_size % 8 == 0 && (int64_t)R * K * H < (1ll << 31), KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE((int64_t)max_pages * page_size < (1ll << 31), KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
-    if (R == 0 || K == 0) return KDA_OK;
-    KDA_REQUIRE(rows_ok(q_latent) && rows_ok(q_rope) && rows_ok(out), KDA_ERR_INVALID_ARG);
-    const void* ptrs[] = {cache, block_table, seq_len, workspace};
-    for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
-    KDA_REQUIRE(aligned16(q_len) && aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
-    KDA_REQUIRE(ws_bytes >= kda_latent_decode_workspace_size(R, K, H), KDA_ERR_INVALID_ARG);
-    const DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, scale, static_cast<const uint16_t*>(cache), P,
-                       page_size, page_stride, block_table, max_pages, seq_len, const_cast<void*>(out->base),
-                       out->row_stride, out->head_stride, out_dtype, lse, dev_status};
-    const dim3 grid((unsigned)R, (unsigned)((K * H + kRowsB - 1) / kRowsB));
-    constexpr int smem = smem_of(kLatentRow, kLatent);
-    auto* f = in_dtype == KDA_BF16 ? decode_kernel<KDA_BF16> : decode_kernel<KDA_F16>;
-    cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    f<<<grid, 128, smem, as_stream(stream)>>>(a);
-    return launch_status();
-}
 
 extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
                                          const void* k_rope, int64_t k_rope_stride,
@@ -265,7 +152,7 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
                                          int32_t* dev_status, void* stream) {
     KDA_REQUIRE(N >= 0 && Tq >= 0 && Tk >= 0 && H > 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(d_nope == kNope && d_rope == kRope && dv == kHeadV, KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && out_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((flags & ~KDA_LATENT_FULL) == 0 && H < 65536, KDA_ERR_UNSUPPORTED);
     if (N == 0 || Tq == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(q) && rows_ok(out), KDA_ERR_INVALID_ARG);

@@ -69,6 +69,11 @@ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_m
            ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The same with both operands in fp16 (f16 = true) or both in bf16.
+__device__ __forceinline__ uint32_t idesc_16(bool f16, int M, int N, bool a_mn, bool b_mn, bool neg_a) {
+    return idesc_bf16(M, N, a_mn, b_mn, neg_a) & (f16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
+
 __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                     uint32_t accumulate) {
     asm volatile(
@@ -285,6 +290,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
         "%3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+        : "memory");
+}
+
+// One box of a 3-D tensor map at (x, y, z), under the same rules.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
         : "memory");
 }
 
