@@ -285,83 +285,90 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             if ((uint32_t)i < rfilled) wait(L::B_RFULL + i, ((rfilled - 1 - i) / L::ROPES) & 1);
     } else if (warp == 1) {
         // ================================================================ MMAs
-        if (lane == 0) {
-            const uint32_t sb4 = sb >> 4;
-            const uint32_t ids = idesc_16(DT == KDA_F16, 128, kTile, false, false, a.negate);
-            const uint32_t idv = idesc_16(DT == KDA_F16, 128, N, true, false, false);
-            Walk ws = w;  // S runs up to one tile ahead of O, over its own copy of the walk
-            bool more_s = ws.next(a), more_v = w.next(a);
-            int js = ws.j0, jv = w.j0;
-            uint32_t s_it = 0, v_it = 0;                  // tiles issued
-            uint32_t s_slot = 0, s_ph = 0, v_slot = 0, r_slot = 0, r_ph = 0, vr_slot = 0, segs = 0;
-            uint32_t idle = 0;
-            while (more_v && !dead) {
-                bool did = false;
-                if (more_s && s_it <= v_it + 1) {
-                    bool ready = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
-                    if (ready && js == ws.j0) ready = mbar_test(bar(L::B_Q), segs & 1);
-                    if (ready) {
-                        if (js == ws.j0) ++segs;
-                        const uint32_t d = tmem + L::TM_S + (s_it & 1) * kTile;
-                        for (int p = 0; p < 4; ++p) {
-                            wait(L::B_FULL + s_slot, s_ph);
-                            fence_after();
-                            const uint32_t b4 = sb4 + (L::PAIR + s_slot * kPairBytes) / 16;
+        // the whole warp runs this, one lane issues (umma.cuh, mma_by); votes keep the control uniform
+        const uint32_t lead = elect_lane();
+        const uint32_t sb4 = sb >> 4;
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint32_t ids = idesc_16(DT == KDA_F16, 128, kTile, false, false, a.negate);
+        const uint32_t idv = idesc_16(DT == KDA_F16, 128, N, true, false, false);
+        Walk ws = w;  // S runs up to one tile ahead of O, over its own copy of the walk
+        bool more_s = __any_sync(~0u, ws.next(a)), more_v = __any_sync(~0u, w.next(a));
+        int js = ws.j0, jv = w.j0;
+        bool first_s = true, first_v = true;          // of a segment
+        uint32_t s_it = 0, v_it = 0;                  // tiles issued
+        uint32_t s_slot = 0, s_ph = 0, v_slot = 0, r_slot = 0, r_ph = 0, vr_slot = 0, segs = 0;
+        uint32_t idle = 0;
+        bool stop = false;
+        while (more_v && !stop) {
+            bool did = false;
+            if (more_s && s_it <= v_it + 1) {
+                bool ready = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
+                if (first_s) ready = ready && mbar_test(bar(L::B_Q), segs & 1);
+                if (__all_sync(~0u, ready)) {
+                    if (first_s) ++segs;
+                    const uint32_t d = tm + L::TM_S + (s_it & 1) * kTile;
 #pragma unroll
-                            for (int s = 0; s < 8; ++s)
-                                mma(d, desc_k4(sb4 + L::Q / 16, N, 8 * p + s), desc_k4(b4, kTile, s), ids, p + s != 0);
-                            if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
-                        }
-                        const uint32_t b4 = sb4 + (L::ROPE + r_slot * kRopeBytes) / 16;
+                    for (int p = 0; p < 4; ++p) {
+                        wait(L::B_FULL + s_slot, s_ph);
+                        fence_after();
+                        const uint32_t b4 = sb4 + L::PAIR / 16 + s_slot * (kPairBytes / 16);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma(d, desc_k4(sb4 + L::Q / 16, N, 32 + s), desc_k4(b4, kTile, s), ids, 1);
-                        commit(bar(L::B_S + (s_it & 1)));
-                        if (++r_slot == L::ROPES) r_slot = 0, r_ph ^= 1;
-                        ++s_it;
-                        if (++js == ws.j1) {
-                            more_s = ws.next(a);
-                            js = ws.j0;
-                        }
-                        did = true;
+                        for (int s = 0; s < 8; ++s)
+                            mma_by(lead, d, desc_k4(sb4 + L::Q / 16, N, 8 * p + s), desc_k4(b4, kTile, s), ids,
+                                   p + s != 0);
+                        if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
                     }
-                }
-                if (v_it < s_it && mbar_test(bar(L::B_P), v_it & 1)) {
-                    fence_after();
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t a4 = sb4 + (L::PAIR + v_slot * kPairBytes) / 16;
+                    const uint32_t b4 = sb4 + L::ROPE / 16 + r_slot * (kRopeBytes / 16);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma(tmem + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(sb4 + L::P / 16, N, s), idv,
-                                jv != w.j0 || s != 0);
-                        commit(bar(L::B_EMPTY + v_slot));
-                        if (++v_slot == L::PAIRS) v_slot = 0;
-                    }
-                    // the rope slot goes back with the tile, not with S: the softmax of this tile has
-                    // read the slot's bad boxes and waited on its barrier by now
-                    commit(bar(L::B_REMPTY + vr_slot));
-                    if (++vr_slot == L::ROPES) vr_slot = 0;
-                    commit(bar(L::B_PV));
-                    ++v_it;
-                    if (++jv == w.j1) {
-                        more_v = w.next(a);
-                        jv = w.j0;
+                    for (int s = 0; s < 4; ++s)
+                        mma_by(lead, d, desc_k4(sb4 + L::Q / 16, N, 32 + s), desc_k4(b4, kTile, s), ids, 1);
+                    commit_by(lead, bar(L::B_S + (s_it & 1)));
+                    if (++r_slot == L::ROPES) r_slot = 0, r_ph ^= 1;
+                    ++s_it;
+                    first_s = __any_sync(~0u, ++js == ws.j1);
+                    if (first_s) {
+                        more_s = __any_sync(~0u, ws.next(a));
+                        js = ws.j0;
                     }
                     did = true;
                 }
-                if (did) {
-                    idle = 0;
-                } else if (++idle > (1u << 24) || ctrl[1]) {  // test_wait polls of some tens of cycles: about a second
-                    dead = true;
-                    ctrl[1] = 1;
-                    report(a.dev_status, KDA_DEV_TIMEOUT);
-                }
             }
-            commit(bar(L::B_DRAIN));
-            dead = false;
-            wait(L::B_DRAIN, 0);
+            if (v_it < s_it && __all_sync(~0u, mbar_test(bar(L::B_P), v_it & 1))) {
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a4 = sb4 + L::PAIR / 16 + v_slot * (kPairBytes / 16);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_by(lead, tm + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(sb4 + L::P / 16, N, s), idv,
+                               s != 0 || !first_v);
+                    commit_by(lead, bar(L::B_EMPTY + v_slot));
+                    if (++v_slot == L::PAIRS) v_slot = 0;
+                }
+                // the rope slot goes back with the tile, not with S: the softmax of this tile has
+                // read the slot's bad boxes and waited on its barrier by now
+                commit_by(lead, bar(L::B_REMPTY + vr_slot));
+                if (++vr_slot == L::ROPES) vr_slot = 0;
+                commit_by(lead, bar(L::B_PV));
+                ++v_it;
+                first_v = __any_sync(~0u, ++jv == w.j1);
+                if (first_v) {
+                    more_v = __any_sync(~0u, w.next(a));
+                    jv = w.j0;
+                }
+                did = true;
+            }
+            // polls of some tens of cycles: it gives up after about a second without work
+            idle = did ? 0 : idle + 1;
+            stop = __any_sync(~0u, dead || idle > (1u << 23) || ctrl[1]);
         }
-        __syncwarp();
+        if (stop && lane == 0) {
+            ctrl[1] = 1;
+            report(a.dev_status, KDA_DEV_TIMEOUT);
+        }
+        commit_by(lead, bar(L::B_DRAIN));
+        dead = false;
+        wait(L::B_DRAIN, 0);
     } else if (warp >= 4) {
         // ================================================================ softmax, queries, results
         const int q4 = warp - 4, t = tid - 128;
