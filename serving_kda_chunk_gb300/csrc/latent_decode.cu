@@ -3,8 +3,8 @@
 // One latent row (1152 bytes) serves every head as key and, its first 1024 bytes, as value, so a
 // request's tokens are read once for up to 64 query rows (positions x heads).  Tokens come 64 at a
 // time; with Q the query rows [N, 576], C a tile [64, 576] and V its first 512 channels:
-//   S   = Q C^T          M = 128 (rows N.. of A are whatever follows Q; their lanes are not read), N = 64
-//   P   = 2^(c S - m)    c = scale log2 e, one thread a query row, m a running maximum
+//   S   = Q C^T          M = 128 (the N rows repeated), N = 64 tokens, K = 576
+//   P   = 2^(c S - m)    c = scale log2 e, m a running maximum of the row
 //   O^T += V^T P^T       4 products M = 128 value channels, N rows, K = 64 tokens
 // O stays transposed in TMEM (lane = value channel): 512 fp32 channels of 128 rows would take all
 // 512 columns, transposed they take 4 N, and few query rows waste no tensor-core rows in this
@@ -60,28 +60,36 @@ struct DecodeArgs {
     int32_t* dev_status;
 };
 
+// The plan of a CTA with N query rows a tile.  Q is the A operand of S with M = 128: its N rows are
+// repeated 128 / N times along M, so that every softmax thread has a row and N / 2 of the tile's 64
+// scores.  Q lies in TMEM (32 columns a 64-channel part) as far as there are columns beside O and S:
+// all of it for N <= 32, six parts of nine for N = 64, the rest in shared memory.  An S product then
+// reads 2 KiB of shared memory instead of 6 (a product of M = 128, N = 64, K = 16 is bound by that:
+// 44 cycles against 32), and the shared memory saved holds a third tile in flight.
 template <int N>
 struct DecLayout {
-    static constexpr int PAIRS = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of channel pairs, 4 a tile
+    static constexpr int CW = N / 2;                  // scores a thread and tile
+    static constexpr int REP = 128 / N;               // copies of a row along M
+    static constexpr int QT = N == 64 ? 6 : 9;        // parts of Q in TMEM
+    static constexpr int PAIRS = N == 64 ? 9 : 12;    // ring of channel pairs, 4 a tile
     static constexpr int ROPES = N == 64 ? 2 : 3;
-    static constexpr uint32_t Q = 0;
-    static constexpr uint32_t PAIR = Q + N * kLatentRow * 2;
+    static constexpr uint32_t QS = 0;                 // parts QT .. 8 of Q, 128 rows
+    static constexpr uint32_t PAIR = QS + (9 - QT) * 128 * 128;
     static constexpr uint32_t ROPE = PAIR + PAIRS * kPairBytes;
-    static constexpr uint32_t P = ROPE + ROPES * kRopeBytes;
-    static constexpr uint32_t MISC = P + N * 128;
-    // MISC: barriers, then per-row floats
+    static constexpr uint32_t P = ROPE + ROPES * kRopeBytes;  // two buffers
+    static constexpr uint32_t MISC = P + 2 * N * 128;
     static constexpr int B_FULL = 0, B_EMPTY = PAIRS, B_RFULL = 2 * PAIRS, B_REMPTY = B_RFULL + ROPES,
-                         B_S = B_REMPTY + ROPES, B_P = B_S + 2, B_PV = B_P + 1, B_Q = B_PV + 1, B_DRAIN = B_Q + 1,
-                         BARS = B_DRAIN + 1;
+                         B_S = B_REMPTY + ROPES, B_SFREE = B_S + 1, B_P = B_SFREE + 1, B_PV = B_P + 2, B_Q = B_PV + 2,
+                         B_DRAIN = B_Q + 1, BARS = B_DRAIN + 1;
     static constexpr uint32_t ROWF = MISC + 8 * 40;      // [N] row factors
     static constexpr uint32_t BAD = ROWF + 4 * N;        // [ROPES] bad boxes of the tile in a rope slot
     static constexpr uint32_t CTRL = BAD + 16;           // tmem address, dead flag, start of the range
     static constexpr uint32_t SCAN = CTRL + 48;          // [8] warp sums
     static constexpr uint32_t ROWO = SCAN + 64;          // [N] output offsets of the rows
-    static constexpr uint32_t SMEM = ROWO + 8 * N;
-    static constexpr int TMEM = N == 64 ? 512 : 256;
-    static constexpr uint32_t TM_S = 4 * N;
-    static_assert(BARS <= 40 && SMEM <= 232448, "shared memory plan");
+    static constexpr uint32_t PMAX = ROWO + 8 * N;       // [2][128] partial maxima
+    static constexpr uint32_t SMEM = PMAX + 1024;
+    static constexpr uint32_t TM_S = 4 * N, TM_Q = TM_S + kTile;
+    static_assert(BARS <= 40 && SMEM <= 232448 && TM_Q + 32 * QT <= 512, "shared memory and TMEM plan");
 };
 
 // Length and query count of a request as the kernel uses them: an invalid one has none.
@@ -133,6 +141,21 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// This thread's CW scores: columns col0 .. of its TMEM lane.  A load's address is the warp's, so with
+// CW = 8 (two copies of the rows in a warp) each half of the warp takes its half of 16 columns.
+template <int CW>
+__device__ __forceinline__ void ld_scores(uint32_t taddr, int col0, int lane, float (&v)[CW]) {
+    constexpr int n = CW < 16 ? 1 : CW / 16;
+    uint32_t u[n][16];
+    const uint32_t base = taddr + (CW < 16 ? col0 & ~15 : col0);
+#pragma unroll
+    for (int i = 0; i < n; ++i) ld16_issue(base + 16 * i, u[i]);
+    wait_ld();
+#pragma unroll
+    for (int i = 0; i < CW; ++i)
+        v[i] = __uint_as_float(CW < 16 && lane >= 16 ? u[0][(8 + i) & 15] : u[i / 16][i % 16]);
+}
+
 template <int N, int DT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ DecodeArgs a) {
@@ -143,6 +166,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) { return sb + L::MISC + 8 * i; };
     float* rowf = reinterpret_cast<float*>(sm + L::ROWF);
+    float* pmax = reinterpret_cast<float*>(sm + L::PMAX);
     volatile int* bad_box = reinterpret_cast<int*>(sm + L::BAD);
     volatile int* ctrl = reinterpret_cast<int*>(sm + L::CTRL);  // 0 tmem, 1 dead, 2 r, 3 rt, 4 j
     int64_t* rowo = reinterpret_cast<int64_t*>(sm + L::ROWO);
@@ -151,11 +175,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        for (int i = 0; i < L::BARS; ++i) mbar_init(bar(i), i == L::B_P || i == L::B_Q ? 4 : 1);
+        for (int i = 0; i < L::BARS; ++i) mbar_init(bar(i), i == L::B_P || i == L::B_P + 1 || i == L::B_Q || i == L::B_SFREE ? 4 : 1);
         ctrl[1] = 0;
         ctrl[2] = -1;
     }
-    if (warp == 1) tmem_alloc(sb + L::CTRL, L::TMEM);
+    if (warp == 1) tmem_alloc(sb + L::CTRL, 512);
 
     // ---- this CTA's range: tiles of all requests, then the request its start falls into
     long long mine = 0;
@@ -291,7 +315,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
         const uint32_t ids = idesc_16(DT == KDA_F16, 128, kTile, false, false, a.negate);
         const uint32_t idv = idesc_16(DT == KDA_F16, 128, N, true, false, false);
-        Walk ws = w;  // S runs up to one tile ahead of O, over its own copy of the walk
+        Walk ws = w;  // S runs ahead of O, over its own copy of the walk
         bool more_s = __any_sync(~0u, ws.next(a)), more_v = __any_sync(~0u, w.next(a));
         int js = ws.j0, jv = w.j0;
         bool first_s = true, first_v = true;          // of a segment
@@ -301,28 +325,63 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         bool stop = false;
         while (more_v && !stop) {
             bool did = false;
-            if (more_s && s_it <= v_it + 1) {
+            if (v_it < s_it && __all_sync(~0u, mbar_test(bar(L::B_P + (v_it & 1)), (v_it >> 1) & 1))) {
+                fence_after();
+                const uint32_t p4 = sb4 + L::P / 16 + (v_it & 1) * (N * 128 / 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a4 = sb4 + L::PAIR / 16 + v_slot * (kPairBytes / 16);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_by(lead, tm + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(p4, N, s), idv,
+                               s != 0 || !first_v);
+                    commit_by(lead, bar(L::B_EMPTY + v_slot));
+                    if (++v_slot == L::PAIRS) v_slot = 0;
+                }
+                // the rope slot goes back with the tile, not with S: the softmax of this tile has
+                // read the slot's bad boxes and waited on its barrier by now
+                commit_by(lead, bar(L::B_REMPTY + vr_slot));
+                if (++vr_slot == L::ROPES) vr_slot = 0;
+                commit_by(lead, bar(L::B_PV + (v_it & 1)));
+                ++v_it;
+                first_v = __any_sync(~0u, ++jv == w.j1);
+                if (first_v) {
+                    more_v = __any_sync(~0u, w.next(a));
+                    jv = w.j0;
+                }
+                did = true;
+            }
+            if (more_s) {
                 bool ready = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
+                if (s_it > 0) ready = ready && mbar_test(bar(L::B_SFREE), (s_it - 1) & 1);
                 if (first_s) ready = ready && mbar_test(bar(L::B_Q), segs & 1);
                 if (__all_sync(~0u, ready)) {
                     if (first_s) ++segs;
-                    const uint32_t d = tm + L::TM_S + (s_it & 1) * kTile;
+                    const uint32_t d = tm + L::TM_S;
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        wait(L::B_FULL + s_slot, s_ph);
-                        fence_after();
-                        const uint32_t b4 = sb4 + L::PAIR / 16 + s_slot * (kPairBytes / 16);
+                    for (int c = 0; c < 9; ++c) {
+                        uint32_t b4;
+                        if (c < 8) {
+                            if (c % 2 == 0) {
+                                wait(L::B_FULL + s_slot, s_ph);
+                                fence_after();
+                            }
+                            b4 = sb4 + L::PAIR / 16 + s_slot * (kPairBytes / 16) + (c % 2) * (kTile * 128 / 16);
+                        } else {
+                            b4 = sb4 + L::ROPE / 16 + r_slot * (kRopeBytes / 16);
+                        }
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            mma_by(lead, d, desc_k4(sb4 + L::Q / 16, N, 8 * p + s), desc_k4(b4, kTile, s), ids,
-                                   p + s != 0);
-                        if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
+                        for (int s = 0; s < 4; ++s) {
+                            if (c < L::QT)
+                                mma_ta_by(lead, d, tm + L::TM_Q + 32 * c + 8 * s, desc_k4(b4, kTile, s), ids, c + s != 0);
+                            else
+                                mma_by(lead, d, desc_k4(sb4 + L::QS / 16 + (c - L::QT) * 1024, 128, s),
+                                       desc_k4(b4, kTile, s), ids, 1);
+                        }
+                        if (c < 8 && c % 2 == 1)
+                            if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
                     }
-                    const uint32_t b4 = sb4 + L::ROPE / 16 + r_slot * (kRopeBytes / 16);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_by(lead, d, desc_k4(sb4 + L::Q / 16, N, 32 + s), desc_k4(b4, kTile, s), ids, 1);
-                    commit_by(lead, bar(L::B_S + (s_it & 1)));
+                    commit_by(lead, bar(L::B_S));
                     if (++r_slot == L::ROPES) r_slot = 0, r_ph ^= 1;
                     ++s_it;
                     first_s = __any_sync(~0u, ++js == ws.j1);
@@ -332,31 +391,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                     did = true;
                 }
-            }
-            if (v_it < s_it && __all_sync(~0u, mbar_test(bar(L::B_P), v_it & 1))) {
-                fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t a4 = sb4 + L::PAIR / 16 + v_slot * (kPairBytes / 16);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_by(lead, tm + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(sb4 + L::P / 16, N, s), idv,
-                               s != 0 || !first_v);
-                    commit_by(lead, bar(L::B_EMPTY + v_slot));
-                    if (++v_slot == L::PAIRS) v_slot = 0;
-                }
-                // the rope slot goes back with the tile, not with S: the softmax of this tile has
-                // read the slot's bad boxes and waited on its barrier by now
-                commit_by(lead, bar(L::B_REMPTY + vr_slot));
-                if (++vr_slot == L::ROPES) vr_slot = 0;
-                commit_by(lead, bar(L::B_PV));
-                ++v_it;
-                first_v = __any_sync(~0u, ++jv == w.j1);
-                if (first_v) {
-                    more_v = __any_sync(~0u, w.next(a));
-                    jv = w.j0;
-                }
-                did = true;
             }
             // polls of some tens of cycles: it gives up after about a second without work
             idle = did ? 0 : idle + 1;
@@ -371,26 +405,41 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         wait(L::B_DRAIN, 0);
     } else if (warp >= 4) {
         // ================================================================ softmax, queries, results
+        constexpr int CW = L::CW, NR = N == 64 ? 2 : 1;
         const int q4 = warp - 4, t = tid - 128;
         const uint32_t tq = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool has_rows = q4 * 32 < N;
-        const int row = t;  // of the row tile, when has_rows and row < N
+        const int row = t % N, col0 = t / N * CW;  // this thread's query row and first score
+        // the row's queries: to this thread's TMEM lane, and the parts without columns to shared memory
         auto load_q = [&](int r, int rt) {
-            // 16-byte words of the rows: 72 a row; rows past the end are zero
-            const int rows = min(N, a.K * a.H - rt * N);
-            for (int e = t; e < N * 72; e += 128) {
-                const int i = e / 72, x = e - i * 72;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (i < rows) {
-                    const int f = rt * N + i, tt = f / a.H, h = f - tt * a.H;
-                    const int64_t qrow = (int64_t)r * a.K + tt;
-                    const uint16_t* src = x < 64 ? a.ql.base + qrow * a.ql.rs + h * a.ql.hs + x * 8
-                                                 : a.qr.base + qrow * a.qr.rs + h * a.qr.hs + (x - 64) * 8;
-                    v = __ldg(reinterpret_cast<const uint4*>(src));
+            const int f = rt * N + row;
+            const bool live = f < a.K * a.H;
+            const int tt = f / a.H, h = f - tt * a.H;
+            const int64_t qrow = (int64_t)r * a.K + tt;
+            const uint4* ql = reinterpret_cast<const uint4*>(a.ql.base + qrow * a.ql.rs + h * a.ql.hs);
+            const uint4* qr = reinterpret_cast<const uint4*>(a.qr.base + qrow * a.qr.rs + h * a.qr.hs);
+            auto word = [&](int x) {  // 16-byte word x of the 72 of a row
+                return !live ? make_uint4(0, 0, 0, 0) : __ldg(x < 64 ? ql + x : qr + (x - 64));
+            };
+#pragma unroll
+            for (int c = 0; c < L::QT; c += 3) {
+                uint4 v[24];
+#pragma unroll
+                for (int i = 0; i < 24; ++i) v[i] = word(8 * c + i);
+#pragma unroll
+                for (int i = 0; i < 24; i += 4) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        u[4 * q] = v[i + q].x, u[4 * q + 1] = v[i + q].y, u[4 * q + 2] = v[i + q].z, u[4 * q + 3] = v[i + q].w;
+                    st16u(tq + L::TM_Q + 32 * c + 4 * i, u);
                 }
-                sts16(sb + L::Q + chunk_k(i, x * 8, N), v);
             }
-            fence_async_smem();
+#pragma unroll
+            for (int x = 8 * L::QT; x < 72; ++x)
+                sts16(sb + L::QS + chunk_k(t, (x - 8 * L::QT) * 8, 128), word(x));
+            wait_st();
+            if (L::QT < 9) fence_async_smem();
+            fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::B_Q));
         };
@@ -401,75 +450,78 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         while (more && !quit) {
             const Walk g = w;  // this segment
             if (t == 0 && g.j0 == 0 && g.crt == 0 && g.err) report(a.dev_status, g.err);
-            float m = -inf, l = 0.f;
+            // the running maximum of this thread's row and, for N = 64, of the row its warp does not
+            // hold: every warp then knows by itself whether any row moves its maximum
+            float m[NR];
+#pragma unroll
+            for (int q = 0; q < NR; ++q) m[q] = -inf;
+            float l = 0.f;  // over this thread's columns
             int last = -1;  // last token this thread's row sees
             const int f = g.crt * N + row;
-            if (has_rows && row < N && f < a.K * a.H) {
+            if (f < a.K * a.H) {
                 const int tt = f / a.H;
                 if (tt < g.ql) last = g.len - g.ql + tt;
             }
             for (int j = g.j0; j < g.j1; ++j, ++it) {
-                float s[kTile];
-                float f_old = 1.f;
-                bool need = false;
-                wait(L::B_S + (it & 1), (it >> 1) & 1);
+                wait(L::B_S, it & 1);
                 wait(L::B_RFULL + rslot, rph);
                 fence_after();
                 const int t0 = j * kTile;
                 const uint32_t bad = (uint32_t)bad_box[rslot];
                 if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
                 const int valid = g.len - t0;  // tokens of this tile (may exceed it)
-                if (has_rows) {
-                    float x0[32];
-                    ld32(tq + L::TM_S + (it & 1) * kTile, x0);
+                float s[CW];
+                ld_scores(tq + L::TM_S, col0, lane, s);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_SFREE));
+                if (bad) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = x0[i];
-                    ld32(tq + L::TM_S + (it & 1) * kTile + 32, x0);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[32 + i] = x0[i];
-                    if (bad) {
-#pragma unroll
-                        for (int i = 0; i < kTile; ++i)
-                            if ((bad >> (i / a.box)) & 1) s[i] = -inf;
-                    }
-                    const int lim = last - t0;  // columns 0 .. lim are seen
-                    if (lim < kTile - 1) {
-#pragma unroll
-                        for (int i = 0; i < kTile; ++i)
-                            if (i > lim) s[i] = -inf;
-                    }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int i = 4; i < kTile; i += 4)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], s[i + q]);
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (j == g.j0) {
-                        m = mt;
-                    } else if (mt > m && (m == -inf || (mt - m) * a.c > 8.f)) {
-                        f_old = ex2((m - mt) * a.c);
-                        m = mt;
-                        need = true;
-                        l *= f_old;
-                    }
-                    if (row < N) rowf[row] = f_old;
-                    const float mc = m == -inf ? 0.f : m * a.c;
-                    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 2) {
-                        s[i] = ex2(fmaf(s[i], a.c, -mc));
-                        s[i + 1] = ex2(fmaf(s[i + 1], a.c, -mc));
-                        l0 += s[i];
-                        l1 += s[i + 1];
-                    }
-                    l += l0 + l1;
+                    for (int i = 0; i < CW; ++i)
+                        if ((bad >> ((col0 + i) / a.box)) & 1) s[i] = -inf;
                 }
-                // every thread of the role: does any row move its maximum (or has a wait given up)?
-                const bool any = bar_named_or(1, 128, need || dead);
-                if (j > g.j0 || it > 0) wait(L::B_PV, (it - 1) & 1);  // O and P free of the previous tile's product
-                if (any) {
-                    quit = bar_named_or(1, 128, dead || ctrl[1]);
-                    if (quit) break;
+                const int lim = last - t0 - col0;  // columns 0 .. lim of this thread are seen
+                if (lim < CW - 1) {
+#pragma unroll
+                    for (int i = 0; i < CW; ++i)
+                        if (i > lim) s[i] = -inf;
+                }
+                float mx = s[0];
+#pragma unroll
+                for (int i = 1; i < CW; ++i) mx = fmaxf(mx, s[i]);
+                float* pm = pmax + (it & 1) * 128;
+                pm[t] = mx;
+                quit = bar_named_or(1, 128, dead || ctrl[1]);
+                if (quit) break;
+                bool need = false;
+                float f_old = 1.f;
+#pragma unroll
+                for (int q = 0; q < NR; ++q) {
+                    const int r = q ? row ^ 32 : row;
+                    float mt = pm[r];
+#pragma unroll
+                    for (int k = 1; k < L::REP; ++k) mt = fmaxf(mt, pm[r + k * N]);
+                    if (j == g.j0) {
+                        m[q] = mt;
+                    } else if (mt > m[q] && (m[q] == -inf || (mt - m[q]) * a.c > 8.f)) {
+                        const float x = ex2((m[q] - mt) * a.c);
+                        if (q == 0) f_old = x;
+                        m[q] = mt;
+                        need = true;
+                    }
+                }
+                const float mc = m[0] == -inf ? 0.f : m[0] * a.c;
+                float ls[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < CW; ++i) {
+                    s[i] = ex2(fmaf(s[i], a.c, -mc));
+                    ls[i & 1] += s[i];
+                }
+                l = fmaf(l, f_old, ls[0] + ls[1]);
+                if (__any_sync(~0u, need)) {  // the same in all four warps
+                    if (t < N) rowf[row] = f_old;
+                    bar_named(1, 128);
+                    wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
                     fence_after();
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -483,13 +535,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     wait_st();
                     bar_named(1, 128);  // rowf has been read
                 }
-                if (has_rows && row < N) {
+                if (it >= 2) wait(L::B_PV + (it & 1), ((it - 2) >> 1) & 1);  // this P buffer's last product
 #pragma unroll
-                    for (int i = 0; i < kTile; i += 8)
-                        sts16(sb + L::P + chunk_k(row, i, N),
-                              make_uint4(E::put2(s[i], s[i + 1]), E::put2(s[i + 2], s[i + 3]),
-                                         E::put2(s[i + 4], s[i + 5]), E::put2(s[i + 6], s[i + 7])));
-                }
+                for (int i = 0; i < CW; i += 8)
+                    sts16(sb + L::P + (it & 1) * (N * 128) + chunk_k(row, col0 + i, N),
+                          make_uint4(E::put2(s[i], s[i + 1]), E::put2(s[i + 2], s[i + 3]),
+                                     E::put2(s[i + 4], s[i + 5]), E::put2(s[i + 6], s[i + 7])));
                 if (valid < kTile || bad) {
                     // tokens that are not there: their weight is zero, and so has to be the value
                     // (what lies in the buffer, or past the end of a page, may be anything)
@@ -506,7 +557,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 fence_async_smem();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::B_P));
+                if (lane == 0) mbar_arrive(bar(L::B_P + (it & 1)));
             }
             if (quit) break;
             // the next segment's queries: every S of this one has been read
@@ -516,11 +567,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const bool whole = g.j0 == 0 && g.j1 == g.n;
             const int slot = 2 * (int)blockIdx.x + (g.j0 == 0);
             const int rows = min(N, a.K * a.H - g.crt * N);
-            bar_named(1, 128);  // rowf of the last tile has been read
-            if (has_rows && row < N) {
+            pmax[(it & 1) * 128 + t] = l;  // the buffer that the last tile did not use
+            bar_named(1, 128);
+            if (t < N) {
+#pragma unroll
+                for (int k = 1; k < L::REP; ++k) l += pmax[(it & 1) * 128 + row + k * N];
                 rowf[row] = l > 0.f ? 1.f / l : 0.f;
                 rowo[row] = ((int64_t)g.cr * a.K + f / a.H) * a.out_rs + (f % a.H) * a.out_hs;
-                const float m2 = m == -inf ? -inf : m * a.c;
+                const float m2 = m[0] == -inf ? -inf : m[0] * a.c;
                 if (!whole) {
                     a.ml[(int64_t)slot * N + row] = make_float2(m2, l);
                 } else if (a.lse != nullptr && row < rows) {
@@ -537,7 +591,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 a.meta[blockIdx.x] = make_int4(g.cr, g.crt, (int)last_cta, 0);
             }
             bar_named(1, 128);
-            wait(L::B_PV, (it - 1) & 1);
+            wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
             fence_after();
             for (int c = 0; c < 4; ++c) {
                 const int ch = c * 128 + t;
@@ -564,7 +618,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 1) tmem_dealloc(tmem, L::TMEM);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of a request that several CTAs hold: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i.
