@@ -17,9 +17,9 @@
 // whole requests (written as results) and at most two partial ones (unnormalised O, m and l to the
 // workspace, joined by combine_kernel).
 //
-// Roles: warp 0 loads (TMA boxes of one page's rows, a ring of 128-channel pairs so that a part is
-// free for the next tile as soon as its product is done), warp 1 issues MMAs, whichever of S(i+1)
-// and O(i) is ready first, warps 4-7 do softmax, rescaling, queries and results.
+// Roles: warps 0, 2 and 3 load (TMA boxes of one page's rows, a ring of 128-channel pairs so that a
+// part is free for the next tile as soon as its product is done), warp 1 issues MMAs, whichever of
+// S(i+1) and O(i) is ready first, warps 4-7 do softmax, rescaling, queries and results.
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "latent_host.h"
@@ -158,7 +158,8 @@ __device__ __forceinline__ void ld_scores(uint32_t taddr, int col0, int lane, fl
 
 template <int N, int DT>
 __global__ void __launch_bounds__(kDecThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ DecodeArgs a) {
+    decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rmap,
+                  const __grid_constant__ DecodeArgs a) {
     using L = DecLayout<N>;
     using E = Elem<DT>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -247,66 +248,80 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         // ================================================================ loads
-        const int per = kTile / a.box;
-        uint32_t slot = 0, sph = 1, rslot = 0, rph = 1;  // empty barriers: the first pass finds them free
-        uint32_t filled = 0, rfilled = 0;
+        // warp 0: the rope part and, with 64-row boxes, everything (5 boxes a tile: a pair is one box
+        // of two 64-channel columns); with smaller boxes (8 pages or fewer a tile, 9 boxes each)
+        // warps 2 and 3 take two pairs each, since one warp issues a box in some 100 cycles
+        const bool whole_box = a.box == kTile;
+        const int part = warp;  // 0: rope (and pairs 0..3), 2: pairs 0, 1, 3: pairs 2, 3
+        const int p_lo = part == 3 ? 2 : 0, p_hi = whole_box ? (part == 0 ? 4 : 0) : part == 0 ? 0 : p_lo + 2;
+        const uint32_t per = kTile / a.box;
+        uint32_t tile = 0;
         while (!dead && w.next(a)) {
             const int32_t* tab = a.table + (int64_t)w.cr * a.max_pages;
-            auto page_of = [&](int j) {
-                const int64_t t = (int64_t)j * kTile + lane * a.box;
-                return lane < per && t < w.len ? tab[t / a.page_size] : -1;
+            // page of this lane's box in tile j (-1: none) and the box's first row in it
+            auto page_of = [&](int j, uint32_t& y) {
+                const uint32_t t = (uint32_t)j * kTile + lane * a.box;
+                const uint32_t pg = t / (uint32_t)a.page_size;
+                y = t - pg * a.page_size;
+                return lane < (int)per && t < (uint32_t)w.len ? tab[pg] : INT32_MIN;
             };
-            int next = page_of(w.j0);
-            for (int j = w.j0; j < w.j1 && !dead; ++j) {
+            uint32_t ynext = 0;
+            int next = page_of(w.j0, ynext);
+            for (int j = w.j0; j < w.j1 && !dead; ++j, ++tile) {
                 const int page = next;
-                if (j + 1 < w.j1) next = page_of(j + 1);
-                const int y = (int)(((int64_t)j * kTile + lane * a.box) % a.page_size);
-                const bool has = lane < per && (int64_t)j * kTile + lane * a.box < w.len;
+                const uint32_t y = ynext;
+                const bool has = lane < (int)per && (uint32_t)j * kTile + lane * a.box < (uint32_t)w.len;
+                if (j + 1 < w.j1) next = page_of(j + 1, ynext);
                 const bool ok = has && page >= 0 && page < a.P;
                 const uint32_t okm = __ballot_sync(~0u, ok);
                 const uint32_t badm = __ballot_sync(~0u, has && !ok);
                 const uint32_t bytes = (uint32_t)__popc(okm) * a.box * 128;
-                if (badm && lane == 0) report(a.dev_status, KDA_DEV_BAD_SLOT);
-                for (int p = 0; p < 4; ++p) {
-                    wait(L::B_EMPTY + slot, sph);
+                for (int p = p_lo; p < p_hi; ++p) {
+                    const uint32_t n = tile * 4 + p, slot = n % L::PAIRS;
+                    wait(L::B_EMPTY + slot, (n / L::PAIRS & 1) ^ 1);  // the first pass finds the slots free
                     dead = __any_sync(~0u, dead);
                     if (dead) break;
                     if (lane == 0) mbar_expect_tx(bar(L::B_FULL + slot), 2 * bytes);
                     __syncwarp();
                     if (ok) {
                         const uint32_t dst = sb + L::PAIR + slot * kPairBytes + lane * a.box * 128;
-                        tma_load_3d(dst, &map, p * 128, y, page, bar(L::B_FULL + slot));
-                        tma_load_3d(dst + kTile * 128, &map, p * 128 + 64, y, page, bar(L::B_FULL + slot));
+                        tma_load_4d(dst, &map, 0, y, 2 * p, page, bar(L::B_FULL + slot));
+                        if (!whole_box)
+                            tma_load_4d(dst + kTile * 128, &map, 0, y, 2 * p + 1, page, bar(L::B_FULL + slot));
                     }
-                    ++filled;
-                    if (++slot == L::PAIRS) slot = 0, sph ^= 1;
                 }
                 if (dead) break;
-                wait(L::B_REMPTY + rslot, rph);
-                dead = __any_sync(~0u, dead);
-                if (dead) break;
-                if (lane == 0) {
-                    bad_box[rslot] = (int)badm;
-                    mbar_expect_tx(bar(L::B_RFULL + rslot), bytes);
+                if (part == 0) {
+                    const uint32_t slot = tile % L::ROPES;
+                    wait(L::B_REMPTY + slot, (tile / L::ROPES & 1) ^ 1);
+                    dead = __any_sync(~0u, dead);
+                    if (dead) break;
+                    if (lane == 0) {
+                        if (badm) report(a.dev_status, KDA_DEV_BAD_SLOT);
+                        bad_box[slot] = (int)badm;
+                        mbar_expect_tx(bar(L::B_RFULL + slot), bytes);
+                    }
+                    __syncwarp();
+                    if (ok)
+                        tma_load_4d(sb + L::ROPE + slot * kRopeBytes + lane * a.box * 128, &rmap, 0, y, 8, page,
+                                    bar(L::B_RFULL + slot));
                 }
-                __syncwarp();
-                if (ok)
-                    tma_load_3d(sb + L::ROPE + rslot * kRopeBytes + lane * a.box * 128, &map, kLatent, y, page,
-                                bar(L::B_RFULL + rslot));
-                ++rfilled;
-                if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
             }
             if (ctrl[1]) dead = true;
             dead = __any_sync(~0u, dead);
         }
-        // nothing may be in flight when the CTA ends: every slot's last load has landed
+        // nothing may be in flight when the CTA ends: the last loads of this warp have landed
         dead = false;
-        for (int i = 0; i < L::PAIRS; ++i)
-            if ((uint32_t)i < filled) wait(L::B_FULL + i, ((filled - 1 - i) / L::PAIRS) & 1);
-        for (int i = 0; i < L::ROPES; ++i)
-            if ((uint32_t)i < rfilled) wait(L::B_RFULL + i, ((rfilled - 1 - i) / L::ROPES) & 1);
+        const uint32_t back = min(tile, (uint32_t)L::ROPES);
+        for (uint32_t k = tile - back; k < tile; ++k) {
+            for (int p = p_lo; p < p_hi; ++p) {
+                const uint32_t n = k * 4 + p;
+                wait(L::B_FULL + n % L::PAIRS, n / L::PAIRS & 1);
+            }
+            if (part == 0) wait(L::B_RFULL + k % L::ROPES, k / L::ROPES & 1);
+        }
     } else if (warp == 1) {
         // ================================================================ MMAs
         // the whole warp runs this, one lane issues (umma.cuh, mma_by); votes keep the control uniform
@@ -664,7 +679,7 @@ int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 template <int N, int DT>
-kda_status launch(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
+kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
     using L = DecLayout<N>;
     auto* f = decode_kernel<N, DT>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM) != cudaSuccess)
@@ -672,7 +687,7 @@ kda_status launch(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles
     // every (row tile, request) has at least one tile and at most max_tiles
     const int64_t most = (int64_t)a.n_rt * a.R * max_tiles;
     const unsigned grid = (unsigned)(most < kDecCtas ? most : kDecCtas);
-    f<<<grid, kDecThreads, L::SMEM, s>>>(map, a);
+    f<<<grid, kDecThreads, L::SMEM, s>>>(map[0], map[1], a);
     if (max_tiles <= 1) return launch_status();  // one tile a request: nothing is split
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, N / 4);
@@ -688,7 +703,7 @@ kda_status launch(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles
 }
 
 template <int DT>
-kda_status launch_n(const CUtensorMap& map, const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
+kda_status launch_n(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
     const int n = tile_rows((int64_t)a.K * a.H);
     if (n == 16) return launch<16, DT>(map, a, max_tiles, s);
     if (n == 32) return launch<32, DT>(map, a, max_tiles, s);
@@ -728,12 +743,15 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     KDA_REQUIRE(aligned16(q_len) && aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(ws_bytes >= kda_latent_decode_workspace_size(R, K, H), KDA_ERR_INVALID_ARG);
     const int box = lowbit_box(page_size, kTile);
-    CUtensorMap map;
-    // the cache as pages of rows: one box is `box` rows of one page, 64 channels (a 128-byte swizzle row)
-    const cuuint64_t dims[3] = {kLatentRow, (cuuint64_t)page_size, (cuuint64_t)(P > 0 ? P : 1)};
-    const cuuint64_t strides[2] = {kLatentRow * 2, (cuuint64_t)page_stride * 2};
-    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
-    KDA_REQUIRE(encode_16bit(&map, in_dtype, 3, cache, dims, strides, boxes), KDA_ERR_CUDA);
+    CUtensorMap map[2];
+    // the cache as (channel of 64, row, 64-channel column, page): one box is `box` rows of one page
+    // and one column (a 128-byte swizzle row), or with a whole tile of rows a pair of columns
+    const cuuint64_t dims[4] = {64, (cuuint64_t)page_size, 9, (cuuint64_t)(P > 0 ? P : 1)};
+    const cuuint64_t strides[3] = {kLatentRow * 2, 128, (cuuint64_t)page_stride * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, box == kTile ? 2u : 1u, 1};
+    const cuuint32_t rope_boxes[4] = {64, (cuuint32_t)box, 1, 1};
+    KDA_REQUIRE(encode_16bit(&map[0], in_dtype, 4, cache, dims, strides, boxes), KDA_ERR_CUDA);
+    KDA_REQUIRE(encode_16bit(&map[1], in_dtype, 4, cache, dims, strides, rope_boxes), KDA_ERR_CUDA);
     const int n = tile_rows((int64_t)K * H);
     DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
                  block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
