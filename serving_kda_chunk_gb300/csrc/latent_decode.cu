@@ -156,6 +156,12 @@ __device__ __forceinline__ void ld_scores(uint32_t taddr, int col0, int lane, fl
         v[i] = __uint_as_float(CW < 16 && lane >= 16 ? u[0][(8 + i) & 15] : u[i / 16][i % 16]);
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 template <int N, int DT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rmap,
@@ -424,34 +430,56 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int q4 = warp - 4, t = tid - 128;
         const uint32_t tq = tmem + ((uint32_t)(q4 * 32) << 16);
         const int row = t % N, col0 = t / N * CW;  // this thread's query row and first score
-        // the row's queries: to this thread's TMEM lane, and the parts without columns to shared memory
+        uint32_t it = 0, rslot = 0, rph = 0;
+        // The queries of a row tile: read from global memory along the rows (16 threads a row's 256
+        // bytes), turned in the two P buffers, 128 channels at a time, and written by the thread that
+        // has the row to its TMEM lane; the parts without columns go to shared memory.
         auto load_q = [&](int r, int rt) {
-            const int f = rt * N + row;
-            const bool live = f < a.K * a.H;
-            const int tt = f / a.H, h = f - tt * a.H;
-            const int64_t qrow = (int64_t)r * a.K + tt;
-            const uint4* ql = reinterpret_cast<const uint4*>(a.ql.base + qrow * a.ql.rs + h * a.ql.hs);
-            const uint4* qr = reinterpret_cast<const uint4*>(a.qr.base + qrow * a.qr.rs + h * a.qr.hs);
-            auto word = [&](int x) {  // 16-byte word x of the 72 of a row
-                return !live ? make_uint4(0, 0, 0, 0) : __ldg(x < 64 ? ql + x : qr + (x - 64));
-            };
+            uint4 v[N / 8][5];
 #pragma unroll
-            for (int c = 0; c < L::QT; c += 3) {
-                uint4 v[24];
+            for (int i = 0; i < N / 8; ++i) {
+                const int f = rt * N + 8 * i + (t >> 4);
+                const int tt = f / a.H, h = f - tt * a.H;
+                const int64_t qrow = (int64_t)r * a.K + tt;
+                const uint4* ql = reinterpret_cast<const uint4*>(a.ql.base + qrow * a.ql.rs + h * a.ql.hs) + (t & 15);
+                const uint4* qr = reinterpret_cast<const uint4*>(a.qr.base + qrow * a.qr.rs + h * a.qr.hs) + (t & 15);
 #pragma unroll
-                for (int i = 0; i < 24; ++i) v[i] = word(8 * c + i);
-#pragma unroll
-                for (int i = 0; i < 24; i += 4) {
-                    uint32_t u[16];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        u[4 * q] = v[i + q].x, u[4 * q + 1] = v[i + q].y, u[4 * q + 2] = v[i + q].z, u[4 * q + 3] = v[i + q].w;
-                    st16u(tq + L::TM_Q + 32 * c + 4 * i, u);
+                for (int g = 0; g < 5; ++g) {
+                    v[i][g] = make_uint4(0, 0, 0, 0);
+                    if (f < a.K * a.H) {
+                        if (g < 4) v[i][g] = __ldg(ql + 16 * g);
+                        else if ((t & 15) < 8) v[i][g] = __ldg(qr);
+                    }
                 }
             }
+            // the last product that reads P (and so every earlier one) is done
+            if (it > 0) wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
+            const uint32_t stage = sb + L::P;
 #pragma unroll
-            for (int x = 8 * L::QT; x < 72; ++x)
-                sts16(sb + L::QS + chunk_k(t, (x - 8 * L::QT) * 8, 128), word(x));
+            for (int g = 0; g < 5; ++g) {
+                if (g) bar_named(1, 128);
+#pragma unroll
+                for (int i = 0; i < N / 8; ++i) {
+                    const int rr = 8 * i + (t >> 4);
+                    sts16(stage + ((t >> 3) & 1) * (N * 128) + rr * 128 + (((t ^ rr) & 7) << 4), v[i][g]);
+                }
+                bar_named(1, 128);
+#pragma unroll
+                for (int c = 2 * g; c < 2 * g + 2 && c < 9; ++c) {
+                    uint32_t u[2][16];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const uint4 y = lds16(stage + (c & 1) * (N * 128) + row * 128 + (((x ^ row) & 7) << 4));
+                        const int o = 4 * (x & 3);
+                        u[x >> 2][o] = y.x, u[x >> 2][o + 1] = y.y, u[x >> 2][o + 2] = y.z, u[x >> 2][o + 3] = y.w;
+                        if (c >= L::QT) sts16(sb + L::QS + chunk_k(t, (c - L::QT) * 64 + 8 * x, 128), y);
+                    }
+                    if (c < L::QT) {
+                        st16u(tq + L::TM_Q + 32 * c, u[0]);
+                        st16u(tq + L::TM_Q + 32 * c + 16, u[1]);
+                    }
+                }
+            }
             wait_st();
             if (L::QT < 9) fence_async_smem();
             fence_before();
@@ -459,7 +487,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             if (lane == 0) mbar_arrive(bar(L::B_Q));
         };
         if (t == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        uint32_t it = 0, rslot = 0, rph = 0;
         bool more = w.next(a), quit = false;  // quit: agreed by the four warps, so that barriers stay matched
         if (more) load_q(w.cr, w.crt);
         while (more && !quit) {
@@ -559,15 +586,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 if (valid < kTile || bad) {
                     // tokens that are not there: their weight is zero, and so has to be the value
                     // (what lies in the buffer, or past the end of a page, may be anything)
-                    const uint32_t first = it * 4;
-                    for (int e = t; e < kTile * 64; e += 128) {
-                        const int k = e >> 6, x = e & 63;  // token, 16-byte word of 512 channels
-                        if (k >= valid || ((bad >> (k / a.box)) & 1)) {
-                            const uint32_t slot = (first + (x >> 4)) % L::PAIRS;
-                            sts16(sb + L::PAIR + slot * kPairBytes + (uint32_t)(((x >> 3) & 1) * kTile * 128 + k * 128 + (x & 7) * 16),
-                                  make_uint4(0, 0, 0, 0));
-                        }
-                    }
+                    // a thread clears one 16-byte word (of 64) of every other token
+                    const int x = t & 63;
+                    const uint32_t at = sb + L::PAIR + (it * 4 + (x >> 4)) % L::PAIRS * kPairBytes +
+                                        ((x >> 3) & 1) * (kTile * 128) + (x & 7) * 16;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    for (int k = max(valid, 0) + (t >> 6); k < kTile; k += 2) sts16(at + k * 128, zero);
+                    if (bad)
+                        for (int k = t >> 6; k < kTile; k += 2)
+                            if ((bad >> (k / a.box)) & 1) sts16(at + k * 128, zero);
                 }
                 fence_async_smem();
                 fence_before();
@@ -608,23 +635,31 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             bar_named(1, 128);
             wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
             fence_after();
-            for (int c = 0; c < 4; ++c) {
-                const int ch = c * 128 + t;
+            // channel c * 128 + t of every row; put(row, channel, value) is chosen once
+            auto emit = [&](auto put) {
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 16) {
-                    float o[16];
-                    ld16(tq + c * N + n0, o);
+                    for (int n0 = 0; n0 < N; n0 += 16) {
+                        if (n0 >= rows) break;
+                        float o[16];
+                        ld16(tq + c * N + n0, o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int rr = n0 + i;
-                        if (rr >= rows) continue;
-                        if (whole) {
-                            store1_as(a.out, rowo[rr] + ch, o[i] * rowf[rr], a.out_dt);
-                        } else {
-                            a.part[((int64_t)slot * N + rr) * kLatent + ch] = o[i];
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            if (n0 + i < rows) put(n0 + i, c * 128 + t, o[i]);
                     }
-                }
+            };
+            if (!whole) {
+                float* part = a.part + (int64_t)slot * N * kLatent;
+                emit([&](int rr, int ch, float x) { part[rr * kLatent + ch] = x; });
+            } else if (a.out_dt == KDA_BF16) {
+                auto* o = static_cast<__nv_bfloat16*>(a.out);
+                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = __float2bfloat16_rn(x * rowf[rr]); });
+            } else if (a.out_dt == KDA_F16) {
+                auto* o = static_cast<__half*>(a.out);
+                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = __float2half_rn(x * rowf[rr]); });
+            } else {
+                auto* o = static_cast<float*>(a.out);
+                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = x * rowf[rr]; });
             }
             fence_before();
             bar_named(1, 128);  // rowf read by all before the next segment writes it
@@ -637,41 +672,60 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 }
 
 // Joins the parts of a request that several CTAs hold: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i.
-// Block (g, y): rows 4y .. 4y + 3 of the request whose first part CTA g holds; a thread has 4 channels.
+// Block (g, row): a row of the request whose first part CTA g holds; a thread has 4 channels.  The
+// factors of all parts (at most one a CTA) are taken first, side by side, so that the loads of the
+// parts do not wait on one another.
 template <int N>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeArgs a) {
+    __shared__ float fac[kDecCtas];
+    __shared__ float red[2][4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int g = blockIdx.x, t = threadIdx.x;
+    const int g = blockIdx.x, row = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int4 me = a.meta[g];
-    if (me.x < 0) return;
-    const int rows = min(N, a.K * a.H - me.y * N);
+    if (me.x < 0 || row >= a.K * a.H - me.y * N) return;
+    const int parts = me.z - g + 1;
     const float inf = __int_as_float(0x7f800000);
-    for (int row = blockIdx.y * 4; row < min(rows, (int)blockIdx.y * 4 + 4); ++row) {
-        float m = -inf;
-        for (int i = g; i <= me.z; ++i) m = fmaxf(m, a.ml[(int64_t)(2 * i + (i == g)) * N + row].x);
-        const float mr = m == -inf ? 0.f : m;
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = g; i <= me.z; ++i) {
-            const int64_t at = (int64_t)(2 * i + (i == g)) * N + row;
-            const float2 ml = a.ml[at];
-            const float4 x = *reinterpret_cast<const float4*>(a.part + at * kLatent + 4 * t);
-            const float f = ex2(ml.x - mr);
-            l = fmaf(f, ml.y, l);
-            o.x = fmaf(f, x.x, o.x);
-            o.y = fmaf(f, x.y, o.y);
-            o.z = fmaf(f, x.z, o.z);
-            o.w = fmaf(f, x.w, o.w);
-        }
-        const float il = l > 0.f ? 1.f / l : 0.f;
-        const int f = me.y * N + row, tt = f / a.H, h = f - tt * a.H;
-        const int64_t orow = (int64_t)me.x * a.K + tt;
-        store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il),
-                  a.out_dt);
-        if (t == 0 && a.lse != nullptr)
-            a.lse[orow * a.H + h] = l > 0.f ? (mr + log2f(l)) * 0.69314718055994531f : -inf;
+    // part i is CTA g + i's: the first in its second place, the others in their first
+    auto at = [&](int i) { return (int64_t)(2 * (g + i) + (i == 0)) * N + row; };
+    float2 ml[(kDecCtas + 127) / 128];
+    float m = -inf;
+#pragma unroll
+    for (int k = 0; k < (kDecCtas + 127) / 128; ++k) {
+        ml[k] = t + 128 * k < parts ? a.ml[at(t + 128 * k)] : make_float2(-inf, 0.f);
+        m = fmaxf(m, ml[k].x);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float mr = m == -inf ? 0.f : m;
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < (kDecCtas + 127) / 128; ++k) {
+        const float f = ex2(ml[k].x - mr);
+        l = fmaf(f, ml[k].y, l);
+        if (t + 128 * k < parts) fac[t + 128 * k] = f;
+    }
+    l = warp_sum(l);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(a.part + at(i) * kLatent + 4 * t);
+        const float f = fac[i];
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
+    }
+    const float il = l > 0.f ? 1.f / l : 0.f;
+    const int f = me.y * N + row, tt = f / a.H, h = f - tt * a.H;
+    const int64_t orow = (int64_t)me.x * a.K + tt;
+    store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il), a.out_dt);
+    if (t == 0 && a.lse != nullptr) a.lse[orow * a.H + h] = l > 0.f ? (mr + log2f(l)) * 0.69314718055994531f : -inf;
 }
 
 int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -690,7 +744,7 @@ kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_
     f<<<grid, kDecThreads, L::SMEM, s>>>(map[0], map[1], a);
     if (max_tiles <= 1) return launch_status();  // one tile a request: nothing is split
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, N / 4);
+    cfg.gridDim = dim3(grid, N);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
