@@ -162,6 +162,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int N, int DT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rmap,
@@ -508,6 +510,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 wait(L::B_S, it & 1);
                 wait(L::B_RFULL + rslot, rph);
                 fence_after();
+                if (j == max(g.j0, g.j1 - 3)) {
+                    // the next segment's query rows into L2: behind the loads of the ring, a read from
+                    // HBM takes some microseconds, and S waits for it
+                    Walk nx = w;
+                    if (nx.next(a)) {
+                        const int rr = t % N, ff = nx.crt * N + rr, tt = ff / a.H, h = ff - tt * a.H;
+                        if (ff < a.K * a.H) {
+                            const int64_t qrow = (int64_t)nx.cr * a.K + tt;
+                            for (int x = t / N; x < 9; x += L::REP)
+                                prefetch_l2(x < 8 ? a.ql.base + qrow * a.ql.rs + h * a.ql.hs + x * 64
+                                                  : a.qr.base + qrow * a.qr.rs + h * a.qr.hs);
+                        }
+                    }
+                }
                 const int t0 = j * kTile;
                 const uint32_t bad = (uint32_t)bad_box[rslot];
                 if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
@@ -635,31 +651,34 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             bar_named(1, 128);
             wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
             fence_after();
-            // channel c * 128 + t of every row; put(row, channel, value) is chosen once
+            // channel c * 128 + t of every row; put is chosen once
             auto emit = [&](auto put) {
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int n0 = 0; n0 < N; n0 += 16) {
                         if (n0 >= rows) break;
-                        float o[16];
+                        float o[16], fac[16];
+                        int64_t off[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) fac[i] = rowf[n0 + i], off[i] = rowo[n0 + i];
                         ld16(tq + c * N + n0, o);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (n0 + i < rows) put(n0 + i, c * 128 + t, o[i]);
+                            if (n0 + i < rows) put(n0 + i, off[i], c * 128 + t, o[i], fac[i]);
                     }
             };
             if (!whole) {
                 float* part = a.part + (int64_t)slot * N * kLatent;
-                emit([&](int rr, int ch, float x) { part[rr * kLatent + ch] = x; });
+                emit([&](int rr, int64_t, int ch, float x, float) { part[rr * kLatent + ch] = x; });
             } else if (a.out_dt == KDA_BF16) {
                 auto* o = static_cast<__nv_bfloat16*>(a.out);
-                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = __float2bfloat16_rn(x * rowf[rr]); });
+                emit([&](int, int64_t at, int ch, float x, float f) { o[at + ch] = __float2bfloat16_rn(x * f); });
             } else if (a.out_dt == KDA_F16) {
                 auto* o = static_cast<__half*>(a.out);
-                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = __float2half_rn(x * rowf[rr]); });
+                emit([&](int, int64_t at, int ch, float x, float f) { o[at + ch] = __float2half_rn(x * f); });
             } else {
                 auto* o = static_cast<float*>(a.out);
-                emit([&](int rr, int ch, float x) { o[rowo[rr] + ch] = x * rowf[rr]; });
+                emit([&](int, int64_t at, int ch, float x, float f) { o[at + ch] = x * f; });
             }
             fence_before();
             bar_named(1, 128);  // rowf read by all before the next segment writes it
