@@ -1,25 +1,43 @@
-// latent_prefill.cu -- kda_latent_prefill: expanded latent attention, in its plain blocked form
-// on the CUDA cores.
+// latent_prefill.cu -- kda_latent_prefill: expanded latent attention of packed sequences.
 //
-// A block owns 32 query rows (8 a warp) and walks its keys 32 at a time through shared memory
-// with the running maximum and sum of a softmax: o = sum_p e^{s_p - m} v_p, l = sum_p e^{s_p - m}
-// in registers, rescaled by e^{m - m'} when the maximum moves.
+// A CTA takes 256 query rows of one (sequence, head) as two tiles of 128 and walks the keys 128 at a
+// time.  Per tile of keys and tile of queries
+//   S = Q K^T       M = 128, N = 128, K = 192 (128 nope, 64 rope: the rope key is loaded from its one
+//                   row a token, so it is not repeated per head anywhere)
+//   P = 2^(c S - m) c = scale log2 e, one thread a query row; P goes back to TMEM over S, rounded
+//                   to the input type, as the A operand of
+//   O += P V        M = 128, N = 128, K = 128; V as it lies in shared memory (MN-major)
+// The two query tiles take turns: while the tensor cores work on one, the four warps of the other do
+// its exponentials.  m moves only when a row's maximum exceeds it by 8 (a factor of 256, far inside
+// fp32 and fp16), so that O is rarely rescaled.
+//
+// Roles: warps 0-3 and 4-7 softmax of query tile 0 and 1 (and its results), warp 8 loads by TMA (the
+// queries once, then a ring of 16 KiB parts: three of K, two of V a tile), warp 9 issues MMAs.
+// Long rows first: the CTAs of a sequence's last queries have the most keys.
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "latent_host.h"
+#include "umma.cuh"
 
 namespace kda {
 namespace {
 
+using namespace umma;
+
+constexpr int kQTile = 128, kQBlock = 2 * kQTile, kKTile = 128;
+constexpr int kPreThreads = 320;
+constexpr uint32_t kPreWait = 1u << 18;  // polls, about a second: loads and MMAs take microseconds
+constexpr uint32_t kPart = 128 * 128;    // 128 rows of 64 16-bit channels
+constexpr int kSlots = 8;
+
 struct PrefillArgs {
-    LatentRows q, k, v;
-    const uint16_t* kr;
-    int64_t kr_stride;
     const int32_t* cu_q;
     const int32_t* cu_k;
     int32_t N, Tq, Tk, H;
-    float scale;
-    int32_t full;
+    int32_t hq, hk, hv;  // 1, or 0 where the heads share a row (head stride 0)
+    float c;             // |scale| log2 e
+    bool negate;         // scale < 0
+    bool full;
     void* out;
     int64_t out_rs, out_hs;
     int32_t out_dt;
@@ -27,115 +45,340 @@ struct PrefillArgs {
     int32_t* dev_status;
 };
 
-constexpr int kRowsB = 32, kKeysB = 32, kWarps = 4, kRowsW = kRowsB / kWarps;
+struct PreMaps {
+    CUtensorMap q, k, kr, v;
+};
 
-// The walk over keys of one block.  qrow(i, d): query channel; key(p, d), val(p, d): channels of
-// key p (only for p with ok(p)); last(i): last key row i sees; store(i, o[], lse).
-template <int DK, int DV, class Q, class KF, class VF, class OK, class LAST, class ST>
-__device__ void attend(float* sm, int rows, int n_keys, float scale, Q qrow, KF key, VF val, OK ok, LAST last, ST store) {
-    float* sq = sm;                      // [32][DK]
-    float* sk = sq + kRowsB * DK;        // [32][DK + 1]
-    float* sv = sk + kKeysB * (DK + 1);  // [32][DV]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const float inf = __int_as_float(0x7f800000);
-    for (int e = tid; e < kRowsB * DK; e += kWarps * 32) sq[e] = e / DK < rows ? qrow(e / DK, e % DK) * scale : 0.f;
-    float m[kRowsW], l[kRowsW], o[kRowsW][DV / 32];
-#pragma unroll
-    for (int i = 0; i < kRowsW; ++i) {
-        m[i] = -inf;
-        l[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < DV / 32; ++j) o[i][j] = 0.f;
-    }
-    for (int p0 = 0; p0 < n_keys; p0 += kKeysB) {
-        __syncthreads();
-        for (int e = tid; e < kKeysB * DK; e += kWarps * 32) {
-            const int p = p0 + e / DK;
-            sk[(e / DK) * (DK + 1) + e % DK] = p < n_keys && ok(p) ? key(p, e % DK) : 0.f;
-        }
-        for (int e = tid; e < kKeysB * DV; e += kWarps * 32) {
-            const int p = p0 + e / DV;
-            sv[e] = p < n_keys && ok(p) ? val(p, e % DV) : 0.f;
-        }
-        __syncthreads();
-        const int p = p0 + lane;
-        const bool pok = p < n_keys && ok(p);
-#pragma unroll
-        for (int i = 0; i < kRowsW; ++i) {
-            const int row = warp * kRowsW + i;
-            float s = 0.f;
-            for (int d = 0; d < DK; ++d) s = fmaf(sq[row * DK + d], sk[lane * (DK + 1) + d], s);
-            if (!pok || p > last(row)) s = -inf;
-            float mx = s;
-#pragma unroll
-            for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
-            const float mn = fmaxf(m[i], mx);
-            if (mn == -inf) continue;
-            const float f = expf(m[i] - mn), e = expf(s - mn);
-            m[i] = mn;
-            l[i] = l[i] * f + warp_sum(e);
-#pragma unroll
-            for (int j = 0; j < DV / 32; ++j) o[i][j] *= f;
-            for (int q = 0; q < kKeysB; ++q) {
-                const float pq = __shfl_sync(~0u, e, q);
-#pragma unroll
-                for (int j = 0; j < DV / 32; ++j) o[i][j] = fmaf(pq, sv[q * DV + lane + 32 * j], o[i][j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsW; ++i) {
-        const int row = warp * kRowsW + i;
-        if (row >= rows) continue;
-        const float il = l[i] > 0.f ? 1.f / l[i] : 0.f;
-#pragma unroll
-        for (int j = 0; j < DV / 32; ++j) store(row, lane + 32 * j, o[i][j] * il);
-        if (lane == 0) store(row, -1, l[i] > 0.f ? m[i] + logf(l[i]) : -inf);
-    }
-}
+// shared memory: Q (2 x 3 parts), the ring, barriers
+constexpr uint32_t PS_RING = 6 * kPart, PS_BAR = PS_RING + kSlots * kPart;
+constexpr int PB_Q = 0, PB_FULL = 2, PB_EMPTY = PB_FULL + kSlots, PB_S = PB_EMPTY + kSlots, PB_P = PB_S + 2,
+              PB_O = PB_P + 2, PB_DRAIN = PB_O + 2, PB_BARS = PB_DRAIN + 1;
+constexpr uint32_t PS_CTRL = PS_BAR + 8 * 32, PS_SCAN = PS_CTRL + 32, PS_SMEM = PS_SCAN + 4 * 16;
+static_assert(PB_BARS <= 32 && PS_SMEM <= 232448, "shared memory plan");
+// TMEM: S of the two query tiles, then O
+constexpr uint32_t PT_S = 0, PT_O = 256;
 
-__device__ __forceinline__ void put(void* out, int64_t i, float x, int dt) {
-    if (dt == KDA_F32) static_cast<float*>(out)[i] = x;
-    else if (dt == KDA_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
-    else static_cast<__half*>(out)[i] = __float2half_rn(x);
+__device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 }
 
 template <int DT>
-__global__ void __launch_bounds__(128) prefill_kernel(const __grid_constant__ PrefillArgs a) {
-    extern __shared__ float sm[];
+__global__ void __launch_bounds__(kPreThreads, 1)
+    prefill_kernel(const __grid_constant__ PreMaps maps, const __grid_constant__ PrefillArgs a) {
     using E = Elem<DT>;
-    auto ld = [](const uint16_t* p) { return E::get(*reinterpret_cast<const typename E::T*>(p)); };
-    int tile = blockIdx.x, q0 = 0, q1 = 0, k0 = 0, k1 = 0, n = 0;
-    for (; n < a.N; ++n) {
-        q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
-        if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
-            if (threadIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
-            continue;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* ctrl = reinterpret_cast<int*>(sm + PS_CTRL);  // 0 tmem, 1 sequence, 2 its tile
+    int* scan = reinterpret_cast<int*>(sm + PS_SCAN);
+    auto bar = [&](int i) { return sb + PS_BAR + 8 * i; };
+    const float inf = __int_as_float(0x7f800000);
+
+    // ---- which block of 256 rows: the last first, over all sequences
+    const int h = blockIdx.x % a.H, y = blockIdx.x / a.H;
+    auto blocks_of = [&](int n, bool& bad) {
+        const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
+        bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
+        return bad ? 0 : (q1 - q0 + kQBlock - 1) / kQBlock;
+    };
+    if (tid == 0) ctrl[1] = -1;
+    int before = 0;
+    for (int base = 0; base < a.N; base += kPreThreads) {
+        __syncthreads();
+        // from the last sequence to the first
+        const int n = a.N - 1 - (base + tid);
+        bool bad = false;
+        const int b = n >= 0 ? blocks_of(n, bad) : 0;
+        if (bad && blockIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
+        int x = b;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += z;
         }
-        const int tiles = (q1 - q0 + kRowsB - 1) / kRowsB;
-        if (tile < tiles) break;
-        tile -= tiles;
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int off = before;
+        for (int w = 0; w < kPreThreads / 32; ++w) {
+            if (w < warp) off += scan[w];
+            before += scan[w];
+        }
+        const int lo = off + x - b;
+        if (b > 0 && y >= lo && y < lo + b) {
+            ctrl[1] = n;
+            ctrl[2] = b - 1 - (y - lo);
+        }
+        // block 0 looks at every sequence, for the report
+        if (before > y && blockIdx.x != 0) break;
     }
-    if (n == a.N) return;
-    const int h = blockIdx.y, row0 = tile * kRowsB, rows = min(kRowsB, q1 - q0 - row0);
-    auto ok = [&](int) { return true; };
-    auto key = [&](int p, int d) {
-        return d < kNope ? ld(a.k.base + (k0 + p) * a.k.rs + h * a.k.hs + d) : ld(a.kr + (k0 + p) * a.kr_stride + d - kNope);
+    __syncthreads();
+    const int n = ctrl[1];
+    if (n < 0) return;
+    if (tid == 0) {
+        for (int i = 0; i < PB_BARS; ++i) mbar_init(bar(i), i == PB_P || i == PB_P + 1 ? 4 : 1);
+    }
+    if (warp == 9) tmem_alloc(sb + PS_CTRL, 512);
+    const int q0 = a.cu_q[n], Lq = a.cu_q[n + 1] - q0, k0 = a.cu_k[n], Lk = a.cu_k[n + 1] - k0;
+    const int row0 = ctrl[2] * kQBlock;
+    // key tiles of query tile q: up to the last key its last row sees
+    auto tiles_of = [&](int q) {
+        const int rows = min(kQTile, Lq - row0 - q * kQTile);
+        if (rows <= 0) return 0;
+        const int keys = a.full ? Lk : min(Lk, Lk - Lq + row0 + q * kQTile + rows);
+        return keys > 0 ? (keys + kKTile - 1) / kKTile : 0;
     };
-    auto val = [&](int p, int d) { return ld(a.v.base + (k0 + p) * a.v.rs + h * a.v.hs + d); };
-    auto q = [&](int i, int d) { return ld(a.q.base + (q0 + row0 + i) * a.q.rs + h * a.q.hs + d); };
-    const int off = a.full ? 1 << 30 : (k1 - k0) - (q1 - q0) + row0;
-    auto last = [&](int i) { return off + i; };
-    auto store = [&](int i, int d, float x) {
-        const int64_t row = q0 + row0 + i;
-        if (d >= 0) put(a.out, row * a.out_rs + h * a.out_hs + d, x, a.out_dt);
-        else if (a.lse) a.lse[row * a.H + h] = x;
+    const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctrl[0];
+    bool dead = false;
+    auto wait = [&](int b, uint32_t parity) {
+        if (dead) return;
+        if (!mbar_wait(bar(b), parity, kPreWait)) {
+            dead = true;
+            report(a.dev_status, KDA_DEV_TIMEOUT);
+        }
     };
-    const int n_keys = a.full ? k1 - k0 : max(0, min(k1 - k0, off + rows));
-    attend<kHeadK, kHeadV>(sm, rows, n_keys, a.scale, q, key, val, ok, last, store);
+
+    if (warp == 8) {
+        // ================================================================ loads
+        if (lane == 0) {
+            uint32_t issued = 0;
+            auto load_queries = [&](int q) {
+                mbar_expect_tx(bar(PB_Q + q), 3 * kPart);
+                for (int c = 0; c < 3; ++c)
+                    tma_load_3d(sb + (q * 3 + c) * kPart, &maps.q, 64 * c, h * a.hq, q0 + row0 + q * kQTile, bar(PB_Q + q));
+            };
+            if (n0 > 0) load_queries(0);
+            for (int i = 0; i < nt && !dead; ++i) {
+                const int t = k0 + i * kKTile;
+                for (int c = 0; c < 5; ++c, ++issued) {
+                    const uint32_t slot = issued % kSlots;
+                    wait(PB_EMPTY + slot, (issued / kSlots & 1) ^ 1);
+                    if (dead) break;
+                    const uint32_t dst = sb + PS_RING + slot * kPart;
+                    mbar_expect_tx(bar(PB_FULL + slot), kPart);
+                    if (c < 2) tma_load_3d(dst, &maps.k, 64 * c, h * a.hk, t, bar(PB_FULL + slot));
+                    else if (c == 2) tma_load_2d(dst, &maps.kr, 0, t, bar(PB_FULL + slot));
+                    else tma_load_3d(dst, &maps.v, 64 * (c - 3), h * a.hv, t, bar(PB_FULL + slot));
+                    if (issued == 2 && n1 > 0) load_queries(1);
+                }
+            }
+            // nothing may be in flight when the CTA ends
+            dead = false;
+            if (n0 > 0) wait(PB_Q, 0);
+            if (n1 > 0 && issued > 2) wait(PB_Q + 1, 0);
+            for (uint32_t k = issued > kSlots ? issued - kSlots : 0; k < issued; ++k) wait(PB_FULL + k % kSlots, k / kSlots & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ================================================================ MMAs
+        // the whole warp runs this, one lane issues (umma.cuh, mma_by)
+        const uint32_t lead = elect_lane();
+        const uint32_t sb4 = sb >> 4;
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const int m0 = __shfl_sync(~0u, n0, 0), m1 = __shfl_sync(~0u, n1, 0), mt = max(m0, m1);
+        const uint32_t ids = idesc_16(DT == KDA_F16, 128, kKTile, false, false, a.negate);
+        const uint32_t idv = idesc_16(DT == KDA_F16, 128, 64, false, true, false);
+        // S of query tile q against key tile i; `fresh`: the first of the tile waits for its parts
+        auto do_s = [&](int q, int i, bool fresh) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const uint32_t k = 5 * i + c, slot = k % kSlots;
+                if (fresh) {
+                    wait(PB_FULL + slot, k / kSlots & 1);
+                    fence_after();
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_by(lead, tm + PT_S + q * 128, desc_k4(sb4 + (q * 3 + c) * (kPart / 16), 128, s),
+                           desc_k4(sb4 + PS_RING / 16 + slot * (kPart / 16), 128, s), ids, c + s != 0);
+            }
+            commit_by(lead, bar(PB_S + q));
+        };
+        auto release = [&](uint32_t k) { commit_by(lead, bar(PB_EMPTY + k % kSlots)); };
+        for (int q = 0; q < 2; ++q) {
+            if ((q ? m1 : m0) == 0) continue;
+            wait(PB_Q + q, 0);
+            do_s(q, 0, q == 0 || m0 == 0);
+        }
+        if (mt > 0)
+            for (int c = 0; c < 3; ++c) release(c);
+        bool stop = false;
+        for (int i = 0; i < mt && !stop; ++i) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int mq = q ? m1 : m0, mo = q ? m0 : m1;
+                if (i >= mq) continue;
+                const bool first = q == 0 || i >= mo;       // of the two query tiles at key tile i
+                const bool final = q == 1 || i >= mo;
+                wait(PB_P + q, i & 1);
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t k = 5 * i + 3 + c, slot = k % kSlots;
+                    if (first) {
+                        wait(PB_FULL + slot, k / kSlots & 1);
+                        fence_after();
+                    }
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_ta_by(lead, tm + PT_O + q * 128 + c * 64, tm + PT_S + q * 128 + 8 * s,
+                                  desc_mn4(sb4 + PS_RING / 16 + slot * (kPart / 16), 16, 1024, s), idv, i + s != 0);
+                }
+                commit_by(lead, bar(PB_O + q));
+                if (final)
+                    for (int c = 3; c < 5; ++c) release(5 * i + c);
+                if (i + 1 < mq) {
+                    do_s(q, i + 1, q == 0 || i + 1 >= mo);
+                    if (q == 1 || i + 1 >= mo)
+                        for (int c = 0; c < 3; ++c) release(5 * (i + 1) + c);
+                }
+            }
+            stop = __any_sync(~0u, dead);
+        }
+        commit_by(lead, bar(PB_DRAIN));
+        dead = false;
+        wait(PB_DRAIN, 0);
+    } else {
+        // ================================================================ softmax and results
+        const int q = warp >> 2, t = tid & 127;
+        const int my_tiles = q ? n1 : n0;
+        const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = tq + PT_S + q * 128, to = tq + PT_O + q * 128;
+        const int row = row0 + q * kQTile + t;  // of the sequence
+        const int last = row >= Lq ? -1 : a.full ? Lk - 1 : Lk - Lq + row;
+        float m = -inf, l = 0.f;
+        for (int i = 0; i < my_tiles && !__any_sync(~0u, dead); ++i) {
+            uint32_t s[4][32];
+            wait(PB_S + q, i & 1);
+            fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) ld32_issue(ts + 32 * b, s[b]);
+            wait_ld();
+            const int lim = last - i * kKTile;  // columns 0 .. lim are seen
+            if (lim < kKTile - 1) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * b + e > lim) s[b][e] = __float_as_uint(-inf);
+            }
+            float mx[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                mx[b] = __uint_as_float(s[b][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][e]));
+            }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float f = 1.f;
+            bool need = false;
+            if (i == 0) {
+                m = mt;
+            } else if (mt > m && (m == -inf || (mt - m) * a.c > 8.f)) {
+                f = ex2((m - mt) * a.c);
+                m = mt;
+                need = true;
+            }
+            if (__any_sync(~0u, need)) {
+                wait(PB_O + q, (i - 1) & 1);
+                fence_after();
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    ld32(to + 32 * b, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                    st32(to + 32 * b, o);
+                }
+                l *= f;
+            }
+            const float mc = m == -inf ? 0.f : m * a.c;
+            const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), cc, nm);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    ls[e & 1] = __fadd2_rn(ls[e & 1], x);
+                    p[e] = E::put2(x.x, x.y);
+                }
+                st16u(ts + 16 * b, p);
+            }
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+            if ((i + 1) * kKTile > Lk) {
+                // keys past the sequence: their weight is zero, and so has to be the value (what lies
+                // there belongs to another sequence)
+                const uint32_t k = 5 * i + 3;
+                wait(PB_FULL + k % kSlots, k / kSlots & 1);
+                wait(PB_FULL + (k + 1) % kSlots, (k + 1) / kSlots & 1);
+                const int valid = Lk - i * kKTile;
+                for (int e = t; e < (kKTile - valid) * 16; e += 128) {
+                    const uint32_t at = sb + PS_RING + ((k + (e >> 3 & 1)) % kSlots) * kPart + (valid + (e >> 4)) * 128 + (e & 7) * 16;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
+                }
+                fence_async_smem();
+            }
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(PB_P + q));
+        }
+        if (my_tiles > 0) {
+            wait(PB_O + q, (my_tiles - 1) & 1);
+            fence_after();
+        }
+        const float il = l > 0.f ? 1.f / l : 0.f;
+        const int64_t orow = (int64_t)q0 + row;
+        if (row < Lq && a.lse != nullptr)
+            a.lse[orow * a.H + h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
+        const int64_t at = orow * a.out_rs + (int64_t)h * a.out_hs;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float o[32];
+            if (my_tiles > 0) {
+                ld32(to + 32 * b, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+            if (row < Lq) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    store4_as(a.out, at + 32 * b + e, make_float4(o[e] * il, o[e + 1] * il, o[e + 2] * il, o[e + 3] * il),
+                              a.out_dt);
+            }
+        }
+        fence_before();
+    }
+    __syncthreads();
+    fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-constexpr int smem_of(int dk, int dv) { return (kRowsB * dk + kKeysB * (dk + 1) + kKeysB * dv) * 4; }
+// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head, 128 rows.
+bool rows_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int channels, int H, int T) {
+    // a dimension that is not stepped along (one head or row, or heads that share a row) has size 1
+    // and any legal stride
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)(r.hs ? H : 1), (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)(r.hs ? r.hs : channels) * 2, (cuuint64_t)(r.rs ? r.rs : channels) * 2};
+    const cuuint32_t box[3] = {64, 1, 128};
+    return encode_16bit(map, dt, 3, r.base, dims, strides, box);
+}
 
 }  // namespace
 }  // namespace kda
@@ -153,25 +396,43 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     KDA_REQUIRE(N >= 0 && Tq >= 0 && Tk >= 0 && H > 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(d_nope == kNope && d_rope == kRope && dv == kHeadV, KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE((flags & ~KDA_LATENT_FULL) == 0 && H < 65536, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE((flags & ~KDA_LATENT_FULL) == 0, KDA_ERR_UNSUPPORTED);
+    const int64_t blocks = ((int64_t)Tq / kQBlock + N) * H;
+    KDA_REQUIRE(blocks < (1ll << 31) && Tk < (1 << 30) && Tq < (1 << 30), KDA_ERR_UNSUPPORTED);
     if (N == 0 || Tq == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(q) && rows_ok(out), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(k_nope != nullptr && v != nullptr, KDA_ERR_INVALID_ARG);
     if (Tk > 0) {
         KDA_REQUIRE(rows_ok(k_nope) && rows_ok(v), KDA_ERR_INVALID_ARG);
         KDA_REQUIRE(k_rope != nullptr && aligned16(k_rope), KDA_ERR_INVALID_ARG);
     }
-    KDA_REQUIRE(k_nope != nullptr && v != nullptr, KDA_ERR_INVALID_ARG);
+    const kda_rows_desc* ds[] = {q, k_nope, v, out};
+    for (const kda_rows_desc* d : ds) KDA_REQUIRE(d->row_stride >= 0 && d->head_stride >= 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE((q->row_stride > 0 || Tq == 1) && ((k_nope->row_stride > 0 && v->row_stride > 0) || Tk <= 1),
+                KDA_ERR_INVALID_ARG);
     const void* ptrs[] = {cu_q, cu_k};
     for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(k_rope_stride % 8 == 0 && k_rope_stride >= kRope, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
-    const PrefillArgs a{as_rows(q), as_rows(k_nope), as_rows(v), static_cast<const uint16_t*>(k_rope), k_rope_stride,
-                        cu_q, cu_k, N, Tq, Tk, H, scale, (flags & KDA_LATENT_FULL) != 0, const_cast<void*>(out->base),
-                        out->row_stride, out->head_stride, out_dtype, lse, dev_status};
-    const dim3 grid((unsigned)(Tq / kRowsB + N), (unsigned)H);
-    constexpr int smem = smem_of(kHeadK, kHeadV);
+    PreMaps maps;
+    const LatentRows rq = as_rows(q), rk = Tk > 0 ? as_rows(k_nope) : rq, rv = Tk > 0 ? as_rows(v) : rq;
+    KDA_REQUIRE(rows_map(&maps.q, in_dtype, rq, kHeadK, H, Tq), KDA_ERR_CUDA);
+    if (Tk > 0) {
+        KDA_REQUIRE(rows_map(&maps.k, in_dtype, rk, kNope, H, Tk), KDA_ERR_CUDA);
+        KDA_REQUIRE(rows_map(&maps.v, in_dtype, rv, kHeadV, H, Tk), KDA_ERR_CUDA);
+        const cuuint64_t dims[2] = {kRope, (cuuint64_t)Tk};
+        const cuuint64_t strides[1] = {(cuuint64_t)k_rope_stride * 2};
+        const cuuint32_t box[2] = {64, 128};
+        KDA_REQUIRE(encode_16bit(&maps.kr, in_dtype, 2, k_rope, dims, strides, box), KDA_ERR_CUDA);
+    } else {
+        maps.k = maps.kr = maps.v = maps.q;  // no key, no load
+    }
+    const PrefillArgs a{cu_q, cu_k, N, Tq, Tk, H, rq.hs != 0, rk.hs != 0, rv.hs != 0, log2_scale(scale), scale < 0.f,
+                        (flags & KDA_LATENT_FULL) != 0, const_cast<void*>(out->base), out->row_stride, out->head_stride,
+                        out_dtype, lse, dev_status};
     auto* f = in_dtype == KDA_BF16 ? prefill_kernel<KDA_BF16> : prefill_kernel<KDA_F16>;
-    cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    f<<<grid, 128, smem, as_stream(stream)>>>(a);
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PS_SMEM) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    f<<<(unsigned)blocks, kPreThreads, PS_SMEM, as_stream(stream)>>>(maps, a);
     return launch_status();
 }

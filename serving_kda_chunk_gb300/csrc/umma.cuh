@@ -325,6 +325,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x
         : "memory");
 }
 
+// One box of a 3-D tensor map at (x, y, z), under the same rules.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+
 // One box of a 4-D tensor map at (x, y, z, w), under the same rules.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t mbar) {
     asm volatile(
