@@ -189,15 +189,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int m0 = __shfl_sync(~0u, n0, 0), m1 = __shfl_sync(~0u, n1, 0), mt = max(m0, m1);
         const uint32_t ids = idesc_16(DT == KDA_F16, 128, kKTile, false, false, a.negate);
         const uint32_t idv = idesc_16(DT == KDA_F16, 128, 64, false, true, false);
-        // S of query tile q against key tile i; `fresh`: the first of the tile waits for its parts
-        auto do_s = [&](int q, int i, bool fresh) {
+        auto release = [&](uint32_t k) { commit_by(lead, bar(PB_EMPTY + k % kSlots)); };
+        // Part k of the ring has landed.  A wait queues behind the MMAs issued before it, so V is waited
+        // for ahead of the weights; K has only just been requested and is taken part by part.
+        auto landed = [&](uint32_t k) { wait(PB_FULL + k % kSlots, k / kSlots & 1); };
+        auto do_s = [&](int q, int i, bool first) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
-                const uint32_t k = 5 * i + c, slot = k % kSlots;
-                if (fresh) {
-                    wait(PB_FULL + slot, k / kSlots & 1);
+                if (first) {
+                    landed(5 * i + c);
                     fence_after();
                 }
+                const uint32_t slot = (5 * i + c) % kSlots;
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     mma_by(lead, tm + PT_S + q * 128, desc_k4(sb4 + (q * 3 + c) * (kPart / 16), 128, s),
@@ -205,43 +208,42 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             commit_by(lead, bar(PB_S + q));
         };
-        auto release = [&](uint32_t k) { commit_by(lead, bar(PB_EMPTY + k % kSlots)); };
-        for (int q = 0; q < 2; ++q) {
-            if ((q ? m1 : m0) == 0) continue;
-            wait(PB_Q + q, 0);
-            do_s(q, 0, q == 0 || m0 == 0);
+        auto do_pv = [&](int q, int i) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t slot = (5 * i + 3 + c) % kSlots;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_ta_by(lead, tm + PT_O + q * 128 + c * 64, tm + PT_S + q * 128 + 8 * s,
+                              desc_mn4(sb4 + PS_RING / 16 + slot * (kPart / 16), 16, 1024, s), idv, i + s != 0);
+            }
+            commit_by(lead, bar(PB_O + q));
+        };
+        if (m0 > 0) {
+            wait(PB_Q, 0);
+            do_s(0, 0, true);
+        }
+        if (m1 > 0) {
+            wait(PB_Q + 1, 0);
+            do_s(1, 0, m0 == 0);
         }
         if (mt > 0)
             for (int c = 0; c < 3; ++c) release(c);
         bool stop = false;
         for (int i = 0; i < mt && !stop; ++i) {
+            for (int c = 3; c < 5; ++c) landed(5 * i + c);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int mq = q ? m1 : m0, mo = q ? m0 : m1;
-                if (i >= mq) continue;
-                const bool first = q == 0 || i >= mo;       // of the two query tiles at key tile i
-                const bool final = q == 1 || i >= mo;
-                wait(PB_P + q, i & 1);
-                fence_after();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t k = 5 * i + 3 + c, slot = k % kSlots;
-                    if (first) {
-                        wait(PB_FULL + slot, k / kSlots & 1);
-                        fence_after();
-                    }
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ta_by(lead, tm + PT_O + q * 128 + c * 64, tm + PT_S + q * 128 + 8 * s,
-                                  desc_mn4(sb4 + PS_RING / 16 + slot * (kPart / 16), 16, 1024, s), idv, i + s != 0);
-                }
-                commit_by(lead, bar(PB_O + q));
-                if (final)
-                    for (int c = 3; c < 5; ++c) release(5 * i + c);
-                if (i + 1 < mq) {
-                    do_s(q, i + 1, q == 0 || i + 1 >= mo);
-                    if (q == 1 || i + 1 >= mo)
-                        for (int c = 0; c < 3; ++c) release(5 * (i + 1) + c);
+                if (i < mq) {
+                    wait(PB_P + q, i & 1);
+                    fence_after();
+                    do_pv(q, i);
+                    if (q == 1 || i >= mo)
+                        for (int c = 3; c < 5; ++c) release(5 * i + c);
+                    if (i + 1 < mq) do_s(q, i + 1, q == 0 || i + 1 >= mo);
+                    if (i + 1 < mq && (q == 1 || i + 1 >= mo))
+                        for (int c = 5; c < 8; ++c) release(5 * i + c);
                 }
             }
             stop = __any_sync(~0u, dead);
@@ -273,14 +275,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (32 * b + e > lim) s[b][e] = __float_as_uint(-inf);
             }
-            float mx[4];
+            float mx[8];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                mx[b] = __uint_as_float(s[b][0]);
+            for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k >> 1][k & 1]);
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][e]));
-            }
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            for (int e = 2; e < 32; e += 4)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[k >> 1][e + (k & 1)])),
+                                  __uint_as_float(s[k >> 1][(e + 2 + (k & 1)) & 31]));
+            const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
             float f = 1.f;
             bool need = false;
             if (i == 0) {
@@ -294,32 +299,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 wait(PB_O + q, (i - 1) & 1);
                 fence_after();
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    float o[32];
-                    ld32(to + 32 * b, o);
+                for (int b = 0; b < 8; ++b) {
+                    float o[16];
+                    ld16(to + 16 * b, o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= f;
-                    st32(to + 32 * b, o);
+                    for (int e = 0; e < 16; ++e) o[e] *= f;
+                    st16f(to + 16 * b, o);
                 }
                 l *= f;
             }
             const float mc = m == -inf ? 0.f : m * a.c;
             const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), cc, nm);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    ls[e & 1] = __fadd2_rn(ls[e & 1], x);
-                    p[e] = E::put2(x.x, x.y);
-                }
-                st16u(ts + 16 * b, p);
-            }
-            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
             if ((i + 1) * kKTile > Lk) {
                 // keys past the sequence: their weight is zero, and so has to be the value (what lies
                 // there belongs to another sequence)
@@ -333,10 +324,24 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 }
                 fence_async_smem();
             }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), cc, nm);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    ls[e & 1] = __fadd2_rn(ls[e & 1], x);
+                    p[e] = E::put2(x.x, x.y);
+                }
+                st16u(ts + 16 * b, p);
+            }
             wait_st();
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(PB_P + q));
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         }
         if (my_tiles > 0) {
             wait(PB_O + q, (my_tiles - 1) & 1);
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (row < Lq && a.lse != nullptr)
             a.lse[orow * a.H + h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
         const int64_t at = orow * a.out_rs + (int64_t)h * a.out_hs;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             float o[32];
             if (my_tiles > 0) {

@@ -1,15 +1,31 @@
 // logprobs.cu -- kda_token_logprobs: log probability of given tokens, entropy and top
 // alternatives of logits rows.
 //
-// A block per row.  Every thread keeps a running maximum m and, relative to it, z = sum e^{x-m}
-// and w = sum e^{x-m} (x-m) over its elements; the block joins them, so
-//   logprob = (x_token - m) - log z,  entropy = log z - w / z.
-// The top ids are taken one after another: the largest (value, -id) below the last one taken.
+// One pass over the logits, which is what bounds it (HBM).  A thread keeps, over its elements and
+// relative to a reference v of its own (moved when an element exceeds it by 8 ln2),
+//   z = sum 2^d,  w = sum 2^d d,  d = (x - v) log2 e
+// and its largest element; the block joins them to
+//   logprob = (x_token - max) - ln z,  entropy = ln2 (log2 z - w / z)    (relative to the maximum).
+//
+// Top ids without a second pass: elements lie in columns, column t being thread t's.  Every element
+// of the top k is in one of the k columns with the largest maxima, and not below the least of
+// these.  So the columns are ranked by their maxima, only the k best are read again (a warp a
+// column, out of L2) and the few elements at or above the threshold are ranked by (value, -id).
+// Ties at the threshold can make them many (a mask of -inf over most of a vocabulary): then
+// the columns' maxima take part with their ids, and the k best elements are drawn one after another,
+// the column that gave one being read again for its next.
+//
+// Few rows: a row is split over a cluster of up to 8 blocks, whose sums and lists the first joins
+// through distributed shared memory.
+#include <cooperative_groups.h>
+
 #include "kda_host.h"
 #include "latent_common.cuh"
 
 namespace kda {
 namespace {
+
+namespace cg = cooperative_groups;
 
 struct LogprobArgs {
     const void* logits;
@@ -24,88 +40,345 @@ struct LogprobArgs {
     int32_t* dev_status;
 };
 
-// (value, id) as one unsigned key: larger value first, then smaller id; -0 equals +0 and NaN
-// lies below -inf.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t id) {
-    const uint32_t b = __float_as_uint(x + 0.f);
-    uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    if (x != x) o = 0;
-    return ((uint64_t)o << 32) | (uint32_t)~id;
-}
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kMaxTop = 32;
+constexpr int kCand = 256;      // candidates of the ranked path
+constexpr int kColumns = 64;    // columns it reads again
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kFloor = -200.f;  // 2^-200 is 0 in fp32: below this an element adds nothing
 
-constexpr int kLpThreads = 256;
+// A value as an unsigned number of the same order; -0 equals +0 and NaN lies below -inf.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+// (value, id) as one key: larger value first, then smaller id; 0 is below every element's
+__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t id) { return ((uint64_t)order << 32) | (uint32_t)~id; }
+
+// 16 bytes of a row: unpacking, and their largest element (NaN if one is NaN)
+template <int DT>
+struct Vec {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&x)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = Elem<DT>::get2(w[i]);
+            x[2 * i] = p.x;
+            x[2 * i + 1] = p.y;
+        }
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        if constexpr (DT == KDA_BF16)
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float max_of(uint4 v) {
+        const float2 p = Elem<DT>::get2(max2(max2(v.x, v.y), max2(v.z, v.w)));
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(p.x), "f"(p.y));
+        return r;
+    }
+};
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+template <>
+struct Vec<KDA_F32> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x);
+        x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z);
+        x[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float max_of(uint4 v) {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+};
+
+// The running sums of a thread.  The difference is taken before the factor: products of values near
+// the type's largest would overflow, and near the maximum the difference is exact.
+struct Sums {
+    float v = 0.f;                                  // reference
+    float limit = -__builtin_huge_valf();           // an element above this moves it
+    float2 z = {0.f, 0.f}, w = {0.f, 0.f};
+    __device__ __forceinline__ void raise(float vmax) {
+        if (z.x + z.y > 0.f) {  // else nothing yet, whatever v was
+            const float d = fmaxf((v - vmax) * kLog2e, kFloor), f = ex2(d);
+            w = make_float2(f * (w.x + z.x * d), f * (w.y + z.y * d));
+            z = make_float2(f * z.x, f * z.y);
+        }
+        v = vmax;
+        limit = vmax + 8.f * kLn2;
+    }
+    __device__ __forceinline__ void add2(float a, float b) {
+        float2 d = __fadd2_rn(make_float2(a, b), make_float2(-v, -v));
+        d = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+        d.x = fmaxf(d.x, kFloor);
+        d.y = fmaxf(d.y, kFloor);
+        const float2 e = make_float2(ex2(d.x), ex2(d.y));
+        z = __fadd2_rn(z, e);
+        w = __ffma2_rn(e, d, w);
+    }
+};
+
+struct LpShared {
+    float m[kLpWarps], z[kLpWarps], w[kLpWarps];
+    float bm, bz, bw;                  // the block's: maximum (NaN possible), sums relative to it
+    alignas(16) uint32_t col[kLpThreads];          // column maxima as ordered numbers
+    uint64_t ckey[kLpWarps];
+    uint32_t tau;
+    int n_cols, n_cand;
+    int cols[kColumns];
+    uint64_t cand[kCand];
+    uint64_t list[kMaxTop];            // the block's top keys, descending
+};
 
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobArgs a, const int C) {
     using E = Elem<DT>;
-    __shared__ float sm[kLpThreads], sz[kLpThreads], sw[kLpThreads];
-    __shared__ uint64_t sk[kLpThreads];
-    const int tid = threadIdx.x;
-    const int64_t r = blockIdx.x;
-    const typename E::T* row = static_cast<const typename E::T*>(a.logits) + r * a.row_stride;
+    using T = typename E::T;
+    using X = Vec<DT>;
+    constexpr int VE = X::n;
+    __shared__ LpShared s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float inf = __int_as_float(0x7f800000);
-    float m = -inf, z = 0.f, w = 0.f;
-    for (int i = tid; i < a.V; i += kLpThreads) {
+    const int64_t r = blockIdx.x / C;
+    const int part = blockIdx.x % C;
+    const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
+    // head elements up to a 16-byte boundary, vectors, tail elements; the vectors are cut over the
+    // blocks, the head goes to the first and the tail to the last
+    const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int head = min(a.V, mis ? VE - mis : 0);
+    const int nv = (a.V - head) / VE;
+    const int v0 = (int)((int64_t)nv * part / C), v1 = (int)((int64_t)nv * (part + 1) / C);
+    const int n_head = part == 0 ? head : 0;
+    const int tail0 = head + nv * VE, n_tail = part == C - 1 ? a.V - tail0 : 0;
+    const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+
+    Sums su;
+    float cm = -inf;  // this column's maximum, NaN if it holds one
+    auto one = [&](int i) {
         const float x = E::get(row[i]);
-        if (x > m) {
-            const float d = m - x, f = expf(d);
-            w = z > 0.f ? f * (w + z * d) : 0.f;
-            z *= f;
-            m = x;
-        }
-        if (x != -inf) {
-            const float d = x - m, e = expf(d);
-            z += e;
-            w += e > 0.f ? e * d : e;
-        }
+        cm = max_nan(cm, x);
+        if (x > su.limit) su.raise(x);
+        su.add2(x, -inf);
+    };
+    auto take = [&](uint4 v) {
+        const float vm = X::max_of(v);
+        cm = max_nan(cm, vm);
+        if (vm > su.limit) su.raise(vm);
+        float x[VE];
+        X::unpack(v, x);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) su.add2(x[i], x[i + 1]);
+    };
+    if (tid < n_head) one(tid);
+    if (tid < n_tail) one(tail0 + tid);
+    int j = v0 + tid;
+    for (; j + 3 * kLpThreads < v1; j += 4 * kLpThreads) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = __ldg(vec + j + u * kLpThreads);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) take(v[u]);
     }
-    sm[tid] = m; sz[tid] = z; sw[tid] = w;
-    __syncthreads();
-    for (int s = kLpThreads / 2; s; s >>= 1) {
-        if (tid < s) {
-            const float m1 = sm[tid], m2 = sm[tid + s], mm = fmaxf(m1, m2);
-            const float d1 = m1 - mm, d2 = m2 - mm;
-            const float f1 = sz[tid] == 0.f ? 0.f : expf(d1), f2 = sz[tid + s] == 0.f ? 0.f : expf(d2);
-            const float w1 = f1 == 0.f ? 0.f : f1 * (sw[tid] + sz[tid] * d1);
-            const float w2 = f2 == 0.f ? 0.f : f2 * (sw[tid + s] + sz[tid + s] * d2);
-            sw[tid] = w1 + w2;
-            sz[tid] = f1 * sz[tid] + f2 * sz[tid + s];
-            sm[tid] = mm;
+    for (; j < v1; j += kLpThreads) take(__ldg(vec + j));
+
+    // ---- the block's sums, relative to its maximum
+    const uint32_t mine = order_of(cm);
+    float bmax;
+    {
+        bmax = cm;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) bmax = max_nan(bmax, __shfl_xor_sync(~0u, bmax, o));
+        if (lane == 0) s.m[warp] = bmax;
+        s.col[tid] = mine;
+        if (tid == 0) {
+            s.tau = ~0u;
+            s.n_cols = s.n_cand = 0;
         }
         __syncthreads();
+        bmax = s.m[0];
+#pragma unroll
+        for (int i = 1; i < kLpWarps; ++i) bmax = max_nan(bmax, s.m[i]);
+        const float d = fmaxf((su.v - bmax) * kLog2e, kFloor), tz = su.z.x + su.z.y;
+        const float f = ex2(d);
+        float z = tz > 0.f ? f * tz : 0.f, w = tz > 0.f ? f * ((su.w.x + su.w.y) + tz * d) : 0.f;
+        warp_sum2(z, w);
+        if (lane == 0) {
+            s.z[warp] = z;
+            s.w[warp] = w;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            z = w = 0.f;
+#pragma unroll
+            for (int i = 0; i < kLpWarps; ++i) z += s.z[i], w += s.w[i];
+            s.bm = bmax;
+            s.bz = z;
+            s.bw = w;
+        }
     }
-    m = sm[0]; z = sz[0]; w = sw[0];
+
+    // ---- the block's top keys
+    const int top = a.top;
+    // every element of column c, split over a warp's lanes: f(value, id)
+    auto column = [&](int c, auto f) {
+        if (lane == 0 && c < n_head) f(E::get(row[c]), c);
+        if (lane == 0 && c < n_tail) f(E::get(row[tail0 + c]), tail0 + c);
+        for (int q = v0 + c + lane * kLpThreads; q < v1; q += 32 * kLpThreads) {
+            float x[VE];
+            X::unpack(__ldg(vec + q), x);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) f(x[i], head + q * VE + i);
+        }
+    };
+    if (top > 0) {
+        int rank = 0;  // columns with a larger maximum
+#pragma unroll 8
+        for (int i = 0; i < kLpThreads; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&s.col[i]);
+            rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        }
+        if (rank < top) {
+            atomicMin(&s.tau, mine);
+            const int at = atomicAdd(&s.n_cols, 1);
+            if (at < kColumns) s.cols[at] = tid;
+        }
+        if (tid < kMaxTop) s.list[tid] = 0;
+        __syncthreads();
+        const uint32_t tau = s.tau;
+        const int n_cols = bmax != bmax ? kLpThreads : s.n_cols;  // a column with NaN has no rank
+        if (n_cols <= kColumns) {
+            for (int c = warp; c < n_cols; c += kLpWarps)
+                column(s.cols[c], [&](float x, int id) {
+                    const uint32_t o = order_of(x);
+                    if (o >= tau) {
+                        const int at = atomicAdd(&s.n_cand, 1);
+                        if (at < kCand) s.cand[at] = key_of(o, (uint32_t)id);
+                    }
+                });
+        }
+        __syncthreads();
+        const int n = s.n_cand;
+        if (n_cols <= kColumns && n <= kCand) {
+            // keys are distinct, so every rank is taken once
+            if (tid < n) {
+                const uint64_t k = s.cand[tid];
+                int rk = 0;
+                for (int i = 0; i < n; ++i) rk += s.cand[i] > k;
+                if (rk < top) s.list[rk] = k;
+            }
+        } else {
+            // one after another: `best` is this column's largest key below the last one drawn
+            uint64_t best = 0;
+            auto better = [&](float x, int id, uint64_t below, uint64_t& b) {
+                const uint64_t k = key_of(order_of(x), (uint32_t)id);
+                if (k < below && k > b) b = k;
+            };
+            if (tid < n_head) better(E::get(row[tid]), tid, ~0ull, best);
+            if (tid < n_tail) better(E::get(row[tail0 + tid]), tail0 + tid, ~0ull, best);
+            for (int q = v0 + tid; q < v1; q += kLpThreads) {
+                float x[VE];
+                X::unpack(__ldg(vec + q), x);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) better(x[i], head + q * VE + i, ~0ull, best);
+            }
+            for (int k = 0; k < top; ++k) {
+                uint64_t b = best;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    const uint64_t y = __shfl_xor_sync(~0u, b, o);
+                    b = y > b ? y : b;
+                }
+                if (lane == 0) s.ckey[warp] = b;
+                __syncthreads();
+                uint64_t win = s.ckey[0];
+#pragma unroll
+                for (int i = 1; i < kLpWarps; ++i) win = s.ckey[i] > win ? s.ckey[i] : win;
+                if (win == 0) break;  // fewer elements than places
+                if (tid == 0) s.list[k] = win;
+                const uint32_t who = __ballot_sync(~0u, best == win);
+                if (who) {  // the warp of the column that gave it
+                    const int c = warp * 32 + __ffs(who) - 1;
+                    uint64_t nb = 0;
+                    column(c, [&](float x, int id) { better(x, id, win, nb); });
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) {
+                        const uint64_t y = __shfl_xor_sync(~0u, nb, o);
+                        nb = y > nb ? y : nb;
+                    }
+                    if (tid == c) best = nb;
+                }
+                __syncthreads();
+            }
+        }
+    }
+
+    // ---- the row's results: the first block joins the cluster's
+    float m, z, w;
+    uint64_t key = 0;
+    int rank = tid;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (C > 1) {
+        cluster.sync();
+        if (part == 0) {
+            m = s.bm;
+            for (int c = 1; c < C; ++c) m = max_nan(m, cluster.map_shared_rank(&s, c)->bm);
+            z = w = 0.f;
+            for (int c = 0; c < C; ++c) {
+                const LpShared* o = cluster.map_shared_rank(&s, c);
+                const float d = fmaxf((o->bm - m) * kLog2e, kFloor), oz = o->bz;
+                const float f = ex2(d);
+                z += oz > 0.f ? f * oz : 0.f;
+                w += oz > 0.f ? f * (o->bw + oz * d) : 0.f;
+            }
+            if (top > 0) {
+                __syncthreads();
+                if (tid < C * kMaxTop) key = cluster.map_shared_rank(&s, tid / kMaxTop)->list[tid % kMaxTop];
+                static_assert(8 * kMaxTop <= kCand && 8 * kMaxTop <= kLpThreads, "a thread a key");
+                s.cand[tid] = key;
+                __syncthreads();
+                rank = 0;
+                for (int i = 0; i < C * kMaxTop; ++i) rank += s.cand[i] > key;
+                if (key == 0) rank = kMaxTop;
+            }
+        }
+        cluster.sync();  // the others' shared memory has been read
+        if (part != 0) return;
+    } else {
+        __syncthreads();
+        m = s.bm;
+        z = s.bz;
+        w = s.bw;
+        if (tid < kMaxTop) key = s.list[tid];
+    }
     const float nan = __int_as_float(0x7fffffff);
-    const bool none = !(z > 0.f) || m == inf;
-    const float logz = none ? nan : logf(z);
+    const bool none = !(z > 0.f) || !(m < inf);  // only -inf, or +inf or NaN in the row
+    const float lz = none ? nan : log2f(z);
     if (tid == 0) {
         const int tok = a.tokens[r];
         float lp = 0.f;
         if (tok >= a.V) report(a.dev_status, KDA_DEV_BAD_SLOT);
-        else if (tok >= 0) lp = E::get(row[tok]) - m - logz;
+        else if (tok >= 0) lp = (E::get(row[tok]) - m) - lz * kLn2;
         a.logprob[r] = lp;
-        if (a.entropy) a.entropy[r] = logz - w / z;
+        if (a.entropy) a.entropy[r] = (lz - w / z) * kLn2;
     }
-    uint64_t last = ~0ull;
-    for (int j = 0; j < a.top; ++j) {
-        uint64_t best = 0;
-        for (int i = tid; i < a.V; i += kLpThreads) {
-            const uint64_t k = order_key(E::get(row[i]), (uint32_t)i);
-            if (k < last && k > best) best = k;
-        }
-        __syncthreads();
-        sk[tid] = best;
-        __syncthreads();
-        for (int s = kLpThreads / 2; s; s >>= 1) {
-            if (tid < s && sk[tid + s] > sk[tid]) sk[tid] = sk[tid + s];
-            __syncthreads();
-        }
-        last = sk[0];
-        if (tid == 0) {
-            const int id = (int)~(uint32_t)last;
-            a.top_ids[r * a.top + j] = id;
-            a.top_logprobs[r * a.top + j] = E::get(row[id]) - m - logz;
-        }
+    if (rank < top && key != 0) {
+        const int id = (int)~(uint32_t)key;
+        a.top_ids[r * top + rank] = id;
+        a.top_logprobs[r * top + rank] = (E::get(row[id]) - m) - lz * kLn2;
     }
 }
 
@@ -120,7 +393,7 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
                                          float* top_logprobs, int32_t* dev_status, void* stream) {
     KDA_REQUIRE(R >= 0 && V > 0 && top >= 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(dtype == KDA_BF16 || dtype == KDA_F32 || dtype == KDA_F16, KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE(top <= 32 && top <= V, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(top <= kMaxTop && top <= V && R < (1 << 28), KDA_ERR_UNSUPPORTED);
     if (R == 0) return KDA_OK;
     KDA_REQUIRE(logits != nullptr && reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype) == 0,
                 KDA_ERR_INVALID_ARG);
@@ -130,9 +403,23 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
     const void* ptrs[] = {tokens, logprob, entropy, top_ids, top_logprobs, dev_status};
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
     const LogprobArgs a{logits, row_stride, V, tokens, logprob, entropy, top, top_ids, top_logprobs, dev_status};
-    cudaStream_t s = as_stream(stream);
-    if (dtype == KDA_BF16) logprob_kernel<KDA_BF16><<<(unsigned)R, kLpThreads, 0, s>>>(a);
-    else if (dtype == KDA_F16) logprob_kernel<KDA_F16><<<(unsigned)R, kLpThreads, 0, s>>>(a);
-    else logprob_kernel<KDA_F32><<<(unsigned)R, kLpThreads, 0, s>>>(a);
+    // blocks a row: enough rows fill the SMs by themselves; else split, down to a few vectors a thread
+    int C = 1;
+    while (C < 8 && (int64_t)R * C < 304 && (int64_t)V * dtype_bytes(dtype) >= 2ll * C * kLpThreads * 32) C *= 2;
+    auto* f = dtype == KDA_BF16 ? logprob_kernel<KDA_BF16> : dtype == KDA_F16 ? logprob_kernel<KDA_F16> : logprob_kernel<KDA_F32>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(R * C));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, f, a, C) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
     return launch_status();
 }
