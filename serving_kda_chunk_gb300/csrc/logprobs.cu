@@ -7,10 +7,12 @@
 // and its largest element; the block joins them to
 //   logprob = (x_token - max) - ln z,  entropy = ln2 (log2 z - w / z)    (relative to the maximum).
 //
-// Top ids without a second pass: elements lie in columns, column t being thread t's.  Every element
-// of the top k is in one of the k columns with the largest maxima, and not below the least of
-// these.  So the columns are ranked by their maxima, only the k best are read again (a warp a
-// column, out of L2) and the few elements at or above the threshold are ranked by (value, -id).
+// Top ids without a second pass: elements lie in columns, column t being thread t's.  A threshold
+// that at least k column maxima reach is reached by the top k elements as well, and only by elements
+// of those columns.  Each column also leaves the maximum of every piece of it (8 vectors, more in the
+// longest rows) in shared memory, so only the pieces that reach the threshold are read again: about k
+// times 128 bytes.  (Reading the columns again whole cost a quarter of the time: strided, and by then
+// out of L2.)  The few elements at or above the threshold are ranked by (value, -id).
 // Ties at the threshold can make them many (a mask of -inf over most of a vocabulary): then
 // the columns' maxima take part with their ids, and the k best elements are drawn one after another,
 // the column that gave one being read again for its next.
@@ -43,7 +45,9 @@ struct LogprobArgs {
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kCand = 256;      // candidates of the ranked path
-constexpr int kColumns = 64;    // columns it reads again
+constexpr int kPieces = 128;    // pieces of columns it reads again
+constexpr int kBatch = 8;       // vectors of a column asked for at once
+constexpr int kMaxSeg = 32;     // pieces of a column
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kFloor = -200.f;  // 2^-200 is 0 in fp32: below this an element adds nothing
 
@@ -138,19 +142,20 @@ struct LpShared {
     alignas(16) uint32_t col[kLpThreads];          // column maxima as ordered numbers
     uint64_t ckey[kLpWarps];
     uint32_t tau;
-    int n_cols, n_cand;
-    int cols[kColumns];
+    int n_pieces, n_cand;
+    int pieces[kPieces];               // piece * kLpThreads + column
     uint64_t cand[kCand];
     uint64_t list[kMaxTop];            // the block's top keys, descending
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobArgs a, const int C) {
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobArgs a, const int C, const int per) {
     using E = Elem<DT>;
     using T = typename E::T;
     using X = Vec<DT>;
     constexpr int VE = X::n;
     __shared__ LpShared s;
+    extern __shared__ float seg[];  // [pieces][kLpThreads] maxima
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float inf = __int_as_float(0x7f800000);
     const int64_t r = blockIdx.x / C;
@@ -166,6 +171,9 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     const int tail0 = head + nv * VE, n_tail = part == C - 1 ? a.V - tail0 : 0;
     const uint4* vec = reinterpret_cast<const uint4*>(row + head);
 
+    // the token's logit, asked for ahead of the pass
+    const int tok = tid == 0 && part == 0 ? a.tokens[r] : -1;
+    const float x_tok = tok >= 0 && tok < a.V ? E::get(row[tok]) : 0.f;
     Sums su;
     float cm = -inf;  // this column's maximum, NaN if it holds one
     auto one = [&](int i) {
@@ -176,24 +184,41 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     };
     auto take = [&](uint4 v) {
         const float vm = X::max_of(v);
-        cm = max_nan(cm, vm);
         if (vm > su.limit) su.raise(vm);
         float x[VE];
         X::unpack(v, x);
 #pragma unroll
         for (int i = 0; i < VE; i += 2) su.add2(x[i], x[i + 1]);
+        return vm;
     };
     if (tid < n_head) one(tid);
     if (tid < n_tail) one(tail0 + tid);
-    int j = v0 + tid;
-    for (; j + 3 * kLpThreads < v1; j += 4 * kLpThreads) {
-        uint4 v[4];
+    float pm = cm;  // the piece's maximum; the head and tail elements belong to piece 0
+    cm = -inf;
+    const int batches = (v1 - v0 + kBatch * kLpThreads - 1) / (kBatch * kLpThreads);
+    for (int b = 0, in = 0, sg = 0; b < batches; ++b) {
+        const int j = v0 + b * (kBatch * kLpThreads) + tid;
+        float bm = -inf;
+        if (j + (kBatch - 1) * kLpThreads < v1) {
+            uint4 v[kBatch];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = __ldg(vec + j + u * kLpThreads);
+            for (int u = 0; u < kBatch; ++u) v[u] = __ldcs(vec + j + u * kLpThreads);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) take(v[u]);
+            for (int u = 0; u < kBatch; ++u) bm = max_nan(bm, take(v[u]));
+        } else {
+            for (int q = j; q < v1; q += kLpThreads) bm = max_nan(bm, take(__ldg(vec + q)));
+        }
+        pm = max_nan(pm, bm);
+        if (++in == per || b + 1 == batches) {
+            seg[sg * kLpThreads + tid] = pm;
+            cm = max_nan(cm, pm);
+            pm = -inf;
+            in = 0;
+            ++sg;
+        }
     }
-    for (; j < v1; j += kLpThreads) take(__ldg(vec + j));
+    cm = max_nan(cm, pm);  // a row without a whole vector
+    const int n_seg = (batches + per - 1) / per;
 
     // ---- the block's sums, relative to its maximum
     const uint32_t mine = order_of(cm);
@@ -205,8 +230,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         if (lane == 0) s.m[warp] = bmax;
         s.col[tid] = mine;
         if (tid == 0) {
-            s.tau = ~0u;
-            s.n_cols = s.n_cand = 0;
+            s.n_pieces = s.n_cand = 0;
         }
         __syncthreads();
         bmax = s.m[0];
@@ -245,34 +269,74 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         }
     };
     if (top > 0) {
-        int rank = 0;  // columns with a larger maximum
-#pragma unroll 8
-        for (int i = 0; i < kLpThreads; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(&s.col[i]);
-            rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        if (warp == 0) {
+            // a threshold that at least `top` column maxima reach and not many more: bit by bit from
+            // the highest in which they differ (the bits above are common to all)
+            uint32_t o[kLpThreads / 32], any = 0, all = ~0u;
+#pragma unroll
+            for (int i = 0; i < kLpThreads / 32; ++i) {
+                o[i] = s.col[i * 32 + lane];
+                any |= o[i];
+                all &= o[i];
+            }
+            any = __reduce_or_sync(~0u, any);
+            all = __reduce_and_sync(~0u, all);
+            const uint32_t differ = any ^ all;
+            uint32_t t = differ ? all & ~(0xffffffffu >> __clz(differ)) : all;
+            for (uint32_t bit = differ ? 0x80000000u >> __clz(differ) : 0; bit; bit >>= 1) {
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kLpThreads / 32; ++i) n += o[i] >= (t | bit);
+                n = __reduce_add_sync(~0u, n);
+                if (n >= top) {
+                    t |= bit;
+                    if (n <= top + top / 2) break;
+                }
+            }
+            if (lane == 0) s.tau = t;
         }
-        if (rank < top) {
-            atomicMin(&s.tau, mine);
-            const int at = atomicAdd(&s.n_cols, 1);
-            if (at < kColumns) s.cols[at] = tid;
+        __syncthreads();
+        const uint32_t tau = s.tau;
+        const float floor = value_of(tau);
+        if (mine >= tau) {
+            for (int g = 0; g < max(n_seg, 1); ++g) {
+                if (n_seg > 0 && !(seg[g * kLpThreads + tid] >= floor)) continue;
+                const int at = atomicAdd(&s.n_pieces, 1);
+                if (at < kPieces) s.pieces[at] = g * kLpThreads + tid;
+            }
         }
         if (tid < kMaxTop) s.list[tid] = 0;
         __syncthreads();
-        const uint32_t tau = s.tau;
-        const int n_cols = bmax != bmax ? kLpThreads : s.n_cols;  // a column with NaN has no rank
-        if (n_cols <= kColumns) {
-            for (int c = warp; c < n_cols; c += kLpWarps)
-                column(s.cols[c], [&](float x, int id) {
-                    const uint32_t o = order_of(x);
-                    if (o >= tau) {
-                        const int at = atomicAdd(&s.n_cand, 1);
-                        if (at < kCand) s.cand[at] = key_of(o, (uint32_t)id);
-                    }
-                });
+        const int n_pieces = bmax != bmax ? kPieces + 1 : s.n_pieces;  // a column with NaN has no rank
+        if (n_pieces <= kPieces) {
+            auto keep = [&](float x, int id) {
+                const uint32_t o = order_of(x);
+                if (o >= tau) {
+                    const int at = atomicAdd(&s.n_cand, 1);
+                    if (at < kCand) s.cand[at] = key_of(o, (uint32_t)id);
+                }
+            };
+            // eight lanes a piece
+            for (int i = tid >> 3; i < n_pieces; i += kLpThreads / 8) {
+                const int g = s.pieces[i] / kLpThreads, c = s.pieces[i] % kLpThreads;
+                if (g == 0 && (tid & 7) == 0) {
+                    if (c < n_head) keep(E::get(row[c]), c);
+                    if (c < n_tail) keep(E::get(row[tail0 + c]), tail0 + c);
+                }
+                const int end = min(v1, v0 + (g + 1) * per * kBatch * kLpThreads);
+                for (int q = v0 + (g * per * kBatch + (tid & 7)) * kLpThreads + c; q < end; q += 8 * kLpThreads) {
+                    const uint4 v = __ldg(vec + q);
+                    if (X::max_of(v) < floor) continue;
+                    float x[VE];
+                    X::unpack(v, x);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) keep(x[e], head + q * VE + e);
+                }
+            }
         }
         __syncthreads();
         const int n = s.n_cand;
-        if (n_cols <= kColumns && n <= kCand) {
+        if (n_pieces <= kPieces && n <= kCand) {
             // keys are distinct, so every rank is taken once
             if (tid < n) {
                 const uint64_t k = s.cand[tid];
@@ -368,17 +432,16 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     const bool none = !(z > 0.f) || !(m < inf);  // only -inf, or +inf or NaN in the row
     const float lz = none ? nan : log2f(z);
     if (tid == 0) {
-        const int tok = a.tokens[r];
         float lp = 0.f;
         if (tok >= a.V) report(a.dev_status, KDA_DEV_BAD_SLOT);
-        else if (tok >= 0) lp = (E::get(row[tok]) - m) - lz * kLn2;
+        else if (tok >= 0) lp = (x_tok - m) - lz * kLn2;
         a.logprob[r] = lp;
         if (a.entropy) a.entropy[r] = (lz - w / z) * kLn2;
     }
     if (rank < top && key != 0) {
         const int id = (int)~(uint32_t)key;
         a.top_ids[r * top + rank] = id;
-        a.top_logprobs[r * top + rank] = (E::get(row[id]) - m) - lz * kLn2;
+        a.top_logprobs[r * top + rank] = (value_of((uint32_t)(key >> 32)) - m) - lz * kLn2;
     }
 }
 
@@ -403,13 +466,19 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
     const void* ptrs[] = {tokens, logprob, entropy, top_ids, top_logprobs, dev_status};
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
     const LogprobArgs a{logits, row_stride, V, tokens, logprob, entropy, top, top_ids, top_logprobs, dev_status};
-    // blocks a row: enough rows fill the SMs by themselves; else split, down to a few vectors a thread
+    // blocks a row: enough rows fill the SMs by themselves (splitting 448 rows in two: 33 -> 45 us);
+    // else split, down to 8 vectors a thread (one row of 32768: 8.5 us in two blocks, 10.3 in eight)
     int C = 1;
-    while (C < 8 && (int64_t)R * C < 304 && (int64_t)V * dtype_bytes(dtype) >= 2ll * C * kLpThreads * 32) C *= 2;
+    while (C < 8 && (int64_t)R * C < 304 && (int64_t)V * dtype_bytes(dtype) >= 2ll * C * kLpThreads * 128) C *= 2;
+    // batches of a block's share, at most kMaxSeg pieces of them
+    const int64_t batches = ((int64_t)V * dtype_bytes(dtype) / 16 / C + 1 + kBatch * kLpThreads - 1) / (kBatch * kLpThreads);
+    const int per = (int)((batches + kMaxSeg - 1) / kMaxSeg);
+    const int pieces = (int)((batches + per - 1) / per);
     auto* f = dtype == KDA_BF16 ? logprob_kernel<KDA_BF16> : dtype == KDA_F16 ? logprob_kernel<KDA_F16> : logprob_kernel<KDA_F32>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(R * C));
     cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = (size_t)pieces * kLpThreads * sizeof(float);
     cfg.stream = as_stream(stream);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -417,7 +486,7 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = C > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, f, a, C) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, f, a, C, per) != cudaSuccess) {
         cudaGetLastError();
         return KDA_ERR_CUDA;
     }
