@@ -1,19 +1,25 @@
 // latent_prefill.cu -- kda_latent_prefill: expanded latent attention of packed sequences.
 //
-// A CTA takes 256 query rows of one (sequence, head) as two tiles of 128 and walks the keys 128 at a
-// time.  Per tile of keys and tile of queries
-//   S = Q K^T       M = 128, N = 128, K = 192 (128 nope, 64 rope: the rope key is loaded from its one
+// A pair of CTAs (a cluster of two SMs, one MMA over both) takes 512 query rows of one (sequence,
+// head) as two tiles of 256, 128 rows a CTA, and walks the keys 128 at a time.  Per tile of keys and
+// tile of queries
+//   S = Q K^T       M = 256, N = 128, K = 192 (128 nope, 64 rope: the rope key is loaded from its one
 //                   row a token, so it is not repeated per head anywhere)
 //   P = 2^(c S - m) c = scale log2 e, one thread a query row; P goes back to TMEM over S, rounded
 //                   to the input type, as the A operand of
-//   O += P V        M = 128, N = 128, K = 128; V as it lies in shared memory (MN-major)
+//   O += P V        M = 256, N = 128, K = 128; V as it lies in shared memory (MN-major)
+// Each CTA loads half of K's rows and half of V's channels.  That halves the shared memory a tile
+// takes (three tiles in flight beside the 96 KiB of queries; alone a CTA has room for one and a half,
+// and its products wait for their keys) and the operand bytes an MMA reads.
 // The two query tiles take turns: while the tensor cores work on one, the four warps of the other do
 // its exponentials.  m moves only when a row's maximum exceeds it by 8 (a factor of 256, far inside
 // fp32 and fp16), so that O is rarely rescaled.
 //
 // Roles: warps 0-3 and 4-7 softmax of query tile 0 and 1 (and its results), warp 8 loads by TMA (the
-// queries once, then a ring of 16 KiB parts: three of K, two of V a tile), warp 9 issues MMAs.
-// Long rows first: the CTAs of a sequence's last queries have the most keys.
+// queries once, then rings of K and V tiles), warp 9 of the first CTA issues the MMAs of both.
+// Barriers that the MMAs wait on lie in the first CTA and take both CTAs' arrivals; completed MMAs
+// arrive in both.
+// Long rows first: the pairs of a sequence's last queries have the most keys.
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "latent_host.h"
@@ -24,11 +30,14 @@ namespace {
 
 using namespace umma;
 
-constexpr int kQTile = 128, kQBlock = 2 * kQTile, kKTile = 128;
+constexpr int kQTile = 256, kQBlock = 2 * kQTile, kKTile = 128;
+constexpr int kRows = 128;               // query rows of a tile in one CTA
 constexpr int kPreThreads = 320;
 constexpr uint32_t kPreWait = 1u << 18;  // polls, about a second: loads and MMAs take microseconds
-constexpr uint32_t kPart = 128 * 128;    // 128 rows of 64 16-bit channels
-constexpr int kSlots = 8;
+constexpr uint32_t kQPart = 128 * 128;   // 128 rows of 64 16-bit channels
+constexpr uint32_t kKPart = 64 * 128;    // 64 rows
+constexpr int kStages = 3;
+constexpr uint32_t kKBytes = 3 * kKPart, kVBytes = 128 * 128;  // a CTA's half of a tile
 
 struct PrefillArgs {
     const int32_t* cu_q;
@@ -49,10 +58,11 @@ struct PreMaps {
     CUtensorMap q, k, kr, v;
 };
 
-// shared memory: Q (2 x 3 parts), the ring, barriers
-constexpr uint32_t PS_RING = 6 * kPart, PS_BAR = PS_RING + kSlots * kPart;
-constexpr int PB_Q = 0, PB_FULL = 2, PB_EMPTY = PB_FULL + kSlots, PB_S = PB_EMPTY + kSlots, PB_P = PB_S + 2,
-              PB_O = PB_P + 2, PB_DRAIN = PB_O + 2, PB_BARS = PB_DRAIN + 1;
+// shared memory: Q (2 x 3 parts), the rings, barriers
+constexpr uint32_t PS_K = 6 * kQPart, PS_V = PS_K + kStages * kKBytes, PS_BAR = PS_V + kStages * kVBytes;
+constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_KFREE = PB_V + kStages, PB_VFREE = PB_KFREE + kStages,
+              PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_O = PB_P + 2, PB_EDGE = PB_O + 2, PB_DRAIN = PB_EDGE + 1,
+              PB_BARS = PB_DRAIN + 1;
 constexpr uint32_t PS_CTRL = PS_BAR + 8 * 32, PS_SCAN = PS_CTRL + 32, PS_SMEM = PS_SCAN + 4 * 16;
 static_assert(PB_BARS <= 32 && PS_SMEM <= 232448, "shared memory plan");
 // TMEM: S of the two query tiles, then O
@@ -82,8 +92,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     auto bar = [&](int i) { return sb + PS_BAR + 8 * i; };
     const float inf = __int_as_float(0x7f800000);
 
-    // ---- which block of 256 rows: the last first, over all sequences
-    const int h = blockIdx.x % a.H, y = blockIdx.x / a.H;
+    // ---- which block of 512 rows: the last first, over all sequences
+    const uint32_t rank = blockIdx.x & 1;  // in the cluster
+    const int h = (blockIdx.x >> 1) % a.H, y = (blockIdx.x >> 1) / a.H;
     auto blocks_of = [&](int n, bool& bad) {
         const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
         bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
@@ -123,12 +134,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int n = ctrl[1];
     if (n < 0) return;
     if (tid == 0) {
-        for (int i = 0; i < PB_BARS; ++i) mbar_init(bar(i), i == PB_P || i == PB_P + 1 ? 4 : 1);
+        for (int i = 0; i < PB_BARS; ++i) {
+            const bool both = i < PB_KFREE;  // an arrival of each CTA
+            mbar_init(bar(i), both ? 2 : i == PB_P || i == PB_P + 1 ? 8 : 1);
+        }
     }
-    if (warp == 9) tmem_alloc(sb + PS_CTRL, 512);
+    if (warp == 9) tmem2_alloc(sb + PS_CTRL, 512);
     const int q0 = a.cu_q[n], Lq = a.cu_q[n + 1] - q0, k0 = a.cu_k[n], Lk = a.cu_k[n + 1] - k0;
     const int row0 = ctrl[2] * kQBlock;
-    // key tiles of query tile q: up to the last key its last row sees
+    // key tiles of query tile q (of both CTAs): up to the last key its last row sees
     auto tiles_of = [&](int q) {
         const int rows = min(kQTile, Lq - row0 - q * kQTile);
         if (rows <= 0) return 0;
@@ -138,6 +152,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
     fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers are there
     fence_after();
     const uint32_t tmem = ctrl[0];
     bool dead = false;
@@ -151,87 +166,108 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
     if (warp == 8) {
         // ================================================================ loads
-        if (lane == 0) {
-            uint32_t issued = 0;
-            auto load_queries = [&](int q) {
-                mbar_expect_tx(bar(PB_Q + q), 3 * kPart);
-                for (int c = 0; c < 3; ++c)
-                    tma_load_3d(sb + (q * 3 + c) * kPart, &maps.q, 64 * c, h * a.hq, q0 + row0 + q * kQTile, bar(PB_Q + q));
-            };
-            if (n0 > 0) load_queries(0);
-            for (int i = 0; i < nt && !dead; ++i) {
-                const int t = k0 + i * kKTile;
-                for (int c = 0; c < 5; ++c, ++issued) {
-                    const uint32_t slot = issued % kSlots;
-                    wait(PB_EMPTY + slot, (issued / kSlots & 1) ^ 1);
-                    if (dead) break;
-                    const uint32_t dst = sb + PS_RING + slot * kPart;
-                    mbar_expect_tx(bar(PB_FULL + slot), kPart);
-                    if (c < 2) tma_load_3d(dst, &maps.k, 64 * c, h * a.hk, t, bar(PB_FULL + slot));
-                    else if (c == 2) tma_load_2d(dst, &maps.kr, 0, t, bar(PB_FULL + slot));
-                    else tma_load_3d(dst, &maps.v, 64 * (c - 3), h * a.hv, t, bar(PB_FULL + slot));
-                    if (issued == 2 && n1 > 0) load_queries(1);
+        // into this CTA, counted on the barriers of the first
+        auto first = [&](int b) { return map_rank(bar(b), 0); };
+        bool edge = false;
+        auto load_queries = [&](int q) {
+            mbar_expect_tx_cluster(first(PB_Q + q), 3 * kQPart);
+            for (int c = 0; c < 3; ++c)
+                tma2_load_3d(sb + (q * 3 + c) * kQPart, &maps.q, 64 * c, h * a.hq,
+                             q0 + row0 + q * kQTile + (int)rank * kRows, first(PB_Q + q));
+        };
+        auto load_k = [&](int i) {
+            const uint32_t st = i % kStages;
+            wait(PB_KFREE + st, (i / kStages & 1) ^ 1);
+            if (dead || lane != 0) return;
+            const int t = k0 + i * kKTile + (int)rank * 64;
+            const uint32_t dst = sb + PS_K + st * kKBytes, b = first(PB_K + st);
+            mbar_expect_tx_cluster(b, kKBytes);
+            tma2_load_3d(dst, &maps.k, 0, h * a.hk, t, b);
+            tma2_load_3d(dst + kKPart, &maps.k, 64, h * a.hk, t, b);
+            tma2_load_2d(dst + 2 * kKPart, &maps.kr, 0, t, b);
+        };
+        auto load_v = [&](int i) {
+            const uint32_t st = i % kStages;
+            wait(PB_VFREE + st, (i / kStages & 1) ^ 1);
+            if (dead) return;
+            const uint32_t dst = sb + PS_V + st * kVBytes, b = first(PB_V + st);
+            const int valid = Lk - i * kKTile;
+            if (valid >= kKTile) {
+                if (lane == 0) {
+                    mbar_expect_tx_cluster(b, kVBytes);
+                    tma2_load_3d(dst, &maps.v, 64 * (int)rank, h * a.hv, k0 + i * kKTile, b);
                 }
+            } else {
+                // keys past the sequence (its last tile): their weight is zero, and so has to be the
+                // value (what lies there belongs to another sequence).  This warp waits for the tile,
+                // clears them and only then lets it be used.
+                if (lane == 0) {
+                    mbar_expect_tx(bar(PB_EDGE), kVBytes);
+                    tma_load_3d(dst, &maps.v, 64 * (int)rank, h * a.hv, k0 + i * kKTile, bar(PB_EDGE));
+                }
+                wait(PB_EDGE, 0);
+                edge = true;
+                for (uint32_t e = valid * 128 + lane * 16; e < kVBytes; e += 512)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + e), "r"(0u) : "memory");
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(b);
             }
-            // nothing may be in flight when the CTA ends
-            dead = false;
-            if (n0 > 0) wait(PB_Q, 0);
-            if (n1 > 0 && issued > 2) wait(PB_Q + 1, 0);
-            for (uint32_t k = issued > kSlots ? issued - kSlots : 0; k < issued; ++k) wait(PB_FULL + k % kSlots, k / kSlots & 1);
+        };
+        if (lane == 0 && n0 > 0) load_queries(0);
+        if (nt > 0) load_k(0);
+        if (lane == 0 && n1 > 0) load_queries(1);
+        for (int i = 0; i < nt; ++i) {
+            load_v(i);
+            if (i + 1 < nt) load_k(i + 1);
+            if (__any_sync(~0u, dead)) break;
         }
-        __syncwarp();
-    } else if (warp == 9) {
+        // Every load was waited for by an MMA that is done when the CTAs leave.  After a wait that gave
+        // up that does not hold: one more (bounded) wait on a phase that does not end lets them land.
+        if (__any_sync(~0u, dead)) mbar_wait(bar(PB_EDGE), edge ? 1 : 0, kPreWait);
+    } else if (warp == 9 && rank == 0) {
         // ================================================================ MMAs
         // the whole warp runs this, one lane issues (umma.cuh, mma_by)
         const uint32_t lead = elect_lane();
-        const uint32_t sb4 = sb >> 4;
+        const uint32_t sb4 = (sb & 0x3ffffu) >> 4;
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
         const int m0 = __shfl_sync(~0u, n0, 0), m1 = __shfl_sync(~0u, n1, 0), mt = max(m0, m1);
-        const uint32_t ids = idesc_16(DT == KDA_F16, 128, kKTile, false, false, a.negate);
-        const uint32_t idv = idesc_16(DT == KDA_F16, 128, 64, false, true, false);
-        auto release = [&](uint32_t k) { commit_by(lead, bar(PB_EMPTY + k % kSlots)); };
-        // Part k of the ring has landed.  A wait queues behind the MMAs issued before it, so V is waited
-        // for ahead of the weights; K has only just been requested and is taken part by part.
-        auto landed = [&](uint32_t k) { wait(PB_FULL + k % kSlots, k / kSlots & 1); };
-        auto do_s = [&](int q, int i, bool first) {
+        const uint32_t ids = idesc_16(DT == KDA_F16, 256, kKTile, false, false, a.negate);
+        const uint32_t idv = idesc_16(DT == KDA_F16, 256, 128, false, true, false);
+        auto do_s = [&](int q, int i) {
+            const uint32_t b4 = sb4 + PS_K / 16 + i % kStages * (kKBytes / 16);
 #pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                if (first) {
-                    landed(5 * i + c);
-                    fence_after();
-                }
-                const uint32_t slot = (5 * i + c) % kSlots;
+            for (int c = 0; c < 3; ++c)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    mma_by(lead, tm + PT_S + q * 128, desc_k4(sb4 + (q * 3 + c) * (kPart / 16), 128, s),
-                           desc_k4(sb4 + PS_RING / 16 + slot * (kPart / 16), 128, s), ids, c + s != 0);
-            }
-            commit_by(lead, bar(PB_S + q));
+                    mma2_by(lead, tm + PT_S + q * 128, desc_k4(sb4 + (q * 3 + c) * (kQPart / 16), 128, s),
+                            desc_k4(b4 + c * (kKPart / 16), 64, s), ids, c + s != 0);
+            commit2_by(lead, bar(PB_S + q));
         };
         auto do_pv = [&](int q, int i) {
+            const uint32_t b4 = sb4 + PS_V / 16 + i % kStages * (kVBytes / 16);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint32_t slot = (5 * i + 3 + c) % kSlots;
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ta_by(lead, tm + PT_O + q * 128 + c * 64, tm + PT_S + q * 128 + 8 * s,
-                              desc_mn4(sb4 + PS_RING / 16 + slot * (kPart / 16), 16, 1024, s), idv, i + s != 0);
-            }
-            commit_by(lead, bar(PB_O + q));
+            for (int s = 0; s < 8; ++s)
+                mma2_ta_by(lead, tm + PT_O + q * 128, tm + PT_S + q * 128 + 8 * s, desc_mn4(b4, 16, 1024, s), idv, i + s != 0);
+            commit2_by(lead, bar(PB_O + q));
         };
+        if (mt > 0) wait(PB_K, 0);
         if (m0 > 0) {
             wait(PB_Q, 0);
-            do_s(0, 0, true);
+            fence_after();
+            do_s(0, 0);
         }
         if (m1 > 0) {
             wait(PB_Q + 1, 0);
-            do_s(1, 0, m0 == 0);
+            fence_after();
+            do_s(1, 0);
         }
-        if (mt > 0)
-            for (int c = 0; c < 3; ++c) release(c);
+        if (mt > 0) commit2_by(lead, bar(PB_KFREE));
         bool stop = false;
         for (int i = 0; i < mt && !stop; ++i) {
-            for (int c = 3; c < 5; ++c) landed(5 * i + c);
+            // loads ahead of the weights: a wait queues behind the MMAs issued before it
+            if (!mbar_wait_cluster(bar(PB_V + i % kStages), i / kStages & 1, kPreWait)) dead = true;  // cleared edges
+            if (i + 1 < mt) wait(PB_K + (i + 1) % kStages, (i + 1) / kStages & 1);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int mq = q ? m1 : m0, mo = q ? m0 : m1;
@@ -239,25 +275,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     wait(PB_P + q, i & 1);
                     fence_after();
                     do_pv(q, i);
-                    if (q == 1 || i >= mo)
-                        for (int c = 3; c < 5; ++c) release(5 * i + c);
-                    if (i + 1 < mq) do_s(q, i + 1, q == 0 || i + 1 >= mo);
-                    if (i + 1 < mq && (q == 1 || i + 1 >= mo))
-                        for (int c = 5; c < 8; ++c) release(5 * i + c);
+                    if (q == 1 || i >= mo) commit2_by(lead, bar(PB_VFREE + i % kStages));
+                    if (i + 1 < mq) {
+                        do_s(q, i + 1);
+                        if (q == 1 || i + 1 >= mo) commit2_by(lead, bar(PB_KFREE + (i + 1) % kStages));
+                    }
                 }
             }
             stop = __any_sync(~0u, dead);
         }
-        commit_by(lead, bar(PB_DRAIN));
+        commit2_by(lead, bar(PB_DRAIN));
         dead = false;
         wait(PB_DRAIN, 0);
-    } else {
+    } else if (warp < 8) {
         // ================================================================ softmax and results
         const int q = warp >> 2, t = tid & 127;
         const int my_tiles = q ? n1 : n0;
         const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = tq + PT_S + q * 128, to = tq + PT_O + q * 128;
-        const int row = row0 + q * kQTile + t;  // of the sequence
+        const int row = row0 + q * kQTile + (int)rank * kRows + t;  // of the sequence
+        const uint32_t p_full = map_rank(bar(PB_P + q), 0);
         const int last = row >= Lq ? -1 : a.full ? Lk - 1 : Lk - Lq + row;
         float m = -inf, l = 0.f;
         for (int i = 0; i < my_tiles && !__any_sync(~0u, dead); ++i) {
@@ -311,19 +348,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const float mc = m == -inf ? 0.f : m * a.c;
             const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            if ((i + 1) * kKTile > Lk) {
-                // keys past the sequence: their weight is zero, and so has to be the value (what lies
-                // there belongs to another sequence)
-                const uint32_t k = 5 * i + 3;
-                wait(PB_FULL + k % kSlots, k / kSlots & 1);
-                wait(PB_FULL + (k + 1) % kSlots, (k + 1) / kSlots & 1);
-                const int valid = Lk - i * kKTile;
-                for (int e = t; e < (kKTile - valid) * 16; e += 128) {
-                    const uint32_t at = sb + PS_RING + ((k + (e >> 3 & 1)) % kSlots) * kPart + (valid + (e >> 4)) * 128 + (e & 7) * 16;
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
-                }
-                fence_async_smem();
-            }
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t p[16];
@@ -340,7 +364,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(PB_P + q));
+            if (lane == 0) mbar_arrive_remote(p_full);
             l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         }
         if (my_tiles > 0) {
@@ -371,17 +395,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         fence_before();
     }
     __syncthreads();
+    cluster_sync();  // no CTA leaves while the other's MMAs, loads or arrivals may still reach it
     fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 9) tmem2_dealloc(tmem, 512);
 }
 
-// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head, 128 rows.
-bool rows_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int channels, int H, int T) {
+// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head.
+bool rows_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int channels, int H, int T, int rows) {
     // a dimension that is not stepped along (one head or row, or heads that share a row) has size 1
     // and any legal stride
     const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)(r.hs ? H : 1), (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)(r.hs ? r.hs : channels) * 2, (cuuint64_t)(r.rs ? r.rs : channels) * 2};
-    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     return encode_16bit(map, dt, 3, r.base, dims, strides, box);
 }
 
@@ -403,7 +428,7 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((flags & ~KDA_LATENT_FULL) == 0, KDA_ERR_UNSUPPORTED);
     const int64_t blocks = ((int64_t)Tq / kQBlock + N) * H;
-    KDA_REQUIRE(blocks < (1ll << 31) && Tk < (1 << 30) && Tq < (1 << 30), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(blocks < (1ll << 30) && Tk < (1 << 30) && Tq < (1 << 30), KDA_ERR_UNSUPPORTED);
     if (N == 0 || Tq == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(q) && rows_ok(out), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(k_nope != nullptr && v != nullptr, KDA_ERR_INVALID_ARG);
@@ -421,13 +446,13 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     KDA_REQUIRE(aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
     PreMaps maps;
     const LatentRows rq = as_rows(q), rk = Tk > 0 ? as_rows(k_nope) : rq, rv = Tk > 0 ? as_rows(v) : rq;
-    KDA_REQUIRE(rows_map(&maps.q, in_dtype, rq, kHeadK, H, Tq), KDA_ERR_CUDA);
+    KDA_REQUIRE(rows_map(&maps.q, in_dtype, rq, kHeadK, H, Tq, 128), KDA_ERR_CUDA);
     if (Tk > 0) {
-        KDA_REQUIRE(rows_map(&maps.k, in_dtype, rk, kNope, H, Tk), KDA_ERR_CUDA);
-        KDA_REQUIRE(rows_map(&maps.v, in_dtype, rv, kHeadV, H, Tk), KDA_ERR_CUDA);
+        KDA_REQUIRE(rows_map(&maps.k, in_dtype, rk, kNope, H, Tk, 64), KDA_ERR_CUDA);
+        KDA_REQUIRE(rows_map(&maps.v, in_dtype, rv, kHeadV, H, Tk, 128), KDA_ERR_CUDA);
         const cuuint64_t dims[2] = {kRope, (cuuint64_t)Tk};
         const cuuint64_t strides[1] = {(cuuint64_t)k_rope_stride * 2};
-        const cuuint32_t box[2] = {64, 128};
+        const cuuint32_t box[2] = {64, 64};
         KDA_REQUIRE(encode_16bit(&maps.kr, in_dtype, 2, k_rope, dims, strides, box), KDA_ERR_CUDA);
     } else {
         maps.k = maps.kr = maps.v = maps.q;  // no key, no load
@@ -438,6 +463,20 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     auto* f = in_dtype == KDA_BF16 ? prefill_kernel<KDA_BF16> : prefill_kernel<KDA_F16>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PS_SMEM) != cudaSuccess)
         return KDA_ERR_CUDA;
-    f<<<(unsigned)blocks, kPreThreads, PS_SMEM, as_stream(stream)>>>(maps, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks * 2);
+    cfg.blockDim = dim3(kPreThreads);
+    cfg.dynamicSmemBytes = PS_SMEM;
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, f, maps, a) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
     return launch_status();
 }
