@@ -61,7 +61,7 @@ struct PreMaps {
 // shared memory: Q (2 x 3 parts), the rings, barriers
 constexpr uint32_t PS_K = 6 * kQPart, PS_V = PS_K + kStages * kKBytes, PS_BAR = PS_V + kStages * kVBytes;
 constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_KFREE = PB_V + kStages, PB_VFREE = PB_KFREE + kStages,
-              PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_O = PB_P + 2, PB_EDGE = PB_O + 2, PB_DRAIN = PB_EDGE + 1,
+              PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_P2 = PB_P + 2, PB_O = PB_P2 + 2, PB_EDGE = PB_O + 2, PB_DRAIN = PB_EDGE + 1,
               PB_BARS = PB_DRAIN + 1;
 constexpr uint32_t PS_CTRL = PS_BAR + 8 * 32, PS_SCAN = PS_CTRL + 32, PS_SMEM = PS_SCAN + 4 * 16;
 static_assert(PB_BARS <= 32 && PS_SMEM <= 232448, "shared memory plan");
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < PB_BARS; ++i) {
             const bool both = i < PB_KFREE;  // an arrival of each CTA
-            mbar_init(bar(i), both ? 2 : i == PB_P || i == PB_P + 1 ? 8 : 1);
+            mbar_init(bar(i), both ? 2 : i >= PB_P && i < PB_P + 4 ? 8 : 1);
         }
     }
     if (warp == 9) tmem2_alloc(sb + PS_CTRL, 512);
@@ -244,12 +244,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                             desc_k4(b4 + c * (kKPart / 16), 64, s), ids, c + s != 0);
             commit2_by(lead, bar(PB_S + q));
         };
-        auto do_pv = [&](int q, int i) {
+        auto do_pv = [&](int q, int i, int s0, int s1) {
             const uint32_t b4 = sb4 + PS_V / 16 + i % kStages * (kVBytes / 16);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
+            for (int s = s0; s < s1; ++s)
                 mma2_ta_by(lead, tm + PT_O + q * 128, tm + PT_S + q * 128 + 8 * s, desc_mn4(b4, 16, 1024, s), idv, i + s != 0);
-            commit2_by(lead, bar(PB_O + q));
+            if (s1 == 8) commit2_by(lead, bar(PB_O + q));
         };
         if (mt > 0) wait(PB_K, 0);
         if (m0 > 0) {
@@ -274,7 +274,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (i < mq) {
                     wait(PB_P + q, i & 1);
                     fence_after();
-                    do_pv(q, i);
+                    do_pv(q, i, 0, 6);
+                    wait(PB_P2 + q, i & 1);
+                    fence_after();
+                    do_pv(q, i, 6, 8);
                     if (q == 1 || i >= mo) commit2_by(lead, bar(PB_VFREE + i % kStages));
                     if (i + 1 < mq) {
                         do_s(q, i + 1);
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = tq + PT_S + q * 128, to = tq + PT_O + q * 128;
         const int row = row0 + q * kQTile + (int)rank * kRows + t;  // of the sequence
-        const uint32_t p_full = map_rank(bar(PB_P + q), 0);
+        const uint32_t p_full = map_rank(bar(PB_P + q), 0), p_full2 = map_rank(bar(PB_P2 + q), 0);
         const int last = row >= Lq ? -1 : a.full ? Lk - 1 : Lk - Lq + row;
         float m = -inf, l = 0.f;
         for (int i = 0; i < my_tiles && !__any_sync(~0u, dead); ++i) {
@@ -360,11 +363,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     p[e] = E::put2(x.x, x.y);
                 }
                 st16u(ts + 16 * b, p);
+                // the first 96 keys go ahead: their product runs under the last exponentials
+                if (b >= 2) {
+                    wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(b == 2 ? p_full : p_full2);
+                }
             }
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(p_full);
             l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         }
         if (my_tiles > 0) {
@@ -375,22 +381,67 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int64_t orow = (int64_t)q0 + row;
         if (row < Lq && a.lse != nullptr)
             a.lse[orow * a.H + h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
-        const int64_t at = orow * a.out_rs + (int64_t)h * a.out_hs;
+        // Rows leave through the query tile's shared memory (every S has read it), 64 channels at a
+        // time, so that a warp writes whole 128-byte lines: thread t puts its row there, and the warp
+        // takes its 32 rows out along the channels.
+        const uint32_t stage = sb + q * 3 * kQPart;
+        const int wrow = t & ~31;  // the warp's first row
+        auto emit = [&](auto pack, int words, int bytes) {  // 16-byte words of 64 channels; bytes of an element
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            float o[32];
-            if (my_tiles > 0) {
-                ld32(to + 32 * b, o);
-            } else {
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                for (int b = 0; b < 2; ++b) {
+                    float o[32];
+                    if (my_tiles > 0) {
+                        ld32(to + 64 * half + 32 * b, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= il;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    pack(o, b);
+                }
+                __syncwarp();
+                const int per = 32 / words, x = lane % words;  // rows a step
+                for (int r = lane / words; r < 32; r += per) {
+                    const int rr = wrow + r, grow = row - t + rr;
+                    if (grow < Lq) {
+                        const uint32_t at = stage + (x >> 3) * kQPart + rr * 128 + (((x ^ rr) & 7) << 4);
+                        uint4 v;
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+                        const int64_t off = ((int64_t)q0 + grow) * a.out_rs + (int64_t)h * a.out_hs + half * 64;
+                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + off * bytes + x * 16) = v;
+                    }
+                }
+                __syncwarp();
             }
-            if (row < Lq) {
+        };
+        auto put = [&](int x, uint4 v) {  // word x of this thread's row
+            const uint32_t at = stage + (x >> 3) * kQPart + t * 128 + (((x ^ t) & 7) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        };
+        if (a.out_dt == KDA_F32) {
+            emit([&](const float (&o)[32], int b) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                    store4_as(a.out, at + 32 * b + e, make_float4(o[e] * il, o[e + 1] * il, o[e + 2] * il, o[e + 3] * il),
-                              a.out_dt);
-            }
+                    put(8 * b + e / 4, make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                                                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3])));
+            }, 16, 4);
+        } else if (a.out_dt == KDA_BF16) {
+            emit([&](const float (&o)[32], int b) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    put(4 * b + e / 8, make_uint4(Elem<KDA_BF16>::put2(o[e], o[e + 1]), Elem<KDA_BF16>::put2(o[e + 2], o[e + 3]),
+                                                  Elem<KDA_BF16>::put2(o[e + 4], o[e + 5]), Elem<KDA_BF16>::put2(o[e + 6], o[e + 7])));
+            }, 8, 2);
+        } else {
+            emit([&](const float (&o)[32], int b) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    put(4 * b + e / 8, make_uint4(Elem<KDA_F16>::put2(o[e], o[e + 1]), Elem<KDA_F16>::put2(o[e + 2], o[e + 3]),
+                                                  Elem<KDA_F16>::put2(o[e + 4], o[e + 5]), Elem<KDA_F16>::put2(o[e + 6], o[e + 7])));
+            }, 8, 2);
         }
         fence_before();
     }
