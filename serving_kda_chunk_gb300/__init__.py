@@ -413,55 +413,84 @@ def _slot_sets(pools, clear_slots, src_slots, dst_offsets, dst_slots):
 
 # --------------------------------------------------------------------------
 # latent attention and token log probabilities
+#
+# These marshal with one pass over each tensor's properties: a torch attribute costs about 0.1 us,
+# and at the smallest sizes the marshalling is most of a call.
+
+_ANY_DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16}
 
 
 def _dt3(t) -> int:
     """Element type of the latent attention and log-probability calls (bf16, fp16 or fp32)."""
-    return KDA_F16 if t.dtype == torch.float16 else _dt(t)
+    dt = _ANY_DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return dt
+
+
+def _arr(t, dtype, name, shape=None):
+    """Device pointer of a contiguous CUDA tensor of the given dtype and shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be a tensor of {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("libkda takes contiguous CUDA tensors")
+    return t.data_ptr()
 
 
 def _rows(t, name):
-    """Descriptor of a CUDA tensor [rows, heads, channels] whose channels are contiguous; rows
-    and heads may be strided (a view of a wider tensor)."""
-    if t.dim() != 3 or (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [rows, heads, channels] with contiguous channels")
+    """Descriptor of a CUDA tensor [rows, heads, channels] whose channels are contiguous; rows and
+    heads may be strided (a view of a wider tensor)."""
+    (n, h, _), (rs, hs, cs) = t.shape, t.stride()
+    if cs != 1 and n and h:
+        raise ValueError(f"{name} needs contiguous channels")
+    if not t.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
     # a dimension of one element is never stepped along: torch may give it any stride
-    rs = t.stride(0) if t.shape[0] > 1 else 0
-    hs = t.stride(1) if t.shape[1] > 1 else 0
-    return ctypes.byref(RowsDesc(_p_any(t), rs, hs))
+    return RowsDesc(t.data_ptr(), rs if n > 1 else 0, hs if h > 1 else 0)
 
 
-def _same(name, t, *shape):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _one_dtype(what, *ts):
+    """The element type that all of the given tensors have."""
+    dt = ts[0].dtype
+    for t in ts:
+        if t.dtype is not dt:
+            raise ValueError(f"{what} must share one dtype, got {sorted({str(x.dtype) for x in ts})}")
+    return _dt3(ts[0])
 
 
-def _cache_pages(cache):
-    """(pages, page size, page stride) of a paged cache [P, page_size, width]."""
-    if cache.dim() != 3 or cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
+def _pages(cache, width):
+    """(pointer, pages, page size, page stride) of a paged cache [P, page_size, width]."""
+    P, page, w = cache.shape
+    ps, rs, cs = cache.stride()
+    if cs != 1 or rs != w:
         raise ValueError("cache must be [pages, page_size, width] with contiguous pages")
-    P, page, width = cache.shape
-    return P, page, cache.stride(0) if P > 1 else page * width
+    if w != width:
+        raise ValueError(f"cache must have rows of {width} channels, got {w}")
+    if not cache.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
+    return cache.data_ptr(), P, page, ps if P > 1 else page * w
 
 
 def kda_latent_append(kv, cache, slot, *, weight=None, eps=1e-6, dev_status=None, stream=None):
     """Latent vectors (normalised when weight is given) and rope keys of new tokens into the
     paged cache (see include/kda.h).  kv: [T, 576], rows may be strided."""
     T, width = kv.shape
-    P, page, stride = _cache_pages(cache)
-    _same("cache", cache, P, page, width)
-    _same("slot", slot, T)
-    if T and kv.stride(1) != 1:
+    ks, cs = kv.stride()
+    if T and cs != 1:
         raise ValueError("kv needs contiguous rows")
-    if weight is not None:
-        _same("weight", weight, width - 64)
-    dt = {t.dtype for t in (kv, cache, weight) if t is not None}
-    if len(dt) != 1:
-        raise ValueError(f"kv, cache and weight must share one dtype, got {sorted(map(str, dt))}")
+    dt = _one_dtype("kv, cache and weight", kv, cache, cache if weight is None else weight)
+    slot_p = _arr(slot, torch.int32, "slot", (T,))
+    base, P, page, stride = _pages(cache, width)
+    if not kv.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
     st = lib().kda_latent_append(
-        _p_any(kv), kv.stride(0) if T > 1 else width, _p(weight), float(eps), _dt3(kv), T,
-        width - 64, 64, _idx(slot, "slot"), _p_any(cache), P, page, stride,
-        _idx(dev_status, "dev_status"), _stream(stream))
+        kv.data_ptr(), ks if T > 1 else width, _arr(weight, kv.dtype, "weight", (width - 64,)),
+        eps, dt, T, width - 64, 64, slot_p, base, P, page, stride,
+        _arr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "kda_latent_append")
 
 
@@ -474,31 +503,26 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_len, out, worksp
     """Absorbed latent attention of K query positions a request over a paged cache (see
     include/kda.h).  q_latent [R*K, H, 512], q_rope [R*K, H, 64] and out [R*K, H, 512] may be
     strided over rows and heads."""
-    RK, H, dl = q_latent.shape
+    shape = q_latent.shape
+    RK, H, dl = shape
     dr = q_rope.shape[2]
-    R = int(block_table.shape[0])
-    K = int(K)
+    R, max_pages = block_table.shape
     if K < 0 or RK != R * K:
         raise ValueError(f"q_latent has {RK} rows, not {R} requests x K = {K}")
-    _same("q_rope", q_rope, RK, H, dr)
-    _same("out", out, RK, H, dl)
-    _same("seq_len", seq_len, R)
-    if q_len is not None:
-        _same("q_len", q_len, R)
-    if lse is not None:
-        _same("lse", lse, RK, H)
-    P, page, stride = _cache_pages(cache)
-    _same("cache", cache, P, page, dl + dr)
-    dt = {t.dtype for t in (q_latent, q_rope, cache)}
-    if len(dt) != 1:
-        raise ValueError(f"queries and cache must share one dtype, got {sorted(map(str, dt))}")
+    dt = _one_dtype("queries and cache", q_latent, q_rope, cache)
+    i32 = torch.int32
+    if q_rope.shape != (RK, H, dr):
+        raise ValueError(f"q_rope must have shape {(RK, H, dr)}, got {tuple(q_rope.shape)}")
+    if out.shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    base, P, page, stride = _pages(cache, dl + dr)
+    ql, qr, o = _rows(q_latent, "q_latent"), _rows(q_rope, "q_rope"), _rows(out, "out")
     st = lib().kda_latent_decode(
-        _rows(q_latent, "q_latent"), _rows(q_rope, "q_rope"), _dt3(q_latent), R, K,
-        _idx(q_len, "q_len"), H, dl, dr, float(scale), _p_any(cache), P, page, stride,
-        _idx(block_table, "block_table"), int(block_table.shape[1]), _idx(seq_len, "seq_len"),
-        _rows(out, "out"), _dt3(out), None if lse is None else _f32(lse, "lse"), _p(workspace),
-        workspace.numel() * workspace.element_size(), _idx(dev_status, "dev_status"),
-        _stream(stream))
+        ql, qr, dt, R, K, _arr(q_len, i32, "q_len", (R,)), H, dl, dr, scale, base, P, page,
+        stride, _arr(block_table, i32, "block_table"), max_pages,
+        _arr(seq_len, i32, "seq_len", (R,)), o, _dt3(out),
+        _arr(lse, torch.float32, "lse", (RK, H)), _p(workspace), workspace.nbytes,
+        _arr(dev_status, i32, "dev_status"), _stream(stream))
     _check(st, "kda_latent_decode")
 
 
@@ -507,28 +531,29 @@ def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, *, scale=1.0, flag
     """Expanded latent attention of packed sequences (see include/kda.h).  q [Tq, H, 192],
     k_nope and v [Tk, H, 128] and out [Tq, H, 128] may be strided over rows and heads;
     k_rope [Tk, 64] over rows."""
-    Tq, H, dq = q.shape
+    Tq, H, _ = q.shape
     Tk, _, dn = k_nope.shape
     dr, dv = k_rope.shape[1], v.shape[2]
-    _same("q", q, Tq, H, dn + dr)
-    _same("k_nope", k_nope, Tk, H, dn)
-    _same("k_rope", k_rope, Tk, dr)
-    _same("v", v, Tk, H, dv)
-    _same("out", out, Tq, H, dv)
-    _same("cu_k", cu_k, *cu_q.shape)
-    if lse is not None:
-        _same("lse", lse, Tq, H)
-    if Tk and k_rope.stride(1) != 1:
+    if k_rope.shape[0] != Tk:
+        raise ValueError(f"k_rope must have {Tk} rows, got {k_rope.shape[0]}")
+    krs, cs = k_rope.stride()
+    if Tk and cs != 1:
         raise ValueError("k_rope needs contiguous rows")
-    dt = {t.dtype for t in (q, k_nope, k_rope, v)}
-    if len(dt) != 1:
-        raise ValueError(f"queries, keys and values must share one dtype, got {sorted(map(str, dt))}")
+    dt = _one_dtype("queries, keys and values", q, k_nope, k_rope, v)
+    for name, t, shape in (("q", q, (Tq, H, dn + dr)), ("k_nope", k_nope, (Tk, H, dn)),
+                           ("v", v, (Tk, H, dv)), ("out", out, (Tq, H, dv))):
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    qd, kd, vd, od = _rows(q, "q"), _rows(k_nope, "k_nope"), _rows(v, "v"), _rows(out, "out")
+    if not k_rope.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
+    N = cu_q.shape[0] - 1
+    i32 = torch.int32
     st = lib().kda_latent_prefill(
-        _rows(q, "q"), _rows(k_nope, "k_nope"), _p_any(k_rope),
-        k_rope.stride(0) if Tk > 1 else dr, _rows(v, "v"), _dt3(q), _idx(cu_q, "cu_q"),
-        _idx(cu_k, "cu_k"), int(cu_q.shape[0]) - 1, Tq, Tk, H, dn, dr, dv, float(scale),
-        int(flags), _rows(out, "out"), _dt3(out), None if lse is None else _f32(lse, "lse"),
-        _idx(dev_status, "dev_status"), _stream(stream))
+        qd, kd, k_rope.data_ptr(), krs if Tk > 1 else dr, vd, dt, _arr(cu_q, i32, "cu_q"),
+        _arr(cu_k, i32, "cu_k", (N + 1,)), N, Tq, Tk, H, dn, dr, dv, scale, flags, od, _dt3(out),
+        _arr(lse, torch.float32, "lse", (Tq, H)), _arr(dev_status, i32, "dev_status"),
+        _stream(stream))
     _check(st, "kda_latent_prefill")
 
 
@@ -538,22 +563,19 @@ def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, t
     include/kda.h).  logits [R, V] (rows may be strided), tokens [R]; top_ids and top_logprobs
     [R, top]."""
     R, V = logits.shape
-    _same("tokens", tokens, R)
-    _same("logprob", logprob, R)
+    rs, cs = logits.stride()
+    if cs != 1 and R and V > 1:
+        raise ValueError("logits needs contiguous rows")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    top = 0 if top_ids is None else int(top_ids.shape[1])
-    if top_ids is not None:
-        _same("top_ids", top_ids, R, top)
-        _same("top_logprobs", top_logprobs, R, top)
-    if entropy is not None:
-        _same("entropy", entropy, R)
-    if R and logits.stride(1) != 1 and V > 1:
-        raise ValueError("logits needs contiguous rows")
+    f32, i32 = torch.float32, torch.int32
+    top = 0 if top_ids is None else top_ids.shape[1]
+    ids, tl = _arr(top_ids, i32, "top_ids", (R, top)), _arr(top_logprobs, f32, "top_logprobs", (R, top))
+    if not logits.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
     st = lib().kda_token_logprobs(
-        _p_any(logits), logits.stride(0) if R > 1 else V, _dt3(logits), R, V,
-        _idx(tokens, "tokens"), _f32(logprob, "logprob"),
-        None if entropy is None else _f32(entropy, "entropy"), top, _idx(top_ids, "top_ids"),
-        None if top_logprobs is None else _f32(top_logprobs, "top_logprobs"),
-        _idx(dev_status, "dev_status"), _stream(stream))
+        logits.data_ptr(), rs if R > 1 else V, _dt3(logits), R, V,
+        _arr(tokens, i32, "tokens", (R,)), _arr(logprob, f32, "logprob", (R,)),
+        _arr(entropy, f32, "entropy", (R,)), top, ids, tl,
+        _arr(dev_status, i32, "dev_status"), _stream(stream))
     _check(st, "kda_token_logprobs")
