@@ -54,7 +54,11 @@ struct DecodeArgs {
     int32_t out_dt;
     float* lse;
     int32_t n_rt;   // row tiles of a request
-    int4* meta;     // [CTAs] the request whose first part this CTA holds: (r, row tile, last CTA, -) or r = -1
+    // Where split requests lie: (r, row tile, first CTA, last CTA), r = -1 for none.  With at most as many
+    // (request, row tile)s as CTAs an entry for each of these, else one for each CTA: for the request
+    // whose first part, but not the last, it holds.
+    int4* meta;
+    bool by_unit;
     float2* ml;     // [2 CTAs][N] (m in log2 units, l)
     float* part;    // [2 CTAs][N][512]
     int32_t* dev_status;
@@ -84,11 +88,12 @@ struct DecLayout {
     static constexpr uint32_t ROWF = MISC + 8 * 40;      // [N] row factors
     static constexpr uint32_t BAD = ROWF + 4 * N;        // [ROPES] bad boxes of the tile in a rope slot
     static constexpr uint32_t CTRL = BAD + 16;           // tmem address, dead flag, start of the range
-    static constexpr uint32_t SCAN = CTRL + 48;          // [8] warp sums
-    static constexpr uint32_t ROWO = SCAN + 64;          // [N] output offsets of the rows
+    static constexpr uint32_t SCAN = CTRL + 48;          // [2][8] warp sums
+    static constexpr uint32_t ROWO = SCAN + 128;         // [N] output offsets of the rows
     static constexpr uint32_t PMAX = ROWO + 8 * N;       // [2][128] partial maxima
     static constexpr uint32_t SMEM = PMAX + 1024;
     static constexpr uint32_t TM_S = 4 * N, TM_Q = TM_S + kTile;
+    static_assert(4 * ROPES <= PAIRS, "the loads waited for at the end are the last of their slots");
     static_assert(BARS <= 40 && SMEM <= 232448 && TM_Q + 32 * QT <= 512, "shared memory and TMEM plan");
 };
 
@@ -109,31 +114,40 @@ __device__ __forceinline__ int request(const DecodeArgs& a, int r, int& ql, int&
 }
 // token tiles of a request; one without tokens takes one (empty) tile, for its zero rows
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+// Turning to another request (its queries in, the last one's results out) takes as long as this many
+// tiles: every request counts so much longer in the line of work that is cut into equal ranges.  With
+// 256 requests of about 64 tiles the slowest CTA was 4 % behind the mean without it.  Not with few
+// tiles a CTA, where a tile more on one of them would cost more.
+constexpr int turn_of(int N, long long tiles, int ctas) { return tiles < 8ll * ctas ? 0 : N == 64 ? 3 : 2; }
 
 // The walk over a CTA's range: next() gives the tiles [j0, j1) of request r, row tile rt.
 struct Walk {
-    int r, rt, j;
+    int r, rt, j, turn;
     long long left;
     int j0, j1, n, len, ql, err;
     int cr, crt;
     __device__ __forceinline__ bool next(const DecodeArgs& a) {
-        if (left <= 0) return false;
-        cr = r;
-        crt = rt;
-        len = request(a, r, ql, err);
-        n = tiles_of(len);
-        j0 = j;
-        j1 = (long long)(n - j) <= left ? n : j + (int)left;
-        left -= j1 - j0;
-        j = j1;
-        if (j == n) {
-            j = 0;
-            if (++r == a.R) {
-                r = 0;
-                ++rt;
+        while (left > 0) {
+            cr = r;
+            crt = rt;
+            len = request(a, r, ql, err);
+            n = tiles_of(len);
+            const int all = n + turn;
+            const int end = (long long)(all - j) <= left ? all : j + (int)left;
+            j0 = j;
+            j1 = min(end, n);
+            left -= end - j;
+            j = end;
+            if (j == all) {
+                j = 0;
+                if (++r == a.R) {
+                    r = 0;
+                    ++rt;
+                }
             }
+            if (j0 < j1) return true;  // else only the turn falls into this range
         }
-        return true;
+        return false;
     }
 };
 
@@ -162,6 +176,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <int N, int DT>
@@ -183,58 +200,76 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const float inf = __int_as_float(0x7f800000);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid < L::BARS) mbar_init(bar(tid), tid == L::B_P || tid == L::B_P + 1 || tid == L::B_Q || tid == L::B_SFREE ? 4 : 1);
     if (tid == 0) {
-        for (int i = 0; i < L::BARS; ++i) mbar_init(bar(i), i == L::B_P || i == L::B_P + 1 || i == L::B_Q || i == L::B_SFREE ? 4 : 1);
         ctrl[1] = 0;
         ctrl[2] = -1;
     }
+    if (tid == 64) prefetch_map(&map);
+    if (tid == 96) prefetch_map(&rmap);
     if (warp == 1) tmem_alloc(sb + L::CTRL, 512);
 
-    // ---- this CTA's range: tiles of all requests, then the request its start falls into
-    long long mine = 0;
-    for (int r = tid; r < a.R; r += kDecThreads) {
+    // ---- this CTA's range: the tiles of all requests, then the request its start falls into
+    auto tiles_at = [&](int r) {
         int ql, err;
-        mine += tiles_of(request(a, r, ql, err));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) scan[warp] = mine;
-    __syncthreads();
-    long long S = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) S += scan[w];
-    const long long T = S * a.n_rt;
-    const long long G = T < gridDim.x ? T : gridDim.x;  // CTAs with work: each has a tile at least
-    const bool work = blockIdx.x < G;
-    const long long g0 = work ? T * blockIdx.x / G : 0, g1 = work ? T * (blockIdx.x + 1) / G : 0;
-    const int rt0 = (int)(g0 / S);
-    const long long want = g0 - rt0 * S;
-    long long before = 0;
-    for (int base = 0; base < a.R; base += kDecThreads) {
-        __syncthreads();
-        int ql, err;
-        const int r = base + tid;
-        const long long n = r < a.R ? tiles_of(request(a, r, ql, err)) : 0;
-        long long x = n;
+        return r < a.R ? (long long)tiles_of(request(a, r, ql, err)) : 0ll;
+    };
+    auto inclusive = [&](long long x) {  // over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(~0u, x, o);
             if (lane >= o) x += y;
         }
+        return x;
+    };
+    long long n = tiles_at(tid), more_n = 0;  // of the first requests, one a thread, and of the others
+    for (int r = tid + kDecThreads; r < a.R; r += kDecThreads) more_n += tiles_at(r);
+    long long x = inclusive(n);
+    more_n = inclusive(more_n);
+    if (lane == 31) {
+        scan[warp] = x;
+        scan[8 + warp] = more_n;
+    }
+    __syncthreads();
+    long long S = 0, before = 0, off = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) off += scan[w];
+        before += scan[w];
+        S += scan[w] + scan[8 + w];
+    }
+    const int turn = turn_of(N, S * a.n_rt, gridDim.x);
+    S += (long long)turn * a.R;
+    const long long T = S * a.n_rt;
+    const long long G = T < gridDim.x ? T : gridDim.x;  // CTAs with work
+    const bool work = blockIdx.x < G;
+    const long long g0 = work ? T * blockIdx.x / G : 0, g1 = work ? T * (blockIdx.x + 1) / G : 0;
+    const int rt0 = (int)(g0 / S);
+    const long long want = g0 - rt0 * S;
+    auto found = [&](int r) {
+        const long long lo = off + x - n + (long long)turn * r;
+        if (n > 0 && want >= lo && want < lo + n + turn) {
+            ctrl[2] = r;
+            ctrl[3] = rt0;
+            ctrl[4] = (int)(want - lo);
+            // the first pages of the range: they are asked for before the CTA is set up
+            const int64_t page = min((want - lo) * kTile / a.page_size, (long long)a.max_pages - 1);
+            if (page >= 0) prefetch_l2(a.table + (int64_t)r * a.max_pages + page);
+        }
+    };
+    found(tid);
+    for (int base = kDecThreads; base < a.R && before + (long long)turn * base <= want; base += kDecThreads) {
+        __syncthreads();
+        n = tiles_at(base + tid);
+        x = inclusive(n);
         if (lane == 31) scan[warp] = x;
         __syncthreads();
-        long long off = before;
+        off = before;
         for (int w = 0; w < 8; ++w) {
             if (w < warp) off += scan[w];
             before += scan[w];
         }
-        const long long lo = off + x - n;
-        if (n > 0 && want >= lo && want < lo + n) {
-            ctrl[2] = r;
-            ctrl[3] = rt0;
-            ctrl[4] = (int)(want - lo);
-        }
-        if (before > want) break;
+        found(base + tid);
     }
     fence_before();
     __syncthreads();
@@ -244,6 +279,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     w.r = ctrl[2];
     w.rt = ctrl[3];
     w.j = ctrl[4];
+    w.turn = turn;
     w.left = w.r < 0 ? 0 : g1 - g0;
     bool dead = false;
     // a wait that gives up marks the CTA: every role leaves its loop at its next wait
@@ -488,7 +524,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::B_Q));
         };
-        if (t == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (t == 0 && !a.by_unit) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
         bool more = w.next(a), quit = false;  // quit: agreed by the four warps, so that barriers stay matched
         if (more) load_q(w.cr, w.crt);
         while (more && !quit) {
@@ -642,11 +678,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
             if (t == 0 && !whole && g.j0 == 0) {
                 // the last CTA with a part of this request
-                const long long end = g1 + (g.n - g.j1);  // this part ends the range
+                const long long end = g1 + (g.n - g.j1);  // this part ends the range; of the request's tiles
                 long long last_cta = (end - 1) * G / T;
                 while (T * (last_cta + 1) / G < end) ++last_cta;
                 while (T * last_cta / G >= end) --last_cta;
-                a.meta[blockIdx.x] = make_int4(g.cr, g.crt, (int)last_cta, 0);
+                a.meta[a.by_unit ? g.crt * a.R + g.cr : blockIdx.x] = make_int4(g.cr, g.crt, blockIdx.x, (int)last_cta);
+            } else if (t == 0 && whole && a.by_unit) {
+                a.meta[g.crt * a.R + g.cr] = make_int4(-1, 0, 0, 0);
             }
             bar_named(1, 128);
             wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
@@ -691,60 +729,120 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 }
 
 // Joins the parts of a request that several CTAs hold: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i.
-// Block (g, row): a row of the request whose first part CTA g holds; a thread has 4 channels.  The
-// factors of all parts (at most one a CTA) are taken first, side by side, so that the loads of the
-// parts do not wait on one another.
+// Entry blockIdx.x of meta; 128 threads a row, 4 channels a thread.
+//   few requests over many CTAs (kSplit): block y has row y, and its four groups of 128 threads a
+//     quarter of the parts each;
+//   else: one group, rows 4y .. 4y + 3 side by side in each thread (a row a group took four waves of
+//     blocks, each as long as its chain of dependent loads: 17 us against 6 for 256 units of 64 rows).
+struct Split {
+    int r, rt, g, parts;
+};
+__device__ __forceinline__ Split split_at(const DecodeArgs& a, int e) {
+    const int4 me = a.meta[e];
+    // an entry is only missing after a wait gave up: what lies there then is not taken
+    const bool ok = me.x >= 0 && me.x < a.R && me.y >= 0 && me.y < a.n_rt && me.z >= 0 && me.w >= me.z && me.w < kDecCtas;
+    return {me.x, me.y, me.z, ok ? me.w - me.z + 1 : 0};
+}
+// place of part i (CTA g + i's): the first part in its CTA's second place, the others in the first
 template <int N>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeArgs a) {
-    __shared__ float fac[kDecCtas];
-    __shared__ float red[2][4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int g = blockIdx.x, row = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int4 me = a.meta[g];
-    if (me.x < 0 || row >= a.K * a.H - me.y * N) return;
-    const int parts = me.z - g + 1;
+__device__ __forceinline__ int64_t part_at(int g, int i, int row) { return (int64_t)(2 * (g + i) + (i == 0)) * N + row; }
+
+// The factors of a row's parts, by one warp: fac[i] = 2^{m_i - m}; returns (m, l) in every lane.
+template <int N>
+__device__ __forceinline__ float2 part_factors(const DecodeArgs& a, int g, int parts, int row, float* fac, int lane) {
+    constexpr int n = (kDecCtas + 31) / 32;
     const float inf = __int_as_float(0x7f800000);
-    // part i is CTA g + i's: the first in its second place, the others in their first
-    auto at = [&](int i) { return (int64_t)(2 * (g + i) + (i == 0)) * N + row; };
-    float2 ml[(kDecCtas + 127) / 128];
-    float m = -inf;
+    float2 ml[n];
+    float m = -inf, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < (kDecCtas + 127) / 128; ++k) {
-        ml[k] = t + 128 * k < parts ? a.ml[at(t + 128 * k)] : make_float2(-inf, 0.f);
+    for (int k = 0; k < n; ++k) {
+        const int i = lane + 32 * k;
+        ml[k] = i < parts ? a.ml[part_at<N>(g, i, row)] : make_float2(-inf, 0.f);
         m = fmaxf(m, ml[k].x);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     const float mr = m == -inf ? 0.f : m;
-    float l = 0.f;
 #pragma unroll
-    for (int k = 0; k < (kDecCtas + 127) / 128; ++k) {
+    for (int k = 0; k < n; ++k) {
         const float f = ex2(ml[k].x - mr);
         l = fmaf(f, ml[k].y, l);
-        if (t + 128 * k < parts) fac[t + 128 * k] = f;
+        if (lane + 32 * k < parts) fac[lane + 32 * k] = f;
     }
-    l = warp_sum(l);
-    if (lane == 0) red[1][warp] = l;
-    __syncthreads();
-    l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part + at(i) * kLatent + 4 * t);
-        const float f = fac[i];
-        o.x = fmaf(f, x.x, o.x);
-        o.y = fmaf(f, x.y, o.y);
-        o.z = fmaf(f, x.z, o.z);
-        o.w = fmaf(f, x.w, o.w);
-    }
-    const float il = l > 0.f ? 1.f / l : 0.f;
-    const int f = me.y * N + row, tt = f / a.H, h = f - tt * a.H;
-    const int64_t orow = (int64_t)me.x * a.K + tt;
+    return make_float2(mr, warp_sum(l));
+}
+__device__ __forceinline__ void fma4(float4& o, float f, float4 x) {
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+}
+__device__ __forceinline__ void put_row(const DecodeArgs& a, const Split& u, int f, float2 ml, float4 o, int t) {
+    const float il = ml.y > 0.f ? 1.f / ml.y : 0.f;
+    const int tt = f / a.H, h = f - tt * a.H;
+    const int64_t orow = (int64_t)u.r * a.K + tt;
     store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il), a.out_dt);
-    if (t == 0 && a.lse != nullptr) a.lse[orow * a.H + h] = l > 0.f ? (mr + log2f(l)) * 0.69314718055994531f : -inf;
+    if (t == 0 && a.lse != nullptr)
+        a.lse[orow * a.H + h] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994531f : -__int_as_float(0x7f800000);
+}
+
+template <int N, bool kSplit>
+__global__ void __launch_bounds__(kSplit ? 512 : 128) combine_kernel(const __grid_constant__ DecodeArgs a) {
+    __shared__ float fac[4][kDecCtas];
+    __shared__ float2 sml[4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Split u = split_at(a, blockIdx.x);
+    if (u.parts == 0) return;
+    const int t = threadIdx.x & 127, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* part = a.part + 4 * t;
+    const int rows = a.K * a.H - u.rt * N;  // of this row tile, if less than N
+    if constexpr (kSplit) {
+        __shared__ float4 acc[3][128];
+        const int row = blockIdx.y, sub = threadIdx.x >> 7;
+        if (row >= rows) return;
+        if (warp == 0) {
+            const float2 ml = part_factors<N>(a, u.g, u.parts, row, fac[0], lane);
+            if (lane == 0) sml[0] = ml;
+        }
+        __syncthreads();
+        float4 o = zero;
+#pragma unroll 10
+        for (int i = sub; i < u.parts; i += 4)
+            fma4(o, fac[0][i], *reinterpret_cast<const float4*>(part + part_at<N>(u.g, i, row) * kLatent));
+        if (sub > 0) acc[sub - 1][t] = o;
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) fma4(o, 1.f, acc[k][t]);
+        put_row(a, u, u.rt * N + row, sml[0], o, t);
+    } else {
+        const int row0 = blockIdx.y * 4;
+        if (row0 >= rows) return;
+        float4 x[2][4], o[4] = {zero, zero, zero, zero};
+        // the first two parts are asked for ahead of the factors (a split request has at least two)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[i][k] = i < u.parts ? *reinterpret_cast<const float4*>(part + part_at<N>(u.g, i, row0 + k) * kLatent) : zero;
+        const float2 ml = part_factors<N>(a, u.g, u.parts, row0 + warp, fac[warp], lane);
+        if (lane == 0) sml[warp] = ml;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i < u.parts) fma4(o[k], fac[k][i], x[i][k]);
+#pragma unroll 2
+        for (int i = 2; i < u.parts; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                fma4(o[k], fac[k][i], *reinterpret_cast<const float4*>(part + part_at<N>(u.g, i, row0 + k) * kLatent));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (row0 + k < rows) put_row(a, u, u.rt * N + row0 + k, sml[k], o[k], t);
+    }
 }
 
 int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -762,16 +860,19 @@ kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_
     const unsigned grid = (unsigned)(most < kDecCtas ? most : kDecCtas);
     f<<<grid, kDecThreads, L::SMEM, s>>>(map[0], map[1], a);
     if (max_tiles <= 1) return launch_status();  // one tile a request: nothing is split
+    // few requests: many parts each (one request of 38 CTAs: 10 us a row a group, 4 us split)
+    const int64_t units = (int64_t)a.n_rt * a.R;
+    const bool split = units * 4 <= grid;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, N);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(a.by_unit ? (unsigned)units : grid, split ? N : N / 4);
+    cfg.blockDim = dim3(split ? 512 : 128);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<N>, a) != cudaSuccess) return KDA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, split ? combine_kernel<N, true> : combine_kernel<N, false>, a) != cudaSuccess) return KDA_ERR_CUDA;
     return launch_status();
 }
 
@@ -828,7 +929,8 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     const int n = tile_rows((int64_t)K * H);
     DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
                  block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
-                 out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, nullptr, nullptr, dev_status};
+                 out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, false, nullptr, nullptr, dev_status};
+    a.by_unit = (int64_t)a.n_rt * R <= kDecCtas;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.meta = reinterpret_cast<int4*>(ws);
     ws += align16(kDecCtas * sizeof(int4));
