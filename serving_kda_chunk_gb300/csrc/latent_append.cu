@@ -32,22 +32,27 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
+    // the place, the row and the weights are asked for together: the row does not wait for the place
     const int32_t slot = a.slot[t];
+    const uint4* src = reinterpret_cast<const uint4*>(a.kv + t * a.kv_stride);
+    uint4 w[2] = {__ldcs(src + lane), __ldcs(src + 32 + lane)};
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (lane < kRope / 8) r = __ldcs(src + kLatent / 8 + lane);
+    uint4 g[2] = {r, r};
+    if (a.weight != nullptr) {
+        const uint4* wt = reinterpret_cast<const uint4*>(a.weight);
+        g[0] = __ldg(wt + lane);
+        g[1] = __ldg(wt + 32 + lane);
+    }
     if (slot < 0) return;
     const int32_t page = slot / a.page_size;
     if (page >= a.P) {
         if (lane == 0) report(a.dev_status, KDA_DEV_BAD_SLOT);
         return;
     }
-    const uint4* src = reinterpret_cast<const uint4*>(a.kv + t * a.kv_stride);
     uint4* dst = reinterpret_cast<uint4*>(a.cache + (int64_t)page * a.page_stride +
                                           (int64_t)(slot - page * a.page_size) * kLatentRow);
-    uint4 w[2] = {__ldcs(src + lane), __ldcs(src + 32 + lane)};
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (lane < kRope / 8) r = __ldcs(src + kLatent / 8 + lane);
     if (a.weight != nullptr) {
-        const uint4* wt = reinterpret_cast<const uint4*>(a.weight);
-        const uint4 g[2] = {__ldg(wt + lane), __ldg(wt + 32 + lane)};
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
