@@ -176,9 +176,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void prefetch_map(const void* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <int N, int DT>

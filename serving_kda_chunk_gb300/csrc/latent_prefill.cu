@@ -92,6 +92,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     auto bar = [&](int i) { return sb + PS_BAR + 8 * i; };
     const float inf = __int_as_float(0x7f800000);
 
+    if (tid == 32) prefetch_map(&maps.q);
+    if (tid == 64) prefetch_map(&maps.k);
+    if (tid == 96) prefetch_map(&maps.kr);
+    if (tid == 128) prefetch_map(&maps.v);
+
     // ---- which block of 512 rows: the last first, over all sequences
     const uint32_t rank = blockIdx.x & 1;  // in the cluster
     const int h = (blockIdx.x >> 1) % a.H, y = (blockIdx.x >> 1) / a.H;
@@ -133,11 +138,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     __syncthreads();
     const int n = ctrl[1];
     if (n < 0) return;
-    if (tid == 0) {
-        for (int i = 0; i < PB_BARS; ++i) {
-            const bool both = i < PB_KFREE;  // an arrival of each CTA
-            mbar_init(bar(i), both ? 2 : i >= PB_P && i < PB_P + 4 ? 8 : 1);
-        }
+    if (tid < PB_BARS) {
+        const bool both = tid < PB_KFREE;  // an arrival of each CTA
+        mbar_init(bar(tid), both ? 2 : tid >= PB_P && tid < PB_P + 4 ? 8 : 1);
     }
     if (warp == 9) tmem2_alloc(sb + PS_CTRL, 512);
     const int q0 = a.cu_q[n], Lq = a.cu_q[n + 1] - q0, k0 = a.cu_k[n], Lk = a.cu_k[n + 1] - k0;

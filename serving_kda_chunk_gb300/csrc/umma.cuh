@@ -354,6 +354,10 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
                  "r"(x), "r"(y)
                  : "memory");
 }
+// A tensor map into the descriptor cache, ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // One box of shared memory to a 2-D tensor map at (x, y), in the thread's bulk group (rows or
 // columns outside the tensor are not written).
 __device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint32_t src) {
