@@ -526,6 +526,9 @@ size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t H);
  *                 sees the last key); KDA_LATENT_FULL: all Lk keys.
  *   out         : rows Tq, H heads, 128 channels of out_dtype (any of the three)
  *   lse         : [Tq, H] fp32 or NULL
+ * Strides are >= 0; the row strides of q, k_nope and v are > 0 where there is
+ * more than one row (a head stride of 0 shares a row between the heads).
+ * Tq, Tk < 2^30.
  */
 kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
                               const void* k_rope, int64_t k_rope_stride, const kda_rows_desc* v,
