@@ -16,10 +16,13 @@
 // fp32 and fp16), so that O is rarely rescaled.
 //
 // Roles: warps 0-3 and 4-7 softmax of query tile 0 and 1 (and its results), warp 8 loads by TMA (the
-// queries once, then rings of K and V tiles), warp 9 of the first CTA issues the MMAs of both.
-// Barriers that the MMAs wait on lie in the first CTA and take both CTAs' arrivals; completed MMAs
-// arrive in both.
-// Long rows first: the pairs of a sequence's last queries have the most keys.
+// queries, rings of K and V tiles), warp 9 of the first CTA issues the MMAs of both.  Barriers that the
+// MMAs wait on lie in the first CTA and take both CTAs' arrivals; completed MMAs arrive in both.
+//
+// Blocks of rows follow one another without the pair leaving its SMs: the loading warp asks the launch
+// hardware for the next block (cluster launch control) while it loads one, so that a block's first loads
+// and products run under the last block's results (5 us of about 50 a block otherwise).  Long blocks
+// first: the grid's order is from a sequence's last queries, which have the most keys, to its first.
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "latent_host.h"
@@ -60,11 +63,13 @@ struct PreMaps {
 
 // shared memory: Q (2 x 3 parts), the rings, barriers
 constexpr uint32_t PS_K = 6 * kQPart, PS_V = PS_K + kStages * kKBytes, PS_BAR = PS_V + kStages * kVBytes;
-constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_KFREE = PB_V + kStages, PB_VFREE = PB_KFREE + kStages,
-              PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_P2 = PB_P + 2, PB_O = PB_P2 + 2, PB_EDGE = PB_O + 2, PB_DRAIN = PB_EDGE + 1,
-              PB_BARS = PB_DRAIN + 1;
-constexpr uint32_t PS_CTRL = PS_BAR + 8 * 32, PS_SCAN = PS_CTRL + 32, PS_SMEM = PS_SCAN + 4 * 16;
-static_assert(PB_BARS <= 32 && PS_SMEM <= 232448, "shared memory plan");
+constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_NEXT = PB_V + kStages, PB_KFREE = PB_NEXT + 1,
+              PB_VFREE = PB_KFREE + kStages, PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_P2 = PB_P + 2,
+              PB_O = PB_P2 + 2, PB_QFREE = PB_O + 2, PB_EDGE = PB_QFREE + 2, PB_CLC = PB_EDGE + 1, PB_INFO = PB_CLC + 1,
+              PB_IFREE = PB_INFO + 2, PB_DRAIN = PB_IFREE + 2, PB_BARS = PB_DRAIN + 1;
+constexpr uint32_t PS_CTRL = PS_BAR + 8 * 40, PS_SCAN = PS_CTRL + 32, PS_CLC = PS_SCAN + 64, PS_INFO = PS_CLC + 16,
+                   PS_SMEM = PS_INFO + 2 * 32;
+static_assert(PB_BARS <= 40 && PS_CLC % 16 == 0 && PS_SMEM <= 232448, "shared memory plan");
 // TMEM: S of the two query tiles, then O
 constexpr uint32_t PT_S = 0, PT_O = 256;
 
@@ -80,6 +85,13 @@ __device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
+// Eight results from o[e] as one 16-byte word.
+template <int DT>
+__device__ __forceinline__ uint4 pack16(const float (&o)[32], int e) {
+    return make_uint4(Elem<DT>::put2(o[e], o[e + 1]), Elem<DT>::put2(o[e + 2], o[e + 3]),
+                      Elem<DT>::put2(o[e + 4], o[e + 5]), Elem<DT>::put2(o[e + 6], o[e + 7]));
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefill_kernel(const __grid_constant__ PreMaps maps, const __grid_constant__ PrefillArgs a) {
@@ -87,7 +99,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int* ctrl = reinterpret_cast<int*>(sm + PS_CTRL);  // 0 tmem, 1 sequence, 2 its tile
+    volatile int* ctrl = reinterpret_cast<int*>(sm + PS_CTRL);  // 0 tmem, 1 sequence, 2 its block, 3 and 4 where its scan stood
+    volatile int* info = reinterpret_cast<int*>(sm + PS_INFO);  // two blocks' (head, sequence, first row); sequence -1: no more
     int* scan = reinterpret_cast<int*>(sm + PS_SCAN);
     auto bar = [&](int i) { return sb + PS_BAR + 8 * i; };
     const float inf = __int_as_float(0x7f800000);
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
     // ---- which block of 512 rows: the last first, over all sequences
     const uint32_t rank = blockIdx.x & 1;  // in the cluster
-    const int h = (blockIdx.x >> 1) % a.H, y = (blockIdx.x >> 1) / a.H;
+    const int y = (blockIdx.x >> 1) / a.H;
     auto blocks_of = [&](int n, bool& bad) {
         const int q0 = a.cu_q[n], q1 = a.cu_q[n + 1], k0 = a.cu_k[n], k1 = a.cu_k[n + 1];
         bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
@@ -122,6 +135,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (lane == 31) scan[warp] = x;
         __syncthreads();
+        const int start = before;
         int off = before;
         for (int w = 0; w < kPreThreads / 32; ++w) {
             if (w < warp) off += scan[w];
@@ -131,28 +145,41 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (b > 0 && y >= lo && y < lo + b) {
             ctrl[1] = n;
             ctrl[2] = b - 1 - (y - lo);
+            ctrl[3] = base;
+            ctrl[4] = start;
         }
         // block 0 looks at every sequence, for the report
         if (before > y && blockIdx.x != 0) break;
     }
     __syncthreads();
-    const int n = ctrl[1];
-    if (n < 0) return;
+    if (ctrl[1] < 0) return;
     if (tid < PB_BARS) {
-        const bool both = tid < PB_KFREE;  // an arrival of each CTA
-        mbar_init(bar(tid), both ? 2 : tid >= PB_P && tid < PB_P + 4 ? 8 : 1);
+        int count = 1;
+        if (tid < PB_KFREE) count = 2;                          // an arrival of each CTA
+        if (tid >= PB_P && tid < PB_O) count = 8;               // four warps of each
+        if (tid >= PB_IFREE && tid < PB_DRAIN) count = rank == 0 ? 9 : 8;  // the warps that read a block's place
+        mbar_init(bar(tid), count);
     }
     if (warp == 9) tmem2_alloc(sb + PS_CTRL, 512);
-    const int q0 = a.cu_q[n], Lq = a.cu_q[n + 1] - q0, k0 = a.cu_k[n], Lk = a.cu_k[n + 1] - k0;
-    const int row0 = ctrl[2] * kQBlock;
-    // key tiles of query tile q (of both CTAs): up to the last key its last row sees
-    auto tiles_of = [&](int q) {
-        const int rows = min(kQTile, Lq - row0 - q * kQTile);
-        if (rows <= 0) return 0;
-        const int keys = a.full ? Lk : min(Lk, Lk - Lq + row0 + q * kQTile + rows);
-        return keys > 0 ? (keys + kKTile - 1) / kKTile : 0;
+    // a block: its place, and the key tiles of its two query tiles (over both CTAs), up to the last key
+    // that the tile's last row sees
+    struct Block {
+        int h, q0, Lq, k0, Lk, row0, n0, n1, nt;
     };
-    const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
+    auto block_at = [&](int h, int n, int row0) {
+        Block u;
+        u.h = h;
+        u.row0 = row0;
+        u.q0 = a.cu_q[n], u.Lq = a.cu_q[n + 1] - u.q0, u.k0 = a.cu_k[n], u.Lk = a.cu_k[n + 1] - u.k0;
+        auto tiles_of = [&](int q) {
+            const int rows = min(kQTile, u.Lq - row0 - q * kQTile);
+            if (rows <= 0) return 0;
+            const int keys = a.full ? u.Lk : min(u.Lk, u.Lk - u.Lq + row0 + q * kQTile + rows);
+            return keys > 0 ? (keys + kKTile - 1) / kKTile : 0;
+        };
+        u.n0 = tiles_of(0), u.n1 = tiles_of(1), u.nt = max(u.n0, u.n1);
+        return u;
+    };
     fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are there
@@ -171,34 +198,42 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // ================================================================ loads
         // into this CTA, counted on the barriers of the first
         auto first = [&](int b) { return map_rank(bar(b), 0); };
-        bool edge = false;
+        Block u = block_at((int)(blockIdx.x >> 1) % a.H, ctrl[1], ctrl[2] * kQBlock);
+        uint32_t kt = 0, vt = 0, n_q[2] = {0, 0}, edges = 0;  // tiles, query tiles and edges loaded so far
+        int scan_base = ctrl[3], scan_before = ctrl[4];
         auto load_queries = [&](int q) {
+            if ((q ? u.n1 : u.n0) == 0) return;
+            if (n_q[q] > 0) wait(PB_QFREE + q, (n_q[q] - 1) & 1);
+            ++n_q[q];
+            if (dead || lane != 0) return;
             mbar_expect_tx_cluster(first(PB_Q + q), 3 * kQPart);
             for (int c = 0; c < 3; ++c)
-                tma2_load_3d(sb + (q * 3 + c) * kQPart, &maps.q, 64 * c, h * a.hq,
-                             q0 + row0 + q * kQTile + (int)rank * kRows, first(PB_Q + q));
+                tma2_load_3d(sb + (q * 3 + c) * kQPart, &maps.q, 64 * c, u.h * a.hq,
+                             u.q0 + u.row0 + q * kQTile + (int)rank * kRows, first(PB_Q + q));
         };
         auto load_k = [&](int i) {
-            const uint32_t st = i % kStages;
-            wait(PB_KFREE + st, (i / kStages & 1) ^ 1);
+            const uint32_t st = kt % kStages;
+            wait(PB_KFREE + st, (kt / kStages & 1) ^ 1);
+            ++kt;
             if (dead || lane != 0) return;
-            const int t = k0 + i * kKTile + (int)rank * 64;
+            const int t = u.k0 + i * kKTile + (int)rank * 64;
             const uint32_t dst = sb + PS_K + st * kKBytes, b = first(PB_K + st);
             mbar_expect_tx_cluster(b, kKBytes);
-            tma2_load_3d(dst, &maps.k, 0, h * a.hk, t, b);
-            tma2_load_3d(dst + kKPart, &maps.k, 64, h * a.hk, t, b);
+            tma2_load_3d(dst, &maps.k, 0, u.h * a.hk, t, b);
+            tma2_load_3d(dst + kKPart, &maps.k, 64, u.h * a.hk, t, b);
             tma2_load_2d(dst + 2 * kKPart, &maps.kr, 0, t, b);
         };
         auto load_v = [&](int i) {
-            const uint32_t st = i % kStages;
-            wait(PB_VFREE + st, (i / kStages & 1) ^ 1);
+            const uint32_t st = vt % kStages;
+            wait(PB_VFREE + st, (vt / kStages & 1) ^ 1);
+            ++vt;
             if (dead) return;
             const uint32_t dst = sb + PS_V + st * kVBytes, b = first(PB_V + st);
-            const int valid = Lk - i * kKTile;
+            const int valid = u.Lk - i * kKTile;
             if (valid >= kKTile) {
                 if (lane == 0) {
                     mbar_expect_tx_cluster(b, kVBytes);
-                    tma2_load_3d(dst, &maps.v, 64 * (int)rank, h * a.hv, k0 + i * kKTile, b);
+                    tma2_load_3d(dst, &maps.v, 64 * (int)rank, u.h * a.hv, u.k0 + i * kKTile, b);
                 }
             } else {
                 // keys past the sequence (its last tile): their weight is zero, and so has to be the
@@ -206,10 +241,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 // clears them and only then lets it be used.
                 if (lane == 0) {
                     mbar_expect_tx(bar(PB_EDGE), kVBytes);
-                    tma_load_3d(dst, &maps.v, 64 * (int)rank, h * a.hv, k0 + i * kKTile, bar(PB_EDGE));
+                    tma_load_3d(dst, &maps.v, 64 * (int)rank, u.h * a.hv, u.k0 + i * kKTile, bar(PB_EDGE));
                 }
-                wait(PB_EDGE, 0);
-                edge = true;
+                wait(PB_EDGE, edges++ & 1);
                 for (uint32_t e = valid * 128 + lane * 16; e < kVBytes; e += 512)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + e), "r"(0u) : "memory");
                 fence_async_smem();
@@ -217,28 +251,87 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(b);
             }
         };
-        if (lane == 0 && n0 > 0) load_queries(0);
-        if (nt > 0) load_k(0);
-        if (lane == 0 && n1 > 0) load_queries(1);
-        for (int i = 0; i < nt; ++i) {
-            load_v(i);
-            if (i + 1 < nt) load_k(i + 1);
+        // The place of block `id` of the grid: heads side by side, blocks of rows from the last of the last
+        // sequence to the first of the first.  Answers come in rising order, so the scan goes on where it
+        // stood (and starts again if one should not).
+        auto place = [&](int id, int& n, int& row0) {
+            const int want = id / a.H;
+            if (want < scan_before) scan_base = scan_before = 0;
+            n = -1;
+            for (; scan_base < a.N; scan_base += 32) {
+                const int c = a.N - 1 - (scan_base + lane);
+                bool bad = false;
+                const int b = c >= 0 ? blocks_of(c, bad) : 0;
+                int x = b;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int z = __shfl_up_sync(~0u, x, o);
+                    if (lane >= o) x += z;
+                }
+                const int lo = scan_before + x - b, total = __shfl_sync(~0u, x, 31);
+                const uint32_t hit = __ballot_sync(~0u, b > 0 && want >= lo && want < lo + b);
+                if (hit) {
+                    const int who = __ffs(hit) - 1;
+                    n = __shfl_sync(~0u, c, who);
+                    row0 = __shfl_sync(~0u, b - 1 - (want - lo), who) * kQBlock;
+                    return;
+                }
+                scan_before += total;
+            }
+        };
+        for (uint32_t it = 0;; ++it) {
+            // the next block is asked for while this one is loaded, once both CTAs have read the last answer
+            if (rank == 0 && it > 0) wait(PB_NEXT, (it - 1) & 1);
+            if (lane == 0 && !dead) {
+                mbar_expect_tx(bar(PB_CLC), 16);
+                if (rank == 0) clc_request(sb + PS_CLC, bar(PB_CLC));
+            }
+            __syncwarp();
+            load_queries(0);
+            if (u.nt > 0) load_k(0);
+            load_queries(1);
+            for (int i = 0; i < u.nt; ++i) {
+                load_v(i);
+                if (i + 1 < u.nt) load_k(i + 1);
+                if (__any_sync(~0u, dead)) break;
+            }
+            wait(PB_CLC, it & 1);
             if (__any_sync(~0u, dead)) break;
+            const int got = clc_block(sb + PS_CLC);
+            fence_async_smem();  // the answer has been read before the next one is written
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(first(PB_NEXT));
+            int n = -1, row0 = 0;
+            if (got >= 0) place(got >> 1, n, row0);
+            // the place for the other warps (their first block is the CTA's own)
+            const uint32_t b = it & 1;
+            if (it >= 2) wait(PB_IFREE + b, ((it - 2) >> 1) & 1);
+            const int h = got >= 0 ? (got >> 1) % a.H : 0;
+            if (lane == 0) {
+                info[8 * b] = h;
+                info[8 * b + 1] = n;
+                info[8 * b + 2] = row0;
+                mbar_arrive(bar(PB_INFO + b));
+            }
+            __syncwarp();
+            if (n < 0) break;
+            u = block_at(h, n, row0);
         }
-        // Every load was waited for by an MMA that is done when the CTAs leave.  After a wait that gave
-        // up that does not hold: one more (bounded) wait on a phase that does not end lets them land.
-        if (__any_sync(~0u, dead)) mbar_wait(bar(PB_EDGE), edge ? 1 : 0, kPreWait);
+        // Every load was waited for by an MMA that is done when the CTAs leave, and the last answer was
+        // read.  After a wait that gave up that does not hold: one more (bounded) wait on a phase that does
+        // not end lets them land.
+        if (__any_sync(~0u, dead)) mbar_wait(bar(PB_EDGE), edges & 1, kPreWait);
     } else if (warp == 9 && rank == 0) {
         // ================================================================ MMAs
         // the whole warp runs this, one lane issues (umma.cuh, mma_by)
         const uint32_t lead = elect_lane();
         const uint32_t sb4 = (sb & 0x3ffffu) >> 4;
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-        const int m0 = __shfl_sync(~0u, n0, 0), m1 = __shfl_sync(~0u, n1, 0), mt = max(m0, m1);
         const uint32_t ids = idesc_16(DT == KDA_F16, 256, kKTile, false, false, a.negate);
         const uint32_t idv = idesc_16(DT == KDA_F16, 256, 128, false, true, false);
-        auto do_s = [&](int q, int i) {
-            const uint32_t b4 = sb4 + PS_K / 16 + i % kStages * (kKBytes / 16);
+        uint32_t kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};  // K / V tiles, query tiles, products of S so far
+        auto do_s = [&](int q, uint32_t st) {
+            const uint32_t b4 = sb4 + PS_K / 16 + st * (kKBytes / 16);
 #pragma unroll
             for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -247,48 +340,64 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                             desc_k4(b4 + c * (kKPart / 16), 64, s), ids, c + s != 0);
             commit2_by(lead, bar(PB_S + q));
         };
-        auto do_pv = [&](int q, int i, int s0, int s1) {
-            const uint32_t b4 = sb4 + PS_V / 16 + i % kStages * (kVBytes / 16);
+        auto do_pv = [&](int q, uint32_t st, int fresh, int s0, int s1) {
+            const uint32_t b4 = sb4 + PS_V / 16 + st * (kVBytes / 16);
 #pragma unroll
             for (int s = s0; s < s1; ++s)
-                mma2_ta_by(lead, tm + PT_O + q * 128, tm + PT_S + q * 128 + 8 * s, desc_mn4(b4, 16, 1024, s), idv, i + s != 0);
+                mma2_ta_by(lead, tm + PT_O + q * 128, tm + PT_S + q * 128 + 8 * s, desc_mn4(b4, 16, 1024, s), idv,
+                           !fresh || s != 0);
             if (s1 == 8) commit2_by(lead, bar(PB_O + q));
         };
-        if (mt > 0) wait(PB_K, 0);
-        if (m0 > 0) {
-            wait(PB_Q, 0);
-            fence_after();
-            do_s(0, 0);
-        }
-        if (m1 > 0) {
-            wait(PB_Q + 1, 0);
-            fence_after();
-            do_s(1, 0);
-        }
-        if (mt > 0) commit2_by(lead, bar(PB_KFREE));
+        Block u = block_at((int)(blockIdx.x >> 1) % a.H, ctrl[1], ctrl[2] * kQBlock);
         bool stop = false;
-        for (int i = 0; i < mt && !stop; ++i) {
-            // loads ahead of the weights: a wait queues behind the MMAs issued before it
-            if (!mbar_wait_cluster(bar(PB_V + i % kStages), i / kStages & 1, kPreWait)) dead = true;  // cleared edges
-            if (i + 1 < mt) wait(PB_K + (i + 1) % kStages, (i + 1) / kStages & 1);
+        for (uint32_t it = 0; !stop; ++it) {
+            const int m0 = __shfl_sync(~0u, u.n0, 0), m1 = __shfl_sync(~0u, u.n1, 0), mt = max(m0, m1);
+            if (mt > 0) wait(PB_K + kv % kStages, kv / kStages & 1);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int mq = q ? m1 : m0, mo = q ? m0 : m1;
-                if (i < mq) {
-                    wait(PB_P + q, i & 1);
+                const int mq = q ? m1 : m0;
+                if (mq > 0) {
+                    wait(PB_Q + q, n_q[q]++ & 1);
                     fence_after();
-                    do_pv(q, i, 0, 6);
-                    wait(PB_P2 + q, i & 1);
-                    fence_after();
-                    do_pv(q, i, 6, 8);
-                    if (q == 1 || i >= mo) commit2_by(lead, bar(PB_VFREE + i % kStages));
-                    if (i + 1 < mq) {
-                        do_s(q, i + 1);
-                        if (q == 1 || i + 1 >= mo) commit2_by(lead, bar(PB_KFREE + (i + 1) % kStages));
-                    }
+                    do_s(q, kv % kStages);
+                    if (mq == 1) commit2_by(lead, bar(PB_QFREE + q));
                 }
             }
+            if (mt > 0) commit2_by(lead, bar(PB_KFREE + kv % kStages));
+            for (int i = 0; i < mt && !stop; ++i, ++kv) {
+                const uint32_t st = kv % kStages, sn = (kv + 1) % kStages;
+                // loads ahead of the weights: a wait queues behind the MMAs issued before it
+                if (!mbar_wait_cluster(bar(PB_V + st), kv / kStages & 1, kPreWait)) dead = true;  // cleared edges
+                if (i + 1 < mt) wait(PB_K + sn, (kv + 1) / kStages & 1);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int mq = q ? m1 : m0, mo = q ? m0 : m1;
+                    if (i < mq) {
+                        wait(PB_P + q, n_p[q] & 1);
+                        fence_after();
+                        do_pv(q, st, i == 0, 0, 6);
+                        wait(PB_P2 + q, n_p[q]++ & 1);
+                        fence_after();
+                        do_pv(q, st, 0, 6, 8);
+                        if (q == 1 || i >= mo) commit2_by(lead, bar(PB_VFREE + st));
+                        if (i + 1 < mq) {
+                            do_s(q, sn);
+                            if (i + 2 == mq) commit2_by(lead, bar(PB_QFREE + q));  // the last S that reads these queries
+                            if (q == 1 || i + 1 >= mo) commit2_by(lead, bar(PB_KFREE + sn));
+                        }
+                    }
+                }
+                stop = __any_sync(~0u, dead);
+            }
+            if (stop) break;
+            const uint32_t b = it & 1;
+            wait(PB_INFO + b, (it >> 1) & 1);
             stop = __any_sync(~0u, dead);
+            const int h = info[8 * b], n = info[8 * b + 1], row0 = info[8 * b + 2];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(PB_IFREE + b));
+            stop = stop || __any_sync(~0u, n < 0);
+            if (!stop) u = block_at(h, n, row0);
         }
         commit2_by(lead, bar(PB_DRAIN));
         dead = false;
@@ -296,158 +405,145 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     } else if (warp < 8) {
         // ================================================================ softmax and results
         const int q = warp >> 2, t = tid & 127;
-        const int my_tiles = q ? n1 : n0;
         const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = tq + PT_S + q * 128, to = tq + PT_O + q * 128;
-        const int row = row0 + q * kQTile + (int)rank * kRows + t;  // of the sequence
         const uint32_t p_full = map_rank(bar(PB_P + q), 0), p_full2 = map_rank(bar(PB_P2 + q), 0);
-        const int last = row >= Lq ? -1 : a.full ? Lk - 1 : Lk - Lq + row;
-        float m = -inf, l = 0.f;
-        for (int i = 0; i < my_tiles && !__any_sync(~0u, dead); ++i) {
-            uint32_t s[4][32];
-            wait(PB_S + q, i & 1);
-            fence_after();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) ld32_issue(ts + 32 * b, s[b]);
-            wait_ld();
-            const int lim = last - i * kKTile;  // columns 0 .. lim are seen
-            if (lim < kKTile - 1) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * b + e > lim) s[b][e] = __float_as_uint(-inf);
-            }
-            float mx[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k >> 1][k & 1]);
-#pragma unroll
-            for (int e = 2; e < 32; e += 4)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[k >> 1][e + (k & 1)])),
-                                  __uint_as_float(s[k >> 1][(e + 2 + (k & 1)) & 31]));
-            const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-            float f = 1.f;
-            bool need = false;
-            if (i == 0) {
-                m = mt;
-            } else if (mt > m && (m == -inf || (mt - m) * a.c > 8.f)) {
-                f = ex2((m - mt) * a.c);
-                m = mt;
-                need = true;
-            }
-            if (__any_sync(~0u, need)) {
-                wait(PB_O + q, (i - 1) & 1);
+        uint32_t done = 0;  // key tiles of this query tile so far
+        Block u = block_at((int)(blockIdx.x >> 1) % a.H, ctrl[1], ctrl[2] * kQBlock);
+        for (uint32_t it = 0;; ++it) {
+            const int my_tiles = q ? u.n1 : u.n0;
+            const int row = u.row0 + q * kQTile + (int)rank * kRows + t;  // of the sequence
+            const int last = row >= u.Lq ? -1 : a.full ? u.Lk - 1 : u.Lk - u.Lq + row;
+            float m = -inf, l = 0.f;
+            for (int i = 0; i < my_tiles && !__any_sync(~0u, dead); ++i, ++done) {
+                uint32_t s[4][32];
+                wait(PB_S + q, done & 1);
                 fence_after();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) ld32_issue(ts + 32 * b, s[b]);
+                wait_ld();
+                const int lim = last - i * kKTile;  // columns 0 .. lim are seen
+                if (lim < kKTile - 1) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * b + e > lim) s[b][e] = __float_as_uint(-inf);
+                }
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k >> 1][k & 1]);
+#pragma unroll
+                for (int e = 2; e < 32; e += 4)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[k >> 1][e + (k & 1)])),
+                                      __uint_as_float(s[k >> 1][(e + 2 + (k & 1)) & 31]));
+                const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                float f = 1.f;
+                bool need = false;
+                if (i == 0) {
+                    m = mt;
+                } else if (mt > m && (m == -inf || (mt - m) * a.c > 8.f)) {
+                    f = ex2((m - mt) * a.c);
+                    m = mt;
+                    need = true;
+                }
+                if (__any_sync(~0u, need)) {
+                    wait(PB_O + q, (done - 1) & 1);
+                    fence_after();
 #pragma unroll 1
-                for (int b = 0; b < 8; ++b) {
-                    float o[16];
-                    ld16(to + 16 * b, o);
+                    for (int b = 0; b < 8; ++b) {
+                        float o[16];
+                        ld16(to + 16 * b, o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= f;
-                    st16f(to + 16 * b, o);
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        st16f(to + 16 * b, o);
+                    }
+                    l *= f;
                 }
-                l *= f;
+                const float mc = m == -inf ? 0.f : m * a.c;
+                const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), cc, nm);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        ls[e & 1] = __fadd2_rn(ls[e & 1], x);
+                        p[e] = E::put2(x.x, x.y);
+                    }
+                    st16u(ts + 16 * b, p);
+                    // the first 96 keys go ahead: their product runs under the last exponentials
+                    if (b >= 2) {
+                        wait_st();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(b == 2 ? p_full : p_full2);
+                    }
+                }
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
             }
-            const float mc = m == -inf ? 0.f : m * a.c;
-            const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
-            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), cc, nm);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    ls[e & 1] = __fadd2_rn(ls[e & 1], x);
-                    p[e] = E::put2(x.x, x.y);
-                }
-                st16u(ts + 16 * b, p);
-                // the first 96 keys go ahead: their product runs under the last exponentials
-                if (b >= 2) {
-                    wait_st();
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(b == 2 ? p_full : p_full2);
-                }
+            if (my_tiles > 0) {
+                wait(PB_O + q, (done - 1) & 1);
+                fence_after();
             }
-            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-        }
-        if (my_tiles > 0) {
-            wait(PB_O + q, (my_tiles - 1) & 1);
-            fence_after();
-        }
-        const float il = l > 0.f ? 1.f / l : 0.f;
-        const int64_t orow = (int64_t)q0 + row;
-        if (row < Lq && a.lse != nullptr)
-            a.lse[orow * a.H + h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
-        // Rows leave through the query tile's shared memory (every S has read it), 64 channels at a
-        // time, so that a warp writes whole 128-byte lines: thread t puts its row there, and the warp
-        // takes its 32 rows out along the channels.
-        const uint32_t stage = sb + q * 3 * kQPart;
-        const int wrow = t & ~31;  // the warp's first row
-        auto emit = [&](auto pack, int words, int bytes) {  // 16-byte words of 64 channels; bytes of an element
+            const float il = l > 0.f ? 1.f / l : 0.f;
+            const int64_t orow = (int64_t)u.q0 + row;
+            if (row < u.Lq && a.lse != nullptr)
+                a.lse[orow * a.H + u.h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
+            const int64_t at = orow * a.out_rs + (int64_t)u.h * a.out_hs;
+            // a thread's row, whole 32-byte sectors at a time; the other query tile's products go on meanwhile
+            auto emit = [&](auto put) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < 4; ++b) {
                     float o[32];
                     if (my_tiles > 0) {
-                        ld32(to + 64 * half + 32 * b, o);
+                        ld32(to + 32 * b, o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= il;
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     }
-                    pack(o, b);
+                    if (row < u.Lq) put(o, 32 * b);
                 }
-                __syncwarp();
-                const int per = 32 / words, x = lane % words;  // rows a step
-                for (int r = lane / words; r < 32; r += per) {
-                    const int rr = wrow + r, grow = row - t + rr;
-                    if (grow < Lq) {
-                        const uint32_t at = stage + (x >> 3) * kQPart + rr * 128 + (((x ^ rr) & 7) << 4);
-                        uint4 v;
-                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-                        const int64_t off = ((int64_t)q0 + grow) * a.out_rs + (int64_t)h * a.out_hs + half * 64;
-                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + off * bytes + x * 16) = v;
-                    }
-                }
-                __syncwarp();
+            };
+            if (a.out_dt == KDA_F32) {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+                emit([&](const float (&o)[32], int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) p[(c + e) / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                });
+            } else if (a.out_dt == KDA_BF16) {
+                uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+                emit([&](const float (&o)[32], int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) p[(c + e) / 8] = pack16<KDA_BF16>(o, e);
+                });
+            } else {
+                uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+                emit([&](const float (&o)[32], int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) p[(c + e) / 8] = pack16<KDA_F16>(o, e);
+                });
             }
-        };
-        auto put = [&](int x, uint4 v) {  // word x of this thread's row
-            const uint32_t at = stage + (x >> 3) * kQPart + t * 128 + (((x ^ t) & 7) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-        };
-        if (a.out_dt == KDA_F32) {
-            emit([&](const float (&o)[32], int b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    put(8 * b + e / 4, make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
-                                                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3])));
-            }, 16, 4);
-        } else if (a.out_dt == KDA_BF16) {
-            emit([&](const float (&o)[32], int b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    put(4 * b + e / 8, make_uint4(Elem<KDA_BF16>::put2(o[e], o[e + 1]), Elem<KDA_BF16>::put2(o[e + 2], o[e + 3]),
-                                                  Elem<KDA_BF16>::put2(o[e + 4], o[e + 5]), Elem<KDA_BF16>::put2(o[e + 6], o[e + 7])));
-            }, 8, 2);
-        } else {
-            emit([&](const float (&o)[32], int b) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    put(4 * b + e / 8, make_uint4(Elem<KDA_F16>::put2(o[e], o[e + 1]), Elem<KDA_F16>::put2(o[e + 2], o[e + 3]),
-                                                  Elem<KDA_F16>::put2(o[e + 4], o[e + 5]), Elem<KDA_F16>::put2(o[e + 6], o[e + 7])));
-            }, 8, 2);
+            fence_before();
+            const uint32_t b = it & 1;
+            wait(PB_INFO + b, (it >> 1) & 1);
+            if (__any_sync(~0u, dead)) break;
+            const int h = info[8 * b], n = info[8 * b + 1], row0 = info[8 * b + 2];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(PB_IFREE + b));
+            if (n < 0) break;
+            u = block_at(h, n, row0);
         }
-        fence_before();
     }
+    fence_before();
     __syncthreads();
     cluster_sync();  // no CTA leaves while the other's MMAs, loads or arrivals may still reach it
     fence_after();

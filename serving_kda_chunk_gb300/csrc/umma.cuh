@@ -509,6 +509,27 @@ __device__ __forceinline__ void commit2_by(uint32_t leader, uint32_t mbar) {
         "r"(leader)
         : "memory");
 }
+// Cluster launch control: asks for a cluster of this grid that has not been launched.  The 16-byte answer
+// lands at the same address in every CTA of the cluster, counted on the mbarrier there.
+__device__ __forceinline__ void clc_request(uint32_t answer, uint32_t mbar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+        "[%0], [%1];" ::"r"(answer),
+        "r"(mbar)
+        : "memory");
+}
+// The x index of the first block of the cluster that an answer gave, -1 if there was none.
+__device__ __forceinline__ int clc_block(uint32_t answer) {
+    int x;
+    asm volatile(
+        "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b32 a, b, c, d;\nld.shared.b128 h, [%1];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nmov.b32 a, -1;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, h;\nmov.b32 %0, a;\n}\n"
+        : "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return x;
+}
 // By one warp of each CTA of the pair.
 __device__ __forceinline__ void tmem2_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols));

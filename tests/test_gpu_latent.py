@@ -377,6 +377,18 @@ def test_prefill(lq, lk, H, dtype):
     p.check(got)
 
 
+@pytest.mark.parametrize("N,most,H", [(900, 40, 2), (350, 700, 3), (33, 1100, 8)])
+def test_prefill_many_sequences(N, most, H):
+    # more sequences than one scan step holds, more blocks than pairs of SMs, some without rows or keys
+    rng = np.random.Generator(np.random.PCG64(N))
+    lq = [int(x) for x in rng.integers(0, most, N)]
+    lk = [max(0, n + int(x)) for n, x in zip(lq, rng.integers(-3, 50, N))]
+    p = Prefill(lq, lk, H, seed=N)
+    got = p.run()
+    assert got[2] == 0
+    p.check(got)
+
+
 def test_prefill_rows_without_keys():
     # fewer keys than queries leave the first rows empty; sequences without queries or keys
     p = Prefill([300, 0, 10, 40, 3], [170, 50, 0, 1, 3], 2, seed=3)
