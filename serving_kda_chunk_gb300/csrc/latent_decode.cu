@@ -1,11 +1,11 @@
 // latent_decode.cu -- kda_latent_decode: absorbed latent attention over a paged cache.
 //
 // One latent row (1152 bytes) serves every head as key and, its first 1024 bytes, as value, so a
-// request's tokens are read once for up to 64 query rows (positions x heads).  Tokens come 64 at a
-// time; with Q the query rows [N, 576], C a tile [64, 576] and V its first 512 channels:
-//   S   = Q C^T          M = 128 (the N rows repeated), N = 64 tokens, K = 576
+// request's tokens are read once for up to 64 query rows (positions x heads).  Tokens come T = 64
+// or 48 at a time; with Q the query rows [N, 576], C a tile [T, 576] and V its first 512 channels:
+//   S   = Q C^T          M = 128 (the N rows repeated), N = T tokens, K = 576
 //   P   = 2^(c S - m)    c = scale log2 e, m a running maximum of the row
-//   O^T += V^T P^T       4 products M = 128 value channels, N rows, K = 64 tokens
+//   O^T += V^T P^T       4 products M = 128 value channels, N rows, K = T tokens
 // O stays transposed in TMEM (lane = value channel): 512 fp32 channels of 128 rows would take all
 // 512 columns, transposed they take 4 N, and few query rows waste no tensor-core rows in this
 // product.  The tile is used as it lies in shared memory: K-major for S, MN-major for V^T.
@@ -30,12 +30,10 @@ namespace {
 
 using namespace umma;
 
-constexpr int kTile = 64;                   // tokens a tile
+constexpr int kMaxTile = 64;                // tokens a tile, at most (DecLayout::T)
 constexpr int kDecCtas = 152;               // one a SM
 constexpr int kDecThreads = 256;
 constexpr uint32_t kDecWait = 1u << 18;     // polls, about a second: loads and MMAs take microseconds
-constexpr uint32_t kPairBytes = 2 * kTile * 128;  // two 64-channel columns of a tile
-constexpr uint32_t kRopeBytes = kTile * 128;
 
 struct DecodeArgs {
     LatentRows ql, qr;
@@ -45,7 +43,7 @@ struct DecodeArgs {
     float c;        // |scale| log2 e
     bool negate;    // scale < 0
     int64_t P;
-    int32_t page_size, box;  // box: rows of one TMA box, a divisor of page_size and of kTile
+    int32_t page_size, box;  // box: rows of one TMA box, a divisor of page_size and of the tile
     const int32_t* table;
     int32_t max_pages;
     const int32_t* seq_len;
@@ -65,23 +63,30 @@ struct DecodeArgs {
 };
 
 // The plan of a CTA with N query rows a tile.  Q is the A operand of S with M = 128: its N rows are
-// repeated 128 / N times along M, so that every softmax thread has a row and N / 2 of the tile's 64
+// repeated 128 / N times along M, so that every softmax thread has a row and its share of the tile's
 // scores.  Q lies in TMEM (32 columns a 64-channel part) as far as there are columns beside O and S:
 // all of it for N <= 32, six parts of nine for N = 64, the rest in shared memory.  An S product then
 // reads 2 KiB of shared memory instead of 6 (a product of M = 128, N = 64, K = 16 is bound by that:
-// 44 cycles against 32), and the shared memory saved holds a third tile in flight.
+// 44 cycles against 32), and the shared memory saved holds a third tile in flight.  With N = 64 three
+// tiles fit at 48 tokens each: two and a quarter of 64 did not cover the chain load, S, softmax, O of a
+// tile (64 x 7 positions of about 6000 tokens, 32 heads: 310 us with 48, 329 with 64).
 template <int N>
 struct DecLayout {
-    static constexpr int CW = N / 2;                  // scores a thread and tile
+    static constexpr int T = N == 64 ? 48 : 64;       // tokens a tile
+    static constexpr uint32_t COL = T * 128;          // bytes of a 64-channel column of a tile
     static constexpr int REP = 128 / N;               // copies of a row along M
+    static constexpr int CW = T / REP;                // scores a thread and tile
     static constexpr int QT = N == 64 ? 6 : 9;        // parts of Q in TMEM
-    static constexpr int PAIRS = N == 64 ? 9 : 12;    // ring of channel pairs, 4 a tile
-    static constexpr int ROPES = N == 64 ? 2 : 3;
+    static constexpr int PAIRS = 12, ROPES = 3;       // rings of column pairs (4 a tile) and rope columns
+    static constexpr int NP = N == 64 ? 1 : 2;        // buffers of P
     static constexpr uint32_t QS = 0;                 // parts QT .. 8 of Q, 128 rows
     static constexpr uint32_t PAIR = QS + (9 - QT) * 128 * 128;
-    static constexpr uint32_t ROPE = PAIR + PAIRS * kPairBytes;
-    static constexpr uint32_t P = ROPE + ROPES * kRopeBytes;  // two buffers
-    static constexpr uint32_t MISC = P + 2 * N * 128;
+    static constexpr uint32_t ROPE = PAIR + PAIRS * 2 * COL;
+    static constexpr uint32_t P = ROPE + ROPES * COL;
+    static constexpr uint32_t MISC = P + NP * N * 128;
+    // two 64-channel columns of all rows, on their way into TMEM: P is free then, and so is QS until its
+    // own parts come
+    static constexpr uint32_t STAGE = N == 64 ? QS + 2 * 128 * 128 : P;
     static constexpr int B_FULL = 0, B_EMPTY = PAIRS, B_RFULL = 2 * PAIRS, B_REMPTY = B_RFULL + ROPES,
                          B_S = B_REMPTY + ROPES, B_SFREE = B_S + 1, B_P = B_SFREE + 1, B_PV = B_P + 2, B_Q = B_PV + 2,
                          B_DRAIN = B_Q + 1, BARS = B_DRAIN + 1;
@@ -92,7 +97,7 @@ struct DecLayout {
     static constexpr uint32_t ROWO = SCAN + 128;         // [N] output offsets of the rows
     static constexpr uint32_t PMAX = ROWO + 8 * N;       // [2][128] partial maxima
     static constexpr uint32_t SMEM = PMAX + 1024;
-    static constexpr uint32_t TM_S = 4 * N, TM_Q = TM_S + kTile;
+    static constexpr uint32_t TM_S = 4 * N, TM_Q = TM_S + 64;
     static_assert(4 * ROPES <= PAIRS, "the loads waited for at the end are the last of their slots");
     static_assert(BARS <= 40 && SMEM <= 232448 && TM_Q + 32 * QT <= 512, "shared memory and TMEM plan");
 };
@@ -113,7 +118,10 @@ __device__ __forceinline__ int request(const DecodeArgs& a, int r, int& ql, int&
     return len;
 }
 // token tiles of a request; one without tokens takes one (empty) tile, for its zero rows
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+template <int N>
+__device__ __forceinline__ int tiles_of(int len) {
+    return len > 0 ? (len + DecLayout<N>::T - 1) / DecLayout<N>::T : 1;
+}
 // Turning to another request (its queries in, the last one's results out) takes as long as this many
 // tiles: every request counts so much longer in the line of work that is cut into equal ranges.  With
 // 256 requests of about 64 tiles the slowest CTA was 4 % behind the mean without it.  Not with few
@@ -121,6 +129,7 @@ __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile
 constexpr int turn_of(int N, long long tiles, int ctas) { return tiles < 8ll * ctas ? 0 : N == 64 ? 3 : 2; }
 
 // The walk over a CTA's range: next() gives the tiles [j0, j1) of request r, row tile rt.
+template <int N>
 struct Walk {
     int r, rt, j, turn;
     long long left;
@@ -131,7 +140,7 @@ struct Walk {
             cr = r;
             crt = rt;
             len = request(a, r, ql, err);
-            n = tiles_of(len);
+            n = tiles_of<N>(len);
             const int all = n + turn;
             const int end = (long long)(all - j) <= left ? all : j + (int)left;
             j0 = j;
@@ -159,15 +168,18 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
 // CW = 8 (two copies of the rows in a warp) each half of the warp takes its half of 16 columns.
 template <int CW>
 __device__ __forceinline__ void ld_scores(uint32_t taddr, int col0, int lane, float (&v)[CW]) {
-    constexpr int n = CW < 16 ? 1 : CW / 16;
-    uint32_t u[n][16];
+    static_assert(CW == 8 || CW == 16 || CW == 24, "one 16-column load, and one of 8 for 24");
+    uint32_t u[16], w[8];
     const uint32_t base = taddr + (CW < 16 ? col0 & ~15 : col0);
-#pragma unroll
-    for (int i = 0; i < n; ++i) ld16_issue(base + 16 * i, u[i]);
+    ld16_issue(base, u);
+    if constexpr (CW == 24)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "r"(base + 16));
     wait_ld();
 #pragma unroll
     for (int i = 0; i < CW; ++i)
-        v[i] = __uint_as_float(CW < 16 && lane >= 16 ? u[0][(8 + i) & 15] : u[i / 16][i % 16]);
+        v[i] = __uint_as_float(CW < 16 && lane >= 16 ? u[(8 + i) & 15] : i < 16 ? u[i & 15] : w[i & 7]);
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
@@ -209,7 +221,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // ---- this CTA's range: the tiles of all requests, then the request its start falls into
     auto tiles_at = [&](int r) {
         int ql, err;
-        return r < a.R ? (long long)tiles_of(request(a, r, ql, err)) : 0ll;
+        return r < a.R ? (long long)tiles_of<N>(request(a, r, ql, err)) : 0ll;
     };
     auto inclusive = [&](long long x) {  // over the warp
 #pragma unroll
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             ctrl[3] = rt0;
             ctrl[4] = (int)(want - lo);
             // the first pages of the range: they are asked for before the CTA is set up
-            const int64_t page = min((want - lo) * kTile / a.page_size, (long long)a.max_pages - 1);
+            const int64_t page = min((want - lo) * L::T / a.page_size, (long long)a.max_pages - 1);
             if (page >= 0) prefetch_l2(a.table + (int64_t)r * a.max_pages + page);
         }
     };
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctrl[0];
-    Walk w;
+    Walk<N> w;
     w.r = ctrl[2];
     w.rt = ctrl[3];
     w.j = ctrl[4];
@@ -294,16 +306,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // warp 0: the rope part and, with 64-row boxes, everything (5 boxes a tile: a pair is one box
         // of two 64-channel columns); with smaller boxes (8 pages or fewer a tile, 9 boxes each)
         // warps 2 and 3 take two pairs each, since one warp issues a box in some 100 cycles
-        const bool whole_box = a.box == kTile;
+        const bool whole_box = a.box == kMaxTile;
         const int part = warp;  // 0: rope (and pairs 0..3), 2: pairs 0, 1, 3: pairs 2, 3
         const int p_lo = part == 3 ? 2 : 0, p_hi = whole_box ? (part == 0 ? 4 : 0) : part == 0 ? 0 : p_lo + 2;
-        const uint32_t per = kTile / a.box;
+        const uint32_t per = L::T / a.box;
         uint32_t tile = 0;
         while (!dead && w.next(a)) {
             const int32_t* tab = a.table + (int64_t)w.cr * a.max_pages;
             // page of this lane's box in tile j (-1: none) and the box's first row in it
             auto page_of = [&](int j, uint32_t& y) {
-                const uint32_t t = (uint32_t)j * kTile + lane * a.box;
+                const uint32_t t = (uint32_t)j * L::T + lane * a.box;
                 const uint32_t pg = t / (uint32_t)a.page_size;
                 y = t - pg * a.page_size;
                 return lane < (int)per && t < (uint32_t)w.len ? tab[pg] : INT32_MIN;
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int j = w.j0; j < w.j1 && !dead; ++j, ++tile) {
                 const int page = next;
                 const uint32_t y = ynext;
-                const bool has = lane < (int)per && (uint32_t)j * kTile + lane * a.box < (uint32_t)w.len;
+                const bool has = lane < (int)per && (uint32_t)j * L::T + lane * a.box < (uint32_t)w.len;
                 if (j + 1 < w.j1) next = page_of(j + 1, ynext);
                 const bool ok = has && page >= 0 && page < a.P;
                 const uint32_t okm = __ballot_sync(~0u, ok);
@@ -327,10 +339,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     if (lane == 0) mbar_expect_tx(bar(L::B_FULL + slot), 2 * bytes);
                     __syncwarp();
                     if (ok) {
-                        const uint32_t dst = sb + L::PAIR + slot * kPairBytes + lane * a.box * 128;
+                        const uint32_t dst = sb + L::PAIR + slot * (2 * L::COL) + lane * a.box * 128;
                         tma_load_4d(dst, &map, 0, y, 2 * p, page, bar(L::B_FULL + slot));
                         if (!whole_box)
-                            tma_load_4d(dst + kTile * 128, &map, 0, y, 2 * p + 1, page, bar(L::B_FULL + slot));
+                            tma_load_4d(dst + L::COL, &map, 0, y, 2 * p + 1, page, bar(L::B_FULL + slot));
                     }
                 }
                 if (dead) break;
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                     __syncwarp();
                     if (ok)
-                        tma_load_4d(sb + L::ROPE + slot * kRopeBytes + lane * a.box * 128, &rmap, 0, y, 8, page,
+                        tma_load_4d(sb + L::ROPE + slot * L::COL + lane * a.box * 128, &rmap, 0, y, 8, page,
                                     bar(L::B_RFULL + slot));
                 }
             }
@@ -369,9 +381,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const uint32_t lead = elect_lane();
         const uint32_t sb4 = sb >> 4;
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-        const uint32_t ids = idesc_16(DT == KDA_F16, 128, kTile, false, false, a.negate);
+        const uint32_t ids = idesc_16(DT == KDA_F16, 128, L::T, false, false, a.negate);
         const uint32_t idv = idesc_16(DT == KDA_F16, 128, N, true, false, false);
-        Walk ws = w;  // S runs ahead of O, over its own copy of the walk
+        Walk<N> ws = w;  // S runs ahead of O, over its own copy of the walk
         bool more_s = __any_sync(~0u, ws.next(a)), more_v = __any_sync(~0u, w.next(a));
         int js = ws.j0, jv = w.j0;
         bool first_s = true, first_v = true;          // of a segment
@@ -381,15 +393,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         bool stop = false;
         while (more_v && !stop) {
             bool did = false;
-            if (v_it < s_it && __all_sync(~0u, mbar_test(bar(L::B_P + (v_it & 1)), (v_it >> 1) & 1))) {
+            if (v_it < s_it && __all_sync(~0u, mbar_test(bar(L::B_P + v_it % L::NP), v_it / L::NP & 1))) {
                 fence_after();
-                const uint32_t p4 = sb4 + L::P / 16 + (v_it & 1) * (N * 128 / 16);
+                const uint32_t p4 = sb4 + L::P / 16 + v_it % L::NP * (N * 128 / 16);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t a4 = sb4 + L::PAIR / 16 + v_slot * (kPairBytes / 16);
+                    const uint32_t a4 = sb4 + L::PAIR / 16 + v_slot * (2 * L::COL / 16);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_by(lead, tm + c * N, desc_mn4(a4, kTile * 128, 1024, s), desc_k4(p4, N, s), idv,
+                    for (int s = 0; s < L::T / 16; ++s)
+                        mma_by(lead, tm + c * N, desc_mn4(a4, L::COL, 1024, s), desc_k4(p4, N, s), idv,
                                s != 0 || !first_v);
                     commit_by(lead, bar(L::B_EMPTY + v_slot));
                     if (++v_slot == L::PAIRS) v_slot = 0;
@@ -398,7 +410,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 // read the slot's bad boxes and waited on its barrier by now
                 commit_by(lead, bar(L::B_REMPTY + vr_slot));
                 if (++vr_slot == L::ROPES) vr_slot = 0;
-                commit_by(lead, bar(L::B_PV + (v_it & 1)));
+                commit_by(lead, bar(L::B_PV + v_it % L::NP));
                 ++v_it;
                 first_v = __any_sync(~0u, ++jv == w.j1);
                 if (first_v) {
@@ -422,17 +434,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                 wait(L::B_FULL + s_slot, s_ph);
                                 fence_after();
                             }
-                            b4 = sb4 + L::PAIR / 16 + s_slot * (kPairBytes / 16) + (c % 2) * (kTile * 128 / 16);
+                            b4 = sb4 + L::PAIR / 16 + s_slot * (2 * L::COL / 16) + (c % 2) * (L::COL / 16);
                         } else {
-                            b4 = sb4 + L::ROPE / 16 + r_slot * (kRopeBytes / 16);
+                            b4 = sb4 + L::ROPE / 16 + r_slot * (L::COL / 16);
                         }
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
                             if (c < L::QT)
-                                mma_ta_by(lead, d, tm + L::TM_Q + 32 * c + 8 * s, desc_k4(b4, kTile, s), ids, c + s != 0);
+                                mma_ta_by(lead, d, tm + L::TM_Q + 32 * c + 8 * s, desc_k4(b4, L::T, s), ids, c + s != 0);
                             else
                                 mma_by(lead, d, desc_k4(sb4 + L::QS / 16 + (c - L::QT) * 1024, 128, s),
-                                       desc_k4(b4, kTile, s), ids, 1);
+                                       desc_k4(b4, L::T, s), ids, 1);
                         }
                         if (c < 8 && c % 2 == 1)
                             if (++s_slot == L::PAIRS) s_slot = 0, s_ph ^= 1;
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int row = t % N, col0 = t / N * CW;  // this thread's query row and first score
         uint32_t it = 0, rslot = 0, rph = 0;
         // The queries of a row tile: read from global memory along the rows (16 threads a row's 256
-        // bytes), turned in the two P buffers, 128 channels at a time, and written by the thread that
+        // bytes), turned in shared memory, 128 channels at a time, and written by the thread that
         // has the row to its TMEM lane; the parts without columns go to shared memory.
         auto load_q = [&](int r, int rt) {
             uint4 v[N / 8][5];
@@ -488,13 +500,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
             }
             // the last product that reads P (and so every earlier one) is done
-            if (it > 0) wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
-            const uint32_t stage = sb + L::P;
+            if (it > 0) wait(L::B_PV + (it - 1) % L::NP, (it - 1) / L::NP & 1);
 #pragma unroll
             for (int g = 0; g < 5; ++g) {
+                const uint32_t stage = sb + (g < 4 ? L::STAGE : L::P);  // the last is one column: P has room for it
                 if (g) bar_named(1, 128);
 #pragma unroll
                 for (int i = 0; i < N / 8; ++i) {
+                    if (g == 4 && (t & 15) >= 8) continue;
                     const int rr = 8 * i + (t >> 4);
                     sts16(stage + ((t >> 3) & 1) * (N * 128) + rr * 128 + (((t ^ rr) & 7) << 4), v[i][g]);
                 }
@@ -525,7 +538,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         bool more = w.next(a), quit = false;  // quit: agreed by the four warps, so that barriers stay matched
         if (more) load_q(w.cr, w.crt);
         while (more && !quit) {
-            const Walk g = w;  // this segment
+            const Walk<N> g = w;  // this segment
             if (t == 0 && g.j0 == 0 && g.crt == 0 && g.err) report(a.dev_status, g.err);
             // the running maximum of this thread's row and, for N = 64, of the row its warp does not
             // hold: every warp then knows by itself whether any row moves its maximum
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 if (j == max(g.j0, g.j1 - 3)) {
                     // the next segment's query rows into L2: behind the loads of the ring, a read from
                     // HBM takes some microseconds, and S waits for it
-                    Walk nx = w;
+                    Walk<N> nx = w;
                     if (nx.next(a)) {
                         const int rr = t % N, ff = nx.crt * N + rr, tt = ff / a.H, h = ff - tt * a.H;
                         if (ff < a.K * a.H) {
@@ -557,7 +570,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         }
                     }
                 }
-                const int t0 = j * kTile;
+                const int t0 = j * L::T;
                 const uint32_t bad = (uint32_t)bad_box[rslot];
                 if (++rslot == L::ROPES) rslot = 0, rph ^= 1;
                 const int valid = g.len - t0;  // tokens of this tile (may exceed it)
@@ -612,7 +625,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 if (__any_sync(~0u, need)) {  // the same in all four warps
                     if (t < N) rowf[row] = f_old;
                     bar_named(1, 128);
-                    wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
+                    wait(L::B_PV + (it - 1) % L::NP, (it - 1) / L::NP & 1);
                     fence_after();
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -626,29 +639,29 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     wait_st();
                     bar_named(1, 128);  // rowf has been read
                 }
-                if (it >= 2) wait(L::B_PV + (it & 1), ((it - 2) >> 1) & 1);  // this P buffer's last product
+                if (it >= L::NP) wait(L::B_PV + it % L::NP, (it - L::NP) / L::NP & 1);  // this P buffer's last product
 #pragma unroll
                 for (int i = 0; i < CW; i += 8)
-                    sts16(sb + L::P + (it & 1) * (N * 128) + chunk_k(row, col0 + i, N),
+                    sts16(sb + L::P + it % L::NP * (N * 128) + chunk_k(row, col0 + i, N),
                           make_uint4(E::put2(s[i], s[i + 1]), E::put2(s[i + 2], s[i + 3]),
                                      E::put2(s[i + 4], s[i + 5]), E::put2(s[i + 6], s[i + 7])));
-                if (valid < kTile || bad) {
+                if (valid < L::T || bad) {
                     // tokens that are not there: their weight is zero, and so has to be the value
                     // (what lies in the buffer, or past the end of a page, may be anything)
                     // a thread clears one 16-byte word (of 64) of every other token
                     const int x = t & 63;
-                    const uint32_t at = sb + L::PAIR + (it * 4 + (x >> 4)) % L::PAIRS * kPairBytes +
-                                        ((x >> 3) & 1) * (kTile * 128) + (x & 7) * 16;
+                    const uint32_t at = sb + L::PAIR + (it * 4 + (x >> 4)) % L::PAIRS * (2 * L::COL) +
+                                        ((x >> 3) & 1) * L::COL + (x & 7) * 16;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
-                    for (int k = max(valid, 0) + (t >> 6); k < kTile; k += 2) sts16(at + k * 128, zero);
+                    for (int k = max(valid, 0) + (t >> 6); k < L::T; k += 2) sts16(at + k * 128, zero);
                     if (bad)
-                        for (int k = t >> 6; k < kTile; k += 2)
+                        for (int k = t >> 6; k < L::T; k += 2)
                             if ((bad >> (k / a.box)) & 1) sts16(at + k * 128, zero);
                 }
                 fence_async_smem();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::B_P + (it & 1)));
+                if (lane == 0) mbar_arrive(bar(L::B_P + it % L::NP));
             }
             if (quit) break;
             // the next segment's queries: every S of this one has been read
@@ -684,7 +697,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 a.meta[g.crt * a.R + g.cr] = make_int4(-1, 0, 0, 0);
             }
             bar_named(1, 128);
-            wait(L::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1);
+            wait(L::B_PV + (it - 1) % L::NP, (it - 1) / L::NP & 1);
             fence_after();
             // channel c * 128 + t of every row; put is chosen once
             auto emit = [&](auto put) {
@@ -905,7 +918,7 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     KDA_REQUIRE(d_latent == kLatent && d_rope == kRope && K <= 16, KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE(page_size % 8 == 0 && (int64_t)R * K * H < (1ll << 31), KDA_ERR_UNSUPPORTED);
-    KDA_REQUIRE((int64_t)max_pages * page_size < (1ll << 31) - kTile && P < (1ll << 31), KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE((int64_t)max_pages * page_size < (1ll << 31) - kMaxTile && P < (1ll << 31), KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
     if (R == 0 || K == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(q_latent) && rows_ok(q_rope) && rows_ok(out), KDA_ERR_INVALID_ARG);
@@ -913,17 +926,17 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(aligned16(q_len) && aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(ws_bytes >= kda_latent_decode_workspace_size(R, K, H), KDA_ERR_INVALID_ARG);
-    const int box = lowbit_box(page_size, kTile);
+    const int n = tile_rows((int64_t)K * H);
+    const int box = lowbit_box(page_size, n == 64 ? 16 : kMaxTile);  // divides the tile as well (48 or 64 tokens)
     CUtensorMap map[2];
     // the cache as (channel of 64, row, 64-channel column, page): one box is `box` rows of one page
     // and one column (a 128-byte swizzle row), or with a whole tile of rows a pair of columns
     const cuuint64_t dims[4] = {64, (cuuint64_t)page_size, 9, (cuuint64_t)(P > 0 ? P : 1)};
     const cuuint64_t strides[3] = {kLatentRow * 2, 128, (cuuint64_t)page_stride * 2};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, box == kTile ? 2u : 1u, 1};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, box == kMaxTile ? 2u : 1u, 1};
     const cuuint32_t rope_boxes[4] = {64, (cuuint32_t)box, 1, 1};
     KDA_REQUIRE(encode_16bit(&map[0], in_dtype, 4, cache, dims, strides, boxes), KDA_ERR_CUDA);
     KDA_REQUIRE(encode_16bit(&map[1], in_dtype, 4, cache, dims, strides, rope_boxes), KDA_ERR_CUDA);
-    const int n = tile_rows((int64_t)K * H);
     DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
                  block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
                  out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, false, nullptr, nullptr, dev_status};
@@ -934,7 +947,8 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     a.part = reinterpret_cast<float*>(ws);
     ws += (size_t)2 * kDecCtas * n * kLatent * sizeof(float);
     a.ml = reinterpret_cast<float2*>(ws);
-    const int64_t max_tiles = ((int64_t)max_pages * page_size + kTile - 1) / kTile;
+    const int tile = n == 64 ? DecLayout<64>::T : DecLayout<32>::T;
+    const int64_t max_tiles = ((int64_t)max_pages * page_size + tile - 1) / tile;
     cudaStream_t s = as_stream(stream);
     if (in_dtype == KDA_BF16) return launch_n<KDA_BF16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
     return launch_n<KDA_F16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
