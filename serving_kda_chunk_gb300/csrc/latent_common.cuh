@@ -21,7 +21,6 @@ template <>
 struct Elem<KDA_BF16> {
     using T = __nv_bfloat16;
     static __device__ __forceinline__ float get(T x) { return __bfloat162float(x); }
-    static __device__ __forceinline__ T put(float x) { return __float2bfloat16_rn(x); }
     static __device__ __forceinline__ float2 get2(uint32_t w) {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
@@ -31,7 +30,6 @@ template <>
 struct Elem<KDA_F16> {
     using T = __half;
     static __device__ __forceinline__ float get(T x) { return __half2float(x); }
-    static __device__ __forceinline__ T put(float x) { return __float2half_rn(x); }
     static __device__ __forceinline__ float2 get2(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
     }
@@ -44,7 +42,6 @@ template <>
 struct Elem<KDA_F32> {
     using T = float;
     static __device__ __forceinline__ float get(T x) { return x; }
-    static __device__ __forceinline__ T put(float x) { return x; }
 };
 
 __host__ __device__ constexpr int dtype_bytes(int dt) { return dt == KDA_F32 ? 4 : 2; }
@@ -54,16 +51,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// One fp32 result rounded into an output of type dt.
-__device__ __forceinline__ void store1_as(void* p, int64_t i, float x, int dt) {
-    if (dt == KDA_F32)
-        static_cast<float*>(p)[i] = x;
-    else if (dt == KDA_BF16)
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
-    else
-        static_cast<__half*>(p)[i] = __float2half_rn(x);
 }
 
 // Four consecutive fp32 results (index i % 4 == 0) rounded into an output of type dt.

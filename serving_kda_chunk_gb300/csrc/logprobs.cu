@@ -467,9 +467,10 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
     const LogprobArgs a{logits, row_stride, V, tokens, logprob, entropy, top, top_ids, top_logprobs, dev_status};
     // blocks a row: enough rows fill the SMs by themselves (splitting 448 rows in two: 33 -> 45 us);
-    // else split, down to 8 vectors a thread (one row of 32768: 8.5 us in two blocks, 10.3 in eight)
+    // else split, down to 16 vectors a thread (one row of 32768: 7.7 us in one block, 8.3 in two, 10.3 in
+    // eight; 32 rows of 160000: 12.3 us in four, 14.4 in eight or two)
     int C = 1;
-    while (C < 8 && (int64_t)R * C < 304 && (int64_t)V * dtype_bytes(dtype) >= 2ll * C * kLpThreads * 128) C *= 2;
+    while (C < 8 && (int64_t)R * C < 304 && (int64_t)V * dtype_bytes(dtype) >= 2ll * C * kLpThreads * 256) C *= 2;
     // batches of a block's share, at most kMaxSeg pieces of them
     const int64_t batches = ((int64_t)V * dtype_bytes(dtype) / 16 / C + 1 + kBatch * kLpThreads - 1) / (kBatch * kLpThreads);
     const int per = (int)((batches + kMaxSeg - 1) / kMaxSeg);
