@@ -22,7 +22,8 @@
 // Blocks of rows follow one another without the pair leaving its SMs: the loading warp asks the launch
 // hardware for the next block (cluster launch control) while it loads one, so that a block's first loads
 // and products run under the last block's results (5 us of about 50 a block otherwise).  Long blocks
-// first: the grid's order is from a sequence's last queries, which have the most keys, to its first.
+// first: see the order of the sequences below, and a sequence's last queries, which have the most keys,
+// before its first.
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "latent_host.h"
@@ -40,6 +41,7 @@ constexpr uint32_t kPreWait = 1u << 18;  // polls, about a second: loads and MMA
 constexpr uint32_t kQPart = 128 * 128;   // 128 rows of 64 16-bit channels
 constexpr uint32_t kKPart = 64 * 128;    // 64 rows
 constexpr int kStages = 3;
+constexpr int kSorted = 256;             // up to so many sequences are taken by falling length
 constexpr uint32_t kKBytes = 3 * kKPart, kVBytes = 128 * 128;  // a CTA's half of a tile
 
 struct PrefillArgs {
@@ -68,7 +70,8 @@ constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_NEXT = PB_V + kStage
               PB_O = PB_P2 + 2, PB_QFREE = PB_O + 2, PB_EDGE = PB_QFREE + 2, PB_CLC = PB_EDGE + 1, PB_INFO = PB_CLC + 1,
               PB_IFREE = PB_INFO + 2, PB_DRAIN = PB_IFREE + 2, PB_BARS = PB_DRAIN + 1;
 constexpr uint32_t PS_CTRL = PS_BAR + 8 * 40, PS_SCAN = PS_CTRL + 32, PS_CLC = PS_SCAN + 64, PS_INFO = PS_CLC + 16,
-                   PS_SMEM = PS_INFO + 2 * 32;
+                   PS_ORDER = PS_INFO + 2 * 32, PS_START = PS_ORDER + 4 * kSorted, PS_LEN = PS_START + 4 * (kSorted + 1),
+                   PS_SMEM = PS_LEN + 4 * kSorted;
 static_assert(PB_BARS <= 40 && PS_CLC % 16 == 0 && PS_SMEM <= 232448, "shared memory plan");
 // TMEM: S of the two query tiles, then O
 constexpr uint32_t PT_S = 0, PT_O = 256;
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     if (tid == 96) prefetch_map(&maps.kr);
     if (tid == 128) prefetch_map(&maps.v);
 
-    // ---- which block of 512 rows: the last first, over all sequences
+    // ---- which block of 512 rows
     const uint32_t rank = blockIdx.x & 1;  // in the cluster
     const int y = (blockIdx.x >> 1) / a.H;
     auto blocks_of = [&](int n, bool& bad) {
@@ -118,38 +121,87 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         bad = q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk;
         return bad ? 0 : (q1 - q0 + kQBlock - 1) / kQBlock;
     };
+    // Blocks are taken from the longest sequence's last one (the most keys) to the shortest's first, so that
+    // what is left at the end is short: in order of the sequences alone eight ragged chunks took 4 % longer.
+    // More than kSorted sequences are taken from the last to the first.
+    volatile int* order = reinterpret_cast<int*>(sm + PS_ORDER);  // sequences by falling length
+    volatile int* start = reinterpret_cast<int*>(sm + PS_START);  // blocks before each, and in all
+    volatile int* len = reinterpret_cast<int*>(sm + PS_LEN);
+    const bool sorted = a.N <= kSorted;
     if (tid == 0) ctrl[1] = -1;
-    int before = 0;
-    for (int base = 0; base < a.N; base += kPreThreads) {
-        __syncthreads();
-        // from the last sequence to the first
-        const int n = a.N - 1 - (base + tid);
+    if (sorted) {
         bool bad = false;
-        const int b = n >= 0 ? blocks_of(n, bad) : 0;
-        if (bad && blockIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
-        int x = b;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(~0u, x, o);
-            if (lane >= o) x += z;
+        int b = 0, mine = -1;
+        if (tid < a.N) {
+            b = blocks_of(tid, bad);
+            mine = bad ? -1 : a.cu_k[tid + 1] - a.cu_k[tid];
+            len[tid] = mine;
+            if (bad && blockIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
         }
-        if (lane == 31) scan[warp] = x;
         __syncthreads();
-        const int start = before;
-        int off = before;
-        for (int w = 0; w < kPreThreads / 32; ++w) {
-            if (w < warp) off += scan[w];
-            before += scan[w];
+        if (tid < a.N) {
+            int rank_of = 0;
+            for (int m = 0; m < a.N; ++m) {
+                const int x = len[m];
+                rank_of += x > mine || (x == mine && m > tid);
+            }
+            order[rank_of] = tid;
+            start[rank_of + 1] = b;
         }
-        const int lo = off + x - b;
-        if (b > 0 && y >= lo && y < lo + b) {
-            ctrl[1] = n;
-            ctrl[2] = b - 1 - (y - lo);
-            ctrl[3] = base;
-            ctrl[4] = start;
+        __syncthreads();
+        if (warp == 0) {
+            int before = 0;
+            for (int base = 0; base < a.N; base += 32) {
+                const int r = base + lane;
+                int x = r < a.N ? start[r + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int z = __shfl_up_sync(~0u, x, o);
+                    if (lane >= o) x += z;
+                }
+                if (r < a.N) start[r + 1] = before + x;
+                before += __shfl_sync(~0u, x, 31);
+            }
+            if (lane == 0) start[0] = 0;
         }
-        // block 0 looks at every sequence, for the report
-        if (before > y && blockIdx.x != 0) break;
+        __syncthreads();
+        if (tid < a.N && y >= start[tid] && y < start[tid + 1]) {
+            ctrl[1] = order[tid];
+            ctrl[2] = start[tid + 1] - 1 - y;
+        }
+    } else {
+        int before = 0;
+        for (int base = 0; base < a.N; base += kPreThreads) {
+            __syncthreads();
+            // from the last sequence to the first
+            const int n = a.N - 1 - (base + tid);
+            bool bad = false;
+            const int b = n >= 0 ? blocks_of(n, bad) : 0;
+            if (bad && blockIdx.x == 0) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
+            int x = b;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int z = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += z;
+            }
+            if (lane == 31) scan[warp] = x;
+            __syncthreads();
+            const int stood = before;
+            int off = before;
+            for (int w = 0; w < kPreThreads / 32; ++w) {
+                if (w < warp) off += scan[w];
+                before += scan[w];
+            }
+            const int lo = off + x - b;
+            if (b > 0 && y >= lo && y < lo + b) {
+                ctrl[1] = n;
+                ctrl[2] = b - 1 - (y - lo);
+                ctrl[3] = base;
+                ctrl[4] = stood;
+            }
+            // block 0 looks at every sequence, for the report
+            if (before > y && blockIdx.x != 0) break;
+        }
     }
     __syncthreads();
     if (ctrl[1] < 0) return;
@@ -251,13 +303,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(b);
             }
         };
-        // The place of block `id` of the grid: heads side by side, blocks of rows from the last of the last
-        // sequence to the first of the first.  Answers come in rising order, so the scan goes on where it
-        // stood (and starts again if one should not).
+        // The place of block `id` of the grid: heads side by side.  Answers come in rising order, so the scan
+        // over many sequences goes on where it stood (and starts again if one should not).
         auto place = [&](int id, int& n, int& row0) {
             const int want = id / a.H;
-            if (want < scan_before) scan_base = scan_before = 0;
             n = -1;
+            if (sorted) {
+                for (int base = 0; base < a.N; base += 32) {
+                    const int r = base + lane;
+                    const uint32_t hit = __ballot_sync(~0u, r < a.N && want >= start[r] && want < start[r + 1]);
+                    if (hit) {
+                        const int at = base + __ffs(hit) - 1;
+                        n = order[at];
+                        row0 = (start[at + 1] - 1 - want) * kQBlock;
+                        return;
+                    }
+                }
+                return;
+            }
+            if (want < scan_before) scan_base = scan_before = 0;
             for (; scan_base < a.N; scan_base += 32) {
                 const int c = a.N - 1 - (scan_base + lane);
                 bool bad = false;

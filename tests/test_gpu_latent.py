@@ -481,6 +481,28 @@ def test_prefill_repeats_bit_for_bit_and_on_another_stream():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_prefill_is_captured_and_replayed():
+    p = Prefill([300, 1200], [300, 1500], 3, seed=16)
+    out = torch.zeros(1500, 3, 128, dtype=p.dt, device="cuda")
+    lse = torch.zeros(1500, 3, device="cuda")
+
+    def step():
+        kda.kda_latent_prefill(p.q, p.kv[..., :128], p.kr, p.kv[..., 128:], p.cu_q, p.cu_k, out, scale=SCALE, lse=lse)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    # the replay reads the bounds anew
+    p.lq, p.lk = [700, 800], [1000, 800]
+    p.cu_q.copy_(i32([0, 700, 1500]))
+    p.cu_k.copy_(i32([0, 1000, 1800]))
+    graph.replay()
+    torch.cuda.synchronize()
+    p.check((out, lse, 0))
+
+
 def test_decode_agrees_with_prefill_on_the_same_model():
     """Both forms of one layer: keys and values expanded from the latent vectors, and the query
     and output products absorbed; the last query of each sequence."""
