@@ -42,6 +42,10 @@ KDA_DEV_BAD_SLOT, KDA_DEV_BAD_TRACK, KDA_DEV_BAD_ACCEPT = 1, 2, 4
 KDA_DEV_BAD_SEQLEN, KDA_DEV_OVERLAP, KDA_DEV_TIMEOUT = 8, 16, 32
 KDA_MAX_POOLS = 16
 
+# absent from torch builds without CUDA, which can do no more with this package than import it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
 LIB_PATH = Path(__file__).resolve().parent / "libkda.so"
 _lib = None
 
@@ -198,7 +202,7 @@ def _f32(t, name):
 def _stream(stream):
     if stream is None:
         # the raw handle: building a Stream object costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -417,6 +421,7 @@ def _slot_sets(pools, clear_slots, src_slots, dst_offsets, dst_slots):
 # These marshal with one pass over each tensor's properties: a torch attribute costs about 0.1 us,
 # and at the smallest sizes the marshalling is most of a call.
 
+_i32, _f32t = torch.int32, torch.float32
 _ANY_DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16}
 
 
@@ -429,9 +434,7 @@ def _dt3(t) -> int:
 
 
 def _arr(t, dtype, name, shape=None):
-    """Device pointer of a contiguous CUDA tensor of the given dtype and shape (None stays None)."""
-    if t is None:
-        return None
+    """Device pointer of a contiguous CUDA tensor of the given dtype and shape."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be a tensor of {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -456,10 +459,11 @@ def _rows(t, name):
 def _one_dtype(what, *ts):
     """The element type that all of the given tensors have."""
     dt = ts[0].dtype
-    for t in ts:
+    for t in ts[1:]:
         if t.dtype is not dt:
             raise ValueError(f"{what} must share one dtype, got {sorted({str(x.dtype) for x in ts})}")
-    return _dt3(ts[0])
+    dt = _ANY_DT.get(dt)
+    return _dt3(ts[0]) if dt is None else dt
 
 
 def _pages(cache, width):
@@ -480,18 +484,20 @@ def kda_latent_append(kv, cache, slot, *, weight=None, eps=1e-6, dev_status=None
     paged cache (see include/kda.h).  kv: [T, 576], rows may be strided."""
     T, width = kv.shape
     ks, cs = kv.stride()
-    if T and cs != 1:
+    if cs != 1 and T:
         raise ValueError("kv needs contiguous rows")
     dt = _one_dtype("kv, cache and weight", kv, cache, cache if weight is None else weight)
-    slot_p = _arr(slot, torch.int32, "slot", (T,))
+    slot_p = _arr(slot, _i32, "slot", (T,))
     base, P, page, stride = _pages(cache, width)
     if not kv.is_cuda:
         raise ValueError("libkda takes CUDA tensors")
-    st = lib().kda_latent_append(
-        kv.data_ptr(), ks if T > 1 else width, _arr(weight, kv.dtype, "weight", (width - 64,)),
-        eps, dt, T, width - 64, 64, slot_p, base, P, page, stride,
-        _arr(dev_status, torch.int32, "dev_status"), _stream(stream))
-    _check(st, "kda_latent_append")
+    st = (_lib or lib()).kda_latent_append(
+        kv.data_ptr(), ks if T > 1 else width,
+        None if weight is None else _arr(weight, kv.dtype, "weight", (width - 64,)), eps, dt, T,
+        width - 64, 64, slot_p, base, P, page, stride,
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_latent_append")
 
 
 def kda_latent_decode_workspace_size(R, K, H) -> int:
@@ -505,25 +511,26 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_len, out, worksp
     strided over rows and heads."""
     shape = q_latent.shape
     RK, H, dl = shape
-    dr = q_rope.shape[2]
+    rope_shape = q_rope.shape
+    dr = rope_shape[2]
     R, max_pages = block_table.shape
     if K < 0 or RK != R * K:
         raise ValueError(f"q_latent has {RK} rows, not {R} requests x K = {K}")
     dt = _one_dtype("queries and cache", q_latent, q_rope, cache)
-    i32 = torch.int32
-    if q_rope.shape != (RK, H, dr):
-        raise ValueError(f"q_rope must have shape {(RK, H, dr)}, got {tuple(q_rope.shape)}")
+    if rope_shape != (RK, H, dr):
+        raise ValueError(f"q_rope must have shape {(RK, H, dr)}, got {tuple(rope_shape)}")
     if out.shape != shape:
         raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
     base, P, page, stride = _pages(cache, dl + dr)
     ql, qr, o = _rows(q_latent, "q_latent"), _rows(q_rope, "q_rope"), _rows(out, "out")
-    st = lib().kda_latent_decode(
-        ql, qr, dt, R, K, _arr(q_len, i32, "q_len", (R,)), H, dl, dr, scale, base, P, page,
-        stride, _arr(block_table, i32, "block_table"), max_pages,
-        _arr(seq_len, i32, "seq_len", (R,)), o, _dt3(out),
-        _arr(lse, torch.float32, "lse", (RK, H)), _p(workspace), workspace.nbytes,
-        _arr(dev_status, i32, "dev_status"), _stream(stream))
-    _check(st, "kda_latent_decode")
+    st = (_lib or lib()).kda_latent_decode(
+        ql, qr, dt, R, K, None if q_len is None else _arr(q_len, _i32, "q_len", (R,)), H, dl, dr,
+        scale, base, P, page, stride, _arr(block_table, _i32, "block_table"), max_pages,
+        _arr(seq_len, _i32, "seq_len", (R,)), o, _dt3(out),
+        None if lse is None else _arr(lse, _f32t, "lse", (RK, H)), _p(workspace), workspace.nbytes,
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_latent_decode")
 
 
 def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, *, scale=1.0, flags=0, lse=None,
@@ -531,30 +538,33 @@ def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, *, scale=1.0, flag
     """Expanded latent attention of packed sequences (see include/kda.h).  q [Tq, H, 192],
     k_nope and v [Tk, H, 128] and out [Tq, H, 128] may be strided over rows and heads;
     k_rope [Tk, 64] over rows."""
-    Tq, H, _ = q.shape
-    Tk, _, dn = k_nope.shape
-    dr, dv = k_rope.shape[1], v.shape[2]
-    if k_rope.shape[0] != Tk:
-        raise ValueError(f"k_rope must have {Tk} rows, got {k_rope.shape[0]}")
+    Tq, H, dq = q.shape
+    k_shape, v_shape, out_shape = k_nope.shape, v.shape, out.shape
+    Tk, _, dn = k_shape
+    rope_rows, dr = k_rope.shape
+    dv = v_shape[2]
+    if dq != dn + dr or k_shape[1] != H or v_shape != (Tk, H, dv) or out_shape != (Tq, H, dv):
+        for name, t, shape in (("q", q, (Tq, H, dn + dr)), ("k_nope", k_nope, (Tk, H, dn)),
+                               ("v", v, (Tk, H, dv)), ("out", out, (Tq, H, dv))):
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if rope_rows != Tk:
+        raise ValueError(f"k_rope must have {Tk} rows, got {rope_rows}")
     krs, cs = k_rope.stride()
-    if Tk and cs != 1:
+    if cs != 1 and Tk:
         raise ValueError("k_rope needs contiguous rows")
     dt = _one_dtype("queries, keys and values", q, k_nope, k_rope, v)
-    for name, t, shape in (("q", q, (Tq, H, dn + dr)), ("k_nope", k_nope, (Tk, H, dn)),
-                           ("v", v, (Tk, H, dv)), ("out", out, (Tq, H, dv))):
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     qd, kd, vd, od = _rows(q, "q"), _rows(k_nope, "k_nope"), _rows(v, "v"), _rows(out, "out")
     if not k_rope.is_cuda:
         raise ValueError("libkda takes CUDA tensors")
     N = cu_q.shape[0] - 1
-    i32 = torch.int32
-    st = lib().kda_latent_prefill(
-        qd, kd, k_rope.data_ptr(), krs if Tk > 1 else dr, vd, dt, _arr(cu_q, i32, "cu_q"),
-        _arr(cu_k, i32, "cu_k", (N + 1,)), N, Tq, Tk, H, dn, dr, dv, scale, flags, od, _dt3(out),
-        _arr(lse, torch.float32, "lse", (Tq, H)), _arr(dev_status, i32, "dev_status"),
-        _stream(stream))
-    _check(st, "kda_latent_prefill")
+    st = (_lib or lib()).kda_latent_prefill(
+        qd, kd, k_rope.data_ptr(), krs if Tk > 1 else dr, vd, dt, _arr(cu_q, _i32, "cu_q"),
+        _arr(cu_k, _i32, "cu_k", (N + 1,)), N, Tq, Tk, H, dn, dr, dv, scale, flags, od, _dt3(out),
+        None if lse is None else _arr(lse, _f32t, "lse", (Tq, H)),
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_latent_prefill")
 
 
 def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, top_logprobs=None,
@@ -568,14 +578,17 @@ def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, t
         raise ValueError("logits needs contiguous rows")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    f32, i32 = torch.float32, torch.int32
-    top = 0 if top_ids is None else top_ids.shape[1]
-    ids, tl = _arr(top_ids, i32, "top_ids", (R, top)), _arr(top_logprobs, f32, "top_logprobs", (R, top))
+    top, ids, tl = 0, None, None
+    if top_ids is not None:
+        top = top_ids.shape[1]
+        ids = _arr(top_ids, _i32, "top_ids", (R, top))
+        tl = _arr(top_logprobs, _f32t, "top_logprobs", (R, top))
     if not logits.is_cuda:
         raise ValueError("libkda takes CUDA tensors")
-    st = lib().kda_token_logprobs(
+    st = (_lib or lib()).kda_token_logprobs(
         logits.data_ptr(), rs if R > 1 else V, _dt3(logits), R, V,
-        _arr(tokens, i32, "tokens", (R,)), _arr(logprob, f32, "logprob", (R,)),
-        _arr(entropy, f32, "entropy", (R,)), top, ids, tl,
-        _arr(dev_status, i32, "dev_status"), _stream(stream))
-    _check(st, "kda_token_logprobs")
+        _arr(tokens, _i32, "tokens", (R,)), _arr(logprob, _f32t, "logprob", (R,)),
+        None if entropy is None else _arr(entropy, _f32t, "entropy", (R,)), top, ids, tl,
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_token_logprobs")

@@ -97,8 +97,9 @@ extern "C" kda_status kda_latent_append(const void* kv, int64_t kv_stride, const
     KDA_REQUIRE(kv_stride % 8 == 0 && kv_stride >= kLatentRow, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
     if (T == 0) return KDA_OK;
-    const void* ptrs[] = {kv, slot, cache};
+    const void* ptrs[] = {kv, slot};
     for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE((P == 0 || cache != nullptr) && aligned16(cache), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(aligned16(weight) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
     const AppendArgs a{static_cast<const uint16_t*>(kv), kv_stride, static_cast<const uint16_t*>(weight), eps, T,
                        slot, static_cast<uint16_t*>(cache), P, page_size, page_stride, dev_status};

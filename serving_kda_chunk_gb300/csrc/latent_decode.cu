@@ -922,12 +922,17 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
     if (R == 0 || K == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(q_latent) && rows_ok(q_rope) && rows_ok(out), KDA_ERR_INVALID_ARG);
-    const void* ptrs[] = {cache, block_table, seq_len, workspace};
+    const void* ptrs[] = {seq_len, workspace};
     for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);
+    // an empty cache or table is never read: it may have no address
+    KDA_REQUIRE(P == 0 || cache != nullptr, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(max_pages == 0 || block_table != nullptr, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(aligned16(cache) && aligned16(block_table), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(aligned16(q_len) && aligned16(lse) && aligned16(dev_status), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(ws_bytes >= kda_latent_decode_workspace_size(R, K, H), KDA_ERR_INVALID_ARG);
     const int n = tile_rows((int64_t)K * H);
     const int box = lowbit_box(page_size, n == 64 ? 16 : kMaxTile);  // divides the tile as well (48 or 64 tokens)
+    const void* base = P > 0 ? cache : q_latent->base;  // a map wants an address, though no page is loaded
     CUtensorMap map[2];
     // the cache as (channel of 64, row, 64-channel column, page): one box is `box` rows of one page
     // and one column (a 128-byte swizzle row), or with a whole tile of rows a pair of columns
@@ -935,8 +940,8 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     const cuuint64_t strides[3] = {kLatentRow * 2, 128, (cuuint64_t)page_stride * 2};
     const cuuint32_t boxes[4] = {64, (cuuint32_t)box, box == kMaxTile ? 2u : 1u, 1};
     const cuuint32_t rope_boxes[4] = {64, (cuuint32_t)box, 1, 1};
-    KDA_REQUIRE(encode_16bit(&map[0], in_dtype, 4, cache, dims, strides, boxes), KDA_ERR_CUDA);
-    KDA_REQUIRE(encode_16bit(&map[1], in_dtype, 4, cache, dims, strides, rope_boxes), KDA_ERR_CUDA);
+    KDA_REQUIRE(encode_16bit(&map[0], in_dtype, 4, base, dims, strides, boxes), KDA_ERR_CUDA);
+    KDA_REQUIRE(encode_16bit(&map[1], in_dtype, 4, base, dims, strides, rope_boxes), KDA_ERR_CUDA);
     DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
                  block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
                  out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, false, nullptr, nullptr, dev_status};

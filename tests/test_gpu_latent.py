@@ -267,6 +267,18 @@ def test_decode_reports_bad_lengths_and_query_lengths():
     assert (out[2:6] == 0).all() and torch.isinf(lse[2:6]).all()
 
 
+def test_decode_with_an_empty_table_or_cache():
+    d = Decode([0, 0], 2, 6, 16, seed=17)
+    out, lse, st = d.run(table=torch.empty(2, 0, dtype=torch.int32, device="cuda"))
+    assert st == 0 and (out == 0).all() and torch.isinf(lse).all()
+    empty = torch.empty(0, 16, W, dtype=d.dt, device="cuda")
+    out, lse, st = d.run(cache=empty, table=i32([[0, 0], [1, 1]]), seq_len=i32([20, 0]))
+    assert st == kda.KDA_DEV_BAD_SLOT and (out == 0).all() and torch.isinf(lse).all()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_latent_append(torch.zeros(2, W, dtype=d.dt, device="cuda"), empty, i32([-1, 0]), dev_status=st)
+    assert int(st) == kda.KDA_DEV_BAD_SLOT
+
+
 def test_decode_masks_the_tokens_of_a_bad_page():
     d = Decode([200, 90], 1, 10, 16, seed=11)
     for bad in (-1, d.cache.shape[0], 2 ** 31 - 1):
