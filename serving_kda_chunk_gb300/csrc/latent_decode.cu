@@ -122,11 +122,11 @@ template <int N>
 __device__ __forceinline__ int tiles_of(int len) {
     return len > 0 ? (len + DecLayout<N>::T - 1) / DecLayout<N>::T : 1;
 }
-// Turning to another request (its queries in, the last one's results out) takes as long as this many
-// tiles: every request counts so much longer in the line of work that is cut into equal ranges.  With
-// 256 requests of about 64 tiles the slowest CTA was 4 % behind the mean without it.  Not with few
-// tiles a CTA, where a tile more on one of them would cost more.
-constexpr int turn_of(int N, long long tiles, int ctas) { return tiles < 8ll * ctas ? 0 : N == 64 ? 3 : 2; }
+// Turning to another request (its queries in, the last one's results out) takes as long as some tiles:
+// every request counts so much longer in the line of work that is cut into equal ranges (256 requests of
+// about 64 tiles 209 -> 207 us, four of 2048 tiles 110 -> 108.5 us; 64 requests of 7 positions 318 us without,
+// 311.5 with 3 tiles, 307 with 6).  Not with few tiles a CTA, where a tile more on one of them would cost more.
+constexpr int turn_of(int N, long long tiles, int ctas) { return tiles < 8ll * ctas ? 0 : N == 64 ? 6 : 2; }
 
 // The walk over a CTA's range: next() gives the tiles [j0, j1) of request r, row tile rt.
 template <int N>
