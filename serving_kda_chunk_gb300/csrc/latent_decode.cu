@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 did = true;
             }
             if (more_s) {
-                bool ready = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
-                if (s_it > 0) ready = ready && mbar_test(bar(L::B_SFREE), (s_it - 1) & 1);
-                if (first_s) ready = ready && mbar_test(bar(L::B_Q), segs & 1);
-                if (__all_sync(~0u, ready)) {
+                const bool t0 = mbar_test(bar(L::B_RFULL + r_slot), r_ph);  // loaded last
+                const bool t1 = mbar_test(bar(L::B_SFREE), (s_it & 1) ^ 1);  // free at first
+                const bool t2 = mbar_test(bar(L::B_Q), (segs & 1) ^ !first_s);
+                if (__all_sync(~0u, t0 & t1 & t2)) {
                     if (first_s) ++segs;
                     const uint32_t d = tm + L::TM_S;
 #pragma unroll
@@ -460,9 +460,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     did = true;
                 }
             }
-            // polls of some tens of cycles: it gives up after about a second without work
-            idle = did ? 0 : idle + 1;
-            stop = __any_sync(~0u, dead || idle > (1u << 23) || ctrl[1]);
+            // polls of some tens of cycles: it gives up after about a second without work.  Nothing else is asked
+            // after a product: this warp's instructions between products bound a tile of N = 64 (votes on
+            // dead and ctrl each time: 307 us for 64 x 7 positions instead of 288).
+            if (did) {
+                idle = 0;
+            } else {
+                ++idle;
+                stop = __any_sync(~0u, dead || idle > (1u << 23) || ctrl[1]);
+            }
         }
         if (stop && lane == 0) {
             ctrl[1] = 1;
