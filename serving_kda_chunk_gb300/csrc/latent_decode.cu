@@ -69,7 +69,7 @@ struct DecodeArgs {
 // reads 2 KiB of shared memory instead of 6 (a product of M = 128, N = 64, K = 16 is bound by that:
 // 44 cycles against 32), and the shared memory saved holds a third tile in flight.  With N = 64 three
 // tiles fit at 48 tokens each: two and a quarter of 64 did not cover the chain load, S, softmax, O of a
-// tile (64 x 7 positions of about 6000 tokens, 32 heads: 310 us with 48, 329 with 64).
+// tile (64 x 7 positions of about 6000 tokens, 32 heads: 310 us with 48, 329 with 64, before later steps).
 template <int N>
 struct DecLayout {
     static constexpr int T = N == 64 ? 48 : 64;       // tokens a tile
