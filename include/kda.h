@@ -485,6 +485,8 @@ kda_status kda_latent_append(const void* kv, int64_t kv_stride, const void* weig
  *                 512 in_dtype;  q_rope: the same rows, 64 channels.
  *   q_len       : [R] int32 in [0, K] or NULL (= K); outside: request skipped,
  *                 KDA_DEV_BAD_ACCEPT.  Rows t >= q_len: zero output, lse -inf.
+ *                 With q_len 0 no page of the request is read (a padding
+ *                 request's table and cache may hold anything).
  *   block_table : [R, max_pages] int32: token p of request r lies in page
  *                 block_table[r][p / page_size].  Entries past the request's
  *                 last token are never read.  An entry outside [0, P): its

@@ -102,7 +102,8 @@ struct DecLayout {
     static_assert(BARS <= 40 && SMEM <= 232448 && TM_Q + 32 * QT <= 512, "shared memory and TMEM plan");
 };
 
-// Length and query count of a request as the kernel uses them: an invalid one has none.
+// Length and query count of a request as the kernel uses them: an invalid one has none.  One without
+// query positions has no length either: nothing of what its table and pages hold is read.
 __device__ __forceinline__ int request(const DecodeArgs& a, int r, int& ql, int& err) {
     int len = a.seq_len[r];
     ql = a.q_len ? a.q_len[r] : a.K;
@@ -113,9 +114,9 @@ __device__ __forceinline__ int request(const DecodeArgs& a, int r, int& ql, int&
     }
     if (ql < 0 || ql > a.K) {
         err |= KDA_DEV_BAD_ACCEPT;
-        ql = len = 0;
+        ql = 0;
     }
-    return len;
+    return ql > 0 ? len : 0;
 }
 // token tiles of a request; one without tokens takes one (empty) tile, for its zero rows
 template <int N>
