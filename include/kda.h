@@ -434,12 +434,13 @@ kda_status kda_slot_copy_noalloc(const kda_pool_desc* pools, int32_t n_pools,
  *     s_p = scale (q_latent . c_p + q_rope . kr_p),  o = sum_p softmax(s)_p c_p.
  * lse is the natural log of sum_p exp(s_p): two results over disjoint keys
  * merge as o = sum_i e^{lse_i - lse} o_i, lse = log sum_i e^{lse_i}.
- * A row whose mask leaves no key gets a zero output and lse = -inf.
+ * A row whose mask leaves no key gets a zero output and lse = -inf, whatever the
+ * keys that other rows see hold.
  * Types: bf16 or fp16 (products on the tensor cores, fp32 accumulation, softmax
  * in fp32; the weights are rounded once to the input type for the product with
  * the values).  Masked positions are never read into a result, whatever bits
- * lie there, with one exception: a key that another row of the same sequence
- * may see has to be finite.
+ * lie there, with one exception: to a row that sees some keys, a key that only
+ * other rows of the same sequence see has to be finite.
  *
  * The cache is paged: [P, page_size, 576], a row c then kr; page i starts at
  * cache + i * page_stride elements.  page_size is a multiple of 8, page_stride a

@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             if (t < N) {
 #pragma unroll
                 for (int k = 1; k < L::REP; ++k) l += pmax[(it & 1) * 128 + row + k * N];
-                rowf[row] = l > 0.f ? 1.f / l : 0.f;
+                rowf[row] = l == 0.f ? 0.f : 1.f / l;
                 rowo[row] = ((int64_t)g.cr * a.K + f / a.H) * a.out_rs + (f % a.H) * a.out_hs;
                 const float m2 = m[0] == -inf ? -inf : m[0] * a.c;
                 if (!whole) {
@@ -736,7 +736,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 emit([&](int, int64_t at, int ch, float x, float f) { o[at + ch] = x * f; });
             }
             fence_before();
-            bar_named(1, 128);  // rowf read by all before the next segment writes it
+            // rowf read by all before the next segment writes it.  A row without keys gets its zeros here and
+            // not from its factor: beside a NaN or infinity that other rows see, its sums are NaN (a choice
+            // for each element above cost 1 to 2 % of the call).
+            if (bar_named_or(1, 128, whole && t < rows && rowf[t & (N - 1)] == 0.f)) {
+                for (int n = 0; n < rows; ++n) {
+                    if (rowf[n] != 0.f) continue;
+                    for (int c = t; c < kLatent; c += 128)
+                        if (a.out_dt == KDA_F32)
+                            static_cast<float*>(a.out)[rowo[n] + c] = 0.f;
+                        else
+                            static_cast<uint16_t*>(a.out)[rowo[n] + c] = 0;
+                }
+                bar_named(1, 128);
+            }
         }
     }
     fence_before();
@@ -795,9 +808,10 @@ __device__ __forceinline__ void fma4(float4& o, float f, float4 x) {
     o.w = fmaf(f, x.w, o.w);
 }
 __device__ __forceinline__ void put_row(const DecodeArgs& a, const Split& u, int f, float2 ml, float4 o, int t) {
-    const float il = ml.y > 0.f ? 1.f / ml.y : 0.f;
+    const float il = ml.y == 0.f ? 0.f : 1.f / ml.y;
     const int tt = f / a.H, h = f - tt * a.H;
     const int64_t orow = (int64_t)u.r * a.K + tt;
+    if (il == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // no key, as in decode_kernel
     store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il), a.out_dt);
     if (t == 0 && a.lse != nullptr)
         a.lse[orow * a.H + h] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994531f : -__int_as_float(0x7f800000);

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 wait(PB_O + q, (done - 1) & 1);
                 fence_after();
             }
-            const float il = l > 0.f ? 1.f / l : 0.f;
+            const float il = 1.f / l;
             const int64_t orow = (int64_t)u.q0 + row;
             if (row < u.Lq && a.lse != nullptr)
                 a.lse[orow * a.H + u.h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
@@ -568,8 +568,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     float o[32];
                     if (my_tiles > 0) {
                         ld32(to + 32 * b, o);
+                        // a row without keys is zero by choice, not by its factor: beside a NaN or infinity
+                        // that other rows see, its sums are NaN
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= il;
+                        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * il;
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
