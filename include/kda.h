@@ -436,6 +436,7 @@ kda_status kda_slot_copy_noalloc(const kda_pool_desc* pools, int32_t n_pools,
  * merge as o = sum_i e^{lse_i - lse} o_i, lse = log sum_i e^{lse_i}.
  * A row whose mask leaves no key gets a zero output and lse = -inf, whatever the
  * keys that other rows see hold.
+ * A row that sees a score of NaN or +inf has a NaN output and a NaN lse.
  * Types: bf16 or fp16 (products on the tensor cores, fp32 accumulation, softmax
  * in fp32; the weights are rounded once to the input type for the product with
  * the values).  Masked positions are never read into a result, whatever bits

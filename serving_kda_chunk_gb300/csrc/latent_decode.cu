@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     a.ml[(int64_t)slot * N + row] = make_float2(m2, l);
                 } else if (a.lse != nullptr && row < rows) {
                     const int tt = f / a.H, h = f - tt * a.H;
-                    a.lse[((int64_t)g.cr * a.K + tt) * a.H + h] = l > 0.f ? (m2 + log2f(l)) * 0.69314718055994531f : -inf;
+                    a.lse[((int64_t)g.cr * a.K + tt) * a.H + h] = l == 0.f ? -inf : (m2 + log2f(l)) * 0.69314718055994531f;
                 }
             }
             if (t == 0 && !whole && g.j0 == 0) {
@@ -814,7 +814,7 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, const Split& u, int
     if (il == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // no key, as in decode_kernel
     store4_as(a.out, orow * a.out_rs + h * a.out_hs + 4 * t, make_float4(o.x * il, o.y * il, o.z * il, o.w * il), a.out_dt);
     if (t == 0 && a.lse != nullptr)
-        a.lse[orow * a.H + h] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994531f : -__int_as_float(0x7f800000);
+        a.lse[orow * a.H + h] = ml.y == 0.f ? -__int_as_float(0x7f800000) : (ml.x + log2f(ml.y)) * 0.69314718055994531f;
 }
 
 template <int N, bool kSplit>

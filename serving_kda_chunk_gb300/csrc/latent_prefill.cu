@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const float il = 1.f / l;
             const int64_t orow = (int64_t)u.q0 + row;
             if (row < u.Lq && a.lse != nullptr)
-                a.lse[orow * a.H + u.h] = l > 0.f ? (m * a.c + log2f(l)) * 0.69314718055994531f : -inf;
+                a.lse[orow * a.H + u.h] = l == 0.f ? -inf : (m * a.c + log2f(l)) * 0.69314718055994531f;
             const int64_t at = orow * a.out_rs + (int64_t)u.h * a.out_hs;
             // a thread's row, whole 32-byte sectors at a time; the other query tile's products go on meanwhile
             auto emit = [&](auto put) {

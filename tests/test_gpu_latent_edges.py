@@ -62,3 +62,65 @@ def test_prefill_rows_without_keys_are_zero_beside_keys_that_are_not_finite(out_
     assert st == 0
     assert (out[:50] == 0).all() and (lse[:50] == -torch.inf).all()
     p.check((out, lse, st), skip=(0,))
+
+
+# ----------------------------------------------------------- scores that are not numbers
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,K,H", [(1, 1, 1), (70, 1, 9), (90, 2, 20), (300, 3, 30), (30000, 1, 12), (30000, 4, 16)])
+def test_decode_rows_that_see_a_nan_score_have_nan_results(n, K, H, dtype):
+    d = Decode([n, 65], K, H, 16, dtype, seed=n)
+    d.ql[0, 0, 7] = float("nan")  # every score of one row
+    out, lse, st = d.run(out_dtype=torch.float32)
+    assert st == 0 and torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0])
+    out[0, 0], lse[0, 0], d.ql[0, 0, 7] = 0, 0, 0
+    if H > 1:
+        o, z, bo, bz = d.ref(0)  # the other rows of the request
+        assert ((out[:K].double() - o).abs() <= bo + 2.0 ** -20).view(K * H, DL)[1:].all()
+        assert ((lse[:K].double() - z).abs() <= bz).view(K * H)[1:].all()
+    d.check((out, lse, st), skip=(0,))
+    # one key: every row that sees it, whichever tile or part it lies in
+    for at in {0, n // 2, n - 1}:
+        e = Decode([n, 65], K, H, 16, dtype, seed=n)
+        e.cache[e.table[0, at // 16].long(), at % 16, DL] = float("nan")  # in the rope part: no value holds it
+        out, lse, st = e.run(out_dtype=torch.float32)
+        sees = torch.tensor([at <= n - K + t for t in range(K)], device="cuda")
+        assert torch.isnan(out[:K][sees]).all() and torch.isnan(lse[:K][sees]).all()
+        assert torch.isfinite(out[:K][~sees]).all()
+        e.check((out, lse, st), skip=(0,))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prefill_rows_that_see_a_nan_score_have_nan_results(dtype):
+    p = Prefill([300, 40], [700, 40], 2, dtype, seed=5)
+    p.q[70, 1, 3] = float("nan")
+    p.kr[650] = float("nan")  # seen by the rows from 250 on
+    out, lse, st = p.run()
+    assert st == 0
+    bad = torch.zeros(300, 2, dtype=torch.bool, device="cuda")
+    bad[70, 1] = True
+    bad[250:] = True
+    assert torch.equal(torch.isnan(out[:300]), bad[..., None].expand(300, 2, 128))
+    assert torch.equal(torch.isnan(lse[:300]), bad)
+    p.check((out, lse, st), skip=(0,))
+
+
+@pytest.mark.parametrize("n,K,H", [(70, 1, 9), (300, 3, 30), (30000, 1, 12)])
+def test_decode_rows_that_see_an_infinite_score(n, K, H):
+    d = Decode([n], K, H, 16, seed=n)
+    at = n // 2
+    d.cache[d.table[0, at // 16].long(), at % 16, DL] = float("inf")  # scores of +inf or -inf, by the query's sign
+    up = (d.qr[..., 0] > 0) & (torch.arange(K, device="cuda") + n - K >= at)[:, None]
+    assert up.any() and not up.all()
+    out, lse, st = d.run()
+    assert st == 0
+    assert torch.equal(torch.isnan(out), up[..., None].expand(K, H, DL)) and torch.equal(torch.isnan(lse), up)
+
+
+def test_prefill_rows_that_see_an_infinite_score():
+    p = Prefill([300], [700], 2, seed=6)
+    p.kr[500, 0] = float("inf")
+    out, lse, _ = p.run()
+    up = (p.q[..., 128] > 0) & (torch.arange(300, device="cuda") + 400 >= 500)[:, None]
+    assert torch.equal(torch.isnan(out), up[..., None].expand(300, 2, 128)) and torch.equal(torch.isnan(lse), up)
