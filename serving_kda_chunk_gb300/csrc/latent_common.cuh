@@ -53,6 +53,22 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A running sum of weights, a tile's at a time, with what its roundings left out (the exact error of an
+// addition): a plain fp32 sum over 10^5 keys behind one far larger weight drifts by 2^-14, alike in each step.
+struct WeightSum {
+    float s = 0.f, e = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, b = t - s;
+        e += (s - (t - b)) + (x - b);
+        s = t;
+    }
+    __device__ __forceinline__ void scale(float f) {
+        s *= f;
+        e *= f;
+    }
+    __device__ __forceinline__ float total() const { return s + e; }
+};
+
 // Four consecutive fp32 results (index i % 4 == 0) rounded into an output of type dt.
 __device__ __forceinline__ void store4_as(void* p, int64_t i, float4 x, int dt) {
     if (dt == KDA_F32)

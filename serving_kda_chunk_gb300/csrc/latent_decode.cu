@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             float m[NR];
 #pragma unroll
             for (int q = 0; q < NR; ++q) m[q] = -inf;
-            float l = 0.f;  // over this thread's columns
+            WeightSum sum;  // over this thread's columns
             int last = -1;  // last token this thread's row sees
             const int f = g.crt * N + row;
             if (f < a.K * a.H) {
@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     s[i] = ex2(fmaf(s[i], a.c, -mc));
                     ls[i & 1] += s[i];
                 }
-                l = fmaf(l, f_old, ls[0] + ls[1]);
+                sum.scale(f_old);
+                sum.add(ls[0] + ls[1]);
                 if (__any_sync(~0u, need)) {  // the same in all four warps
                     if (t < N) rowf[row] = f_old;
                     bar_named(1, 128);
@@ -678,6 +679,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const bool whole = g.j0 == 0 && g.j1 == g.n;
             const int slot = 2 * (int)blockIdx.x + (g.j0 == 0);
             const int rows = min(N, a.K * a.H - g.crt * N);
+            float l = sum.total();
             pmax[(it & 1) * 128 + t] = l;  // the buffer that the last tile did not use
             bar_named(1, 128);
             if (t < N) {

@@ -124,3 +124,72 @@ def test_prefill_rows_that_see_an_infinite_score():
     out, lse, _ = p.run()
     up = (p.q[..., 128] > 0) & (torch.arange(300, device="cuda") + 400 >= 500)[:, None]
     assert torch.equal(torch.isnan(out), up[..., None].expand(300, 2, 128)) and torch.equal(torch.isnan(lse), up)
+
+
+# ----------------------------------------------------------- fp16 weights far below the largest
+#
+# One key scores `drop` above the others (in powers of two) and has value 0, the n others score 0 and
+# have value 1.  The output is z / (1 + z) with z = n 2^-drop.  An fp16 weight (scaled by 2^7) is off by
+# at most 2^-11 of it or, below the normal range, by 2^-25 / 2^7 = 2^-32 of the row's largest.  A score
+# is one product of exact operands with a factor that is 2^-23 off, 2^-16 with the exponential's own
+# error; the n / 16 sums of a product are 2^-23 off each.
+
+DROPS = [12.0, 17.25, 21.375, 25.125]  # exact in bf16
+
+
+def sink_check(out, lse, n, drop, dtype):
+    z = n * 2.0 ** -drop
+    o = z / (1 + z)
+    lim = (UNIT[TYPES[dtype]] + 2.0 ** -15 + n / 16 * 2.0 ** -23) * o
+    if dtype == "f16":
+        lim += n * 2.0 ** -32 / (1 + z)
+    err = (out.double() - o).abs().max().item()
+    assert err <= lim, (err, lim, o)
+    want = drop * np.log(2) + np.log1p(z)
+    err = (lse.double() - want).abs().max().item()
+    assert err <= 2.0 ** -16 + 2.0 ** -20 * (1 + want), (err, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("R,n", [(304, 2048), (1, 131072), (152, 131072)])
+@pytest.mark.parametrize("H", [3, 24, 40])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("drop", DROPS)
+def test_decode_keeps_small_weights_beside_a_large_one(drop, where, H, R, n, dtype):
+    page, dt = 64, TYPES[dtype]
+    pages = n // page + 1
+    cache = torch.zeros(pages, page, W, dtype=dt, device="cuda")
+    x = cache.view(-1, W)
+    x[: n + 1, :DL] = 1
+    sink = 0 if where == "first" else n
+    x[sink, :DL] = 0
+    x[sink, DL] = drop
+    table = torch.arange(pages, device="cuda", dtype=torch.int32).expand(R, pages).contiguous()
+    ql, qr = torch.zeros(R, H, DL, dtype=dt, device="cuda"), torch.zeros(R, H, DR, dtype=dt, device="cuda")
+    qr[..., 0] = 1
+    out, lse = torch.empty(R, H, DL, device="cuda"), torch.empty(R, H, device="cuda")
+    ws = torch.empty(kda.kda_latent_decode_workspace_size(R, 1, H), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_latent_decode(ql, qr, cache, table, i32([n + 1] * R), out, ws, scale=float(np.log(2)), lse=lse,
+                          dev_status=st)
+    assert int(st) == 0
+    sink_check(out, lse, n, drop, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("drop", DROPS)
+def test_prefill_keeps_small_weights_beside_a_large_one(drop, where, dtype):
+    n = 131072
+    p = Prefill([3], [n + 1], 2, dtype, seed=1)
+    sink = 0 if where == "first" else n
+    p.q.zero_()
+    p.q[..., 128] = 1
+    p.kr.zero_()
+    p.kr[sink, 0] = drop
+    p.kv.zero_()
+    p.kv[..., 128:] = 1
+    p.kv[sink, :, 128:] = 0
+    out, lse, st = p.run(out_dtype=torch.float32, scale=float(np.log(2)), flags=kda.KDA_LATENT_FULL)
+    assert st == 0
+    sink_check(out, lse, n, drop, dtype)
