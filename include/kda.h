@@ -439,9 +439,10 @@ kda_status kda_slot_copy_noalloc(const kda_pool_desc* pools, int32_t n_pools,
  * A row that sees a score of NaN or +inf has a NaN output and a NaN lse.
  * Types: bf16 or fp16 (products on the tensor cores, fp32 accumulation, softmax
  * in fp32; the weights are rounded once to the input type for the product with
- * the values).  Masked positions are never read into a result, whatever bits
- * lie there, with one exception: to a row that sees some keys, a key that only
- * other rows of the same sequence see has to be finite.
+ * the values; fp16 weights below 2^-21 of the row's largest lose bits and below
+ * 2^-32 vanish, bf16 ones do not).  Masked positions are never read into a
+ * result, whatever bits lie there, with one exception: to a row that sees some
+ * keys, a key that only other rows of the same sequence see has to be finite.
  *
  * The cache is paged: [P, page_size, 576], a row c then kr; page i starts at
  * cache + i * page_stride elements.  page_size is a multiple of 8, page_stride a

@@ -69,6 +69,16 @@ struct WeightSum {
     __device__ __forceinline__ float total() const { return s + e; }
 };
 
+// Softmax weights are 2^(c s - b), b = log2_base(m): the row's running maximum m in log2 units, m being up to
+// 8 behind the largest score.  For fp16 products b is 7 lower, so that weights end at 2^15 (65504 is the
+// largest fp16) and begin at 2^-32 of the row's largest: without it they began at 2^-25, and 10^5 keys some
+// 25 below one other lost all their weight in the output but not in the sum.  bf16 has fp32's exponents.
+// The sum of the weights has the same base, so lse = (b + log2 sum) ln 2.
+template <int DT>
+__device__ __forceinline__ float log2_base(float m, float c) {
+    return DT == KDA_F16 ? fmaf(m, c, -7.f) : m * c;
+}
+
 // Four consecutive fp32 results (index i % 4 == 0) rounded into an output of type dt.
 __device__ __forceinline__ void store4_as(void* p, int64_t i, float4 x, int dt) {
     if (dt == KDA_F32)

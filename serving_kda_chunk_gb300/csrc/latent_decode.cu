@@ -9,7 +9,7 @@
 // O stays transposed in TMEM (lane = value channel): 512 fp32 channels of 128 rows would take all
 // 512 columns, transposed they take 4 N, and few query rows waste no tensor-core rows in this
 // product.  The tile is used as it lies in shared memory: K-major for S, MN-major for V^T.
-// m moves only when a row's maximum exceeds it by 8 (a factor of 256, far inside fp32 and fp16):
+// m moves only when a row's maximum exceeds it by 8 (a factor of 256; fp16 has room for it, see log2_base):
 // rescaling O is then rare, and exact up to fp32 rounding.
 //
 // Work: all (row tile, request, token tile) triples in one line, cut into equal ranges, one a CTA
@@ -57,7 +57,7 @@ struct DecodeArgs {
     // whose first part, but not the last, it holds.
     int4* meta;
     bool by_unit;
-    float2* ml;     // [2 CTAs][N] (m in log2 units, l)
+    float2* ml;     // [2 CTAs][N] (log2_base of m, l)
     float* part;    // [2 CTAs][N][512]
     int32_t* dev_status;
 };
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         need = true;
                     }
                 }
-                const float mc = m[0] == -inf ? 0.f : m[0] * a.c;
+                const float mc = m[0] == -inf ? 0.f : log2_base<DT>(m[0], a.c);
                 float ls[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < CW; ++i) {
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int k = 1; k < L::REP; ++k) l += pmax[(it & 1) * 128 + row + k * N];
                 rowf[row] = l == 0.f ? 0.f : 1.f / l;
                 rowo[row] = ((int64_t)g.cr * a.K + f / a.H) * a.out_rs + (f % a.H) * a.out_hs;
-                const float m2 = m[0] == -inf ? -inf : m[0] * a.c;
+                const float m2 = m[0] == -inf ? -inf : log2_base<DT>(m[0], a.c);
                 if (!whole) {
                     a.ml[(int64_t)slot * N + row] = make_float2(m2, l);
                 } else if (a.lse != nullptr && row < rows) {

@@ -12,8 +12,8 @@
 // takes (three tiles in flight beside the 96 KiB of queries; alone a CTA has room for one and a half,
 // and its products wait for their keys) and the operand bytes an MMA reads.
 // The two query tiles take turns: while the tensor cores work on one, the four warps of the other do
-// its exponentials.  m moves only when a row's maximum exceeds it by 8 (a factor of 256, far inside
-// fp32 and fp16), so that O is rarely rescaled.
+// its exponentials.  m moves only when a row's maximum exceeds it by 8 (a factor of 256; fp16 has room
+// for it, see log2_base), so that O is rarely rescaled.
 //
 // Roles: warps 0-3 and 4-7 softmax of query tile 0 and 1 (and its results), warp 8 loads by TMA (the
 // queries, rings of K and V tiles), warp 9 of the first CTA issues the MMAs of both.  Barriers that the
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     }
                     sum->scale(f);
                 }
-                const float mc = m == -inf ? 0.f : m * a.c;
+                const float mc = m == -inf ? 0.f : log2_base<DT>(m, a.c);
                 const float2 cc = make_float2(a.c, a.c), nm = make_float2(-mc, -mc);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const float l = sum->total(), il = 1.f / l;
             const int64_t orow = (int64_t)u.q0 + row;
             if (row < u.Lq && a.lse != nullptr)
-                a.lse[orow * a.H + u.h] = l == 0.f ? -inf : (m * a.c + log2f(l)) * 0.69314718055994531f;
+                a.lse[orow * a.H + u.h] = l == 0.f ? -inf : (log2_base<DT>(m, a.c) + log2f(l)) * 0.69314718055994531f;
             const int64_t at = orow * a.out_rs + (int64_t)u.h * a.out_hs;
             // a thread's row, whole 32-byte sectors at a time; the other query tile's products go on meanwhile
             auto emit = [&](auto put) {

@@ -150,7 +150,7 @@ def sink_check(out, lse, n, drop, dtype):
     assert err <= 2.0 ** -16 + 2.0 ** -20 * (1 + want), (err, want)
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("R,n", [(304, 2048), (1, 131072), (152, 131072)])
 @pytest.mark.parametrize("H", [3, 24, 40])
 @pytest.mark.parametrize("where", ["first", "last"])
@@ -176,7 +176,7 @@ def test_decode_keeps_small_weights_beside_a_large_one(drop, where, H, R, n, dty
     sink_check(out, lse, n, drop, dtype)
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("where", ["first", "last"])
 @pytest.mark.parametrize("drop", DROPS)
 def test_prefill_keeps_small_weights_beside_a_large_one(drop, where, dtype):
