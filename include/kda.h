@@ -434,6 +434,7 @@ kda_status kda_slot_copy_noalloc(const kda_pool_desc* pools, int32_t n_pools,
  *     s_p = scale (q_latent . c_p + q_rope . kr_p),  o = sum_p softmax(s)_p c_p.
  * lse is the natural log of sum_p exp(s_p): two results over disjoint keys
  * merge as o = sum_i e^{lse_i - lse} o_i, lse = log sum_i e^{lse_i}.
+ * scale is any finite number (else KDA_ERR_INVALID_ARG).
  * A row whose mask leaves no key gets a zero output and lse = -inf, whatever the
  * keys that other rows see hold.
  * A row that sees a score of NaN or +inf has a NaN output and a NaN lse.

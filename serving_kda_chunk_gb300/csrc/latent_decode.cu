@@ -944,6 +944,7 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     KDA_REQUIRE((int64_t)max_pages * page_size < (1ll << 31) - kMaxTile && P < (1ll << 31), KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE(page_stride % 8 == 0 && page_stride >= (int64_t)page_size * kLatentRow, KDA_ERR_INVALID_ARG);
     if (R == 0 || K == 0) return KDA_OK;
+    KDA_REQUIRE(isfinite(scale), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(rows_ok(q_latent) && rows_ok(q_rope) && rows_ok(out), KDA_ERR_INVALID_ARG);
     const void* ptrs[] = {seq_len, workspace};
     for (const void* p : ptrs) KDA_REQUIRE(p != nullptr && aligned16(p), KDA_ERR_INVALID_ARG);

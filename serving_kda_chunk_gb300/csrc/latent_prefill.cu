@@ -649,6 +649,7 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     const int64_t blocks = ((int64_t)Tq / kQBlock + N) * H;
     KDA_REQUIRE(blocks < (1ll << 30) && Tk < (1 << 30) && Tq < (1 << 30), KDA_ERR_UNSUPPORTED);
     if (N == 0 || Tq == 0) return KDA_OK;
+    KDA_REQUIRE(isfinite(scale), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(rows_ok(q) && rows_ok(out), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(k_nope != nullptr && v != nullptr, KDA_ERR_INVALID_ARG);
     if (Tk > 0) {

@@ -1,0 +1,35 @@
+"""A scale that is not finite is refused on the host (a NaN would pass for a scale of 0)."""
+import ctypes
+
+import pytest
+
+FAKE = 1 << 20  # 16-byte aligned, never dereferenced: the scale is refused first
+OK, INVALID, BF16 = 0, 1, 0
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import serving_kda_chunk_gb300 as kda
+
+    return kda
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+def test_latent_calls_refuse_a_scale_that_is_not_finite(kda, scale):
+    L = kda.lib()
+    d = ctypes.byref(kda.RowsDesc(FAKE, 512, 512))
+    size = L.kda_latent_decode_workspace_size(4, 2, 8)
+
+    def decode(R):
+        return L.kda_latent_decode(d, d, BF16, R, 2, None, 8, 512, 64, scale, FAKE, 8, 16, 16 * 576, FAKE, 4, FAKE, d,
+                                   BF16, None, FAKE, size, None, None)
+
+    def prefill(N):
+        return L.kda_latent_prefill(d, d, FAKE, 64, d, BF16, FAKE, FAKE, N, 10, 10, 4, 128, 64, 128, scale, 0, d, BF16,
+                                    None, None, None)
+
+    assert decode(4) == INVALID and prefill(2) == INVALID
+    assert decode(0) == OK and prefill(0) == OK  # nothing to do
