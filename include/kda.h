@@ -581,6 +581,22 @@ kda_status kda_token_logprobs(const void* logits, int64_t row_stride, kda_dtype 
 kda_status kda_selftest_bounded_wait(uint32_t polls, int32_t* dev_status,
                                      unsigned long long* cycles, void* stream);
 
+/*
+ * kda_selftest_latent_decode_give_up -- diagnostic: kda_latent_decode in which
+ * one wait counts as run out: block `block` of the grid stops before its load
+ * number `load` (4 a tile of 64 tokens, counted over the block's tiles).  The
+ * block's other waits then run out by themselves (about a second), it waits for
+ * the loads it has in flight, and KDA_DEV_TIMEOUT is set.  bf16 and K * H <= 16
+ * only; a block or load that the call does not reach leaves it as it is.
+ */
+kda_status kda_selftest_latent_decode_give_up(
+    const kda_rows_desc* q_latent, const kda_rows_desc* q_rope, kda_dtype in_dtype, int32_t R,
+    int32_t K, const int32_t* q_len, int32_t H, int32_t d_latent, int32_t d_rope, float scale,
+    const void* cache, int64_t P, int32_t page_size, int64_t page_stride,
+    const int32_t* block_table, int32_t max_pages, const int32_t* seq_len,
+    const kda_rows_desc* out, kda_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
+    int32_t* dev_status, void* stream, int32_t block, int32_t load);
+
 const char* kda_status_string(kda_status s);
 
 /* Version of the library ABI (major * 100 + minor). */

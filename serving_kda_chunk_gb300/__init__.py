@@ -120,6 +120,8 @@ def lib():
         L.kda_latent_decode.argtypes = [rows, rows, ctypes.c_int, i32, i32, vp, i32, i32, i32, f32,
                                         vp, i64, i32, i64, vp, i32, vp, rows, ctypes.c_int, vp, vp,
                                         sz, vp, vp]
+        L.kda_selftest_latent_decode_give_up.argtypes = L.kda_latent_decode.argtypes + [i32, i32]
+        L.kda_selftest_latent_decode_give_up.restype = ctypes.c_int
         L.kda_latent_decode_workspace_size.argtypes = [i32, i32, i32]
         L.kda_latent_decode_workspace_size.restype = sz
         L.kda_latent_prefill.argtypes = [rows, rows, vp, i64, rows, ctypes.c_int, vp, vp, i32, i32,

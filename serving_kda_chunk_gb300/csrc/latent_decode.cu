@@ -60,6 +60,7 @@ struct DecodeArgs {
     float2* ml;     // [2 CTAs][N] (log2_base of m, l)
     float* part;    // [2 CTAs][N][512]
     int32_t* dev_status;
+    int32_t give_up_cta, give_up_pair;  // of the self-test: this CTA's loads stop before this column pair
 };
 
 // The plan of a CTA with N query rows a tile.  Q is the A operand of S with M = 128: its N rows are
@@ -191,7 +192,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <int N, int DT>
+// kGiveUp: the self-test's form, in which one wait of a loading warp counts as run out.
+template <int N, int DT, bool kGiveUp>
 __global__ void __launch_bounds__(kDecThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rmap,
                   const __grid_constant__ DecodeArgs a) {
@@ -293,13 +295,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     w.left = w.r < 0 ? 0 : g1 - g0;
     bool dead = false;
     // a wait that gives up marks the CTA: every role leaves its loop at its next wait
+    auto give_up = [&] {
+        dead = true;
+        ctrl[1] = 1;
+        report(a.dev_status, KDA_DEV_TIMEOUT);
+    };
     auto wait = [&](int b, uint32_t parity) {
         if (dead) return;
-        if (!mbar_wait(bar(b), parity, kDecWait)) {
-            dead = true;
-            ctrl[1] = 1;
-            report(a.dev_status, KDA_DEV_TIMEOUT);
-        }
+        if (!mbar_wait(bar(b), parity, kDecWait)) give_up();
     };
 
     if (warp == 0 || warp == 2 || warp == 3) {
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int part = warp;  // 0: rope (and pairs 0..3), 2: pairs 0, 1, 3: pairs 2, 3
         const int p_lo = part == 3 ? 2 : 0, p_hi = whole_box ? (part == 0 ? 4 : 0) : part == 0 ? 0 : p_lo + 2;
         const uint32_t per = L::T / a.box;
-        uint32_t tile = 0;
+        uint32_t tile = 0, pairs = 0, ropes = 0;  // tiles done; column pairs and rope columns asked for
         while (!dead && w.next(a)) {
             const int32_t* tab = a.table + (int64_t)w.cr * a.max_pages;
             // page of this lane's box in tile j (-1: none) and the box's first row in it
@@ -335,6 +338,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int p = p_lo; p < p_hi; ++p) {
                     const uint32_t n = tile * 4 + p, slot = n % L::PAIRS;
                     wait(L::B_EMPTY + slot, (n / L::PAIRS & 1) ^ 1);  // the first pass finds the slots free
+                    if (kGiveUp && !dead && (int)blockIdx.x == a.give_up_cta && (int)n == a.give_up_pair) give_up();
                     dead = __any_sync(~0u, dead);
                     if (dead) break;
                     if (lane == 0) mbar_expect_tx(bar(L::B_FULL + slot), 2 * bytes);
@@ -345,6 +349,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         if (!whole_box)
                             tma_load_4d(dst + L::COL, &map, 0, y, 2 * p + 1, page, bar(L::B_FULL + slot));
                     }
+                    ++pairs;
                 }
                 if (dead) break;
                 if (part == 0) {
@@ -361,21 +366,26 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     if (ok)
                         tma_load_4d(sb + L::ROPE + slot * L::COL + lane * a.box * 128, &rmap, 0, y, 8, page,
                                     bar(L::B_RFULL + slot));
+                    ++ropes;
                 }
             }
             if (ctrl[1]) dead = true;
             dead = __any_sync(~0u, dead);
         }
-        // nothing may be in flight when the CTA ends: the last loads of this warp have landed
-        dead = false;
-        const uint32_t back = min(tile, (uint32_t)L::ROPES);
-        for (uint32_t k = tile - back; k < tile; ++k) {
-            for (int p = p_lo; p < p_hi; ++p) {
-                const uint32_t n = k * 4 + p;
-                wait(L::B_FULL + n % L::PAIRS, n / L::PAIRS & 1);
-            }
-            if (part == 0) wait(L::B_RFULL + k % L::ROPES, k / L::ROPES & 1);
+        // Nothing may be in flight when the CTA ends: the last loads of this warp have landed, those of a tile
+        // that was given up half asked for among them.  Each wait is bounded by itself: one that runs out
+        // does not let the others pass.
+        auto landed = [&](int b, uint32_t parity) {
+            dead = false;
+            wait(b, parity);
+        };
+        const uint32_t per_tile = p_hi - p_lo;
+        for (uint32_t k = pairs - min(pairs, L::ROPES * per_tile); k < pairs; ++k) {
+            const uint32_t n = k / per_tile * 4 + p_lo + k % per_tile;
+            landed(L::B_FULL + n % L::PAIRS, n / L::PAIRS & 1);
         }
+        for (uint32_t k = ropes - min(ropes, (uint32_t)L::ROPES); k < ropes; ++k)
+            landed(L::B_RFULL + k % L::ROPES, k / L::ROPES & 1);
     } else if (warp == 1) {
         // ================================================================ MMAs
         // the whole warp runs this, one lane issues (umma.cuh, mma_by); votes keep the control uniform
@@ -882,10 +892,10 @@ int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
-template <int N, int DT>
+template <int N, int DT, bool kGiveUp = false>
 kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_tiles, cudaStream_t s) {
     using L = DecLayout<N>;
-    auto* f = decode_kernel<N, DT>;
+    auto* f = decode_kernel<N, DT, kGiveUp>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM) != cudaSuccess)
         return KDA_ERR_CUDA;
     // every (row tile, request) has at least one tile and at most max_tiles
@@ -928,15 +938,15 @@ extern "C" size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t
     return align16(kDecCtas * sizeof(int4)) + 2 * kDecCtas * n * (sizeof(float2) + kLatent * sizeof(float));
 }
 
-extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,
-                                        kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
-                                        int32_t H, int32_t d_latent, int32_t d_rope, float scale,
-                                        const void* cache, int64_t P, int32_t page_size,
-                                        int64_t page_stride, const int32_t* block_table,
-                                        int32_t max_pages, const int32_t* seq_len,
-                                        const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
-                                        void* workspace, size_t ws_bytes, int32_t* dev_status,
-                                        void* stream) {
+namespace kda {
+namespace {
+
+// Both entry points; give_up_cta < 0 for the call itself.
+kda_status decode_call(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope, kda_dtype in_dtype, int32_t R, int32_t K,
+                       const int32_t* q_len, int32_t H, int32_t d_latent, int32_t d_rope, float scale, const void* cache,
+                       int64_t P, int32_t page_size, int64_t page_stride, const int32_t* block_table, int32_t max_pages,
+                       const int32_t* seq_len, const kda_rows_desc* out, kda_dtype out_dtype, float* lse, void* workspace,
+                       size_t ws_bytes, int32_t* dev_status, void* stream, int32_t give_up_cta, int32_t give_up_pair) {
     KDA_REQUIRE(R >= 0 && K >= 0 && H > 0 && P >= 0 && page_size > 0 && max_pages >= 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(d_latent == kLatent && d_rope == kRope && K <= 16, KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
@@ -968,7 +978,8 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     KDA_REQUIRE(encode_16bit(&map[1], in_dtype, 4, base, dims, strides, rope_boxes), KDA_ERR_CUDA);
     DecodeArgs a{as_rows(q_latent), as_rows(q_rope), R, K, q_len, H, log2_scale(scale), scale < 0.f, P, page_size, box,
                  block_table, max_pages, seq_len, const_cast<void*>(out->base), out->row_stride, out->head_stride,
-                 out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, false, nullptr, nullptr, dev_status};
+                 out_dtype, lse, (int32_t)(((int64_t)K * H + n - 1) / n), nullptr, false, nullptr, nullptr, dev_status,
+                 give_up_cta, give_up_pair};
     a.by_unit = (int64_t)a.n_rt * R <= kDecCtas;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.meta = reinterpret_cast<int4*>(ws);
@@ -979,6 +990,36 @@ extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda
     const int tile = n == 64 ? DecLayout<64>::T : DecLayout<32>::T;
     const int64_t max_tiles = ((int64_t)max_pages * page_size + tile - 1) / tile;
     cudaStream_t s = as_stream(stream);
+    if (give_up_cta >= 0) return launch<16, KDA_BF16, true>(map, a, max_tiles > 0 ? max_tiles : 1, s);
     if (in_dtype == KDA_BF16) return launch_n<KDA_BF16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
     return launch_n<KDA_F16>(map, a, max_tiles > 0 ? max_tiles : 1, s);
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,
+                                        kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
+                                        int32_t H, int32_t d_latent, int32_t d_rope, float scale,
+                                        const void* cache, int64_t P, int32_t page_size,
+                                        int64_t page_stride, const int32_t* block_table,
+                                        int32_t max_pages, const int32_t* seq_len,
+                                        const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
+                                        void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                        void* stream) {
+    return decode_call(q_latent, q_rope, in_dtype, R, K, q_len, H, d_latent, d_rope, scale, cache, P, page_size, page_stride,
+                       block_table, max_pages, seq_len, out, out_dtype, lse, workspace, ws_bytes, dev_status, stream, -1, 0);
+}
+
+extern "C" kda_status kda_selftest_latent_decode_give_up(
+    const kda_rows_desc* q_latent, const kda_rows_desc* q_rope, kda_dtype in_dtype, int32_t R, int32_t K, const int32_t* q_len,
+    int32_t H, int32_t d_latent, int32_t d_rope, float scale, const void* cache, int64_t P, int32_t page_size,
+    int64_t page_stride, const int32_t* block_table, int32_t max_pages, const int32_t* seq_len, const kda_rows_desc* out,
+    kda_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream, int32_t block,
+    int32_t load) {
+    KDA_REQUIRE(block >= 0 && load >= 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(in_dtype == KDA_BF16 && (int64_t)K * H <= 16, KDA_ERR_UNSUPPORTED);
+    return decode_call(q_latent, q_rope, in_dtype, R, K, q_len, H, d_latent, d_rope, scale, cache, P, page_size, page_stride,
+                       block_table, max_pages, seq_len, out, out_dtype, lse, workspace, ws_bytes, dev_status, stream, block,
+                       load);
 }

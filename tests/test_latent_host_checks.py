@@ -1,10 +1,10 @@
-"""A scale that is not finite is refused on the host (a NaN would pass for a scale of 0)."""
+"""Host-side refusals: a scale that is not finite (a NaN would pass for a scale of 0), and the self-test's."""
 import ctypes
 
 import pytest
 
-FAKE = 1 << 20  # 16-byte aligned, never dereferenced: the scale is refused first
-OK, INVALID, BF16 = 0, 1, 0
+FAKE = 1 << 20  # 16-byte aligned, never dereferenced: checks fail first
+OK, INVALID, UNSUPPORTED, BF16, F16 = 0, 1, 2, 0, 2
 
 
 @pytest.fixture(scope="module")
@@ -33,3 +33,16 @@ def test_latent_calls_refuse_a_scale_that_is_not_finite(kda, scale):
 
     assert decode(4) == INVALID and prefill(2) == INVALID
     assert decode(0) == OK and prefill(0) == OK  # nothing to do
+
+
+def test_decode_self_test_refusals(kda):
+    L = kda.lib()
+    d = ctypes.byref(kda.RowsDesc(FAKE, 512, 512))
+
+    def call(H=8, K=2, dt=BF16, block=0, load=0, table=FAKE):
+        size = L.kda_latent_decode_workspace_size(4, K, H)
+        return L.kda_selftest_latent_decode_give_up(d, d, dt, 4, K, None, H, 512, 64, 1.0, FAKE, 8, 16, 16 * 576, table,
+                                                    4, FAKE, d, BF16, None, FAKE, size, None, None, block, load)
+
+    assert call(block=-1) == INVALID and call(load=-1) == INVALID and call(table=None) == INVALID
+    assert call(H=9) == UNSUPPORTED and call(dt=F16) == UNSUPPORTED
