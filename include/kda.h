@@ -501,8 +501,9 @@ kda_status kda_latent_append(const void* kv, int64_t kv_stride, const void* weig
  *                 output), KDA_DEV_BAD_SEQLEN.
  *   out         : rows R*K, heads H, 512 channels of out_dtype (any of the three).
  *   lse         : [R*K, H] fp32 or NULL.
- *   workspace   : >= kda_latent_decode_workspace_size(R, K, H) bytes, read only
- *                 after this call wrote it.
+ *   workspace   : >= kda_latent_decode_workspace_size(R, K, H) bytes; what an
+ *                 earlier call left there reaches no result.
+ * With KDA_DEV_TIMEOUT, rows that the call did not finish are NaN or not written.
  * 1 <= H, 1 <= K <= 16, R * K * H < 2^31.
  */
 kda_status kda_latent_decode(const kda_rows_desc* q_latent, const kda_rows_desc* q_rope,

@@ -287,12 +287,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctrl[0];
-    Walk<N> w;
-    w.r = ctrl[2];
-    w.rt = ctrl[3];
-    w.j = ctrl[4];
-    w.turn = turn;
-    w.left = w.r < 0 ? 0 : g1 - g0;
+    auto range = [&] {
+        Walk<N> w;
+        w.r = ctrl[2];
+        w.rt = ctrl[3];
+        w.j = ctrl[4];
+        w.turn = turn;
+        w.left = w.r < 0 ? 0 : g1 - g0;
+        return w;
+    };
+    Walk<N> w = range();
     bool dead = false;
     // a wait that gives up marks the CTA: every role leaves its loop at its next wait
     auto give_up = [&] {
@@ -751,14 +755,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             // rowf read by all before the next segment writes it.  A row without keys gets its zeros here and
             // not from its factor: beside a NaN or infinity that other rows see, its sums are NaN (a choice
             // for each element above cost 1 to 2 % of the call).
-            if (bar_named_or(1, 128, whole && t < rows && rowf[t & (N - 1)] == 0.f)) {
+            // Rows whose last product was given up get NaN.
+            if (bar_named_or(1, 128, whole && (dead || (t < rows && rowf[t & (N - 1)] == 0.f)))) {
+                const bool gone = bar_named_or(1, 128, dead);
                 for (int n = 0; n < rows; ++n) {
-                    if (rowf[n] != 0.f) continue;
+                    if (!gone && rowf[n] != 0.f) continue;
                     for (int c = t; c < kLatent; c += 128)
                         if (a.out_dt == KDA_F32)
-                            static_cast<float*>(a.out)[rowo[n] + c] = 0.f;
+                            static_cast<uint32_t*>(a.out)[rowo[n] + c] = gone ? 0x7fffffffu : 0u;
                         else
-                            static_cast<uint16_t*>(a.out)[rowo[n] + c] = 0;
+                            static_cast<uint16_t*>(a.out)[rowo[n] + c] = gone ? 0x7fff : 0;
                 }
                 bar_named(1, 128);
             }
@@ -768,6 +774,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncthreads();
     fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    // A wait that ran out leaves parts unwritten, and the workspace may hold an earlier call's in their place:
+    // this CTA's parts turn what they are joined with to NaN, and a request that starts here is not joined.
+    if (ctrl[1]) {
+        const float nan = __int_as_float(0x7fffffff);
+        if (tid < 2 * N) a.ml[(int64_t)blockIdx.x * 2 * N + tid] = make_float2(nan, nan);
+        if (tid == 0) {
+            if (!a.by_unit) a.meta[blockIdx.x].x = -1;
+            else
+                for (Walk<N> u = range(); u.next(a);)
+                    if (u.j0 == 0) a.meta[u.crt * a.R + u.cr].x = -1;
+        }
+    }
 }
 
 // Joins the parts of a request that several CTAs hold: o = sum_i 2^{m_i - m} O_i / sum_i 2^{m_i - m} l_i.
@@ -781,7 +799,7 @@ struct Split {
 };
 __device__ __forceinline__ Split split_at(const DecodeArgs& a, int e) {
     const int4 me = a.meta[e];
-    // an entry is only missing after a wait gave up: what lies there then is not taken
+    // an entry of no request, or (after a wait ran out) none that this call wrote
     const bool ok = me.x >= 0 && me.x < a.R && me.y >= 0 && me.y < a.n_rt && me.z >= 0 && me.w >= me.z && me.w < kDecCtas;
     return {me.x, me.y, me.z, ok ? me.w - me.z + 1 : 0};
 }

@@ -86,3 +86,21 @@ def test_decode_self_test_beyond_the_call_changes_nothing():
     for stop in ((500, 0), (0, 1 << 20)):
         got = b.run(q, stop=stop)
         assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("lens,page", BATCHES)
+@pytest.mark.parametrize("block", [0, 70, 71, 151])
+@pytest.mark.parametrize("load", [0, 6, 31])
+def test_decode_that_gave_up_joins_nothing_of_an_earlier_call(lens, page, block, load):
+    b = Batch(lens, page, seed=page + 1)
+    want = b.run(b.queries(2))
+    earlier = b.run(b.queries(1))  # leaves its parts in the workspace
+    out, lse, st = b.run(b.queries(2), stop=(block, load))
+    assert st == kda.KDA_DEV_TIMEOUT
+    same = (out == want[0]).flatten(1).all(1) & (lse == want[1]).all(1)
+    assert not same.all()
+    lost = out[~same]
+    assert (torch.isnan(lost) | (lost == 7.0)).all()  # not joined at all, or joined to NaN
+    z = lse[~same]
+    assert (torch.isnan(z) | (z == 7.0) | (z == want[1][~same])).all()
+    assert not torch.equal(earlier[0], want[0])
