@@ -536,6 +536,7 @@ size_t kda_latent_decode_workspace_size(int32_t R, int32_t K, int32_t H);
  * Strides are >= 0; the row strides of q, k_nope and v are > 0 where there is
  * more than one row (a head stride of 0 shares a row between the heads).
  * Tq, Tk < 2^30.
+ * With KDA_DEV_TIMEOUT, rows that the call did not finish are NaN or not written.
  */
 kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
                               const void* k_rope, int64_t k_rope_stride, const kda_rows_desc* v,
@@ -597,6 +598,19 @@ kda_status kda_selftest_latent_decode_give_up(
     const int32_t* block_table, int32_t max_pages, const int32_t* seq_len,
     const kda_rows_desc* out, kda_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
     int32_t* dev_status, void* stream, int32_t block, int32_t load);
+
+/*
+ * kda_selftest_latent_prefill_give_up -- diagnostic: the same for
+ * kda_latent_prefill: block `block` of the grid (two a pair) stops before its
+ * tile of values number `tile` (128 keys each, counted over the blocks of rows
+ * that it takes).  bf16 only.
+ */
+kda_status kda_selftest_latent_prefill_give_up(
+    const kda_rows_desc* q, const kda_rows_desc* k_nope, const void* k_rope, int64_t k_rope_stride,
+    const kda_rows_desc* v, kda_dtype in_dtype, const int32_t* cu_q, const int32_t* cu_k,
+    int32_t N, int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope, int32_t d_rope, int32_t dv,
+    float scale, uint32_t flags, const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
+    int32_t* dev_status, void* stream, int32_t block, int32_t tile);
 
 const char* kda_status_string(kda_status s);
 

@@ -127,6 +127,8 @@ def lib():
         L.kda_latent_prefill.argtypes = [rows, rows, vp, i64, rows, ctypes.c_int, vp, vp, i32, i32,
                                          i32, i32, i32, i32, i32, f32, u32, rows, ctypes.c_int, vp,
                                          vp, vp]
+        L.kda_selftest_latent_prefill_give_up.argtypes = L.kda_latent_prefill.argtypes + [i32, i32]
+        L.kda_selftest_latent_prefill_give_up.restype = ctypes.c_int
         L.kda_token_logprobs.argtypes = [vp, i64, ctypes.c_int, i32, i32, vp, vp, vp, i32, vp, vp,
                                          vp, vp]
         L.kda_status_string.argtypes = [ctypes.c_int]

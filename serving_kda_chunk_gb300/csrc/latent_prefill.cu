@@ -57,6 +57,7 @@ struct PrefillArgs {
     int32_t out_dt;
     float* lse;
     int32_t* dev_status;
+    int32_t give_up_cta, give_up_tile;  // of the self-test: this CTA's loads stop before this tile of V
 };
 
 struct PreMaps {
@@ -68,7 +69,7 @@ constexpr uint32_t PS_K = 6 * kQPart, PS_V = PS_K + kStages * kKBytes, PS_BAR = 
 constexpr int PB_Q = 0, PB_K = 2, PB_V = PB_K + kStages, PB_NEXT = PB_V + kStages, PB_KFREE = PB_NEXT + 1,
               PB_VFREE = PB_KFREE + kStages, PB_S = PB_VFREE + kStages, PB_P = PB_S + 2, PB_P2 = PB_P + 2,
               PB_O = PB_P2 + 2, PB_QFREE = PB_O + 2, PB_EDGE = PB_QFREE + 2, PB_CLC = PB_EDGE + 1, PB_INFO = PB_CLC + 1,
-              PB_IFREE = PB_INFO + 2, PB_DRAIN = PB_IFREE + 2, PB_BARS = PB_DRAIN + 1;
+              PB_IFREE = PB_INFO + 2, PB_DRAIN = PB_IFREE + 2, PB_NEVER = PB_DRAIN + 1, PB_BARS = PB_NEVER + 1;
 constexpr uint32_t PS_CTRL = PS_BAR + 8 * 40, PS_SCAN = PS_CTRL + 32, PS_CLC = PS_SCAN + 64, PS_INFO = PS_CLC + 16,
                    PS_ORDER = PS_INFO + 2 * 32, PS_START = PS_ORDER + 4 * kSorted, PS_LEN = PS_START + 4 * (kSorted + 1),
                    PS_SUM = (PS_LEN + 4 * kSorted + 7) & ~7u, PS_SMEM = PS_SUM + 8 * 256;
@@ -95,14 +96,15 @@ __device__ __forceinline__ uint4 pack16(const float (&o)[32], int e) {
                       Elem<DT>::put2(o[e + 4], o[e + 5]), Elem<DT>::put2(o[e + 6], o[e + 7]));
 }
 
-template <int DT>
+// kGiveUp: the self-test's form, in which one wait of a loading warp counts as run out.
+template <int DT, bool kGiveUp>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefill_kernel(const __grid_constant__ PreMaps maps, const __grid_constant__ PrefillArgs a) {
     using E = Elem<DT>;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int* ctrl = reinterpret_cast<int*>(sm + PS_CTRL);  // 0 tmem, 1 sequence, 2 its block, 3 and 4 where its scan stood
+    volatile int* ctrl = reinterpret_cast<int*>(sm + PS_CTRL);  // 0 tmem, 1 sequence, 2 its block, 3 and 4 where its scan stood, 5 NaN if a wait ran out
     volatile int* info = reinterpret_cast<int*>(sm + PS_INFO);  // two blocks' (head, sequence, first row); sequence -1: no more
     int* scan = reinterpret_cast<int*>(sm + PS_SCAN);
     auto bar = [&](int i) { return sb + PS_BAR + 8 * i; };
@@ -128,7 +130,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     volatile int* start = reinterpret_cast<int*>(sm + PS_START);  // blocks before each, and in all
     volatile int* len = reinterpret_cast<int*>(sm + PS_LEN);
     const bool sorted = a.N <= kSorted;
-    if (tid == 0) ctrl[1] = -1;
+    if (tid == 0) {
+        ctrl[1] = -1;
+        ctrl[5] = 0;
+    }
     if (sorted) {
         bool bad = false;
         int b = 0, mine = -1;
@@ -238,12 +243,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     fence_after();
     const uint32_t tmem = ctrl[0];
     bool dead = false;
+    // A wait that runs out marks both CTAs of the pair and ends its role: rows of the block are NaN then (the
+    // MMA warp may still finish a tile with operands that did not come), the other roles' waits run out too.
+    auto give_up = [&] {
+        dead = true;
+        for (uint32_t c = 0; c < 2; ++c)
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(map_rank(sb + PS_CTRL + 20, c)), "r"(0x7fffffff) : "memory");
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        report(a.dev_status, KDA_DEV_TIMEOUT);
+    };
     auto wait = [&](int b, uint32_t parity) {
         if (dead) return;
-        if (!mbar_wait(bar(b), parity, kPreWait)) {
-            dead = true;
-            report(a.dev_status, KDA_DEV_TIMEOUT);
-        }
+        if (!mbar_wait(bar(b), parity, kPreWait)) give_up();
     };
 
     if (warp == 8) {
@@ -278,8 +289,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         auto load_v = [&](int i) {
             const uint32_t st = vt % kStages;
             wait(PB_VFREE + st, (vt / kStages & 1) ^ 1);
+            if (kGiveUp && !dead && (int)blockIdx.x == a.give_up_cta && (int)vt == a.give_up_tile) give_up();
             ++vt;
-            if (dead) return;
+            if (__any_sync(~0u, dead)) return;
             const uint32_t dst = sb + PS_V + st * kVBytes, b = first(PB_V + st);
             const int valid = u.Lk - i * kKTile;
             if (valid >= kKTile) {
@@ -296,6 +308,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     tma_load_3d(dst, &maps.v, 64 * (int)rank, u.h * a.hv, u.k0 + i * kKTile, bar(PB_EDGE));
                 }
                 wait(PB_EDGE, edges++ & 1);
+                if (__any_sync(~0u, dead)) return;
                 for (uint32_t e = valid * 128 + lane * 16; e < kVBytes; e += 512)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + e), "r"(0u) : "memory");
                 fence_async_smem();
@@ -381,10 +394,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (n < 0) break;
             u = block_at(h, n, row0);
         }
-        // Every load was waited for by an MMA that is done when the CTAs leave, and the last answer was
-        // read.  After a wait that gave up that does not hold: one more (bounded) wait on a phase that does
-        // not end lets them land.
-        if (__any_sync(~0u, dead)) mbar_wait(bar(PB_EDGE), edges & 1, kPreWait);
     } else if (warp == 9 && rank == 0) {
         // ================================================================ MMAs
         // the whole warp runs this, one lane issues (umma.cuh, mma_by)
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             for (int i = 0; i < mt && !stop; ++i, ++kv) {
                 const uint32_t st = kv % kStages, sn = (kv + 1) % kStages;
                 // loads ahead of the weights: a wait queues behind the MMAs issued before it
-                if (!mbar_wait_cluster(bar(PB_V + st), kv / kStages & 1, kPreWait)) dead = true;  // cleared edges
+                if (!mbar_wait_cluster(bar(PB_V + st), kv / kStages & 1, kPreWait)) give_up();  // cleared edges
                 if (i + 1 < mt) wait(PB_K + sn, (kv + 1) / kStages & 1);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -559,7 +568,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 wait(PB_O + q, (done - 1) & 1);
                 fence_after();
             }
-            const float l = sum->total(), il = 1.f / l;
+            float gone;  // 0, or NaN after a wait ran out; by its address: as ctrl[5] the tile loop spilled (1 % slower)
+            asm volatile("ld.volatile.shared.f32 %0, [%1];" : "=f"(gone) : "r"(sb + PS_CTRL + 20) : "memory");
+            const float l = sum->total() + gone, il = 1.f / l;
             const int64_t orow = (int64_t)u.q0 + row;
             if (row < u.Lq && a.lse != nullptr)
                 a.lse[orow * a.H + u.h] = l == 0.f ? -inf : (log2_base<DT>(m, a.c) + log2f(l)) * 0.69314718055994531f;
@@ -614,6 +625,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     fence_before();
     __syncthreads();
+    // Every load and answer was waited for by a role that is done.  After a wait that ran out that does not
+    // hold: a bounded wait on a barrier that nothing arrives on (about a second) lets them land.
+    if (ctrl[5] && warp == 8) {
+        mbar_wait(bar(PB_NEVER), 0, kPreWait);
+        __syncwarp();
+    }
     cluster_sync();  // no CTA leaves while the other's MMAs, loads or arrivals may still reach it
     fence_after();
     if (warp == 9) tmem2_dealloc(tmem, 512);
@@ -634,14 +651,15 @@ bool rows_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int channels,
 
 using namespace kda;
 
-extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
-                                         const void* k_rope, int64_t k_rope_stride,
-                                         const kda_rows_desc* v, kda_dtype in_dtype,
-                                         const int32_t* cu_q, const int32_t* cu_k, int32_t N,
-                                         int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope,
-                                         int32_t d_rope, int32_t dv, float scale, uint32_t flags,
-                                         const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
-                                         int32_t* dev_status, void* stream) {
+namespace kda {
+namespace {
+
+// Both entry points; give_up_cta < 0 for the call itself.
+kda_status prefill_call(const kda_rows_desc* q, const kda_rows_desc* k_nope, const void* k_rope, int64_t k_rope_stride,
+                        const kda_rows_desc* v, kda_dtype in_dtype, const int32_t* cu_q, const int32_t* cu_k, int32_t N,
+                        int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope, int32_t d_rope, int32_t dv, float scale,
+                        uint32_t flags, const kda_rows_desc* out, kda_dtype out_dtype, float* lse, int32_t* dev_status,
+                        void* stream, int32_t give_up_cta, int32_t give_up_tile) {
     KDA_REQUIRE(N >= 0 && Tq >= 0 && Tk >= 0 && H > 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(d_nope == kNope && d_rope == kRope && dv == kHeadV, KDA_ERR_UNSUPPORTED);
     KDA_REQUIRE((in_dtype == KDA_BF16 || in_dtype == KDA_F16) && any_dtype_ok(out_dtype), KDA_ERR_UNSUPPORTED);
@@ -679,8 +697,10 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
     }
     const PrefillArgs a{cu_q, cu_k, N, Tq, Tk, H, rq.hs != 0, rk.hs != 0, rv.hs != 0, log2_scale(scale), scale < 0.f,
                         (flags & KDA_LATENT_FULL) != 0, const_cast<void*>(out->base), out->row_stride, out->head_stride,
-                        out_dtype, lse, dev_status};
-    auto* f = in_dtype == KDA_BF16 ? prefill_kernel<KDA_BF16> : prefill_kernel<KDA_F16>;
+                        out_dtype, lse, dev_status, give_up_cta, give_up_tile};
+    auto* f = give_up_cta >= 0       ? prefill_kernel<KDA_BF16, true>
+              : in_dtype == KDA_BF16 ? prefill_kernel<KDA_BF16, false>
+                                     : prefill_kernel<KDA_F16, false>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PS_SMEM) != cudaSuccess)
         return KDA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -699,4 +719,30 @@ extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_
         return KDA_ERR_CUDA;
     }
     return launch_status();
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nope,
+                                         const void* k_rope, int64_t k_rope_stride,
+                                         const kda_rows_desc* v, kda_dtype in_dtype,
+                                         const int32_t* cu_q, const int32_t* cu_k, int32_t N,
+                                         int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope,
+                                         int32_t d_rope, int32_t dv, float scale, uint32_t flags,
+                                         const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
+                                         int32_t* dev_status, void* stream) {
+    return prefill_call(q, k_nope, k_rope, k_rope_stride, v, in_dtype, cu_q, cu_k, N, Tq, Tk, H, d_nope, d_rope, dv, scale, flags,
+                        out, out_dtype, lse, dev_status, stream, -1, 0);
+}
+
+extern "C" kda_status kda_selftest_latent_prefill_give_up(
+    const kda_rows_desc* q, const kda_rows_desc* k_nope, const void* k_rope, int64_t k_rope_stride, const kda_rows_desc* v,
+    kda_dtype in_dtype, const int32_t* cu_q, const int32_t* cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t H,
+    int32_t d_nope, int32_t d_rope, int32_t dv, float scale, uint32_t flags, const kda_rows_desc* out, kda_dtype out_dtype,
+    float* lse, int32_t* dev_status, void* stream, int32_t block, int32_t tile) {
+    KDA_REQUIRE(block >= 0 && tile >= 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(in_dtype == KDA_BF16, KDA_ERR_UNSUPPORTED);
+    return prefill_call(q, k_nope, k_rope, k_rope_stride, v, in_dtype, cu_q, cu_k, N, Tq, Tk, H, d_nope, d_rope, dv, scale, flags,
+                        out, out_dtype, lse, dev_status, stream, block, tile);
 }

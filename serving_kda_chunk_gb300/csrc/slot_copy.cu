@@ -193,7 +193,7 @@ extern "C" const char* kda_status_string(kda_status st) {
     return "KDA_ERR_UNKNOWN";
 }
 
-extern "C" int32_t kda_abi_version(void) { return 107; }
+extern "C" int32_t kda_abi_version(void) { return 108; }
 
 // ----------------------------------------------------------------------------
 // Allocation-free variant.

@@ -3,12 +3,11 @@ flight and the context usable.  The self-test entry stops one block's loads befo
 other wait of that block then runs out by itself after about a second."""
 import ctypes
 
-import numpy as np
 import pytest
 import torch
 
 from helpers import i32
-from test_gpu_latent import DL, DR, SCALE, W
+from test_gpu_latent import DL, DR, SCALE, Prefill, W
 
 import serving_kda_chunk_gb300 as kda
 
@@ -104,3 +103,40 @@ def test_decode_that_gave_up_joins_nothing_of_an_earlier_call(lens, page, block,
     z = lse[~same]
     assert (torch.isnan(z) | (z == 7.0) | (z == want[1][~same])).all()
     assert not torch.equal(earlier[0], want[0])
+
+
+def run_prefill(p, q, stop=None, fill=7.0):
+    Tq, n = q.shape[:2]
+    out = torch.full((Tq, n, 128), fill, device="cuda")
+    lse = torch.full((Tq, n), fill, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [rows(q), rows(p.kv[..., :128]), p.kr.data_ptr(), 64, rows(p.kv[..., 128:]), kda.KDA_BF16, p.cu_q.data_ptr(),
+            p.cu_k.data_ptr(), len(p.lq), Tq, p.kv.shape[0], n, 128, 64, 128, SCALE, 0, rows(out), kda.KDA_F32,
+            lse.data_ptr(), st.data_ptr(), torch.cuda.current_stream().cuda_stream]
+    L = kda.lib()
+    rc = L.kda_latent_prefill(*args) if stop is None else L.kda_selftest_latent_prefill_give_up(*args, *stop)
+    assert rc == 0
+    torch.cuda.synchronize()
+    return out, lse, int(st)
+
+
+# one block of rows a pair, and several one after another (32 heads); tile 27 of the first pair is the
+# sequence's last, cut short; tile 30 lies in the pair's second block
+@pytest.mark.parametrize("heads,block,tile", [
+    (8, 0, 0), (8, 1, 0), (8, 0, 5), (8, 1, 6), (8, 70, 4), (8, 0, 27), (8, 1, 27), (8, 0, 26), (32, 0, 2), (32, 1, 30),
+    (32, 0, 31), (32, 70, 3),
+])
+def test_prefill_gives_up_and_leaves_no_half_result(heads, block, tile):
+    p = Prefill([3000, 700], [3500, 700], heads, seed=heads)
+    want = run_prefill(p, p.q)
+    assert want[2] == 0
+    out, lse, st = run_prefill(p, p.q, stop=(block, tile))
+    assert st == kda.KDA_DEV_TIMEOUT
+    same = (out == want[0]).all(2) & (lse == want[1])
+    assert not same.all() and same.any()
+    lost, z = out[~same], lse[~same]
+    assert (torch.isnan(lost) | (lost == 7.0)).all() and (torch.isnan(z) | (z == 7.0)).all()
+    again = run_prefill(p, p.q)
+    assert again[2] == 0 and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    never = run_prefill(p, p.q, stop=(block, 1 << 20))
+    assert never[2] == 0 and torch.equal(never[0], want[0])

@@ -46,3 +46,15 @@ def test_decode_self_test_refusals(kda):
 
     assert call(block=-1) == INVALID and call(load=-1) == INVALID and call(table=None) == INVALID
     assert call(H=9) == UNSUPPORTED and call(dt=F16) == UNSUPPORTED
+
+
+def test_prefill_self_test_refusals(kda):
+    L = kda.lib()
+    d = ctypes.byref(kda.RowsDesc(FAKE, 512, 512))
+
+    def call(dt=BF16, block=0, tile=0, cu=FAKE):
+        return L.kda_selftest_latent_prefill_give_up(d, d, FAKE, 64, d, dt, cu, FAKE, 2, 10, 10, 4, 128, 64, 128, 1.0, 0,
+                                                     d, BF16, None, None, None, block, tile)
+
+    assert call(block=-1) == INVALID and call(tile=-1) == INVALID and call(cu=None) == INVALID
+    assert call(dt=F16) == UNSUPPORTED
