@@ -193,3 +193,100 @@ def test_prefill_keeps_small_weights_beside_a_large_one(drop, where, dtype):
     out, lse, st = p.run(out_dtype=torch.float32, scale=float(np.log(2)), flags=kda.KDA_LATENT_FULL)
     assert st == 0
     sink_check(out, lse, n, drop, dtype)
+
+
+# ----------------------------------------------------------- joins of split requests
+#
+# With zero queries every weight is exactly 1 and the sum exactly the number of keys.  Channel j of key p
+# is 1 where p falls into the j-th of 512 equal stretches of the request, else 0: the output is the share
+# of seen keys in each stretch, and a part that is lost, doubled or left over from elsewhere moves whole
+# channels by all they hold.  The counts are exact in fp32; the store, the reciprocal and a join's factors
+# leave 2^-20 of each.
+#
+# Requests, positions and heads reach: one and several row tiles, more and fewer (request, row tile)s
+# than blocks, and with more than 8 x 152 token tiles the turns between requests that count in the ranges
+# (2 tiles up to 32 query rows, 6 above).
+
+JOINS = [
+    # R, K, H, longest, page
+    (40, 1, 8, 6000, 16), (40, 1, 24, 6000, 64), (300, 1, 16, 800, 32), (300, 2, 16, 800, 64), (1300, 1, 4, 130, 16),
+    (30, 3, 40, 4000, 16), (200, 7, 32, 500, 16), (100, 1, 128, 1600, 64), (1500, 1, 40, 90, 8),
+    (3, 1, 16, 50000, 64), (2, 5, 24, 30000, 48), (1, 1, 128, 90000, 16), (5, 16, 16, 9000, 8),
+]
+
+
+def stretches(n, dtype):
+    x = torch.zeros(n, W, dtype=dtype, device="cuda")
+    p = torch.arange(n, device="cuda")
+    x[p, p * DL // max(n, 1)] = 1
+    x[:, DL:] = 1
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("R,K,H,longest,page", JOINS)
+def test_decode_joins_every_part_once(R, K, H, longest, page, dtype):
+    dt = TYPES[dtype]
+    rng = np.random.Generator(np.random.PCG64(R + H))
+    lens = rng.integers(0, longest + 1, R) if R > 1 else np.array([longest])
+    lens[R // 2] = longest
+    if R > 4:
+        lens[1], lens[2] = 0, 1
+    q_len = rng.integers(0, K + 1, R) if K > 1 else np.ones(R, np.int64)
+    used = -(-lens // page)
+    cache = torch.full((int(used.sum()) + 1, page, W), float("nan"), dtype=dt, device="cuda")
+    table = torch.full((R, int(used.max()) + 1), -3, dtype=torch.int32, device="cuda")
+    at = 0
+    for r in range(R):
+        n, u = int(lens[r]), int(used[r])
+        cache[at:at + u].view(-1, W)[:n] = stretches(n, dt)
+        table[r, :u] = torch.arange(at, at + u, device="cuda", dtype=torch.int32)
+        at += u
+    ql, qr = torch.zeros(R * K, H, DL, dtype=dt, device="cuda"), torch.zeros(R * K, H, DR, dtype=dt, device="cuda")
+    out = torch.full((R * K, H, DL), float("nan"), device="cuda")
+    lse = torch.full((R * K, H), float("nan"), device="cuda")
+    ws = torch.full((kda.kda_latent_decode_workspace_size(R, K, H),), 255, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_latent_decode(ql, qr, cache, table, i32(lens), out, ws, K=K, q_len=i32(q_len), scale=SCALE, lse=lse,
+                          dev_status=st)
+    assert int(st) == 0
+    n = torch.from_numpy(lens).cuda().double()
+    qn = torch.from_numpy(q_len).cuda()
+    t = torch.arange(K, device="cuda")
+    seen = (n[:, None] - qn[:, None] + t[None] + 1).clamp(min=0)  # [R, K]: keys 0 .. seen - 1
+    seen = torch.where(t[None] < qn[:, None], torch.minimum(seen, n[:, None]), 0.0).flatten()
+    n = n.repeat_interleave(K)
+    # keys below p that fall into stretches below j: ceil(j n / 512), so far as they are seen
+    j = torch.arange(DL + 1, device="cuda", dtype=torch.float64)
+    upto = torch.minimum(torch.ceil(j[None] * n[:, None] / DL), seen[:, None])
+    want = torch.where(seen[:, None] > 0, (upto[:, 1:] - upto[:, :-1]) / seen.clamp(min=1)[:, None], 0.0)
+    err = (out.double() - want[:, None]).abs()
+    assert (err <= 2.0 ** -20 * want[:, None]).all(), err.max().item()
+    some = seen > 0
+    z = seen.clamp(min=1).log()
+    assert ((lse.double() - z[:, None]).abs()[some] <= 2.0 ** -20 * (1 + z[:, None])[some]).all()
+    assert (lse[~some] == -torch.inf).all()
+
+
+@pytest.mark.parametrize("R,K,H,n", [(1, 1, 16, 40000), (3, 1, 32, 20011), (1, 7, 32, 30000), (40, 1, 8, 3000), (2, 2, 64, 9000)])
+def test_decode_of_long_requests_is_as_close_as_rounded_weights_allow(R, K, H, n):
+    # weights are rounded to bf16 independently of one another: over all channels and rows the outputs are
+    # off by no more than u sqrt(sum p^2 v^2) in the mean square, and by 2 e A from scores that are e off.
+    # One of 152 parts lost or doubled moves them several times as far.
+    d = Decode([n - 37 * r for r in range(R)], K, H, 64, seed=R + H)
+    out, lse, st = d.run(out_dtype=torch.float32)
+    assert st == 0
+    for r in range(0, R, 7):
+        rows = slice(r * K, (r + 1) * K)
+        x = d.tokens[r].double()
+        q = torch.cat([d.ql, d.qr], 2)[rows].reshape(K * H, W).double()
+        L = d.lens[r]
+        t = torch.arange(K, device="cuda").repeat_interleave(H)
+        seen = torch.arange(L, device="cuda")[None] <= (L - K + t)[:, None]
+        p = torch.softmax((q @ x.T * SCALE).masked_fill(~seen, -torch.inf), 1)
+        v = x[:, :DL]
+        e = 64 * 2.0 ** -24 * SCALE * (q.abs() @ x.abs().T).amax()
+        got, want = out[rows].double().view(K * H, DL), p @ v
+        lim = 2.0 ** -8 * (p.square() @ v.square()).mean().sqrt() + 2 * e * (p @ v.abs()).square().mean().sqrt()
+        err = (got - want).square().mean().sqrt()
+        assert err <= lim, (r, err.item(), lim.item())
