@@ -37,6 +37,12 @@ inline kda_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+// A runtime call that failed, as a status: the error does not stay behind for the next call to find.
+inline kda_status runtime_failed() {
+    cudaGetLastError();
+    return KDA_ERR_CUDA;
+}
+
 }  // namespace kda
 
 #define KDA_REQUIRE(cond, code) \

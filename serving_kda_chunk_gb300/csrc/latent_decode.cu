@@ -915,7 +915,7 @@ kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_
     using L = DecLayout<N>;
     auto* f = decode_kernel<N, DT, kGiveUp>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM) != cudaSuccess)
-        return KDA_ERR_CUDA;
+        return runtime_failed();
     // every (row tile, request) has at least one tile and at most max_tiles
     const int64_t most = (int64_t)a.n_rt * a.R * max_tiles;
     const unsigned grid = (unsigned)(most < kDecCtas ? most : kDecCtas);
@@ -933,7 +933,8 @@ kda_status launch(const CUtensorMap (&map)[2], const DecodeArgs& a, int64_t max_
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, split ? combine_kernel<N, true> : combine_kernel<N, false>, a) != cudaSuccess) return KDA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, split ? combine_kernel<N, true> : combine_kernel<N, false>, a) != cudaSuccess)
+        return runtime_failed();
     return launch_status();
 }
 

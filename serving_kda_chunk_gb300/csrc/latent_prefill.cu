@@ -702,7 +702,7 @@ kda_status prefill_call(const kda_rows_desc* q, const kda_rows_desc* k_nope, con
               : in_dtype == KDA_BF16 ? prefill_kernel<KDA_BF16, false>
                                      : prefill_kernel<KDA_F16, false>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PS_SMEM) != cudaSuccess)
-        return KDA_ERR_CUDA;
+        return runtime_failed();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks * 2);
     cfg.blockDim = dim3(kPreThreads);
@@ -714,10 +714,7 @@ kda_status prefill_call(const kda_rows_desc* q, const kda_rows_desc* k_nope, con
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, f, maps, a) != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
+    if (cudaLaunchKernelEx(&cfg, f, maps, a) != cudaSuccess) return runtime_failed();
     return launch_status();
 }
 

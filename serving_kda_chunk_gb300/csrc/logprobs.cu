@@ -487,9 +487,6 @@ extern "C" kda_status kda_token_logprobs(const void* logits, int64_t row_stride,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = C > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, f, a, C, per) != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
+    if (cudaLaunchKernelEx(&cfg, f, a, C, per) != cudaSuccess) return runtime_failed();
     return launch_status();
 }
