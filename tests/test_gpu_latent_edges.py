@@ -290,3 +290,39 @@ def test_decode_of_long_requests_is_as_close_as_rounded_weights_allow(R, K, H, n
         lim = 2.0 ** -8 * (p.square() @ v.square()).mean().sqrt() + 2 * e * (p @ v.abs()).square().mean().sqrt()
         err = (got - want).square().mean().sqrt()
         assert err <= lim, (r, err.item(), lim.item())
+
+
+# ----------------------------------------------------------- a chunk behind an appended context
+
+
+def test_prefill_of_a_chunk_behind_its_appended_context():
+    # two chunks appended to a paged cache; the second's keys are expanded from the rows that the cache holds
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    H, page, lens = 3, 16, [(200, 90), (37, 140)]  # (context, chunk) of each sequence
+    r = lambda *n: torch.randn(*n, generator=g, device="cuda").bfloat16()  # noqa: E731
+    total = sum(a + b for a, b in lens)
+    up = (torch.randn(DL, H * 256, generator=g, device="cuda") * DL ** -0.5).bfloat16()
+    cache = torch.full((total // page + 4, page, W), float("nan"), dtype=torch.bfloat16, device="cuda")
+    places = torch.randperm(cache.shape[0] * page, generator=g, device="cuda")[:total].to(torch.int32)
+    kv, st = r(total, W), torch.zeros(1, dtype=torch.int32, device="cuda")
+    first, chunk, at = [], [], 0
+    for a, b in lens:
+        first += range(at, at + a)
+        chunk += range(at + a, at + a + b)
+        at += a + b
+    q = r(len(chunk), H, 192)
+    for part in (first, chunk):
+        part = torch.tensor(part, device="cuda")
+        kda.kda_latent_append(kv[part], cache, places[part], dev_status=st)
+    rows = cache.view(-1, W)[places.long()]
+    assert torch.equal(rows, kv)
+    k = (rows[:, :DL] @ up).view(total, H, 256)
+    out = torch.empty(len(chunk), H, 128, device="cuda")
+    lse = torch.empty(len(chunk), H, device="cuda")
+    kda.kda_latent_prefill(q, k[..., :128], rows[:, DL:], k[..., 128:], i32([0, 90, 230]), i32([0, 290, 467]), out,
+                           scale=SCALE, lse=lse, dev_status=st)
+    assert int(st) == 0
+    p = Prefill([90, 140], [290, 177], H)
+    p.q, p.kv, p.kr = q, k, rows[:, DL:]
+    p.check((out, lse, 0))
