@@ -3,7 +3,9 @@
 //
 // A warp per token: lane l holds 16 of the 512 latent channels (two 16-byte words) and, for
 // l < 8, 8 of the 64 rope channels; the mean square is a warp sum in fp32 and every result is
-// rounded once.  It moves 1152 bytes in and 1152 out a token and nothing else, so HBM bounds it.
+// rounded once.  It moves 1152 bytes in and 1152 out a token and nothing else, so HBM sets its floor: 14.1 us
+// for 41460 tokens.  It takes 21.8, since a warp's loads, sum and stores follow one another once and only the
+// other blocks of an SM run under them.
 #include "kda_host.h"
 #include "latent_common.cuh"
 

@@ -20,8 +20,8 @@
 // MMAs wait on lie in the first CTA and take both CTAs' arrivals; completed MMAs arrive in both.
 //
 // Blocks of rows follow one another without the pair leaving its SMs: the loading warp asks the launch
-// hardware for the next block (cluster launch control) while it loads one, so that a block's first loads
-// and products run under the last block's results (5 us of about 50 a block otherwise).  Long blocks
+// hardware for the next block (cluster launch control) under the last tiles of one, so that a block's first
+// loads and products run under the last block's results (5 us of about 50 a block otherwise).  Long blocks
 // first: see the order of the sequences below, and a sequence's last queries, which have the most keys,
 // before its first.
 #include "kda_host.h"
