@@ -62,8 +62,8 @@ typedef enum {
     KDA_ERR_CUDA = 3         /* a CUDA launch or runtime call failed         */
 } kda_status;
 
-/* KDA_F16 is taken by the latent attention and log-probability calls only; every
- * recurrent-state call returns KDA_ERR_UNSUPPORTED for it. */
+/* KDA_F16 is taken by the latent attention, decayed attention, norm and log-probability
+ * calls only; every KDA recurrent-state call returns KDA_ERR_UNSUPPORTED for it. */
 typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_F16 = 2 } kda_dtype;
 
 #define KDA_GATE_LOG 1u
@@ -545,6 +545,143 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
                               int32_t d_rope, int32_t dv, float scale, uint32_t flags,
                               const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
                               int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay a head: the recurrent-state layers whose state
+ * fades by one factor a head and token, fixed slopes or a gate, without the
+ * delta rule.  Per value head h (its key head is h / (H / Hk), Hk divides H):
+ *   g_t = min(head_decay[h] + log_decay[t][h], 0)
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = S_t^T (scale q_t).
+ * Either source of the log decay (natural logarithm, fp32) may be NULL, not
+ * both.  Values below -104, -inf included, forget the state: e^-104 is 0 in
+ * fp32 (a state that holds an infinity gives NaN there, as 0 times it does).
+ * NaN stays NaN.
+ *
+ * States are as for the other recurrent-state calls: pool[slot][h][v][k], fp32,
+ * or bf16 / fp16 by KDA_STATE_BF16 / KDA_STATE_F16 (the only flags of these
+ * calls), so kda_slot_copy serves them.  d_k = d_v = 128.  q, k, v and out are
+ * placed by kda_rows_desc: q and k with Hk heads, v and out with H.  scale is
+ * any finite number. */
+
+/*
+ * kda_decay_prefill -- chunked form over packed sequences.
+ *
+ *   q, k, v        : rows T_tot of in_dtype (bf16 or fp16); row strides > 0, head
+ *                    strides >= 0 (0: the heads share a row)
+ *   head_decay     : [H] fp32 or NULL;  log_decay: [T_tot, H] fp32 or NULL
+ *   cu_seqlens     : [N+1] int32 (device).  Sequence n is rows
+ *                    [cu_seqlens[n], cu_seqlens[n+1]); a sequence whose bounds
+ *                    decrease or lie outside [0, T_tot] is skipped, with
+ *                    KDA_DEV_BAD_SEQLEN.  A sequence of no rows passes its
+ *                    initial state on.
+ *   state_pool     : [P, H, 128, 128] states.  init_slot[n] >= 0 reads the
+ *                    initial state (< 0: zero); final_slot[n] >= 0 receives the
+ *                    state after the sequence (< 0: not written).  Either may be
+ *                    NULL (= all -1) and both may name the same slot.  A slot
+ *                    >= P: the sequence is skipped, KDA_DEV_BAD_SLOT.  A final
+ *                    slot must not be another sequence's initial or final slot
+ *                    (not checked).
+ *   track_chunk_idx: [N, M] int32 or NULL when M = 0.  Entry j >= 0 asks for the
+ *                    state after j * 128 tokens of the sequence (j = 0: the
+ *                    initial state), j below its number of chunks of 128; -1 =
+ *                    unused; others set KDA_DEV_BAD_TRACK and write nothing.
+ *   track_state    : [N, M, H, 128, 128] in the state type.
+ *   out            : rows T_tot of out_dtype (any of the three).  Rows of no
+ *                    sequence are left as they were.
+ *   workspace      : NULL, or >= kda_decay_prefill_workspace_size(T_tot, N, H)
+ *                    bytes.  With it long (sequence, head) pairs are cut between
+ *                    SMs; what an earlier call left there reaches no result.
+ * A value or key that is not finite reaches, beside the rows behind it, rows of
+ * its own chunk of 128 before it.  T_tot < 2^30, N * H < 2^27.
+ */
+kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_desc* k,
+                             const kda_rows_desc* v, kda_dtype in_dtype, const float* head_decay,
+                             const float* log_decay, const int32_t* cu_seqlens, int32_t N,
+                             int32_t T_tot, int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                             float scale, uint32_t flags, void* state_pool, int64_t P,
+                             const int32_t* init_slot, const int32_t* final_slot,
+                             const int32_t* track_chunk_idx, int32_t M, void* track_state,
+                             const kda_rows_desc* out, kda_dtype out_dtype, void* workspace,
+                             size_t ws_bytes, int32_t* dev_status, void* stream);
+
+size_t kda_decay_prefill_workspace_size(int32_t T_tot, int32_t N, int32_t H);
+
+/*
+ * kda_decay_decode -- recurrent form: K positions a request (K = 1: decode; K up
+ * to 16: a speculative verify and its commit), rows as for kda_spec_verify.
+ *
+ *   q, k, v     : rows R*K (request r's position t is row r*K + t) of in_dtype
+ *                 (any of the three)
+ *   head_decay  : [H] fp32 or NULL;  log_decay: [R*K, H] fp32 or NULL
+ *   q_len       : [R] int32 in [0, K] or NULL (= K): positions of the request.
+ *                 Rows at or past it are not read and answered with zeros.
+ *   n_commit    : [R] int32 in [0, q_len] or NULL (= q_len): the state after
+ *                 that many positions is written.  0 writes none: a verify reads
+ *                 the state only, and its commit is the same call after
+ *                 acceptance with out = NULL (q may be NULL then too) and
+ *                 n_commit the accepted lengths.
+ *                 q_len or n_commit outside: request skipped (zero outputs),
+ *                 KDA_DEV_BAD_ACCEPT.
+ *   slot        : [R] int32: the state read.  < 0: padding request, skipped, zero
+ *                 outputs; >= P: the same and KDA_DEV_BAD_SLOT.
+ *   dst_slot    : [R] int32 or NULL (= slot, in place): the state written.  < 0:
+ *                 not written; >= P: request skipped, KDA_DEV_BAD_SLOT.  With
+ *                 another slot than the one read it is written for n_commit = 0
+ *                 too (a copy).  A slot written must not be named by another
+ *                 request (not checked).
+ *   out         : rows R*K of out_dtype (any of the three), or NULL.
+ */
+kda_status kda_decay_decode(const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
+                            kda_dtype in_dtype, const float* head_decay, const float* log_decay,
+                            int32_t R, int32_t K, const int32_t* q_len, const int32_t* n_commit,
+                            int32_t H, int32_t Hk, int32_t dk, int32_t dv, float scale,
+                            uint32_t flags, void* state_pool, int64_t P, const int32_t* slot,
+                            const int32_t* dst_slot, const kda_rows_desc* out, kda_dtype out_dtype,
+                            int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms around a block.  All arithmetic is fp32, each output is rounded once.
+ * d is 1 .. 16384; any strides and element alignment (rows of whole, aligned
+ * 16-byte vectors are faster).  eps >= 0 and all scales are finite.  Weights are
+ * [d] of in_dtype, shared by rows and heads, used as weight + weight_offset; NULL
+ * counts as 1. */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SIGMOID = 1, KDA_ACT_SILU = 2 } kda_act;
+
+/* flag of kda_gated_norm: norm(x act(gate)) instead of norm(x) act(gate) */
+#define KDA_NORM_AFTER_GATE 128u
+
+/*
+ * kda_gated_norm -- each head's row of an attention's output, normalised and
+ * gated:  y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset) * act(gate).
+ *
+ *   x, gate : rows R, heads H, d channels of in_dtype (gate may be NULL)
+ *   out     : the same rows and heads of out_dtype; may be x or gate itself
+ */
+kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc* gate, const void* weight,
+                          kda_dtype in_dtype, int32_t R, int32_t H, int32_t d, float eps,
+                          float weight_offset, kda_act act, uint32_t flags,
+                          const kda_rows_desc* out, kda_dtype out_dtype, void* stream);
+
+/*
+ * kda_residual_norm -- from one block's output to the next block's input:
+ *   z = post_weight ? x / sqrt(mean(x^2) + eps) * (post_weight + weight_offset) : x
+ *   hidden = residual_scale * residual + branch_scale * act(gate) * z
+ *   out    = hidden / sqrt(mean(hidden^2) + eps) * (weight + weight_offset)
+ *
+ *   x, gate          : [R, d] of in_dtype; gate may be NULL (= 1), and its stride
+ *                      0 (one row for all)
+ *   residual, hidden : [R, d] of residual_dtype (in_dtype or fp32); hidden may be
+ *                      residual itself, or NULL
+ *   out              : [R, d] of out_dtype, from the unrounded hidden; or NULL
+ * Row r of a tensor starts at base + r * stride elements.
+ */
+kda_status kda_residual_norm(const void* x, int64_t x_stride, const void* residual,
+                             int64_t residual_stride, kda_dtype residual_dtype,
+                             const void* post_weight, const void* gate, int64_t gate_stride,
+                             kda_act act, const void* weight, kda_dtype in_dtype, int32_t R,
+                             int32_t d, float residual_scale, float branch_scale, float eps,
+                             float weight_offset, void* hidden, int64_t hidden_stride, void* out,
+                             int64_t out_stride, kda_dtype out_dtype, void* stream);
 
 /*
  * kda_token_logprobs -- what a serving step answers with beside its tokens: the

@@ -10,7 +10,9 @@ Entry points (same names as the C ABI):
   kda_spec_accept_commit, kda_conv_compact, kda_slot_copy, kda_slot_copy_noalloc,
   kda_chunk_prefill_workspace_size, kda_slot_copy_workspace_size,
   kda_latent_append, kda_latent_decode, kda_latent_decode_workspace_size, kda_latent_prefill,
-  kda_token_logprobs.
+  kda_token_logprobs,
+  kda_decay_prefill, kda_decay_prefill_workspace_size, kda_decay_decode,
+  kda_gated_norm, kda_residual_norm.
 """
 from __future__ import annotations
 
@@ -31,6 +33,9 @@ __all__ = [
     "ConvDesc", "CommitExtras", "RowsDesc",
     "kda_latent_append", "kda_latent_decode", "kda_latent_decode_workspace_size",
     "kda_latent_prefill", "kda_token_logprobs",
+    "kda_decay_prefill", "kda_decay_prefill_workspace_size", "kda_decay_decode",
+    "kda_gated_norm", "kda_residual_norm",
+    "KDA_ACT_NONE", "KDA_ACT_SIGMOID", "KDA_ACT_SILU", "KDA_NORM_AFTER_GATE",
 ]
 
 KDA_BF16, KDA_F32, KDA_F16 = 0, 1, 2
@@ -38,6 +43,8 @@ KDA_GATE_LOG, KDA_BETA_ACT, KDA_PREFILL_RECURRENT = 1, 2, 4
 KDA_STATE_BF16, KDA_STATE_F16 = 8, 16
 KDA_QK_L2NORM = 32
 KDA_LATENT_FULL = 64
+KDA_NORM_AFTER_GATE = 128
+KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU = 0, 1, 2
 KDA_DEV_BAD_SLOT, KDA_DEV_BAD_TRACK, KDA_DEV_BAD_ACCEPT = 1, 2, 4
 KDA_DEV_BAD_SEQLEN, KDA_DEV_OVERLAP, KDA_DEV_TIMEOUT = 8, 16, 32
 KDA_MAX_POOLS = 16
@@ -131,6 +138,19 @@ def lib():
         L.kda_selftest_latent_prefill_give_up.restype = ctypes.c_int
         L.kda_token_logprobs.argtypes = [vp, i64, ctypes.c_int, i32, i32, vp, vp, vp, i32, vp, vp,
                                          vp, vp]
+        L.kda_decay_prefill.argtypes = [rows, rows, rows, ctypes.c_int, vp, vp, vp, i32, i32, i32,
+                                        i32, i32, i32, f32, u32, vp, i64, vp, vp, vp, i32, vp, rows,
+                                        ctypes.c_int, vp, sz, vp, vp]
+        L.kda_decay_prefill_workspace_size.argtypes = [i32, i32, i32]
+        L.kda_decay_prefill_workspace_size.restype = sz
+        L.kda_decay_decode.argtypes = [rows, rows, rows, ctypes.c_int, vp, vp, i32, i32, vp, vp, i32,
+                                       i32, i32, i32, f32, u32, vp, i64, vp, vp, rows, ctypes.c_int,
+                                       vp, vp]
+        L.kda_gated_norm.argtypes = [rows, rows, vp, ctypes.c_int, i32, i32, i32, f32, f32,
+                                     ctypes.c_int, u32, rows, ctypes.c_int, vp]
+        L.kda_residual_norm.argtypes = [vp, i64, vp, i64, ctypes.c_int, vp, vp, i64, ctypes.c_int, vp,
+                                        ctypes.c_int, i32, i32, f32, f32, f32, f32, vp, i64, vp, i64,
+                                        ctypes.c_int, vp]
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_abi_version.restype = i32
@@ -138,7 +158,8 @@ def lib():
                   "kda_spec_accept", "kda_spec_commit", "kda_spec_accept_commit",
                   "kda_conv_compact", "kda_slot_copy", "kda_selftest_bounded_wait",
                   "kda_latent_append", "kda_latent_decode", "kda_latent_prefill",
-                  "kda_token_logprobs"):
+                  "kda_token_logprobs", "kda_decay_prefill", "kda_decay_decode",
+                  "kda_gated_norm", "kda_residual_norm"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -596,3 +617,149 @@ def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, t
         None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
     if st:
         _check(st, "kda_token_logprobs")
+
+
+# --------------------------------------------------------------------------
+# linear attention with a decay a head, and the norms around a block
+
+
+def _here(first, *rest):
+    """All tensors on the device that is current: the calls launch there."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("libkda takes CUDA tensors")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if dev != _current_device():
+        raise ValueError(f"tensors on {first.device}, but device {_current_device()} is current")
+
+
+def _decay_args(q, k, v, out, head_decay, log_decay):
+    """(rows, H, Hk, dk, dv, in_dtype) and the checked decay pointers of the decayed-attention calls."""
+    n, H, dv = v.shape
+    _, Hk, dk = k.shape
+    if k.shape[0] != n or (q is not None and q.shape != k.shape) or (out is not None and out.shape != v.shape):
+        for name, t, shape in (("q", q, (n, Hk, dk)), ("k", k, (n, Hk, dk)), ("out", out, (n, H, dv))):
+            if t is not None and t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if head_decay is None and log_decay is None:
+        raise ValueError("head_decay or log_decay is needed")
+    dt = _one_dtype("q, k and v", k, v, k if q is None else q)
+    return (n, H, Hk, dk, dv, dt,
+            None if head_decay is None else _arr(head_decay, _f32t, "head_decay", (H,)),
+            None if log_decay is None else _arr(log_decay, _f32t, "log_decay", (n, H)))
+
+
+def _pool(state_pool, H, dk, dv):
+    if state_pool.shape[1:] != (H, dv, dk):
+        raise ValueError(f"state_pool must be [slots, {H}, {dv}, {dk}], got {tuple(state_pool.shape)}")
+    return _p(state_pool)
+
+
+def kda_decay_prefill_workspace_size(T_tot, N, H) -> int:
+    return int(lib().kda_decay_prefill_workspace_size(T_tot, N, H))
+
+
+def kda_decay_prefill(q, k, v, cu_seqlens, out, *, head_decay=None, log_decay=None, state_pool=None,
+                      init_slot=None, final_slot=None, track_chunk_idx=None, track_state=None,
+                      scale=1.0, flags=0, workspace=None, dev_status=None, stream=None):
+    """Linear attention with a decay a head over packed sequences (see include/kda.h).  q and k
+    [T, Hk, 128], v and out [T, H, 128] may be strided over rows and heads; head_decay [H] and
+    log_decay [T, H] are natural logarithms in fp32."""
+    T, H, Hk, dk, dv, dt, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
+    _here(v, q, k, out, cu_seqlens, head_decay, log_decay, state_pool, init_slot, final_slot, track_chunk_idx,
+          track_state, workspace, dev_status)
+    N = cu_seqlens.shape[0] - 1
+    M = 0
+    if track_chunk_idx is not None:
+        M = track_chunk_idx.shape[1]
+        if track_state is None or track_state.shape != (N, M, H, dv, dk):
+            raise ValueError(f"track_state must have shape {(N, M, H, dv, dk)}")
+    st = (_lib or lib()).kda_decay_prefill(
+        _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), dt, hd, ld, _arr(cu_seqlens, _i32, "cu_seqlens"), N, T, H, Hk,
+        dk, dv, scale, flags | _state_flag(state_pool, track_state),
+        None if state_pool is None else _pool(state_pool, H, dk, dv), 0 if state_pool is None else state_pool.shape[0],
+        None if init_slot is None else _arr(init_slot, _i32, "init_slot", (N,)),
+        None if final_slot is None else _arr(final_slot, _i32, "final_slot", (N,)),
+        None if track_chunk_idx is None else _arr(track_chunk_idx, _i32, "track_chunk_idx", (N, M)), M,
+        _p(track_state), _rows(out, "out"), _dt3(out), _p(workspace), 0 if workspace is None else workspace.nbytes,
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_decay_prefill")
+
+
+def kda_decay_decode(q, k, v, state_pool, slot, out, *, K=1, q_len=None, n_commit=None, dst_slot=None,
+                     head_decay=None, log_decay=None, scale=1.0, flags=0, dev_status=None, stream=None):
+    """K positions a request from the states of a pool (see include/kda.h).  q and k [R*K, Hk, 128], v
+    and out [R*K, H, 128] may be strided over rows and heads; q and out may be None for a commit."""
+    if q is None and out is not None:
+        raise ValueError("an output needs q")
+    n, H, Hk, dk, dv, dt, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
+    _here(v, q, k, out, state_pool, slot, dst_slot, q_len, n_commit, head_decay, log_decay, dev_status)
+    R = slot.shape[0]
+    if K < 0 or n != R * K:
+        raise ValueError(f"v has {n} rows, not {R} requests x K = {K}")
+    st = (_lib or lib()).kda_decay_decode(
+        None if q is None else _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), dt, hd, ld, R, K,
+        None if q_len is None else _arr(q_len, _i32, "q_len", (R,)),
+        None if n_commit is None else _arr(n_commit, _i32, "n_commit", (R,)), H, Hk, dk, dv, scale,
+        flags | _state_flag(state_pool), _pool(state_pool, H, dk, dv), state_pool.shape[0],
+        _arr(slot, _i32, "slot", (R,)), None if dst_slot is None else _arr(dst_slot, _i32, "dst_slot", (R,)),
+        None if out is None else _rows(out, "out"), dt if out is None else _dt3(out),
+        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+    if st:
+        _check(st, "kda_decay_decode")
+
+
+def kda_gated_norm(x, out, *, gate=None, weight=None, eps=1e-6, weight_offset=0.0, act=KDA_ACT_SIGMOID, flags=0,
+                   stream=None):
+    """Each head's row normalised and multiplied by its activated gate (see include/kda.h).  x, gate and
+    out: [R, H, d], strided over rows and heads; weight: [d]."""
+    R, H, d = x.shape
+    if out.shape != x.shape or (gate is not None and gate.shape != x.shape):
+        raise ValueError(f"gate and out must have the shape of x, {tuple(x.shape)}")
+    dt = _one_dtype("x, gate and weight", x, x if gate is None else gate, x if weight is None else weight)
+    _here(x, out, gate, weight)
+    st = (_lib or lib()).kda_gated_norm(
+        _rows(x, "x"), None if gate is None else _rows(gate, "gate"),
+        None if weight is None else _arr(weight, weight.dtype, "weight", (d,)), dt, R, H, d, eps, weight_offset, act,
+        flags, _rows(out, "out"), _dt3(out), _stream(stream))
+    if st:
+        _check(st, "kda_gated_norm")
+
+
+def _row_stride(t, name, shape):
+    """(pointer, row stride) of a tensor of rows, or of none."""
+    if t is None:
+        return None, 0
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    rs, cs = t.stride()
+    if cs != 1 and shape[0] and shape[1] > 1:
+        raise ValueError(f"{name} needs contiguous rows")
+    return t.data_ptr(), rs if shape[0] > 1 else 0
+
+
+def kda_residual_norm(x, residual, *, hidden=None, out=None, post_weight=None, gate=None, act=KDA_ACT_NONE,
+                      weight=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6, weight_offset=0.0, stream=None):
+    """Norm after a block, gate, residual sum and norm before the next block (see include/kda.h).  x [R, d];
+    residual and hidden [R, d] of x's type or fp32; gate [R, d] or [1, d]; out [R, d]; weights [d]."""
+    shape = R, d = tuple(x.shape)
+    if hidden is None and out is None:
+        raise ValueError("hidden or out is needed")
+    dt = _one_dtype("x, gate and weights", x, *(t for t in (gate, post_weight, weight) if t is not None))
+    if hidden is not None and hidden.dtype is not residual.dtype:
+        raise ValueError(f"hidden must have residual's dtype {residual.dtype}, got {hidden.dtype}")
+    gp, gs = _row_stride(gate, "gate", (1, d) if gate is not None and gate.shape[0] == 1 else shape)
+    xp, xs = _row_stride(x, "x", shape)
+    rp, rs = _row_stride(residual, "residual", shape)
+    hp, hs = _row_stride(hidden, "hidden", shape)
+    op, os_ = _row_stride(out, "out", shape)
+    _here(x, residual, hidden, out, post_weight, gate, weight)
+    st = (_lib or lib()).kda_residual_norm(
+        xp, xs, rp, rs, _dt3(residual), None if post_weight is None else _arr(post_weight, x.dtype, "post_weight", (d,)),
+        gp, gs, act, None if weight is None else _arr(weight, x.dtype, "weight", (d,)), dt, R, d, residual_scale,
+        branch_scale, eps, weight_offset, hp, hs, op, os_, dt if out is None else _dt3(out), _stream(stream))
+    if st:
+        _check(st, "kda_residual_norm")

@@ -1,0 +1,410 @@
+// norms.cu -- kda_gated_norm and kda_residual_norm: the row norms around a block, with the gate and
+// the residual sum that stand beside them.
+//
+//   gated:     y = x / sqrt(mean(x^2) + eps) (w + offset) act(gate)      (per row and head)
+//   residual:  z = post ? x / sqrt(mean(x^2) + eps) (post + offset) : x
+//              h = residual_scale r + branch_scale act(gate) z
+//              y = h / sqrt(mean(h^2) + eps) (w + offset)                (per row)
+//
+// One pass: a row lives in the registers of the TPR threads that share it (NV vectors of eight elements
+// each), so every input is read once and every output written once, and the second norm of the residual
+// form costs a reduction and no traffic.  Bound by HBM.  All arithmetic is fp32; y comes from the
+// unrounded h, and each output is rounded once on its store.
+#include "kda_host.h"
+#include "latent_common.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kNormMaxDim = 16384;
+
+struct NormRows {
+    const void* base;
+    int64_t rs, hs;  // strides of rows and heads, in elements
+};
+
+// The element a thread holds as (vector i, element e): eight neighbours when rows are whole 16-byte
+// vectors, else neighbours lie in neighbouring threads so that single loads are side by side.
+template <bool kVec, int TPR>
+__device__ __forceinline__ int elem_at(int i, int e, int t) {
+    return kVec ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
+}
+
+// Raw bits of eight elements: what a load leaves in registers until it is used.
+template <int DT>
+struct Raw8 {
+    uint32_t w[DT == KDA_F32 ? 8 : 4];
+};
+
+template <int DT, bool kVec, int TPR>
+__device__ __forceinline__ Raw8<DT> load_raw(const void* row, int i, int t, int d) {
+    Raw8<DT> r;
+    if constexpr (kVec) {
+        const int at = elem_at<true, TPR>(i, 0, t);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (DT == KDA_F32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + at);
+            const uint4 a = at < d ? p[0] : zero, b = at < d ? p[1] : zero;
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+            r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+        } else {
+            const uint4 a = at < d ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + at) : zero;
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        }
+    } else {
+        if constexpr (DT == KDA_F32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = elem_at<false, TPR>(i, e, t);
+                r.w[e] = at < d ? static_cast<const uint32_t*>(row)[at] : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const int a = elem_at<false, TPR>(i, e, t), b = elem_at<false, TPR>(i, e + 1, t);
+                const uint32_t lo = a < d ? static_cast<const uint16_t*>(row)[a] : 0;
+                const uint32_t hi = b < d ? static_cast<const uint16_t*>(row)[b] : 0;
+                r.w[e / 2] = lo | hi << 16;
+            }
+        }
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen(const Raw8<DT>& r, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (DT == KDA_F32) {
+            v[2 * e] = __uint_as_float(r.w[2 * e]);
+            v[2 * e + 1] = __uint_as_float(r.w[2 * e + 1]);
+        } else {
+            const float2 f = Elem<DT>::get2(r.w[e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+        }
+    }
+}
+
+template <int DT, bool kVec, int TPR>
+__device__ __forceinline__ void store8(void* row, int i, int t, int d, const float (&v)[8]) {
+    if constexpr (kVec) {
+        const int at = elem_at<true, TPR>(i, 0, t);
+        if (at >= d) return;
+        if constexpr (DT == KDA_F32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + at) =
+                make_uint4(Elem<DT>::put2(v[0], v[1]), Elem<DT>::put2(v[2], v[3]), Elem<DT>::put2(v[4], v[5]),
+                           Elem<DT>::put2(v[6], v[7]));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int at = elem_at<false, TPR>(i, e, t);
+            if (at >= d) continue;
+            if constexpr (DT == KDA_F32)
+                static_cast<float*>(row)[at] = v[e];
+            else
+                static_cast<uint16_t*>(row)[at] = (uint16_t)Elem<DT>::put2(v[e], 0.f);
+        }
+    }
+}
+
+template <bool kVec, int TPR>
+__device__ __forceinline__ void store8_as(void* row, int i, int t, int d, const float (&v)[8], int dt) {
+    if (dt == KDA_F32) store8<KDA_F32, kVec, TPR>(row, i, t, d, v);
+    else if (dt == KDA_BF16) store8<KDA_BF16, kVec, TPR>(row, i, t, d, v);
+    else store8<KDA_F16, kVec, TPR>(row, i, t, d, v);
+}
+
+__device__ __forceinline__ void* at_elem(void* p, int64_t i, int dt) {
+    return static_cast<uint8_t*>(p) + i * dtype_bytes(dt);
+}
+__device__ __forceinline__ const void* at_elem(const void* p, int64_t i, int dt) {
+    return static_cast<const uint8_t*>(p) + i * dtype_bytes(dt);
+}
+
+// Sum over the TPR threads of a row: within a warp, or over the block, which then holds one row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float* part) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) x += part[w];
+    }
+    return x;
+}
+
+__device__ __forceinline__ float act_of(float z, int act) {
+    if (act == KDA_ACT_NONE) return z;
+    // e^-z = inf gives 0; z = -inf gives silu NaN as -inf * 0 does
+    const float s = 1.f / (1.f + __expf(-z));
+    return act == KDA_ACT_SILU ? z * s : s;
+}
+
+template <int NV>
+__device__ __forceinline__ float sum_sq(const float (&v)[NV][8]) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e & 3] = fmaf(v[i][e], v[i][e], s[e & 3]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+constexpr int norm_threads(int tpr) { return tpr > 256 ? tpr : tpr > 32 ? tpr : 256; }
+
+// U rows a thread group at a time: their loads are in flight together.
+template <int DT, bool kVec, int TPR, int NV, int U>
+__global__ void __launch_bounds__(norm_threads(TPR)) gated_norm_kernel(
+    NormRows x, NormRows gate, const void* __restrict__ weight, int64_t n, int H, int d, float inv_d, float eps,
+    float offset, int act, bool gate_first, NormRows out, int out_dt) {
+    __shared__ float part[TPR > 32 ? TPR / 32 : 1];
+    constexpr int G = norm_threads(TPR) / TPR;  // rows a block at a time
+    const int t = threadIdx.x % TPR;
+    const int64_t first = (int64_t)blockIdx.x * (G * U) + threadIdx.x / TPR;
+    Raw8<DT> xr[U][NV], gr[U][NV];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = first + u * G;
+        const int dd = row < n ? d : 0;  // a row past the end loads and stores nothing
+        const int64_t r = row / H, h = row - r * H;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            xr[u][i] = load_raw<DT, kVec, TPR>(at_elem(x.base, r * x.rs + h * x.hs, DT), i, t, dd);
+            if (gate.base) gr[u][i] = load_raw<DT, kVec, TPR>(at_elem(gate.base, r * gate.rs + h * gate.hs, DT), i, t, dd);
+        }
+    }
+    Raw8<DT> wr[NV];
+    if (weight)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) wr[i] = load_raw<DT, kVec, TPR>(weight, i, t, d);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = first + u * G;
+        const int dd = row < n ? d : 0;
+        const int64_t r = row / H, h = row - r * H;
+        float v[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) widen<DT>(xr[u][i], v[i]);
+        if (gate.base && gate_first) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float g[8];
+                widen<DT>(gr[u][i], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] *= elem_at<kVec, TPR>(i, e, t) < dd ? act_of(g[e], act) : 0.f;
+            }
+        }
+        const float f = rsqrtf(row_sum<TPR>(sum_sq<NV>(v), part) * inv_d + eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[8], g[8];
+            if (weight) widen<DT>(wr[i], w);
+            if (gate.base && !gate_first) widen<DT>(gr[u][i], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float y = v[i][e] * f;
+                if (weight) y *= w[e] + offset;
+                if (gate.base && !gate_first) y *= act_of(g[e], act);
+                v[i][e] = y;
+            }
+            store8_as<kVec, TPR>(at_elem(const_cast<void*>(out.base), r * out.rs + h * out.hs, out_dt), i, t, dd, v[i], out_dt);
+        }
+        if (TPR > 32 && U > 1) __syncthreads();  // part is written again
+    }
+}
+
+struct ResidualArgs {
+    const void *x, *residual, *post, *gate, *weight;
+    void *hidden, *out;
+    int64_t xs, rs, gs, hs, os;  // row strides, in elements
+    int64_t n;
+    int d, act, res_dt, out_dt;
+    float inv_d, rscale, bscale, eps, offset;
+};
+
+template <int DT, bool kVec, int TPR, int NV>
+__global__ void __launch_bounds__(norm_threads(TPR)) residual_norm_kernel(const ResidualArgs a) {
+    __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
+    constexpr int G = norm_threads(TPR) / TPR;
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / TPR;
+    const int d = row < a.n ? a.d : 0;
+    Raw8<DT> xr[NV], gr[NV], pr[NV], wr[NV];
+    float r[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) xr[i] = load_raw<DT, kVec, TPR>(at_elem(a.x, row * a.xs, DT), i, t, d);
+    if (a.res_dt == KDA_F32) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) widen<KDA_F32>(load_raw<KDA_F32, kVec, TPR>(at_elem(a.residual, row * a.rs, KDA_F32), i, t, d), r[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) widen<DT>(load_raw<DT, kVec, TPR>(at_elem(a.residual, row * a.rs, DT), i, t, d), r[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (a.gate) gr[i] = load_raw<DT, kVec, TPR>(at_elem(a.gate, row * a.gs, DT), i, t, d);
+        if (a.post) pr[i] = load_raw<DT, kVec, TPR>(a.post, i, t, d);
+        if (a.weight) wr[i] = load_raw<DT, kVec, TPR>(a.weight, i, t, d);
+    }
+    float z[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) widen<DT>(xr[i], z[i]);
+    float f = a.bscale;
+    if (a.post) f *= rsqrtf(row_sum<TPR>(sum_sq<NV>(z), part[0]) * a.inv_d + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float p[8], g[8];
+        if (a.post) widen<DT>(pr[i], p);
+        if (a.gate) widen<DT>(gr[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float y = z[i][e] * f;
+            if (a.post) y *= p[e] + a.offset;
+            if (a.gate) y *= act_of(g[e], a.act);
+            z[i][e] = fmaf(a.rscale, r[i][e], y);
+            // an absent element counts as zero, whatever act(0) and the offset make of it
+            if (elem_at<kVec, TPR>(i, e, t) >= d) z[i][e] = 0.f;
+        }
+    }
+    if (a.hidden) {
+        void* p = at_elem(a.hidden, row * a.hs, a.res_dt);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (a.res_dt == KDA_F32) store8<KDA_F32, kVec, TPR>(p, i, t, d, z[i]);
+            else store8<DT, kVec, TPR>(p, i, t, d, z[i]);
+        }
+    }
+    if (!a.out) return;
+    f = rsqrtf(row_sum<TPR>(sum_sq<NV>(z), part[1]) * a.inv_d + a.eps);
+    void* p = at_elem(a.out, row * a.os, a.out_dt);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float w[8];
+        if (a.weight) widen<DT>(wr[i], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[i][e] *= a.weight ? f * (w[e] + a.offset) : f;
+        store8_as<kVec, TPR>(p, i, t, d, z[i], a.out_dt);
+    }
+}
+
+inline bool dtype_known(kda_dtype d) { return d == KDA_BF16 || d == KDA_F16 || d == KDA_F32; }
+inline bool elem_aligned(const void* p, kda_dtype dt) { return reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt) == 0; }
+// Whole 16-byte vectors of eight elements: the row length, and each tensor's start and strides.
+inline bool vec_ok(const void* p, int64_t rs, int64_t hs) { return p == nullptr || (aligned16(p) && rs % 8 == 0 && hs % 8 == 0); }
+
+// Calls launch(TPR, NV) for the form that holds a row of nvec vectors.  A row goes to as many threads as it
+// has vectors while there are fewer rows than fill the device (`few`): one vector a thread is the shortest
+// path.  With many rows four vectors a thread keep more bytes in flight and share the reductions.
+template <class F>
+void with_row_form(int nvec, bool few, F&& launch) {
+    if (nvec <= 8) launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 16) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 32) launch(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 128 && !few) launch(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+    else if (nvec <= 128) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 512 && !few) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 4>{});
+    else if (nvec <= 512) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+    else launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
+}
+
+template <class F>
+void with_types(kda_dtype dt, bool vec, F&& f) {
+    auto by_vec = [&](auto DT) {
+        if (vec) f(DT, std::true_type{});
+        else f(DT, std::false_type{});
+    };
+    if (dt == KDA_BF16) by_vec(std::integral_constant<int, KDA_BF16>{});
+    else if (dt == KDA_F16) by_vec(std::integral_constant<int, KDA_F16>{});
+    else by_vec(std::integral_constant<int, KDA_F32>{});
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc* gate, const void* weight,
+                                     kda_dtype in_dtype, int32_t R, int32_t H, int32_t d, float eps,
+                                     float weight_offset, kda_act act, uint32_t flags, const kda_rows_desc* out,
+                                     kda_dtype out_dtype, void* stream) {
+    KDA_REQUIRE(R >= 0 && H > 0 && d > 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(dtype_known(in_dtype) && dtype_known(out_dtype) && d <= kNormMaxDim, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(act >= KDA_ACT_NONE && act <= KDA_ACT_SILU && (flags & ~KDA_NORM_AFTER_GATE) == 0, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(isfinite(eps) && eps >= 0.f && isfinite(weight_offset), KDA_ERR_INVALID_ARG);
+    if (R == 0) return KDA_OK;
+    KDA_REQUIRE(x && out && x->base && out->base && (!gate || gate->base), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(elem_aligned(x->base, in_dtype) && elem_aligned(out->base, out_dtype), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE((!gate || elem_aligned(gate->base, in_dtype)) && elem_aligned(weight, in_dtype), KDA_ERR_INVALID_ARG);
+    const NormRows xd{x->base, x->row_stride, x->head_stride}, od{out->base, out->row_stride, out->head_stride};
+    const NormRows gd = gate ? NormRows{gate->base, gate->row_stride, gate->head_stride} : NormRows{nullptr, 0, 0};
+    const bool vec = d % 8 == 0 && vec_ok(xd.base, xd.rs, xd.hs) && vec_ok(od.base, od.rs, od.hs) &&
+                     vec_ok(gd.base, gd.rs, gd.hs) && vec_ok(weight, 0, 0);
+    const int64_t n = (int64_t)R * H;
+    const int nvec = (d + 7) / 8;
+    cudaStream_t s = as_stream(stream);
+    bool fits = true;
+    with_types(in_dtype, vec, [&](auto DT, auto V) {
+        with_row_form(nvec, n < 1024, [&](auto TPR, auto NV) {
+            auto run = [&](auto U) {
+                constexpr int rows = norm_threads(TPR) / TPR * U;
+                const int64_t blocks = (n + rows - 1) / rows;
+                fits = blocks < (1ll << 31);
+                if (fits)
+                    gated_norm_kernel<DT, V, TPR, NV, U><<<(unsigned)blocks, norm_threads(TPR), 0, s>>>(
+                        xd, gd, weight, n, H, d, 1.f / (float)d, eps, weight_offset, act,
+                        (flags & KDA_NORM_AFTER_GATE) != 0, od, out_dtype);
+            };
+            // rows of one vector a thread go four at a time when there are many
+            if constexpr (NV == 1 && TPR <= 32) {
+                if (n >= 65536) run(std::integral_constant<int, 4>{});
+                else run(std::integral_constant<int, 1>{});
+            } else {
+                run(std::integral_constant<int, 1>{});
+            }
+        });
+    });
+    return fits ? launch_status() : KDA_ERR_UNSUPPORTED;
+}
+
+extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                        kda_dtype residual_dtype, const void* post_weight, const void* gate,
+                                        int64_t gate_stride, kda_act act, const void* weight, kda_dtype in_dtype,
+                                        int32_t R, int32_t d, float residual_scale, float branch_scale, float eps,
+                                        float weight_offset, void* hidden, int64_t hidden_stride, void* out,
+                                        int64_t out_stride, kda_dtype out_dtype, void* stream) {
+    KDA_REQUIRE(R >= 0 && d > 0, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(dtype_known(in_dtype) && dtype_known(out_dtype) && d <= kNormMaxDim, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(residual_dtype == in_dtype || residual_dtype == KDA_F32, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(act >= KDA_ACT_NONE && act <= KDA_ACT_SILU, KDA_ERR_UNSUPPORTED);
+    KDA_REQUIRE(isfinite(eps) && eps >= 0.f && isfinite(weight_offset), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(isfinite(residual_scale) && isfinite(branch_scale), KDA_ERR_INVALID_ARG);
+    if (R == 0) return KDA_OK;
+    KDA_REQUIRE(x && residual && (hidden || out), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(elem_aligned(x, in_dtype) && elem_aligned(residual, residual_dtype) && elem_aligned(hidden, residual_dtype) &&
+                    elem_aligned(out, out_dtype) && elem_aligned(gate, in_dtype) && elem_aligned(weight, in_dtype) &&
+                    elem_aligned(post_weight, in_dtype),
+                KDA_ERR_INVALID_ARG);
+    const bool vec = d % 8 == 0 && vec_ok(x, x_stride, 0) && vec_ok(residual, residual_stride, 0) &&
+                     vec_ok(hidden, hidden_stride, 0) && vec_ok(out, out_stride, 0) && vec_ok(gate, gate_stride, 0) &&
+                     vec_ok(weight, 0, 0) && vec_ok(post_weight, 0, 0);
+    const ResidualArgs a{x, residual, post_weight, gate, weight, hidden, out, x_stride, residual_stride, gate_stride,
+                         hidden_stride, out_stride, R, d, act, residual_dtype, out_dtype, 1.f / (float)d, residual_scale,
+                         branch_scale, eps, weight_offset};
+    cudaStream_t s = as_stream(stream);
+    with_types(in_dtype, vec, [&](auto DT, auto V) {
+        with_row_form((d + 7) / 8, R < 1024, [&](auto TPR, auto NV) {
+            constexpr int rows = norm_threads(TPR) / TPR;
+            residual_norm_kernel<DT, V, TPR, NV><<<(unsigned)(((int64_t)R + rows - 1) / rows), norm_threads(TPR), 0, s>>>(a);
+        });
+    });
+    return launch_status();
+}
