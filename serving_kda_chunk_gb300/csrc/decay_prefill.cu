@@ -1,101 +1,778 @@
 // decay_prefill.cu -- kda_decay_prefill: linear attention with a decay a head over packed sequences.
 //
-// Token by token: a block holds 32 value channels of one (sequence, head) state in registers and walks the
-// sequence, 16 tokens staged at a time.  The plainest right form; bound by its serial chain.
+// Chunks of 128 tokens.  With G_i the sum of the log decays up to token i of the chunk (S_0 the state before it):
+//     o_i = scale ( sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j + e^{G_i} S_0^T q_i ),
+//     S_C = e^{G_C} S_0 + sum_j e^{G_C - G_j} k_j v_j^T.
+// Four products of 128 x 128 x 128 a chunk and head on the tensor cores (tcgen05, accumulators in tensor memory):
+//     scores Q K^T;  P V with the weighted, masked scores P;  Q S_0;  V^T K~ with the decayed keys K~.
+// The last does not depend on the state, so the chain from chunk to chunk is S <- a S + V^T K~ in registers, 64
+// elements a thread, and the state never collects the products' own rounding.
+//
+// What is rounded to the input type, and why that is enough: P and S_0, once each, for a product that is then
+// rounded to a 16-bit output (their errors lie on the two summands of o, so together they weigh as much as the
+// output's own rounding).  The decayed keys enter the fp32 state: they are split into parts of the input type,
+// three for bf16 (2^-25 left), two for fp16 (2^-22 left), and V^T K~ is as many products.  fp16 scores and states
+// are scaled by a power of two (a row's, a chunk's) to the upper end of fp16's range first.
+//
+// Decays are kept per block of 32 tokens: D_i = G_i - G_end(block) >= 0 and the blocks' totals, from a sum in
+// 64 bits.  A weight of an earlier block is then e^{G_i - G_end} (a row's factor) times e^{G_end - G_j} (a
+// column's), both at most 1, and only the diagonal blocks take an exponential an element.  A forgotten state
+// (-104 a token) inside a chunk leaves the differences exact enough: |D| is 150 a forgetting, in log2 units.
+//
+// Bound by HBM on paper: 128 KiB a chunk and head, 5700 cycles of an SM's share.  One CTA a SM: a warp loads
+// (TMA), one issues products, one sums decays, four warps weigh scores and write results, eight split keys and
+// carry the state.  K and V are double-buffered, Q single (its load runs under the products that need no Q).
+//
+// Balance: the (sequence, head) pairs' chunks lie in one row, cut into equal ranges, one a CTA.  A pair cut
+// once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its
+// end last.  A pair over more CTAs: those in the middle first sum up their range's own state (K and V only, read
+// twice), leave it, and then start from the states before theirs joined in order.  CTAs wait for one another, so
+// this is a cooperative launch; every wait has a limit.
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
+#include "umma.cuh"
 
 #include <initializer_list>
 
 namespace kda {
 namespace {
 
+using namespace umma;
+
 constexpr int kDecayChunk = 128;
+constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
+constexpr int kCutChunks = 2;          // a CTA's least range: below it one CTA walks the pair
+constexpr int kPreDecayThreads = 512;
+constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
+constexpr uint32_t kWaitLimit = 1u << 18;
+constexpr uint32_t kFlagLimit = 1u << 21;
 
 struct DecayPrefillArgs {
-    LatentRows q, k, v, out;
+    LatentRows out;
     const float *head_decay, *log_decay;
     const int32_t *cu, *init_slot, *final_slot, *track_idx;
     void *pool, *track;
     int32_t* dev_status;
     int64_t P;
-    int32_t N, T, H, group, M, in_dt, out_dt, st;
+    int32_t N, T, H, group, M, hq, hk, hv, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
     float scale;
+    // of a cut launch: a flag and a decay a CTA, then its state
+    uint32_t* flags;
+    float* decays;
+    float4* states;
 };
 
-__global__ void __launch_bounds__(128) decay_serial_kernel(const DecayPrefillArgs a) {
-    constexpr int TT = 16, RW = 8;
-    __shared__ __align__(16) float sq[TT][kD], sk[TT][kD], sv[TT][32];
-    __shared__ float dec[TT];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = blockIdx.x & 3, unit = blockIdx.x >> 2;
-    const int n = unit / a.H, h = unit - n * a.H, hk = h / a.group;
-    const bool lead = threadIdx.x == 0 && part == 0 && h == 0;
-    const int64_t first = a.cu[n], last = a.cu[n + 1];
-    if (first < 0 || last < first || last > a.T) {
-        if (lead) report(a.dev_status, KDA_DEV_BAD_SEQLEN);
-        return;
-    }
-    const int64_t src = a.init_slot ? a.init_slot[n] : -1, dst = a.final_slot ? a.final_slot[n] : -1;
-    if (src >= a.P || dst >= a.P) {
-        if (lead) report(a.dev_status, KDA_DEV_BAD_SLOT);
-        return;
-    }
-    const int row0 = part * 32 + warp * RW;
-    const size_t at = (size_t)row0 * kD + 4 * lane;
-    float4 s[RW];
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-        s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src >= 0) s[i] = state_load4(a.pool, state_elem(src, a.H, h) + at + (size_t)i * kD, a.st);
-    }
-    const int64_t chunks = (last - first + kDecayChunk - 1) / kDecayChunk;
-    for (int m = 0; lead && m < a.M; ++m) {
-        const int c = a.track_idx[(int64_t)n * a.M + m];
-        if (c < -1 || c >= chunks) report(a.dev_status, KDA_DEV_BAD_TRACK);
-    }
-    for (int64_t t0 = first; t0 < last; t0 += TT) {
-        if ((t0 - first) % kDecayChunk == 0)
-            for (int m = 0; m < a.M; ++m)
-                if (a.track_idx[(int64_t)n * a.M + m] == (t0 - first) / kDecayChunk)
-#pragma unroll
-                    for (int i = 0; i < RW; ++i)
-                        state_store4(a.track, state_elem((int64_t)n * a.M + m, a.H, h) + at + (size_t)i * kD, s[i], a.st);
-        const int nt = (int)min((int64_t)TT, last - t0);
-        __syncthreads();
-        for (int t = warp; t < nt; t += 4) {
-            auto row = [&](const LatentRows& d, int head) {
-                return reinterpret_cast<const uint8_t*>(d.base) + ((t0 + t) * d.rs + head * d.hs) * 2;
-            };
-            const float4 q = load4_as(row(a.q, hk), 4 * lane, a.in_dt);
-            *reinterpret_cast<float4*>(&sq[t][4 * lane]) = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
-            *reinterpret_cast<float4*>(&sk[t][4 * lane]) = load4_as(row(a.k, hk), 4 * lane, a.in_dt);
-            sv[t][lane] = load1_as(row(a.v, h), part * 32 + lane, a.in_dt);
-        }
-        if (threadIdx.x < nt) dec[threadIdx.x] = expf(log_decay_of(a.head_decay, a.log_decay, t0 + threadIdx.x, a.H, h));
-        __syncthreads();
-        for (int t = 0; t < nt; ++t) {
-            const float4 k = *reinterpret_cast<const float4*>(&sk[t][4 * lane]);
-            const float4 q = *reinterpret_cast<const float4*>(&sq[t][4 * lane]);
-            float o = 0.f;
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                s[i] = f4_fma(sv[t][warp * RW + i], k, f4_mul(s[i], make_float4(dec[t], dec[t], dec[t], dec[t])));
-                const float x = warp_sum(f4_dot(s[i], q));
-                if (lane == i) o = x;
-            }
-            if (lane < RW) {
-                void* p = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base) +
-                                               ((t0 + t) * a.out.rs + h * a.out.hs) * dtype_bytes(a.out_dt));
-                store1_as(p, row0 + lane, o, a.out_dt);
-            }
-        }
-    }
-    if (dst >= 0)
-#pragma unroll
-        for (int i = 0; i < RW; ++i) state_store4(a.pool, state_elem(dst, a.H, h) + at + (size_t)i * kD, s[i], a.st);
+struct DecayMaps {
+    CUtensorMap q, k, v;
+};
+
+// shared memory
+constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_X1 = 5 * kTile, DS_X2 = 6 * kTile, DS_G = 7 * kTile,
+                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 64, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
+                   DS_MAX = DS_SCAN + 136, DS_SCALE = DS_MAX + 64, DS_SMEM = DS_SCALE + 8;
+static_assert(DS_SMEM <= 232448 && DS_SCAN % 8 == 0 && DS_BAR % 8 == 0, "shared memory plan");
+constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 6, B_SPLIT = 7, B_VK = 8, B_S = 10, B_QS = 11, B_O = 12,
+              B_OFREE = 13, B_GF = 14, B_GFREE = 16, B_DRAIN = 18, B_NEVER = 19, B_COUNT = 20;
+// tensor memory: scores (their weights in the first half), P V, Q S, V^T K~
+constexpr uint32_t DT_SC = 0, DT_PV = 128, DT_QS = 256, DT_VK = 384;
+
+// Chunks of a sequence, one for an empty one (its state is passed on), 0 for a refused one.
+__device__ __forceinline__ int seq_chunks(const DecayPrefillArgs& a, int n, int& bad) {
+    const int first = a.cu[n], last = a.cu[n + 1];
+    bad = 0;
+    if (first < 0 || last < first || last > a.T) bad |= KDA_DEV_BAD_SEQLEN;
+    if ((a.init_slot && a.init_slot[n] >= a.P) || (a.final_slot && a.final_slot[n] >= a.P)) bad |= KDA_DEV_BAD_SLOT;
+    return bad ? 0 : last == first ? 1 : (last - first + kDecayChunk - 1) / kDecayChunk;
 }
+
+enum PieceStart { kFromInit, kFromOthers, kFromZero };
+enum PieceEnd { kNothing, kFinal, kPublish };
+
+// Consecutive chunks c0 .. c1 - 1 of one (sequence, head).
+struct Piece {
+    int n, h, c0, c1, row0, rows;  // the sequence's first row and its rows
+    bool state_only;
+    int start, end;
+};
+
+// A CTA's range of chunks: where it begins (a unit and the chunks of it that lie before) and where its last chunk lies.
+struct Range {
+    int fn, fh, fo, ln, lh, lo;
+};
+
+// The pieces of a range in the order they are taken (see the top).  All roles walk them alike.
+struct Pieces {
+    Range r;
+    int phase = 0, n, h;
+    __device__ explicit Pieces(const Range& x) : r(x), n(x.fn), h(x.fh) {}
+    __device__ __forceinline__ bool emit(const DecayPrefillArgs& a, Piece& p, int n_, int h_, int c0, int c1, bool only,
+                                         int start, int end) {
+        p.n = n_, p.h = h_, p.c0 = c0, p.c1 = c1, p.state_only = only, p.start = start, p.end = end;
+        p.row0 = a.cu[n_];
+        p.rows = a.cu[n_ + 1] - p.row0;
+        return true;
+    }
+    __device__ __forceinline__ void step(const DecayPrefillArgs& a) {
+        int bad;
+        if (++h < a.H) return;
+        h = 0;
+        do ++n;
+        while (n <= r.ln && seq_chunks(a, n, bad) == 0);
+    }
+    __device__ bool next(const DecayPrefillArgs& a, Piece& p) {
+        int bad;
+        const bool same = r.fn == r.ln && r.fh == r.lh;
+        const bool cut = r.lo + 1 < seq_chunks(a, r.ln, bad);  // the last unit goes on in the next range
+        if (phase == 0) {
+            if (same && r.fo > 0 && cut) {
+                phase = 3;
+                return emit(a, p, r.fn, r.fh, r.fo, r.lo + 1, true, kFromZero, kPublish);
+            }
+            phase = 1;
+            if (r.fo > 0) step(a);
+            if (cut) {
+                if (same) phase = 4;
+                return emit(a, p, r.ln, r.lh, 0, r.lo + 1, false, kFromInit, kPublish);
+            }
+        }
+        if (phase == 1) {
+            const bool before = n < r.ln || (n == r.ln && h < r.lh), at = n == r.ln && h == r.lh;
+            if (before || (at && !cut)) {
+                const int un = n, uh = h;
+                step(a);
+                return emit(a, p, un, uh, 0, seq_chunks(a, un, bad), false, kFromInit, kFinal);
+            }
+            phase = 2;
+        }
+        if (phase == 2) {
+            phase = 4;
+            if (r.fo > 0) return emit(a, p, r.fn, r.fh, r.fo, seq_chunks(a, r.fn, bad), false, kFromOthers, kFinal);
+        }
+        if (phase == 3) {
+            phase = 4;
+            return emit(a, p, r.fn, r.fh, r.fo, r.lo + 1, false, kFromOthers, kNothing);
+        }
+        return false;
+    }
+};
+
+// ... and their chunks.
+struct Chunks {
+    Pieces pieces;
+    Piece p;
+    int c;
+    bool any;
+    __device__ Chunks(const DecayPrefillArgs& a, const Range& r) : pieces(r) {
+        any = pieces.next(a, p);
+        c = p.c0;
+    }
+    __device__ __forceinline__ void next(const DecayPrefillArgs& a) {
+        if (++c < p.c1) return;
+        any = pieces.next(a, p);
+        c = p.c0;
+    }
+};
+
+__device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float lds_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The power of two that takes x into [2^13, 2^14); 1 for zero, infinities and NaN.
+__device__ __forceinline__ float range_scale(float x) {
+    const int e = (int)(__float_as_uint(x) >> 23) & 255;
+    return x == 0.f || e == 255 ? 1.f : __uint_as_float((uint32_t)min(max(267 - e, 2), 252) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
+template <int DT>
+__global__ void __launch_bounds__(kPreDecayThreads, 1)
+    decay_prefill_kernel(const __grid_constant__ DecayMaps maps, const __grid_constant__ DecayPrefillArgs a) {
+    using E = Elem<DT>;
+    constexpr bool kF16 = DT == KDA_F16;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* ctrl = reinterpret_cast<int*>(sm + DS_CTRL);  // 0 tensor memory, 1 waits that ran out, 2.. the range, 8 CTAs, 10 all chunks
+    volatile long long* scan = reinterpret_cast<long long*>(sm + DS_SCAN);
+    auto bar = [&](int i) { return sb + DS_BAR + 8 * i; };
+    const bool cut = a.flags != nullptr;
+
+    if (tid == 0) {
+        if (a.T > 0) {
+            prefetch_map(&maps.q);
+            prefetch_map(&maps.k);
+            prefetch_map(&maps.v);
+        }
+        ctrl[1] = 0;
+    }
+    // ---- this CTA's range of chunks
+    Range rg;
+    int64_t x0 = 0, total = 0;
+    int ctas = 1;
+    if (!cut) {
+        int bad;
+        const int n = blockIdx.x / a.H, c = seq_chunks(a, n, bad);
+        rg = Range{n, (int)blockIdx.x - n * a.H, 0, n, (int)blockIdx.x - n * a.H, c - 1};
+        if (tid == 0 && rg.fh == 0 && bad) report(a.dev_status, bad);
+        if (c == 0) return;
+    } else {
+        auto block_scan = [&](int64_t x, int64_t& sum) {  // inclusive
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = x;
+            __syncthreads();
+            int64_t off = 0;
+            sum = 0;
+            for (int w = 0; w < kPreDecayThreads / 32; ++w) {
+                const int64_t y = scan[w];
+                if (w < warp) off += y;
+                sum += y;
+            }
+            return x + off;
+        };
+        int64_t mine = 0;
+        for (int n = tid; n < a.N; n += kPreDecayThreads) {
+            int bad;
+            mine += seq_chunks(a, n, bad);
+            if (bad && blockIdx.x == 0) report(a.dev_status, bad);
+        }
+        block_scan(mine, total);
+        total *= a.H;
+        ctas = (int)min((int64_t)gridDim.x, (total + kCutChunks - 1) / kCutChunks);
+        if ((int)blockIdx.x >= ctas) return;
+        x0 = total * blockIdx.x / ctas;
+        const int64_t x1 = total * (blockIdx.x + 1) / ctas - 1;
+        int64_t before = 0;
+        for (int base = 0; base < a.N; base += kPreDecayThreads) {
+            const int n = base + tid;
+            int bad;
+            const int c = n < a.N ? seq_chunks(a, n, bad) : 0;
+            int64_t sum;
+            const int64_t end = (before + block_scan(c, sum)) * a.H, begin = end - (int64_t)c * a.H;
+            before += sum;
+            for (int e = 0; e < 2; ++e) {
+                const int64_t x = e ? x1 : x0;
+                if (c && x >= begin && x < end) {
+                    ctrl[2 + 3 * e] = n;
+                    ctrl[3 + 3 * e] = (int)((x - begin) / c);
+                    ctrl[4 + 3 * e] = (int)((x - begin) % c);
+                }
+            }
+        }
+        __syncthreads();
+        rg = Range{ctrl[2], ctrl[3], ctrl[4], ctrl[5], ctrl[6], ctrl[7]};
+    }
+    if (tid < B_COUNT) {
+        int count = 1;
+        if (tid == B_P || tid == B_OFREE) count = 4;      // warps
+        if (tid == B_SPLIT || tid == B_S) count = 8;
+        if (tid == B_GFREE || tid == B_GFREE + 1) count = 12;
+        mbar_init(bar(tid), count);
+    }
+    if (warp == 1) tmem_alloc(sb + DS_CTRL, 512);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctrl[0];
+
+    // A wait that runs out ends its role: it arrives nowhere and writes nothing from then on, so the other roles'
+    // waits run out too.  (Roles that meet at named barriers go on meeting there.)
+    bool dead = false;
+    auto give_up = [&] {
+        dead = true;
+        ctrl[1] = 1;
+        report(a.dev_status, KDA_DEV_TIMEOUT);
+    };
+    auto wait = [&](int b, uint32_t parity) {
+        if (dead) return;
+        if (!mbar_wait(bar(b), parity, kWaitLimit)) give_up();
+    };
+    auto arrive = [&](int b) {  // of a warp
+        __syncwarp();
+        if (lane == 0 && !dead) mbar_arrive(bar(b));
+    };
+    const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay
+
+    if (warp == 0) {
+        // ================================================================ loads
+        uint32_t it = 0, m = 0;
+        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+            const uint32_t st = it & 1;
+            const int row = ch.p.row0 + ch.c * kDecayChunk, h = ch.p.h, hk = h / a.group;
+            if (it >= 2) wait(B_VK + st, ((it >> 1) - 1) & 1);
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int head, int b) {
+                if (lane != 0 || dead) return;
+                if (ch.p.rows == 0) {  // an empty sequence's one chunk: its keys and values are cleared, its scores not used
+                    mbar_arrive(bar(b));
+                    return;
+                }
+                mbar_expect_tx(bar(b), kTile);
+                tma_load_3d(sb + dst, map, 0, head, row, bar(b));
+                tma_load_3d(sb + dst + kTile / 2, map, 64, head, row, bar(b));
+            };
+            load(DS_K + st * kTile, &maps.k, hk * a.hk, B_KF + st);
+            load(DS_V + st * kTile, &maps.v, h * a.hv, B_VF + st);
+            if (!ch.p.state_only) {
+                if (m > 0) wait(B_QS, (m - 1) & 1);
+                load(DS_Q, &maps.q, hk * a.hq, B_QF);
+                ++m;
+            }
+        }
+    } else if (warp == 1) {
+        // ================================================================ products
+        // the whole warp runs this, one lane issues (umma.cuh, mma_by)
+        const uint32_t lead = elect_lane();
+        const uint32_t sb4 = (sb & 0x3ffffu) >> 4, t4 = kTile >> 4;
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint32_t i_qk = idesc_16(kF16, 128, 128, false, false, false);
+        const uint32_t i_pv = idesc_16(kF16, 128, 128, false, true, false);
+        const uint32_t i_vk = idesc_16(kF16, 128, 128, true, true, false);
+        auto q_k = [&](uint32_t st) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                mma_by(lead, tm + DT_SC, desc_k4(sb4 + DS_Q / 16, 128, s), desc_k4(sb4 + DS_K / 16 + st * t4, 128, s), i_qk, s != 0);
+            commit_by(lead, bar(B_QK));
+        };
+        auto v_k = [&](uint32_t st, uint32_t keys, uint32_t on) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                mma_by(lead, tm + DT_VK, desc_mn4(sb4 + DS_V / 16 + st * t4, kTile / 2, 1024, s),
+                       desc_mn4(sb4 + keys, kTile / 2, 1024, s), i_vk, on || s != 0);
+        };
+        uint32_t it = 0, m = 0;
+        bool asked = false;  // this chunk's scores were issued with the last chunk
+        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ++it) {
+            const uint32_t st = it & 1;
+            const bool full = !ch.p.state_only;
+            if (full) {
+                if (!asked) {
+                    wait(B_QF, m & 1);
+                    wait(B_KF + st, (it >> 1) & 1);
+                    if (__any_sync(~0u, dead)) break;
+                    q_k(st);
+                }
+                wait(B_S, m & 1);
+                if (m > 0) wait(B_OFREE, (m - 1) & 1);
+                if (__any_sync(~0u, dead)) break;
+                fence_after();
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_by(lead, tm + DT_QS, desc_k4(sb4 + DS_Q / 16, 128, s), desc_k4(sb4 + DS_X1 / 16, 128, s), i_qk, s != 0);
+                commit_by(lead, bar(B_QS));
+            }
+            wait(B_VF + st, (it >> 1) & 1);
+            if (full) wait(B_P, m & 1);
+            wait(B_SPLIT, it & 1);
+            if (__any_sync(~0u, dead)) break;
+            fence_after();
+            if (full) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_ta_by(lead, tm + DT_PV, tm + DT_SC + 8 * s, desc_mn4(sb4 + DS_V / 16 + st * t4, kTile / 2, 1024, s), i_pv, s != 0);
+                commit_by(lead, bar(B_O));
+                ++m;
+            }
+            // the smallest part first: what a sum of products loses goes by its size so far
+            if constexpr (!kF16) v_k(st, DS_X1 / 16, 0);
+            v_k(st, DS_X2 / 16, !kF16);
+            v_k(st, DS_K / 16 + st * t4, 1);
+            commit_by(lead, bar(B_VK + st));
+            ch.next(a);
+            asked = ch.any && !ch.p.state_only;
+            if (asked) {
+                wait(B_QF, m & 1);
+                wait(B_KF + (st ^ 1), ((it + 1) >> 1) & 1);
+                if (__any_sync(~0u, dead)) break;
+                q_k(st ^ 1);
+            }
+        }
+        commit_by(lead, bar(B_DRAIN));
+        dead = false;
+        wait(B_DRAIN, 0);
+    } else if (warp == 2) {
+        // ================================================================ decays: lane l has tokens 4l .. 4l + 3
+        uint32_t it = 0;
+        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+            const uint32_t st = it & 1;
+            const int first = ch.c * kDecayChunk + 4 * lane;
+            double g[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                g[e] = first + e < ch.p.rows ? (double)log_decay_of(a.head_decay, a.log_decay, (int64_t)ch.p.row0 + first + e, a.H, ch.p.h) : 0.0;
+            g[0] *= 1.4426950408889634;
+#pragma unroll
+            for (int e = 1; e < 4; ++e) g[e] = g[e - 1] + g[e] * 1.4426950408889634;
+            double x = g[3];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            const double end = __shfl_sync(~0u, x, lane | 7), all = __shfl_sync(~0u, x, 31);
+            const double last = __shfl_sync(~0u, x, (lane & 24) - 1 < 0 ? 0 : (lane & 24) - 1);
+            const double excl = x - g[3];
+            float4 d;
+            d.x = (float)(excl + g[0] - end);
+            d.y = (float)(excl + g[1] - end);
+            d.z = (float)(excl + g[2] - end);
+            d.w = (float)(x - end);
+            if (it >= 2) wait(B_GFREE + st, ((it >> 1) - 1) & 1);
+            if (!dead) {
+                const uint32_t at = DS_G + st * 1024 + 16 * lane;
+                *reinterpret_cast<float4*>(sm + at) = d;
+                *reinterpret_cast<float4*>(sm + at + 512) = make_float4(ex2(-d.x), ex2(-d.y), ex2(-d.z), ex2(-d.w));
+                float* tot = reinterpret_cast<float*>(sm + DS_TOT + st * 32);
+                if ((lane & 7) == 0) tot[lane >> 3] = (float)(end - (lane < 8 ? 0.0 : last));
+                if (lane == 0) tot[4] = (float)exp2(all);
+            }
+            arrive(B_GF + st);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ================================================================ weights and results: a thread has a row
+        const int w = warp & 3, row = 32 * w + lane;
+        const uint32_t tl = tmem + ((uint32_t)(w * 32) << 16);
+        const float scale = a.scale;
+        uint32_t it = 0, m = 0;
+        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+            const uint32_t st = it & 1;
+            wait(B_GF + st, (it >> 1) & 1);
+            if (ch.p.state_only) {
+                arrive(B_GFREE + st);
+                continue;
+            }
+            const uint32_t gd = g_d + st * 1024;
+            const float4 tot4 = lds_f4(g_tot + st * 32);
+            const float tot[4] = {tot4.x, tot4.y, tot4.z, tot4.w};
+            const float d = lds_f1(gd + 4 * row);
+            wait(B_QK, m & 1);
+            if (__any_sync(~0u, dead)) break;
+            fence_after();
+            float ps = 1.f;  // fp16: the row's scale
+            if constexpr (kF16) {
+                float mx = 0.f;
+                for (int b = 0; b <= w; ++b) {
+                    float s[32];
+                    ld32(tl + DT_SC + 32 * b, s);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * b + e <= row ? fabsf(s[e]) : 0.f);
+                }
+                ps = range_scale(mx * fabsf(scale));
+            }
+            const float sp = kF16 ? scale * ps : scale;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+                if (b < w) {
+                    float e = d;
+#pragma unroll
+                    for (int x = 1; x < 4; ++x) e += x > b && x <= w ? tot[x] : 0.f;
+                    const float f = sp * ex2(e);
+                    float s[32];
+                    ld32(tl + DT_SC + 32 * b, s);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 c = lds_f4(gd + 512 + 4 * (32 * b + x));
+                        p[x / 2] = E::put2(s[x] * c.x * f, s[x + 1] * c.y * f);
+                        p[x / 2 + 1] = E::put2(s[x + 2] * c.z * f, s[x + 3] * c.w * f);
+                    }
+                } else if (b == w) {
+                    float s[32];
+                    ld32(tl + DT_SC + 32 * b, s);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 c = lds_f4(gd + 4 * (32 * b + x));
+                        const float cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) s[x + y] = x + y <= lane ? s[x + y] * sp * ex2(d - cc[y]) : 0.f;
+                        p[x / 2] = E::put2(s[x], s[x + 1]);
+                        p[x / 2 + 1] = E::put2(s[x + 2], s[x + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) p[x] = 0;
+                }
+                st16u(tl + DT_SC + 16 * b, p);
+            }
+            wait_st();
+            fence_before();
+            arrive(B_P);
+            float e = d;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e += x <= w ? tot[x] : 0.f;
+            arrive(B_GFREE + st);
+            wait(B_O, m & 1);
+            if (__any_sync(~0u, dead)) break;
+            fence_after();
+            float fs = scale * ex2(e), fp = 1.f;
+            if constexpr (kF16) {
+                fs *= pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
+                fp = pow2_inverse(ps);
+            }
+            const int at = ch.c * kDecayChunk + row;
+            const int64_t o_at = ((int64_t)ch.p.row0 + at) * a.out.rs + ch.p.h * a.out.hs;
+            uint8_t* o_row = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base)) + o_at * dtype_bytes(a.out_dt);
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t x[32], y[32];
+                ld32_issue(tl + DT_QS + 32 * b, x);
+                ld32_issue(tl + DT_PV + 32 * b, y);
+                wait_ld();
+                if (b == 3) {
+                    fence_before();
+                    arrive(B_OFREE);
+                }
+                float o[32];
+#pragma unroll
+                for (int z = 0; z < 32; ++z)
+                    o[z] = fmaf(__uint_as_float(x[z]), fs, kF16 ? __uint_as_float(y[z]) * fp : __uint_as_float(y[z]));
+                if (at < ch.p.rows) {
+#pragma unroll
+                    for (int z = 0; z < 32; z += 4) store4_as(o_row, 32 * b + z, make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]), a.out_dt);
+                }
+            }
+            ++m;
+        }
+    } else if (warp >= 8) {
+        // ================================================================ keys and state: a thread has half a row of S^T
+        const int t = tid - 256, half = t >> 7, v = t & 127;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + DT_VK + 64 * half;
+        float S[64], decay = 1.f;
+        uint32_t it = 0, m = 0, converted = 0;
+        // the state before chunk c, as the product's operand (and as a snapshot)
+        auto convert = [&](const Piece& p, int c) {
+            if (a.M > 0 && p.rows > 0) {
+                for (int base = 0; base < a.M; base += 32) {
+                    const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
+                    for (uint32_t hit = __ballot_sync(~0u, x == c); hit; hit &= hit - 1) {
+                        const size_t to = state_elem((int64_t)p.n * a.M + base + __ffs(hit) - 1, a.H, p.h) + v * kD + 64 * half;
+                        if (!dead)
+#pragma unroll
+                            for (int e = 0; e < 64; e += 4) state_store4(a.track, to + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]), a.st);
+                    }
+                }
+            }
+            float ss = 1.f;
+            if constexpr (kF16) {
+                float mx = 0.f;
+#pragma unroll
+                for (int e = 0; e < 64; ++e) mx = fmaxf(mx, fabsf(S[e]));
+                const uint32_t wm = __reduce_max_sync(~0u, __float_as_uint(mx));
+                float* maxima = reinterpret_cast<float*>(sm + DS_MAX);
+                bar_named(1, 256);  // the last use has been read
+                if (lane == 0) maxima[warp - 8] = __uint_as_float(wm);
+                bar_named(1, 256);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) mx = fmaxf(mx, maxima[x]);
+                ss = range_scale(mx);
+                if (t == 0) *reinterpret_cast<float*>(sm + DS_SCALE + 4 * (converted & 1)) = ss;
+            }
+            ++converted;
+#pragma unroll
+            for (int e = 0; e < 64; e += 8) {
+                uint4 x;
+                x.x = E::put2(S[e] * ss, S[e + 1] * ss);
+                x.y = E::put2(S[e + 2] * ss, S[e + 3] * ss);
+                x.z = E::put2(S[e + 4] * ss, S[e + 5] * ss);
+                x.w = E::put2(S[e + 6] * ss, S[e + 7] * ss);
+                sts128(sb + DS_X1 + half * (kTile / 2) + v * 128 + (((e >> 3) ^ (v & 7)) << 4), x);
+            }
+            fence_async_smem();
+            arrive(B_S);
+        };
+        for (Chunks ch(a, rg); ch.any; ch.next(a), ++it) {
+            const uint32_t st = it & 1;
+            const Piece& p = ch.p;
+            const bool full = !p.state_only;
+            const int left = p.rows - ch.c * kDecayChunk;  // rows from this chunk on
+            if (ch.c == p.c0) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) S[e] = 0.f;
+                decay = 1.f;
+                if (p.start == kFromInit) {
+                    const int src = a.init_slot ? a.init_slot[p.n] : -1;
+                    if (src >= 0) {
+                        const size_t from = state_elem(src, a.H, p.h) + v * kD + 64 * half;
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4) {
+                            const float4 x = state_load4(a.pool, from + e, a.st);
+                            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
+                        }
+                    }
+                    if (p.h == 0 && t == 0)
+                        for (int x = 0; x < a.M; ++x) {
+                            const int c = a.track_idx[(int64_t)p.n * a.M + x];
+                            if (c < -1 || c >= (p.rows + kDecayChunk - 1) / kDecayChunk) report(a.dev_status, KDA_DEV_BAD_TRACK);
+                        }
+                } else if (p.start == kFromOthers) {
+                    // the CTA with the unit's beginning left a state, those after it their ranges' own
+                    const int j0 = (int)(((x0 - rg.fo + 1) * ctas - 1) / total);
+                    for (int j = j0; j < (int)blockIdx.x; ++j) {
+                        uint32_t set = 0;
+                        for (uint32_t polls = 0; polls < kFlagLimit && !set && !dead; ++polls) {
+                            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(set) : "l"(a.flags + j) : "memory");
+                            if (!set) __nanosleep(64);
+                        }
+                        if (!set && !dead) give_up();
+                        if (dead) break;
+                        const float f = *(volatile float*)(a.decays + j);
+                        const float4* from = a.states + (size_t)j * 4096 + t;
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4) {
+                            const float4 x = __ldcg(from + e * 64);
+                            S[e] = fmaf(f, S[e], x.x), S[e + 1] = fmaf(f, S[e + 1], x.y);
+                            S[e + 2] = fmaf(f, S[e + 2], x.z), S[e + 3] = fmaf(f, S[e + 3], x.w);
+                        }
+                    }
+                }
+                if (full) convert(p, ch.c);
+            }
+            wait(B_GF + st, (it >> 1) & 1);
+            float f[4];
+            {
+                const float4 tot = lds_f4(g_tot + st * 32);
+                const float after[4] = {tot.y + tot.z + tot.w, tot.z + tot.w, tot.w, 0.f};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) f[b] = ex2(after[b] - lds_f1(g_d + st * 1024 + 4 * (32 * b + (t >> 3))));
+            }
+            const float ac = lds_f1(g_tot + st * 32 + 16);
+            arrive(B_GFREE + st);
+            wait(B_KF + st, (it >> 1) & 1);
+            if (full) wait(B_QK, m & 1);
+            if (left < kDecayChunk) {
+                // rows past the sequence have a weight of zero, and so has to be the value
+                wait(B_VF + st, (it >> 1) & 1);
+                for (int x = max(left, 0) * 8 + t; x < 1024 && !dead; x += 256) {
+                    sts128(sb + DS_V + st * kTile + 16 * x, make_uint4(0, 0, 0, 0));
+                    sts128(sb + DS_V + st * kTile + kTile / 2 + 16 * x, make_uint4(0, 0, 0, 0));
+                }
+            }
+            uint4 lo[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t at = 16 * (256 * x + t);
+                const int row = 32 * (x & 3) + (t >> 3);
+                uint4 k = lds128(sb + DS_K + st * kTile + at), mid;
+                if (row >= left) k = make_uint4(0, 0, 0, 0);
+                const float2 ff = make_float2(f[x & 3], f[x & 3]);
+                auto part = [&](uint32_t& hi, uint32_t& md, uint32_t& l) {
+                    float2 y = __fmul2_rn(E::get2(hi), ff);
+                    if (row >= left) y = make_float2(0.f, 0.f);  // whatever the factor
+                    const float2 minus = make_float2(-1.f, -1.f);
+                    hi = E::put2(y.x, y.y);
+                    y = __ffma2_rn(E::get2(hi), minus, y);
+                    md = E::put2(y.x, y.y);
+                    if constexpr (!kF16) {
+                        y = __ffma2_rn(E::get2(md), minus, y);
+                        l = E::put2(y.x, y.y);
+                    }
+                };
+                part(k.x, mid.x, lo[x].x);
+                part(k.y, mid.y, lo[x].y);
+                part(k.z, mid.z, lo[x].z);
+                part(k.w, mid.w, lo[x].w);
+                if (!dead) {
+                    sts128(sb + DS_K + st * kTile + at, k);
+                    sts128(sb + DS_X2 + at, mid);
+                }
+            }
+            if constexpr (!kF16) {
+                if (full) wait(B_QS, m & 1);  // the state's operand has been read
+                if (!dead)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) sts128(sb + DS_X1 + 16 * (256 * x + t), lo[x]);
+            }
+            fence_async_smem();
+            arrive(B_SPLIT);
+            if (full) ++m;
+            wait(B_VK + st, (it >> 1) & 1);
+            fence_after();
+            decay *= ac;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float x[32];
+                ld32(tl + 32 * b, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(ac, S[32 * b + e], x[e]);
+            }
+            fence_before();
+            dead = __any_sync(~0u, dead);
+            if (ch.c + 1 < p.c1) {
+                if (full) convert(p, ch.c + 1);
+            } else if (p.end == kFinal) {
+                const int dst = a.final_slot ? a.final_slot[p.n] : -1;
+                if (dst >= 0 && !dead) {
+                    const size_t to = state_elem(dst, a.H, p.h) + v * kD + 64 * half;
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) state_store4(a.pool, to + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]), a.st);
+                }
+            } else if (p.end == kPublish) {
+                float4* to = a.states + (size_t)blockIdx.x * 4096 + t;
+#pragma unroll
+                for (int e = 0; e < 64; e += 4) __stcg(to + e * 64, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
+                if (t == 0) a.decays[blockIdx.x] = decay;
+                __threadfence();
+                if (!bar_named_or(2, 256, dead) && t == 0)
+                    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + blockIdx.x), "r"(1u) : "memory");
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    // Every load was waited for by a role that is done.  After a wait that ran out that does not hold: a bounded
+    // wait on a barrier that nothing arrives on (about a second) lets them land.
+    if (ctrl[1] && warp == 0) {
+        mbar_wait(bar(B_NEVER), 0, kWaitLimit);
+        __syncwarp();
+    }
+    __syncthreads();
+    fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head and 128 rows.
+bool chunk_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int H, int T) {
+    // a dimension that is not stepped along (one head or row, or heads that share a row) has size 1 and any legal stride
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)(r.hs ? H : 1), (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)(r.hs ? r.hs : kD) * 2, (cuuint64_t)(r.rs ? r.rs : kD) * 2};
+    const cuuint32_t box[3] = {64, 1, kDecayChunk};
+    return encode_16bit(map, dt, 3, r.base, dims, strides, box);
+}
+
+// Bytes of a cut launch's workspace: flags, decays, states; none for prompts that no cut helps.
+bool may_cut(int32_t T_tot) { return T_tot > kDecayChunk * kCutChunks; }
+constexpr size_t kCutBytes = 2 * 4 * kDecayCtas + (size_t)kDecayCtas * kD * kD * 4;
 
 }  // namespace
 }  // namespace kda
@@ -103,8 +780,7 @@ __global__ void __launch_bounds__(128) decay_serial_kernel(const DecayPrefillArg
 using namespace kda;
 
 extern "C" size_t kda_decay_prefill_workspace_size(int32_t T_tot, int32_t N, int32_t H) {
-    (void)T_tot, (void)N, (void)H;
-    return 16;
+    return may_cut(T_tot) && N > 0 && H > 0 ? kCutBytes : 16;
 }
 
 extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
@@ -124,18 +800,70 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
     if (N == 0) return KDA_OK;
     // without rows there is nothing to place, and states are passed on
     KDA_REQUIRE(T_tot == 0 || (rows_ok(q) && rows_ok(k) && rows_ok(v) && rows_ok(out)), KDA_ERR_INVALID_ARG);
-    for (const kda_rows_desc* d : {q, k, v})
-        KDA_REQUIRE(T_tot == 0 || ((d->row_stride > 0 || T_tot == 1) && d->head_stride >= 0), KDA_ERR_INVALID_ARG);
+    if (T_tot > 0)
+        for (const kda_rows_desc* d : {q, k, v})
+            KDA_REQUIRE((d->row_stride > 0 || T_tot == 1) && d->row_stride >= 0 && d->head_stride >= 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(cu_seqlens && (head_decay || log_decay), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(state_pool || (!init_slot && !final_slot), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(M == 0 || (track_chunk_idx && track_state), KDA_ERR_INVALID_ARG);
     const void* ptrs[] = {cu_seqlens, head_decay, log_decay, state_pool, init_slot, final_slot, track_chunk_idx, track_state, workspace};
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
-    (void)ws_bytes;
-    auto rows = [&](const kda_rows_desc* d) { return T_tot ? as_rows(d) : LatentRows{}; };
-    const DecayPrefillArgs a{rows(q), rows(k), rows(v), rows(out), head_decay, log_decay, cu_seqlens,
-                             init_slot, final_slot, track_chunk_idx, state_pool, track_state, dev_status, P, N, T_tot,
-                             H, H / Hk, M, in_dtype, out_dtype, state_type(flags), scale};
-    decay_serial_kernel<<<(unsigned)(N * H * 4), 128, 0, as_stream(stream)>>>(a);
+    DecayMaps maps;
+    DecayPrefillArgs a{};
+    if (T_tot > 0) {
+        const LatentRows rq = as_rows(q), rk = as_rows(k), rv = as_rows(v);
+        KDA_REQUIRE(chunk_map(&maps.q, in_dtype, rq, Hk, T_tot) && chunk_map(&maps.k, in_dtype, rk, Hk, T_tot) &&
+                        chunk_map(&maps.v, in_dtype, rv, H, T_tot),
+                    KDA_ERR_CUDA);
+        a.hq = rq.hs != 0, a.hk = rk.hs != 0, a.hv = rv.hs != 0;
+        a.out = as_rows(out);
+    }
+    a.head_decay = head_decay;
+    a.log_decay = log_decay;
+    a.cu = cu_seqlens;
+    a.init_slot = init_slot;
+    a.final_slot = final_slot;
+    a.track_idx = track_chunk_idx;
+    a.pool = state_pool;
+    a.track = track_state;
+    a.dev_status = dev_status;
+    a.P = P;
+    a.N = N;
+    a.T = T_tot;
+    a.H = H;
+    a.group = H / Hk;
+    a.M = M;
+    a.out_dt = out_dtype;
+    a.st = state_type(flags);
+    a.scale = scale;
+    auto* f = in_dtype == KDA_BF16 ? decay_prefill_kernel<KDA_BF16> : decay_prefill_kernel<KDA_F16>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DS_SMEM) != cudaSuccess)
+        return runtime_failed();
+    cudaStream_t s = as_stream(stream);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(N * H));
+    cfg.blockDim = dim3(kPreDecayThreads);
+    cfg.dynamicSmemBytes = DS_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    if (workspace && may_cut(T_tot)) {
+        KDA_REQUIRE(ws_bytes >= kCutBytes, KDA_ERR_INVALID_ARG);
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return runtime_failed();
+        const int64_t most = ((int64_t)T_tot / kDecayChunk + N) * H;  // chunks
+        const int64_t ctas = (most + kCutChunks - 1) / kCutChunks;
+        const int most_ctas = sms < kDecayCtas ? sms : kDecayCtas;
+        cfg.gridDim.x = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
+        a.flags = static_cast<uint32_t*>(workspace);
+        a.decays = reinterpret_cast<float*>(a.flags + kDecayCtas);
+        a.states = reinterpret_cast<float4*>(a.decays + kDecayCtas);
+        if (cudaMemsetAsync(a.flags, 0, 4 * kDecayCtas, s) != cudaSuccess) return runtime_failed();
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, f, maps, a) != cudaSuccess) return runtime_failed();
     return launch_status();
 }

@@ -294,14 +294,14 @@ def test_prefill_in_graphs_and_on_two_streams():
         s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
             kda.kda_decay_prefill(c["q"], c["k"], c["v"], c["cu"], out, **args)
-        runs.append((g, s, out, pool))
+        runs.append((g, s, out, pool, args))  # a graph keeps no tensor alive
     torch.cuda.synchronize()
     for _ in range(20):
-        for g, s, _, _ in runs:
+        for g, s, *_ in runs:
             with torch.cuda.stream(s):
                 g.replay()
     torch.cuda.synchronize()
-    for (_, _, out, pool), (wo, wp) in zip(runs, wants):
+    for (_, _, out, pool, _), (wo, wp) in zip(runs, wants):
         assert torch.equal(out, wo) and torch.equal(pool, wp)
 
 
