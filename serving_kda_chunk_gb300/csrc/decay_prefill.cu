@@ -56,6 +56,7 @@ struct DecayPrefillArgs {
     int32_t* dev_status;
     int64_t P;
     int32_t N, T, H, group, M, hq, hk, hv, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
+    bool sectors;  // output rows start on 32-byte boundaries
     float scale;
     // of a cut launch: a flag and a decay a CTA, then its state
     uint32_t* flags;
@@ -69,11 +70,11 @@ struct DecayMaps {
 
 // shared memory
 constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_X1 = 5 * kTile, DS_X2 = 6 * kTile, DS_G = 7 * kTile,
-                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 64, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
+                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 128, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
                    DS_MAX = DS_SCAN + 136, DS_SCALE = DS_MAX + 64, DS_SMEM = DS_SCALE + 8;
 static_assert(DS_SMEM <= 232448 && DS_SCAN % 8 == 0 && DS_BAR % 8 == 0, "shared memory plan");
 constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 6, B_SPLIT = 7, B_VK = 8, B_S = 10, B_QS = 11, B_O = 12,
-              B_OFREE = 13, B_GF = 14, B_GFREE = 16, B_DRAIN = 18, B_NEVER = 19, B_COUNT = 20;
+              B_OFREE = 13, B_GF = 14, B_GFREE = 16, B_MEET = 18, B_DRAIN = 19, B_NEVER = 20, B_COUNT = 21;
 // tensor memory: scores (their weights in the first half), P V, Q S, V^T K~
 constexpr uint32_t DT_SC = 0, DT_PV = 128, DT_QS = 256, DT_VK = 384;
 
@@ -157,7 +158,7 @@ struct Pieces {
     }
 };
 
-// ... and their chunks.
+// ... and their chunks, which the loading warp and the decays' warp walk; the latter tells the other roles.
 struct Chunks {
     Pieces pieces;
     Piece p;
@@ -174,6 +175,13 @@ struct Chunks {
     }
 };
 
+// What the other roles know of a chunk.
+enum ChunkFlags { kFull = 1, kFirst = 2, kLast = 4, kJoins = 8, kFinalState = 16, kLeaves = 32, kStop = 64 };
+struct ChunkInfo {
+    int n, h, c, row0;  // row0: the chunk's first row
+    int left, rows, flags, pad;  // left: rows of the sequence from this chunk on
+};
+
 __device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -184,6 +192,19 @@ __device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+
+// mbar_wait with the usual limit, its loop not unrolled (there are thirty of it).
+__device__ __forceinline__ bool wait_for(uint32_t mbar, uint32_t parity) {
+    uint32_t done = 0;
+#pragma unroll 1
+    for (uint32_t it = 0; it < kWaitLimit && !done; ++it)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
+    return done;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -203,6 +224,30 @@ __device__ __forceinline__ float lds_f1(uint32_t addr) {
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// A row's 32 results from column c on, in whole 32-byte sectors where the rows allow it: a warp's lanes write 32
+// rows, so each store is 32 accesses whatever its width (8 bytes a store took 4100 of a chunk's 14000 cycles).
+template <int ODT>
+__device__ __forceinline__ void store_row32(void* row, int c, const float (&o)[32], bool sectors) {
+    constexpr int kWords = ODT == KDA_F32 ? 32 : 16;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int e = 0; e < kWords; ++e)
+        if constexpr (ODT == KDA_F32) w[e] = __float_as_uint(o[e]);
+        else w[e] = Elem<ODT>::put2(o[2 * e], o[2 * e + 1]);
+    uint8_t* p = static_cast<uint8_t*>(row) + c * dtype_bytes(ODT);
+    if (sectors) {
+#pragma unroll
+        for (int e = 0; e < kWords; e += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 4 * e), "r"(w[e]), "r"(w[e + 1]),
+                         "r"(w[e + 2]), "r"(w[e + 3]), "r"(w[e + 4]), "r"(w[e + 5]), "r"(w[e + 6]), "r"(w[e + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < kWords; e += 4)
+            *reinterpret_cast<uint4*>(p + 4 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+    }
 }
 
 // The power of two that takes x into [2^13, 2^14); 1 for zero, infinities and NaN.
@@ -297,8 +342,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     if (tid < B_COUNT) {
         int count = 1;
         if (tid == B_P || tid == B_OFREE) count = 4;      // warps
-        if (tid == B_SPLIT || tid == B_S) count = 8;
-        if (tid == B_GFREE || tid == B_GFREE + 1) count = 12;
+        if (tid == B_SPLIT || tid == B_S || tid == B_MEET) count = 8;
+        if (tid == B_GFREE || tid == B_GFREE + 1) count = 13;
         mbar_init(bar(tid), count);
     }
     if (warp == 1) tmem_alloc(sb + DS_CTRL, 512);
@@ -308,22 +353,20 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     const uint32_t tmem = ctrl[0];
 
     // A wait that runs out ends its role: it arrives nowhere and writes nothing from then on, so the other roles'
-    // waits run out too.  (Roles that meet at named barriers go on meeting there.)
+    // waits run out too.
     bool dead = false;
-    auto give_up = [&] {
-        dead = true;
-        ctrl[1] = 1;
-        report(a.dev_status, KDA_DEV_TIMEOUT);
-    };
     auto wait = [&](int b, uint32_t parity) {
-        if (dead) return;
-        if (!mbar_wait(bar(b), parity, kWaitLimit)) give_up();
+        if (!dead) dead = !wait_for(bar(b), parity);
     };
     auto arrive = [&](int b) {  // of a warp
         __syncwarp();
         if (lane == 0 && !dead) mbar_arrive(bar(b));
     };
-    const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay
+    const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay, its ChunkInfo
+    auto info_of = [&](uint32_t st) {
+        const uint4 x = lds128(g_tot + 64 * st + 32), y = lds128(g_tot + 64 * st + 48);
+        return ChunkInfo{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, 0};
+    };
 
     if (warp == 0) {
         // ================================================================ loads
@@ -359,37 +402,38 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         const uint32_t i_qk = idesc_16(kF16, 128, 128, false, false, false);
         const uint32_t i_pv = idesc_16(kF16, 128, 128, false, true, false);
         const uint32_t i_vk = idesc_16(kF16, 128, 128, true, true, false);
+        // D (+)= A B^T over eight steps of 16; operands K-major, or with their rows along M / N.  Rolled: this
+        // kernel's roles share an instruction cache that their unrolled loops overflow (see the top).
+        auto product = [&](uint32_t d, uint32_t a4, bool a_mn, uint32_t b4, bool b_mn, uint32_t idesc, uint32_t on) {
+#pragma unroll 1
+            for (uint32_t s = 0; s < 8; ++s) {
+                const uint32_t k = (s >> 2) * 1024 + (s & 3) * 2, mn = 128 * s;
+                mma_by(lead, tm + d, desc4(a4 + (a_mn ? mn : k), a_mn ? kTile / 2 : 16, 1024),
+                       desc4(b4 + (b_mn ? mn : k), b_mn ? kTile / 2 : 16, 1024), idesc, on | s);
+            }
+        };
         auto q_k = [&](uint32_t st) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                mma_by(lead, tm + DT_SC, desc_k4(sb4 + DS_Q / 16, 128, s), desc_k4(sb4 + DS_K / 16 + st * t4, 128, s), i_qk, s != 0);
+            product(DT_SC, sb4 + DS_Q / 16, false, sb4 + DS_K / 16 + st * t4, false, i_qk, 0);
             commit_by(lead, bar(B_QK));
         };
-        auto v_k = [&](uint32_t st, uint32_t keys, uint32_t on) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                mma_by(lead, tm + DT_VK, desc_mn4(sb4 + DS_V / 16 + st * t4, kTile / 2, 1024, s),
-                       desc_mn4(sb4 + keys, kTile / 2, 1024, s), i_vk, on || s != 0);
-        };
         uint32_t it = 0, m = 0;
-        bool asked = false;  // this chunk's scores were issued with the last chunk
-        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ++it) {
+        wait(B_GF, 0);
+        int flags = __shfl_sync(~0u, info_of(0).flags, 0);
+        arrive(B_GFREE);
+        if ((flags & (kFull | kStop)) == kFull) {
+            wait(B_QF, 0);
+            wait(B_KF, 0);
+            if (!__any_sync(~0u, dead)) q_k(0);
+        }
+        for (; !(flags & kStop) && !__any_sync(~0u, dead); ++it) {
             const uint32_t st = it & 1;
-            const bool full = !ch.p.state_only;
+            const bool full = flags & kFull;
             if (full) {
-                if (!asked) {
-                    wait(B_QF, m & 1);
-                    wait(B_KF + st, (it >> 1) & 1);
-                    if (__any_sync(~0u, dead)) break;
-                    q_k(st);
-                }
                 wait(B_S, m & 1);
                 if (m > 0) wait(B_OFREE, (m - 1) & 1);
                 if (__any_sync(~0u, dead)) break;
                 fence_after();
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_by(lead, tm + DT_QS, desc_k4(sb4 + DS_Q / 16, 128, s), desc_k4(sb4 + DS_X1 / 16, 128, s), i_qk, s != 0);
+                product(DT_QS, sb4 + DS_Q / 16, false, sb4 + DS_X1 / 16, false, i_qk, 0);
                 commit_by(lead, bar(B_QS));
             }
             wait(B_VF + st, (it >> 1) & 1);
@@ -397,21 +441,24 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             wait(B_SPLIT, it & 1);
             if (__any_sync(~0u, dead)) break;
             fence_after();
+            const uint32_t v4 = sb4 + DS_V / 16 + st * t4;
             if (full) {
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ta_by(lead, tm + DT_PV, tm + DT_SC + 8 * s, desc_mn4(sb4 + DS_V / 16 + st * t4, kTile / 2, 1024, s), i_pv, s != 0);
+#pragma unroll 1
+                for (uint32_t s = 0; s < 8; ++s)
+                    mma_ta_by(lead, tm + DT_PV, tm + DT_SC + 8 * s, desc4(v4 + 128 * s, kTile / 2, 1024), i_pv, s);
                 commit_by(lead, bar(B_O));
                 ++m;
             }
             // the smallest part first: what a sum of products loses goes by its size so far
-            if constexpr (!kF16) v_k(st, DS_X1 / 16, 0);
-            v_k(st, DS_X2 / 16, !kF16);
-            v_k(st, DS_K / 16 + st * t4, 1);
+            if constexpr (!kF16) product(DT_VK, v4, true, sb4 + DS_X1 / 16, true, i_vk, 0);
+            product(DT_VK, v4, true, sb4 + DS_X2 / 16, true, i_vk, !kF16);
+            product(DT_VK, v4, true, sb4 + DS_K / 16 + st * t4, true, i_vk, 1);
             commit_by(lead, bar(B_VK + st));
-            ch.next(a);
-            asked = ch.any && !ch.p.state_only;
-            if (asked) {
+            // the next chunk's scores run under this one's results
+            wait(B_GF + (st ^ 1), ((it + 1) >> 1) & 1);
+            flags = __shfl_sync(~0u, info_of(st ^ 1).flags, 0);
+            arrive(B_GFREE + (st ^ 1));
+            if ((flags & (kFull | kStop)) == kFull) {
                 wait(B_QF, m & 1);
                 wait(B_KF + (st ^ 1), ((it + 1) >> 1) & 1);
                 if (__any_sync(~0u, dead)) break;
@@ -419,61 +466,80 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             }
         }
         commit_by(lead, bar(B_DRAIN));
-        dead = false;
-        wait(B_DRAIN, 0);
+        dead = !wait_for(bar(B_DRAIN), 0) || dead;
     } else if (warp == 2) {
         // ================================================================ decays: lane l has tokens 4l .. 4l + 3
         uint32_t it = 0;
-        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+        for (Chunks ch(a, rg); !__any_sync(~0u, dead); ch.next(a), ++it) {
             const uint32_t st = it & 1;
-            const int first = ch.c * kDecayChunk + 4 * lane;
-            double g[4];
+            double g[4] = {0, 0, 0, 0};
+            if (ch.any) {
+                const int first = ch.c * kDecayChunk + 4 * lane;
+                float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                g[e] = first + e < ch.p.rows ? (double)log_decay_of(a.head_decay, a.log_decay, (int64_t)ch.p.row0 + first + e, a.H, ch.p.h) : 0.0;
-            g[0] *= 1.4426950408889634;
+                for (int e = 0; e < 4; ++e)
+                    x[e] = first + e < ch.p.rows ? log_decay_of(a.head_decay, a.log_decay, (int64_t)ch.p.row0 + first + e, a.H, ch.p.h) : 0.f;
+                double y = 0;
 #pragma unroll
-            for (int e = 1; e < 4; ++e) g[e] = g[e - 1] + g[e] * 1.4426950408889634;
+                for (int e = 0; e < 4; ++e) g[e] = y += (double)x[e] * 1.4426950408889634;
+            }
             double x = g[3];
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const double y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o) x += y;
             }
             const double end = __shfl_sync(~0u, x, lane | 7), all = __shfl_sync(~0u, x, 31);
-            const double last = __shfl_sync(~0u, x, (lane & 24) - 1 < 0 ? 0 : (lane & 24) - 1);
-            const double excl = x - g[3];
-            float4 d;
-            d.x = (float)(excl + g[0] - end);
-            d.y = (float)(excl + g[1] - end);
-            d.z = (float)(excl + g[2] - end);
-            d.w = (float)(x - end);
+            const double last = __shfl_sync(~0u, x, max((lane & 24) - 1, 0));
+            const double excl = x - g[3] - end;
+            const float4 d = make_float4((float)(excl + g[0]), (float)(excl + g[1]), (float)(excl + g[2]), (float)(x - end));
+            // the chunk's decay 2^all, once rounded (it multiplies the state chunk after chunk, and an error alike in each
+            // would grow): 2^n times the exponential series of the rest, |rest ln 2| <= 0.35
+            const double n = rint(fmax(all, -1000.0)), y = (all - n) * 0.6931471805599453;
+            double z = 1.0;
+#pragma unroll
+            for (int k = 10; k > 0; --k) z = fma(z * y, 1.0 / k, 1.0);
+            const float chunk = n < -126.0 ? 0.f : (float)z * __int_as_float(((int)n + 127) << 23);
             if (it >= 2) wait(B_GFREE + st, ((it >> 1) - 1) & 1);
             if (!dead) {
                 const uint32_t at = DS_G + st * 1024 + 16 * lane;
                 *reinterpret_cast<float4*>(sm + at) = d;
                 *reinterpret_cast<float4*>(sm + at + 512) = make_float4(ex2(-d.x), ex2(-d.y), ex2(-d.z), ex2(-d.w));
-                float* tot = reinterpret_cast<float*>(sm + DS_TOT + st * 32);
+                float* tot = reinterpret_cast<float*>(sm + DS_TOT + st * 64);
                 if ((lane & 7) == 0) tot[lane >> 3] = (float)(end - (lane < 8 ? 0.0 : last));
-                if (lane == 0) tot[4] = (float)exp2(all);
+                if (lane == 0) {
+                    tot[4] = isnan(all) ? (float)all : chunk;
+                    const Piece& p = ch.p;
+                    const int before = ch.c * kDecayChunk;
+                    const int flags = !ch.any ? kStop
+                                              : (p.state_only ? 0 : kFull) | (ch.c == p.c0 ? kFirst : 0) | (ch.c + 1 == p.c1 ? kLast : 0) |
+                                                    (p.start == kFromOthers ? kJoins : 0) | (p.end == kFinal ? kFinalState : 0) |
+                                                    (p.end == kPublish ? kLeaves : 0);
+                    *reinterpret_cast<int4*>(tot + 8) = make_int4(p.n, p.h, ch.c, p.row0 + before);
+                    *reinterpret_cast<int4*>(tot + 12) = make_int4(p.rows - before, p.rows, flags, 0);
+                }
             }
             arrive(B_GF + st);
+            if (!ch.any) break;
         }
     } else if (warp >= 4 && warp < 8) {
         // ================================================================ weights and results: a thread has a row
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t tl = tmem + ((uint32_t)(w * 32) << 16);
         const float scale = a.scale;
-        uint32_t it = 0, m = 0;
-        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+        uint32_t m = 0;
+        for (uint32_t it = 0;; ++it) {
             const uint32_t st = it & 1;
             wait(B_GF + st, (it >> 1) & 1);
-            if (ch.p.state_only) {
+            if (__any_sync(~0u, dead)) break;
+            const ChunkInfo ch = info_of(st);
+            if (ch.flags & kStop) break;
+            if (!(ch.flags & kFull)) {
                 arrive(B_GFREE + st);
                 continue;
             }
             const uint32_t gd = g_d + st * 1024;
-            const float4 tot4 = lds_f4(g_tot + st * 32);
+            const float4 tot4 = lds_f4(g_tot + st * 64);
             const float tot[4] = {tot4.x, tot4.y, tot4.z, tot4.w};
             const float d = lds_f1(gd + 4 * row);
             wait(B_QK, m & 1);
@@ -540,8 +606,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 fs *= pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
                 fp = pow2_inverse(ps);
             }
-            const int at = ch.c * kDecayChunk + row;
-            const int64_t o_at = ((int64_t)ch.p.row0 + at) * a.out.rs + ch.p.h * a.out.hs;
+            const int64_t o_at = ((int64_t)ch.row0 + row) * a.out.rs + ch.h * a.out.hs;
             uint8_t* o_row = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base)) + o_at * dtype_bytes(a.out_dt);
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
@@ -557,9 +622,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
 #pragma unroll
                 for (int z = 0; z < 32; ++z)
                     o[z] = fmaf(__uint_as_float(x[z]), fs, kF16 ? __uint_as_float(y[z]) * fp : __uint_as_float(y[z]));
-                if (at < ch.p.rows) {
-#pragma unroll
-                    for (int z = 0; z < 32; z += 4) store4_as(o_row, 32 * b + z, make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]), a.out_dt);
+                if (row < ch.left) {
+                    if (a.out_dt == KDA_BF16) store_row32<KDA_BF16>(o_row, 32 * b, o, a.sectors);
+                    else if (a.out_dt == KDA_F16) store_row32<KDA_F16>(o_row, 32 * b, o, a.sectors);
+                    else store_row32<KDA_F32>(o_row, 32 * b, o, a.sectors);
                 }
             }
             ++m;
@@ -569,13 +635,18 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         const int t = tid - 256, half = t >> 7, v = t & 127;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + DT_VK + 64 * half;
         float S[64], decay = 1.f;
-        uint32_t it = 0, m = 0, converted = 0;
-        // the state before chunk c, as the product's operand (and as a snapshot)
-        auto convert = [&](const Piece& p, int c) {
+        uint32_t it = 0, m = 0, converted = 0, met = 0;
+        // the eight warps wait for one another, with a limit as everywhere
+        auto meet = [&] {
+            arrive(B_MEET);
+            wait(B_MEET, met++ & 1);
+        };
+        // the state before a chunk, as the product's operand (and as a snapshot)
+        auto convert = [&](const ChunkInfo& p) {
             if (a.M > 0 && p.rows > 0) {
                 for (int base = 0; base < a.M; base += 32) {
                     const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
-                    for (uint32_t hit = __ballot_sync(~0u, x == c); hit; hit &= hit - 1) {
+                    for (uint32_t hit = __ballot_sync(~0u, x == p.c); hit; hit &= hit - 1) {
                         const size_t to = state_elem((int64_t)p.n * a.M + base + __ffs(hit) - 1, a.H, p.h) + v * kD + 64 * half;
                         if (!dead)
 #pragma unroll
@@ -590,11 +661,12 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 for (int e = 0; e < 64; ++e) mx = fmaxf(mx, fabsf(S[e]));
                 const uint32_t wm = __reduce_max_sync(~0u, __float_as_uint(mx));
                 float* maxima = reinterpret_cast<float*>(sm + DS_MAX);
-                bar_named(1, 256);  // the last use has been read
+                maxima += 8 * (converted & 1);  // the other eight may still be read
                 if (lane == 0) maxima[warp - 8] = __uint_as_float(wm);
-                bar_named(1, 256);
+                meet();
+                mx = maxima[0];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) mx = fmaxf(mx, maxima[x]);
+                for (int x = 1; x < 8; ++x) mx = fmaxf(mx, maxima[x]);
                 ss = range_scale(mx);
                 if (t == 0) *reinterpret_cast<float*>(sm + DS_SCALE + 4 * (converted & 1)) = ss;
             }
@@ -611,16 +683,19 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             fence_async_smem();
             arrive(B_S);
         };
-        for (Chunks ch(a, rg); ch.any; ch.next(a), ++it) {
+        for (;; ++it) {
             const uint32_t st = it & 1;
-            const Piece& p = ch.p;
-            const bool full = !p.state_only;
-            const int left = p.rows - ch.c * kDecayChunk;  // rows from this chunk on
-            if (ch.c == p.c0) {
+            wait(B_GF + st, (it >> 1) & 1);
+            if (__any_sync(~0u, dead)) break;
+            const ChunkInfo p = info_of(st);
+            if (p.flags & kStop) break;
+            const bool full = p.flags & kFull;
+            const int left = p.left;
+            if (p.flags & kFirst) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e) S[e] = 0.f;
                 decay = 1.f;
-                if (p.start == kFromInit) {
+                if (full && !(p.flags & kJoins)) {
                     const int src = a.init_slot ? a.init_slot[p.n] : -1;
                     if (src >= 0) {
                         const size_t from = state_elem(src, a.H, p.h) + v * kD + 64 * half;
@@ -635,7 +710,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                             const int c = a.track_idx[(int64_t)p.n * a.M + x];
                             if (c < -1 || c >= (p.rows + kDecayChunk - 1) / kDecayChunk) report(a.dev_status, KDA_DEV_BAD_TRACK);
                         }
-                } else if (p.start == kFromOthers) {
+                } else if (full) {
                     // the CTA with the unit's beginning left a state, those after it their ranges' own
                     const int j0 = (int)(((x0 - rg.fo + 1) * ctas - 1) / total);
                     for (int j = j0; j < (int)blockIdx.x; ++j) {
@@ -644,7 +719,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(set) : "l"(a.flags + j) : "memory");
                             if (!set) __nanosleep(64);
                         }
-                        if (!set && !dead) give_up();
+                        dead = dead || !set;
                         if (dead) break;
                         const float f = *(volatile float*)(a.decays + j);
                         const float4* from = a.states + (size_t)j * 4096 + t;
@@ -656,17 +731,16 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         }
                     }
                 }
-                if (full) convert(p, ch.c);
             }
-            wait(B_GF + st, (it >> 1) & 1);
+            if (full) convert(p);
             float f[4];
             {
-                const float4 tot = lds_f4(g_tot + st * 32);
+                const float4 tot = lds_f4(g_tot + st * 64);
                 const float after[4] = {tot.y + tot.z + tot.w, tot.z + tot.w, tot.w, 0.f};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) f[b] = ex2(after[b] - lds_f1(g_d + st * 1024 + 4 * (32 * b + (t >> 3))));
             }
-            const float ac = lds_f1(g_tot + st * 32 + 16);
+            const float ac = lds_f1(g_tot + st * 64 + 16);
             arrive(B_GFREE + st);
             wait(B_KF + st, (it >> 1) & 1);
             if (full) wait(B_QK, m & 1);
@@ -727,33 +801,36 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(ac, S[32 * b + e], x[e]);
             }
             fence_before();
-            dead = __any_sync(~0u, dead);
-            if (ch.c + 1 < p.c1) {
-                if (full) convert(p, ch.c + 1);
-            } else if (p.end == kFinal) {
+            if (!(p.flags & kLast)) continue;
+            if (p.flags & kFinalState) {
                 const int dst = a.final_slot ? a.final_slot[p.n] : -1;
-                if (dst >= 0 && !dead) {
+                if (dst >= 0 && !__any_sync(~0u, dead)) {
                     const size_t to = state_elem(dst, a.H, p.h) + v * kD + 64 * half;
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) state_store4(a.pool, to + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]), a.st);
                 }
-            } else if (p.end == kPublish) {
+            } else if (p.flags & kLeaves) {
                 float4* to = a.states + (size_t)blockIdx.x * 4096 + t;
 #pragma unroll
                 for (int e = 0; e < 64; e += 4) __stcg(to + e * 64, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
                 if (t == 0) a.decays[blockIdx.x] = decay;
                 __threadfence();
-                if (!bar_named_or(2, 256, dead) && t == 0)
+                meet();
+                if (t == 0 && !dead)
                     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + blockIdx.x), "r"(1u) : "memory");
             }
         }
+    }
+    if (dead) {
+        ctrl[1] = 1;
+        report(a.dev_status, KDA_DEV_TIMEOUT);
     }
     fence_before();
     __syncthreads();
     // Every load was waited for by a role that is done.  After a wait that ran out that does not hold: a bounded
     // wait on a barrier that nothing arrives on (about a second) lets them land.
     if (ctrl[1] && warp == 0) {
-        mbar_wait(bar(B_NEVER), 0, kWaitLimit);
+        wait_for(bar(B_NEVER), 0);
         __syncwarp();
     }
     __syncthreads();
@@ -817,6 +894,8 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
                     KDA_ERR_CUDA);
         a.hq = rq.hs != 0, a.hk = rk.hs != 0, a.hv = rv.hs != 0;
         a.out = as_rows(out);
+        const int per = 32 / dtype_bytes(out_dtype);
+        a.sectors = reinterpret_cast<uintptr_t>(out->base) % 32 == 0 && out->row_stride % per == 0 && out->head_stride % per == 0;
     }
     a.head_decay = head_decay;
     a.log_decay = log_decay;
