@@ -47,6 +47,7 @@ constexpr int kPreDecayThreads = 512;
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
 constexpr uint32_t kWaitLimit = 1u << 18;
 constexpr uint32_t kFlagLimit = 1u << 21;
+constexpr uint32_t kPollLimit = 1u << 25;  // of barrier tests, some 40 cycles each
 
 struct DecayPrefillArgs {
     LatentRows out;
@@ -70,11 +71,11 @@ struct DecayMaps {
 
 // shared memory
 constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_X1 = 5 * kTile, DS_X2 = 6 * kTile, DS_G = 7 * kTile,
-                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 128, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
+                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 160, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
                    DS_MAX = DS_SCAN + 136, DS_SCALE = DS_MAX + 64, DS_SMEM = DS_SCALE + 8;
 static_assert(DS_SMEM <= 232448 && DS_SCAN % 8 == 0 && DS_BAR % 8 == 0, "shared memory plan");
-constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 6, B_SPLIT = 7, B_VK = 8, B_S = 10, B_QS = 11, B_O = 12,
-              B_OFREE = 13, B_GF = 14, B_GFREE = 16, B_MEET = 18, B_DRAIN = 19, B_NEVER = 20, B_COUNT = 21;
+constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 7, B_SPLIT = 8, B_VK = 10, B_S = 12, B_QS = 13, B_O = 14,
+              B_OFREE = 15, B_GF = 16, B_GFREE = 18, B_MEET = 20, B_DRAIN = 21, B_NEVER = 22, B_COUNT = 23;
 // tensor memory: scores (their weights in the first half), P V, Q S, V^T K~
 constexpr uint32_t DT_SC = 0, DT_PV = 128, DT_QS = 256, DT_VK = 384;
 
@@ -176,7 +177,7 @@ struct Chunks {
 };
 
 // What the other roles know of a chunk.
-enum ChunkFlags { kFull = 1, kFirst = 2, kLast = 4, kJoins = 8, kFinalState = 16, kLeaves = 32, kStop = 64 };
+enum ChunkFlags { kFull = 1, kFirst = 2, kLast = 4, kJoins = 8, kFinalState = 16, kLeaves = 32, kPartial = 64, kStop = 128 };
 struct ChunkInfo {
     int n, h, c, row0;  // row0: the chunk's first row
     int left, rows, flags, pad;  // left: rows of the sequence from this chunk on
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     if (tid < B_COUNT) {
         int count = 1;
         if (tid == B_P || tid == B_OFREE) count = 4;      // warps
-        if (tid == B_SPLIT || tid == B_S || tid == B_MEET) count = 8;
+        if (tid == B_SPLIT || tid == B_SPLIT + 1 || tid == B_S || tid == B_MEET) count = 8;
         if (tid == B_GFREE || tid == B_GFREE + 1) count = 13;
         mbar_init(bar(tid), count);
     }
@@ -362,9 +363,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         __syncwarp();
         if (lane == 0 && !dead) mbar_arrive(bar(b));
     };
-    const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay, its ChunkInfo
+    const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay, its ChunkInfo, e^ of the totals behind each block [4]
     auto info_of = [&](uint32_t st) {
-        const uint4 x = lds128(g_tot + 64 * st + 32), y = lds128(g_tot + 64 * st + 48);
+        const uint4 x = lds128(g_tot + 80 * st + 32), y = lds128(g_tot + 80 * st + 48);
         return ChunkInfo{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, 0};
     };
 
@@ -402,68 +403,70 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         const uint32_t i_qk = idesc_16(kF16, 128, 128, false, false, false);
         const uint32_t i_pv = idesc_16(kF16, 128, 128, false, true, false);
         const uint32_t i_vk = idesc_16(kF16, 128, 128, true, true, false);
-        // D (+)= A B^T over eight steps of 16; operands K-major, or with their rows along M / N.  Rolled: this
-        // kernel's roles share an instruction cache that their unrolled loops overflow (see the top).
-        auto product = [&](uint32_t d, uint32_t a4, bool a_mn, uint32_t b4, bool b_mn, uint32_t idesc, uint32_t on) {
-#pragma unroll 1
-            for (uint32_t s = 0; s < 8; ++s) {
+        // D (+)= A B^T over steps of 16; operands K-major, or with their rows along M / N
+        auto product = [&](uint32_t d, uint32_t a4, bool a_mn, uint32_t b4, bool b_mn, uint32_t idesc, uint32_t s0,
+                           uint32_t s1, uint32_t on) {
+#pragma unroll
+            for (uint32_t s = s0; s < s1; ++s) {
                 const uint32_t k = (s >> 2) * 1024 + (s & 3) * 2, mn = 128 * s;
                 mma_by(lead, tm + d, desc4(a4 + (a_mn ? mn : k), a_mn ? kTile / 2 : 16, 1024),
-                       desc4(b4 + (b_mn ? mn : k), b_mn ? kTile / 2 : 16, 1024), idesc, on | s);
+                       desc4(b4 + (b_mn ? mn : k), b_mn ? kTile / 2 : 16, 1024), idesc, s == s0 ? on : 1u);
             }
         };
-        auto q_k = [&](uint32_t st) {
-            product(DT_SC, sb4 + DS_Q / 16, false, sb4 + DS_K / 16 + st * t4, false, i_qk, 0);
-            commit_by(lead, bar(B_QK));
-        };
-        uint32_t it = 0, m = 0;
-        wait(B_GF, 0);
-        int flags = __shfl_sync(~0u, info_of(0).flags, 0);
-        arrive(B_GFREE);
-        if ((flags & (kFull | kStop)) == kFull) {
-            wait(B_QF, 0);
-            wait(B_KF, 0);
-            if (!__any_sync(~0u, dead)) q_k(0);
-        }
-        for (; !(flags & kStop) && !__any_sync(~0u, dead); ++it) {
-            const uint32_t st = it & 1;
+        int flags = 0;  // of chunk it
+        uint32_t m = 0;
+        for (uint32_t it = ~0u;; ++it) {
+            // Chunk `it`; the scores of the next are issued on the way, as soon as its operands are there: behind P V,
+            // whose weights they overwrite, and ahead of V^T K~ if they are there before the keys are split.
+            const uint32_t st = it & 1, sn = st ^ 1;
             const bool full = flags & kFull;
+            const uint32_t v4 = sb4 + DS_V / 16 + st * t4;
             if (full) {
                 wait(B_S, m & 1);
                 if (m > 0) wait(B_OFREE, (m - 1) & 1);
                 if (__any_sync(~0u, dead)) break;
                 fence_after();
-                product(DT_QS, sb4 + DS_Q / 16, false, sb4 + DS_X1 / 16, false, i_qk, 0);
+                product(DT_QS, sb4 + DS_Q / 16, false, sb4 + DS_X1 / 16, false, i_qk, 0, 8, 0);
                 commit_by(lead, bar(B_QS));
             }
-            wait(B_VF + st, (it >> 1) & 1);
-            if (full) wait(B_P, m & 1);
-            wait(B_SPLIT, it & 1);
-            if (__any_sync(~0u, dead)) break;
-            fence_after();
-            const uint32_t v4 = sb4 + DS_V / 16 + st * t4;
+            if (it != ~0u) wait(B_VF + st, (it >> 1) & 1);
             if (full) {
-#pragma unroll 1
+                wait(B_P, m & 1);
+                // rows past the sequence are cleared by those who split the keys
+                if (flags & kPartial) wait(B_SPLIT, it & 1);
+                if (__any_sync(~0u, dead)) break;
+                fence_after();
+#pragma unroll
                 for (uint32_t s = 0; s < 8; ++s)
                     mma_ta_by(lead, tm + DT_PV, tm + DT_SC + 8 * s, desc4(v4 + 128 * s, kTile / 2, 1024), i_pv, s);
                 commit_by(lead, bar(B_O));
                 ++m;
             }
-            // the smallest part first: what a sum of products loses goes by its size so far
-            if constexpr (!kF16) product(DT_VK, v4, true, sb4 + DS_X1 / 16, true, i_vk, 0);
-            product(DT_VK, v4, true, sb4 + DS_X2 / 16, true, i_vk, !kF16);
-            product(DT_VK, v4, true, sb4 + DS_K / 16 + st * t4, true, i_vk, 1);
-            commit_by(lead, bar(B_VK + st));
-            // the next chunk's scores run under this one's results
-            wait(B_GF + (st ^ 1), ((it + 1) >> 1) & 1);
-            flags = __shfl_sync(~0u, info_of(st ^ 1).flags, 0);
-            arrive(B_GFREE + (st ^ 1));
-            if ((flags & (kFull | kStop)) == kFull) {
-                wait(B_QF, m & 1);
-                wait(B_KF + (st ^ 1), ((it + 1) >> 1) & 1);
-                if (__any_sync(~0u, dead)) break;
-                q_k(st ^ 1);
+            wait(B_GF + sn, ((it + 1) >> 1) & 1);
+            flags = __shfl_sync(~0u, info_of(sn).flags, 0);
+            if (!(flags & kStop)) arrive(B_GFREE + sn);
+            bool ask = (flags & (kFull | kStop)) == kFull;
+            int halves = it == ~0u ? 2 : 0;  // of the chunk's tokens, in V^T K~
+            for (uint32_t polls = 0; (ask || halves < 2) && !dead; ++polls) {
+                if (halves < 2 && __all_sync(~0u, mbar_test(bar(B_SPLIT + halves), it & 1))) {
+                    fence_after();
+                    // the smallest part first: what a sum of products loses goes by its size so far
+#pragma unroll 1
+                    for (int part = kF16 ? 1 : 0; part < 3; ++part) {
+                        const uint32_t keys = part == 0 ? DS_X1 / 16 : part == 1 ? DS_X2 / 16 : DS_K / 16 + st * t4;
+                        product(DT_VK, v4 + 512 * halves, true, sb4 + keys + 512 * halves, true, i_vk, 0, 4,
+                                halves > 0 || part > (kF16 ? 1 : 0));
+                    }
+                    if (++halves == 2) commit_by(lead, bar(B_VK + st));
+                }
+                if (ask && __all_sync(~0u, mbar_test(bar(B_QF), m & 1) && mbar_test(bar(B_KF + sn), ((it + 1) >> 1) & 1))) {
+                    product(DT_SC, sb4 + DS_Q / 16, false, sb4 + DS_K / 16 + sn * t4, false, i_qk, 0, 8, 0);
+                    commit_by(lead, bar(B_QK + (m & 1)));
+                    ask = false;
+                }
+                dead = polls >= kPollLimit;
             }
+            if ((flags & kStop) || __any_sync(~0u, dead)) break;
         }
         commit_by(lead, bar(B_DRAIN));
         dead = !wait_for(bar(B_DRAIN), 0) || dead;
@@ -505,8 +508,11 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 const uint32_t at = DS_G + st * 1024 + 16 * lane;
                 *reinterpret_cast<float4*>(sm + at) = d;
                 *reinterpret_cast<float4*>(sm + at + 512) = make_float4(ex2(-d.x), ex2(-d.y), ex2(-d.z), ex2(-d.w));
-                float* tot = reinterpret_cast<float*>(sm + DS_TOT + st * 64);
-                if ((lane & 7) == 0) tot[lane >> 3] = (float)(end - (lane < 8 ? 0.0 : last));
+                float* tot = reinterpret_cast<float*>(sm + DS_TOT + st * 80);
+                if ((lane & 7) == 0) {
+                    tot[lane >> 3] = (float)(end - (lane < 8 ? 0.0 : last));
+                    tot[16 + (lane >> 3)] = ex2((float)(all - end));
+                }
                 if (lane == 0) {
                     tot[4] = isnan(all) ? (float)all : chunk;
                     const Piece& p = ch.p;
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     const int flags = !ch.any ? kStop
                                               : (p.state_only ? 0 : kFull) | (ch.c == p.c0 ? kFirst : 0) | (ch.c + 1 == p.c1 ? kLast : 0) |
                                                     (p.start == kFromOthers ? kJoins : 0) | (p.end == kFinal ? kFinalState : 0) |
-                                                    (p.end == kPublish ? kLeaves : 0);
+                                                    (p.end == kPublish ? kLeaves : 0) | (p.rows - before < kDecayChunk ? kPartial : 0);
                     *reinterpret_cast<int4*>(tot + 8) = make_int4(p.n, p.h, ch.c, p.row0 + before);
                     *reinterpret_cast<int4*>(tot + 12) = make_int4(p.rows - before, p.rows, flags, 0);
                 }
@@ -539,10 +545,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 continue;
             }
             const uint32_t gd = g_d + st * 1024;
-            const float4 tot4 = lds_f4(g_tot + st * 64);
+            const float4 tot4 = lds_f4(g_tot + st * 80);
             const float tot[4] = {tot4.x, tot4.y, tot4.z, tot4.w};
             const float d = lds_f1(gd + 4 * row);
-            wait(B_QK, m & 1);
+            wait(B_QK + (m & 1), (m >> 1) & 1);
             if (__any_sync(~0u, dead)) break;
             fence_after();
             float ps = 1.f;  // fp16: the row's scale
@@ -570,8 +576,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const float4 c = lds_f4(gd + 512 + 4 * (32 * b + x));
-                        p[x / 2] = E::put2(s[x] * c.x * f, s[x + 1] * c.y * f);
-                        p[x / 2 + 1] = E::put2(s[x + 2] * c.z * f, s[x + 3] * c.w * f);
+                        const float4 y = f4_mul(f4_mul(make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]), c), make_float4(f, f, f, f));
+                        p[x / 2] = E::put2(y.x, y.y);
+                        p[x / 2 + 1] = E::put2(y.z, y.w);
                     }
                 } else if (b == w) {
                     float s[32];
@@ -641,12 +648,15 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             arrive(B_MEET);
             wait(B_MEET, met++ & 1);
         };
+        ChunkInfo p{};
+        bool goes_on = false;  // in the piece, and so by the last chunk's kind
         // the state before a chunk, as the product's operand (and as a snapshot)
-        auto convert = [&](const ChunkInfo& p) {
+        auto convert = [&] {
             if (a.M > 0 && p.rows > 0) {
+                const int c = p.c + (goes_on ? 1 : 0);  // p is still the last chunk's then
                 for (int base = 0; base < a.M; base += 32) {
                     const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
-                    for (uint32_t hit = __ballot_sync(~0u, x == p.c); hit; hit &= hit - 1) {
+                    for (uint32_t hit = __ballot_sync(~0u, x == c); hit; hit &= hit - 1) {
                         const size_t to = state_elem((int64_t)p.n * a.M + base + __ffs(hit) - 1, a.H, p.h) + v * kD + 64 * half;
                         if (!dead)
 #pragma unroll
@@ -685,13 +695,14 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         };
         for (;; ++it) {
             const uint32_t st = it & 1;
-            wait(B_GF + st, (it >> 1) & 1);
-            if (__any_sync(~0u, dead)) break;
-            const ChunkInfo p = info_of(st);
-            if (p.flags & kStop) break;
+            if (!goes_on) {
+                wait(B_GF + st, (it >> 1) & 1);
+                if (__any_sync(~0u, dead)) break;
+                p = info_of(st);
+                if (p.flags & kStop) break;
+            }
             const bool full = p.flags & kFull;
-            const int left = p.left;
-            if (p.flags & kFirst) {
+            if (!goes_on) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e) S[e] = 0.f;
                 decay = 1.f;
@@ -732,18 +743,16 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     }
                 }
             }
-            if (full) convert(p);
-            float f[4];
-            {
-                const float4 tot = lds_f4(g_tot + st * 64);
-                const float after[4] = {tot.y + tot.z + tot.w, tot.z + tot.w, tot.w, 0.f};
-#pragma unroll
-                for (int b = 0; b < 4; ++b) f[b] = ex2(after[b] - lds_f1(g_d + st * 1024 + 4 * (32 * b + (t >> 3))));
+            if (full) convert();
+            if (goes_on) {
+                wait(B_GF + st, (it >> 1) & 1);
+                if (__any_sync(~0u, dead)) break;
+                p = info_of(st);
             }
-            const float ac = lds_f1(g_tot + st * 64 + 16);
-            arrive(B_GFREE + st);
+            const int left = p.left;
+            const float ac = lds_f1(g_tot + st * 80 + 16);
             wait(B_KF + st, (it >> 1) & 1);
-            if (full) wait(B_QK, m & 1);
+            if (full) wait(B_QK + (m & 1), (m >> 1) & 1);  // the scores have read the keys
             if (left < kDecayChunk) {
                 // rows past the sequence have a weight of zero, and so has to be the value
                 wait(B_VF + st, (it >> 1) & 1);
@@ -752,43 +761,52 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     sts128(sb + DS_V + st * kTile + kTile / 2 + 16 * x, make_uint4(0, 0, 0, 0));
                 }
             }
-            uint4 lo[8];
+            float f[4];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t at = 16 * (256 * x + t);
-                const int row = 32 * (x & 3) + (t >> 3);
-                uint4 k = lds128(sb + DS_K + st * kTile + at), mid;
-                if (row >= left) k = make_uint4(0, 0, 0, 0);
-                const float2 ff = make_float2(f[x & 3], f[x & 3]);
-                auto part = [&](uint32_t& hi, uint32_t& md, uint32_t& l) {
-                    float2 y = __fmul2_rn(E::get2(hi), ff);
-                    if (row >= left) y = make_float2(0.f, 0.f);  // whatever the factor
-                    const float2 minus = make_float2(-1.f, -1.f);
-                    hi = E::put2(y.x, y.y);
-                    y = __ffma2_rn(E::get2(hi), minus, y);
-                    md = E::put2(y.x, y.y);
-                    if constexpr (!kF16) {
-                        y = __ffma2_rn(E::get2(md), minus, y);
-                        l = E::put2(y.x, y.y);
+            for (int b = 0; b < 4; ++b) f[b] = lds_f1(g_d + st * 1024 + 512 + 4 * (32 * b + (t >> 3))) * lds_f1(g_tot + st * 80 + 64 + 4 * b);
+            arrive(B_GFREE + st);
+            // half of the tokens at a time, so that the second's split runs under the first's products
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t k0 = sb + DS_K + st * kTile, at = 16 * (512 * i + t);
+                uint4 k[4], lo[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) k[x] = lds128(k0 + at + 4096 * (x & 1) + 16384 * (x >> 1));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const bool there = 64 * i + 32 * (x & 1) + (t >> 3) < left;
+                    const float f1 = x & 1 ? (i ? f[3] : f[1]) : (i ? f[2] : f[0]);
+                    const float2 ff = make_float2(f1, f1), minus = make_float2(-1.f, -1.f);
+                    uint4 mid;
+                    auto part = [&](uint32_t& hi, uint32_t& md, uint32_t& l) {
+                        float2 y = __fmul2_rn(E::get2(hi), ff);
+                        if (!there) y = make_float2(0.f, 0.f);  // whatever lies there
+                        hi = E::put2(y.x, y.y);
+                        y = __ffma2_rn(E::get2(hi), minus, y);
+                        md = E::put2(y.x, y.y);
+                        if constexpr (!kF16) {
+                            y = __ffma2_rn(E::get2(md), minus, y);
+                            l = E::put2(y.x, y.y);
+                        }
+                    };
+                    part(k[x].x, mid.x, lo[x].x);
+                    part(k[x].y, mid.y, lo[x].y);
+                    part(k[x].z, mid.z, lo[x].z);
+                    part(k[x].w, mid.w, lo[x].w);
+                    if (!dead) {
+                        sts128(k0 + at + 4096 * (x & 1) + 16384 * (x >> 1), k[x]);
+                        sts128(sb + DS_X2 + at + 4096 * (x & 1) + 16384 * (x >> 1), mid);
                     }
-                };
-                part(k.x, mid.x, lo[x].x);
-                part(k.y, mid.y, lo[x].y);
-                part(k.z, mid.z, lo[x].z);
-                part(k.w, mid.w, lo[x].w);
-                if (!dead) {
-                    sts128(sb + DS_K + st * kTile + at, k);
-                    sts128(sb + DS_X2 + at, mid);
                 }
-            }
-            if constexpr (!kF16) {
-                if (full) wait(B_QS, m & 1);  // the state's operand has been read
-                if (!dead)
+                if constexpr (!kF16) {
+                    if (full && i == 0) wait(B_QS, m & 1);  // the state's operand, whose place these take, has been read
+                    if (!dead)
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) sts128(sb + DS_X1 + 16 * (256 * x + t), lo[x]);
+                        for (int x = 0; x < 4; ++x) sts128(sb + DS_X1 + at + 4096 * (x & 1) + 16384 * (x >> 1), lo[x]);
+                }
+                fence_async_smem();
+                arrive(B_SPLIT + i);
             }
-            fence_async_smem();
-            arrive(B_SPLIT);
             if (full) ++m;
             wait(B_VK + st, (it >> 1) & 1);
             fence_after();
@@ -801,7 +819,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(ac, S[32 * b + e], x[e]);
             }
             fence_before();
-            if (!(p.flags & kLast)) continue;
+            goes_on = !(p.flags & kLast);
+            if (goes_on) continue;
             if (p.flags & kFinalState) {
                 const int dst = a.final_slot ? a.final_slot[p.n] : -1;
                 if (dst >= 0 && !__any_sync(~0u, dead)) {
