@@ -62,7 +62,7 @@ struct DecayPrefillArgs {
     // of a cut launch: a flag and a decay a CTA, then its state
     uint32_t* flags;
     float* decays;
-    float4* states;
+    float* states;
 };
 
 struct DecayMaps {
@@ -70,14 +70,15 @@ struct DecayMaps {
 };
 
 // shared memory
-constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_X1 = 5 * kTile, DS_X2 = 6 * kTile, DS_G = 7 * kTile,
-                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 160, DS_CTRL = DS_BAR + 8 * 24, DS_SCAN = DS_CTRL + 64,
+constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_S = 5 * kTile, DS_LO = 6 * kTile, DS_G = 7 * kTile,
+                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 160, DS_CTRL = DS_BAR + 8 * 26, DS_SCAN = DS_CTRL + 64,
                    DS_MAX = DS_SCAN + 136, DS_SCALE = DS_MAX + 64, DS_SMEM = DS_SCALE + 8;
 static_assert(DS_SMEM <= 232448 && DS_SCAN % 8 == 0 && DS_BAR % 8 == 0, "shared memory plan");
-constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 7, B_SPLIT = 8, B_VK = 10, B_S = 12, B_QS = 13, B_O = 14,
-              B_OFREE = 15, B_GF = 16, B_GFREE = 18, B_MEET = 20, B_DRAIN = 21, B_NEVER = 22, B_COUNT = 23;
-// tensor memory: scores (their weights in the first half), P V, Q S, V^T K~
-constexpr uint32_t DT_SC = 0, DT_PV = 128, DT_QS = 256, DT_VK = 384;
+constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 6, B_SPLIT = 7, B_KV = 9, B_S = 11, B_QS = 12, B_SCALED = 13,
+              B_O = 14, B_OFREE = 15, B_GF = 16, B_GFREE = 18, B_MEET = 20, B_FREE = 21, B_DRAIN = 23,
+              B_NEVER = 24, B_COUNT = 25;
+// tensor memory: scores (their weights in the first half), results, K~ V, K~'s first two parts
+constexpr uint32_t DT_SC = 0, DT_O = 128, DT_KV = 256, DT_K1 = 384, DT_K2 = 448;
 
 // Chunks of a sequence, one for an empty one (its state is passed on), 0 for a refused one.
 __device__ __forceinline__ int seq_chunks(const DecayPrefillArgs& a, int n, int& bad) {
@@ -183,18 +184,6 @@ struct ChunkInfo {
     int left, rows, flags, pad;  // left: rows of the sequence from this chunk on
 };
 
-__device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
 // mbar_wait with the usual limit, its loop not unrolled (there are thirty of it).
 __device__ __forceinline__ bool wait_for(uint32_t mbar, uint32_t parity) {
     uint32_t done = 0;
@@ -222,6 +211,22 @@ __device__ __forceinline__ float lds_f1(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
+}
+// Four 8 x 8 blocks of 16-bit elements, transposed on the way to or from registers.
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 16 lanes (rows) of 16 columns: register 2i + j of lane l is row 8j + l / 4, column 4i + l % 4.
+__device__ __forceinline__ void st16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -251,10 +256,10 @@ __device__ __forceinline__ void store_row32(void* row, int c, const float (&o)[3
     }
 }
 
-// The power of two that takes x into [2^13, 2^14); 1 for zero, infinities and NaN.
+// The power of two, at most 2^60, that takes x into [2^13, 2^14); 1 for zero, infinities and NaN.
 __device__ __forceinline__ float range_scale(float x) {
     const int e = (int)(__float_as_uint(x) >> 23) & 255;
-    return x == 0.f || e == 255 ? 1.f : __uint_as_float((uint32_t)min(max(267 - e, 2), 252) << 23);
+    return x == 0.f || e == 255 ? 1.f : __uint_as_float((uint32_t)min(max(267 - e, 2), 187) << 23);
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     }
     if (tid < B_COUNT) {
         int count = 1;
-        if (tid == B_P || tid == B_OFREE) count = 4;      // warps
+        if (tid == B_P || tid == B_SCALED || tid == B_OFREE) count = 4;      // warps
         if (tid == B_SPLIT || tid == B_SPLIT + 1 || tid == B_S || tid == B_MEET) count = 8;
         if (tid == B_GFREE || tid == B_GFREE + 1) count = 13;
         mbar_init(bar(tid), count);
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
             const uint32_t st = it & 1;
             const int row = ch.p.row0 + ch.c * kDecayChunk, h = ch.p.h, hk = h / a.group;
-            if (it >= 2) wait(B_VK + st, ((it >> 1) - 1) & 1);
+            if (it >= 2) wait(B_FREE + st, ((it >> 1) - 1) & 1);
             auto load = [&](uint32_t dst, const CUtensorMap* map, int head, int b) {
                 if (lane != 0 || dead) return;
                 if (ch.p.rows == 0) {  // an empty sequence's one chunk: its keys and values are cleared, its scores not used
@@ -401,71 +406,84 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         const uint32_t sb4 = (sb & 0x3ffffu) >> 4, t4 = kTile >> 4;
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
         const uint32_t i_qk = idesc_16(kF16, 128, 128, false, false, false);
-        const uint32_t i_pv = idesc_16(kF16, 128, 128, false, true, false);
-        const uint32_t i_vk = idesc_16(kF16, 128, 128, true, true, false);
-        // D (+)= A B^T over steps of 16; operands K-major, or with their rows along M / N
-        auto product = [&](uint32_t d, uint32_t a4, bool a_mn, uint32_t b4, bool b_mn, uint32_t idesc, uint32_t s0,
-                           uint32_t s1, uint32_t on) {
-#pragma unroll
-            for (uint32_t s = s0; s < s1; ++s) {
-                const uint32_t k = (s >> 2) * 1024 + (s & 3) * 2, mn = 128 * s;
-                mma_by(lead, tm + d, desc4(a4 + (a_mn ? mn : k), a_mn ? kTile / 2 : 16, 1024),
-                       desc4(b4 + (b_mn ? mn : k), b_mn ? kTile / 2 : 16, 1024), idesc, s == s0 ? on : 1u);
-            }
-        };
+        const uint32_t i_tv = idesc_16(kF16, 128, 128, false, true, false);  // B with its rows along N
+        const uint32_t i_tt = idesc_16(kF16, 128, 128, true, true, false);   // and A with its along M
+        // descriptors of step s: rows of channels, and rows of tokens (a step's 16 tokens behind one another)
+        auto along_k = [&](uint32_t at4, uint32_t s) { return desc4(at4 + (s >> 2) * 1024 + (s & 3) * 2, 16, 1024); };
+        auto along_mn = [&](uint32_t at4, uint32_t s) { return desc4(at4 + 128 * s, kTile / 2, 1024); };
+        const uint32_t q4 = sb4 + DS_Q / 16, s4 = sb4 + DS_S / 16, lo4 = sb4 + DS_LO / 16;
         int flags = 0;  // of chunk it
         uint32_t m = 0;
         for (uint32_t it = ~0u;; ++it) {
-            // Chunk `it`; the scores of the next are issued on the way, as soon as its operands are there: behind P V,
-            // whose weights they overwrite, and ahead of V^T K~ if they are there before the keys are split.
+            // Chunk `it`, each product as soon as its operands are there, and the next chunk's scores (over this one's
+            // weights, so behind P V).
             const uint32_t st = it & 1, sn = st ^ 1;
             const bool full = flags & kFull;
-            const uint32_t v4 = sb4 + DS_V / 16 + st * t4;
-            if (full) {
-                wait(B_S, m & 1);
-                if (m > 0) wait(B_OFREE, (m - 1) & 1);
-                if (__any_sync(~0u, dead)) break;
-                fence_after();
-                product(DT_QS, sb4 + DS_Q / 16, false, sb4 + DS_X1 / 16, false, i_qk, 0, 8, 0);
-                commit_by(lead, bar(B_QS));
-            }
-            if (it != ~0u) wait(B_VF + st, (it >> 1) & 1);
-            if (full) {
-                wait(B_P, m & 1);
-                // rows past the sequence are cleared by those who split the keys
-                if (flags & kPartial) wait(B_SPLIT, it & 1);
-                if (__any_sync(~0u, dead)) break;
-                fence_after();
-#pragma unroll
-                for (uint32_t s = 0; s < 8; ++s)
-                    mma_ta_by(lead, tm + DT_PV, tm + DT_SC + 8 * s, desc4(v4 + 128 * s, kTile / 2, 1024), i_pv, s);
-                commit_by(lead, bar(B_O));
-                ++m;
-            }
-            wait(B_GF + sn, ((it + 1) >> 1) & 1);
-            flags = __shfl_sync(~0u, info_of(sn).flags, 0);
-            if (!(flags & kStop)) arrive(B_GFREE + sn);
-            bool ask = (flags & (kFull | kStop)) == kFull;
-            int halves = it == ~0u ? 2 : 0;  // of the chunk's tokens, in V^T K~
-            for (uint32_t polls = 0; (ask || halves < 2) && !dead; ++polls) {
-                if (halves < 2 && __all_sync(~0u, mbar_test(bar(B_SPLIT + halves), it & 1))) {
+            const uint32_t v4 = sb4 + DS_V / 16 + st * t4, par = m & 1;
+            int next = 0;
+            bool qs = full, pv = full, told = false, ask = false;
+            int halves = it == ~0u ? 2 : 0;  // of each 64 tokens, in K~ V
+            auto have = [&](int b, uint32_t parity) { return __all_sync(~0u, mbar_test(bar(b), parity)); };
+            for (uint32_t polls = 0; (qs || pv || halves < 2 || !told || ask) && !dead; ++polls) {
+                if (halves < 2 && have(B_SPLIT + halves, it & 1) && have(B_VF + st, (it >> 1) & 1)) {
                     fence_after();
+                    const uint32_t fresh = halves == 0;
                     // the smallest part first: what a sum of products loses goes by its size so far
-#pragma unroll 1
-                    for (int part = kF16 ? 1 : 0; part < 3; ++part) {
-                        const uint32_t keys = part == 0 ? DS_X1 / 16 : part == 1 ? DS_X2 / 16 : DS_K / 16 + st * t4;
-                        product(DT_VK, v4 + 512 * halves, true, sb4 + keys + 512 * halves, true, i_vk, 0, 4,
-                                halves > 0 || part > (kF16 ? 1 : 0));
+                    if constexpr (!kF16) {
+#pragma unroll
+                        for (uint32_t x = 0; x < 4; ++x) {
+                            const uint32_t s = 2 * halves + (x & 1) + 4 * (x >> 1);
+                            mma_by(lead, tm + DT_KV, along_mn(lo4, s), along_mn(v4, s), i_tt, x > 0 || !fresh);
+                        }
                     }
-                    if (++halves == 2) commit_by(lead, bar(B_VK + st));
+#pragma unroll 1
+                    for (uint32_t part = 0; part < 2; ++part)
+#pragma unroll
+                        for (uint32_t x = 0; x < 4; ++x) {
+                            const uint32_t s = 2 * halves + (x & 1) + 4 * (x >> 1);
+                            mma_ta_by(lead, tm + DT_KV, tm + (part ? DT_K1 : DT_K2) + 8 * s, along_mn(v4, s), i_tv,
+                                      !kF16 || part > 0 || x > 0 || !fresh);
+                        }
+                    if (++halves == 2) {
+                        commit_by(lead, bar(B_KV));
+                        if (!pv) commit_by(lead, bar(B_FREE + st));
+                    }
                 }
-                if (ask && __all_sync(~0u, mbar_test(bar(B_QF), m & 1) && mbar_test(bar(B_KF + sn), ((it + 1) >> 1) & 1))) {
-                    product(DT_SC, sb4 + DS_Q / 16, false, sb4 + DS_K / 16 + sn * t4, false, i_qk, 0, 8, 0);
-                    commit_by(lead, bar(B_QK + (m & 1)));
+                if (qs && have(B_S, par) && (m == 0 || have(B_OFREE, par ^ 1))) {
+                    fence_after();
+#pragma unroll
+                    for (uint32_t s = 0; s < 8; ++s) mma_by(lead, tm + DT_O, along_k(q4, s), along_mn(s4, s), i_tv, s);
+                    commit_by(lead, bar(B_QS));
+                    qs = false;
+                }
+                // rows past the sequence are cleared by those who split the keys
+                if (pv && !qs && have(B_P, par) && have(B_SCALED, par) && have(B_VF + st, (it >> 1) & 1) &&
+                    (!(flags & kPartial) || halves > 0)) {
+                    fence_after();
+#pragma unroll
+                    for (uint32_t s = 0; s < 8; ++s)
+                        mma_ta_by(lead, tm + DT_O, tm + DT_SC + 8 * s, along_mn(v4, s), i_tv, 1);
+                    commit_by(lead, bar(B_O));
+                    pv = false;
+                    if (halves == 2) commit_by(lead, bar(B_FREE + st));  // keys and values have had all their products
+                }
+                if (!told && have(B_GF + sn, ((it + 1) >> 1) & 1)) {
+                    next = __shfl_sync(~0u, info_of(sn).flags, 0);
+                    if (!(next & kStop)) arrive(B_GFREE + sn);
+                    told = true;
+                    ask = (next & (kFull | kStop)) == kFull;
+                }
+                if (ask && !pv && have(B_QF, full ? par ^ 1 : par) && have(B_KF + sn, ((it + 1) >> 1) & 1)) {
+#pragma unroll
+                    for (uint32_t s = 0; s < 8; ++s)
+                        mma_by(lead, tm + DT_SC, along_k(q4, s), along_k(sb4 + DS_K / 16 + sn * t4, s), i_qk, s);
+                    commit_by(lead, bar(B_QK));
                     ask = false;
                 }
                 dead = polls >= kPollLimit;
             }
+            m += full;
+            flags = next;
             if ((flags & kStop) || __any_sync(~0u, dead)) break;
         }
         commit_by(lead, bar(B_DRAIN));
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             const float4 tot4 = lds_f4(g_tot + st * 80);
             const float tot[4] = {tot4.x, tot4.y, tot4.z, tot4.w};
             const float d = lds_f1(gd + 4 * row);
-            wait(B_QK + (m & 1), (m >> 1) & 1);
+            wait(B_QK, m & 1);
             if (__any_sync(~0u, dead)) break;
             fence_after();
             float ps = 1.f;  // fp16: the row's scale
@@ -605,30 +623,42 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) e += x <= w ? tot[x] : 0.f;
             arrive(B_GFREE + st);
+            // Q S_0 to the scale of the weights, as the sum that P V goes on
+            float fs = scale * ex2(e), fp = 1.f;
+            wait(B_QS, m & 1);
+            if (__any_sync(~0u, dead)) break;
+            fence_after();
+            if constexpr (kF16) {
+                fs *= ps * pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
+                fp = pow2_inverse(ps);
+            }
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                float x[32];
+                ld32(tl + DT_O + 32 * b, x);
+#pragma unroll
+                for (int z = 0; z < 32; ++z) x[z] *= fs;
+                st32(tl + DT_O + 32 * b, x);
+            }
+            wait_st();
+            fence_before();
+            arrive(B_SCALED);
             wait(B_O, m & 1);
             if (__any_sync(~0u, dead)) break;
             fence_after();
-            float fs = scale * ex2(e), fp = 1.f;
-            if constexpr (kF16) {
-                fs *= pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
-                fp = pow2_inverse(ps);
-            }
             const int64_t o_at = ((int64_t)ch.row0 + row) * a.out.rs + ch.h * a.out.hs;
             uint8_t* o_row = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base)) + o_at * dtype_bytes(a.out_dt);
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-                uint32_t x[32], y[32];
-                ld32_issue(tl + DT_QS + 32 * b, x);
-                ld32_issue(tl + DT_PV + 32 * b, y);
-                wait_ld();
+                float o[32];
+                ld32(tl + DT_O + 32 * b, o);
                 if (b == 3) {
                     fence_before();
                     arrive(B_OFREE);
                 }
-                float o[32];
+                if constexpr (kF16)
 #pragma unroll
-                for (int z = 0; z < 32; ++z)
-                    o[z] = fmaf(__uint_as_float(x[z]), fs, kF16 ? __uint_as_float(y[z]) * fp : __uint_as_float(y[z]));
+                    for (int z = 0; z < 32; ++z) o[z] *= fp;
                 if (row < ch.left) {
                     if (a.out_dt == KDA_BF16) store_row32<KDA_BF16>(o_row, 32 * b, o, a.sectors);
                     else if (a.out_dt == KDA_F16) store_row32<KDA_F16>(o_row, 32 * b, o, a.sectors);
@@ -638,83 +668,122 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             ++m;
         }
     } else if (warp >= 8) {
-        // ================================================================ keys and state: a thread has half a row of S^T
-        const int t = tid - 256, half = t >> 7, v = t & 127;
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + DT_VK + 64 * half;
+        // ================================================================ keys and state
+        // A thread has key channel `key` of the state, value channels 64 half .. 64 half + 63; of the keys' split its
+        // warp has 32 channels of 64 tokens.
+        const int t = tid - 256, half = t >> 7, key = t & 127;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         float S[64], decay = 1.f;
-        uint32_t it = 0, m = 0, converted = 0, met = 0;
+        uint32_t it = 0, m = 0, met = 0;
         // the eight warps wait for one another, with a limit as everywhere
         auto meet = [&] {
             arrive(B_MEET);
             wait(B_MEET, met++ & 1);
         };
-        ChunkInfo p{};
-        bool goes_on = false;  // in the piece, and so by the last chunk's kind
-        // the state before a chunk, as the product's operand (and as a snapshot)
-        auto convert = [&] {
-            if (a.M > 0 && p.rows > 0) {
-                const int c = p.c + (goes_on ? 1 : 0);  // p is still the last chunk's then
-                for (int base = 0; base < a.M; base += 32) {
-                    const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
-                    for (uint32_t hit = __ballot_sync(~0u, x == c); hit; hit &= hit - 1) {
-                        const size_t to = state_elem((int64_t)p.n * a.M + base + __ffs(hit) - 1, a.H, p.h) + v * kD + 64 * half;
-                        if (!dead)
+        // this thread's elements of a state in memory, whose rows are value channels
+        auto elems = [&](int64_t slot, int h) { return state_elem(slot, a.H, h) + (size_t)(64 * half) * kD + key; };
+        auto store_state = [&](void* to, size_t at) {
+            if (a.st == kStateF32)
 #pragma unroll
-                            for (int e = 0; e < 64; e += 4) state_store4(a.track, to + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]), a.st);
-                    }
-                }
-            }
-            float ss = 1.f;
-            if constexpr (kF16) {
-                float mx = 0.f;
+                for (int e = 0; e < 64; ++e) static_cast<float*>(to)[at + (size_t)e * kD] = S[e];
+            else if (a.st == kStateBF16)
 #pragma unroll
-                for (int e = 0; e < 64; ++e) mx = fmaxf(mx, fabsf(S[e]));
-                const uint32_t wm = __reduce_max_sync(~0u, __float_as_uint(mx));
-                float* maxima = reinterpret_cast<float*>(sm + DS_MAX);
-                maxima += 8 * (converted & 1);  // the other eight may still be read
-                if (lane == 0) maxima[warp - 8] = __uint_as_float(wm);
-                meet();
-                mx = maxima[0];
+                for (int e = 0; e < 64; ++e) static_cast<__nv_bfloat16*>(to)[at + (size_t)e * kD] = __float2bfloat16_rn(S[e]);
+            else
 #pragma unroll
-                for (int x = 1; x < 8; ++x) mx = fmaxf(mx, maxima[x]);
-                ss = range_scale(mx);
-                if (t == 0) *reinterpret_cast<float*>(sm + DS_SCALE + 4 * (converted & 1)) = ss;
-            }
-            ++converted;
-#pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-                uint4 x;
-                x.x = E::put2(S[e] * ss, S[e + 1] * ss);
-                x.y = E::put2(S[e + 2] * ss, S[e + 3] * ss);
-                x.z = E::put2(S[e + 4] * ss, S[e + 5] * ss);
-                x.w = E::put2(S[e + 6] * ss, S[e + 7] * ss);
-                sts128(sb + DS_X1 + half * (kTile / 2) + v * 128 + (((e >> 3) ^ (v & 7)) << 4), x);
-            }
-            fence_async_smem();
-            arrive(B_S);
+                for (int e = 0; e < 64; ++e) static_cast<__half*>(to)[at + (size_t)e * kD] = __float2half_rn(S[e]);
         };
+        // ldmatrix of 8 x 8 blocks, transposed: block j of four has channels 8 (j & 1) .. and tokens 8 (j >> 1) .., its
+        // row r lies at token r; the other block of 64 channels 16 KiB on
+        const int blk = lane >> 3, chunk16 = (32 * (warp & 3) & 63) / 8 + (blk & 1);
+        const uint32_t k_row = (uint32_t)((warp & 3) >> 1) * (kTile / 2) + (64 * half + 8 * (blk >> 1) + (lane & 7)) * 128;
         for (;; ++it) {
             const uint32_t st = it & 1;
-            if (!goes_on) {
-                wait(B_GF + st, (it >> 1) & 1);
-                if (__any_sync(~0u, dead)) break;
-                p = info_of(st);
-                if (p.flags & kStop) break;
-            }
+            wait(B_GF + st, (it >> 1) & 1);
+            if (__any_sync(~0u, dead)) break;
+            const ChunkInfo p = info_of(st);
+            if (p.flags & kStop) break;
             const bool full = p.flags & kFull;
-            if (!goes_on) {
+            const float ac = lds_f1(g_tot + st * 80 + 16);
+            wait(B_KF + st, (it >> 1) & 1);
+            if (p.left < kDecayChunk) {
+                // rows past the sequence have a weight of zero, and so has to be the value
+                wait(B_VF + st, (it >> 1) & 1);
+                for (int x = max(p.left, 0) * 8 + t; x < 1024 && !dead; x += 256) {
+                    sts128(sb + DS_V + st * kTile + 16 * x, make_uint4(0, 0, 0, 0));
+                    sts128(sb + DS_V + st * kTile + kTile / 2 + 16 * x, make_uint4(0, 0, 0, 0));
+                }
+            }
+            // ---- K~: 32 tokens (a block of the decays) at a time, so that the second's split runs under the first's products
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int token = 64 * half + 32 * i + 2 * (lane & 3);  // and the next one, of each group of 8
+                const float after = lds_f1(g_tot + st * 80 + 64 + 4 * (2 * half + i));
+                float2 f[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                                 : "=f"(f[g].x), "=f"(f[g].y)
+                                 : "r"(g_d + st * 1024 + 512 + 4 * (token + 8 * g)));
+                    f[g] = __fmul2_rn(f[g], make_float2(after, after));
+                }
+                const uint32_t row_at = k_row + 4096 * i;
+#pragma unroll
+                for (int lh = 0; lh < 2; ++lh) {  // 16 channels
+                    const uint32_t at = row_at + (((chunk16 + 2 * lh) ^ (lane & 7)) << 4);
+                    uint32_t k[8], mid[8], lo[8];
+                    ldsm4t(sb + DS_K + st * kTile + at, k);
+                    ldsm4t(sb + DS_K + st * kTile + at + 2048, k + 4);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float2 minus = make_float2(-1.f, -1.f);
+                        float2 y = __fmul2_rn(E::get2(k[x]), f[x >> 1]);
+                        if (p.left < kDecayChunk) {  // whatever lies past the sequence
+                            if (token + 8 * (x >> 1) >= p.left) y.x = 0.f;
+                            if (token + 8 * (x >> 1) + 1 >= p.left) y.y = 0.f;
+                        }
+                        k[x] = E::put2(y.x, y.y);
+                        y = __ffma2_rn(E::get2(k[x]), minus, y);
+                        mid[x] = E::put2(y.x, y.y);
+                        if constexpr (!kF16) {
+                            y = __ffma2_rn(E::get2(mid[x]), minus, y);
+                            lo[x] = E::put2(y.x, y.y);
+                        }
+                    }
+                    if (!__any_sync(~0u, dead)) {
+                        const uint32_t to = tl + ((uint32_t)(16 * lh) << 16) + 32 * half + 16 * i;
+                        st16x128(to + DT_K1, k);
+                        st16x128(to + DT_K2, mid);
+                        if constexpr (!kF16) {
+                            stsm4t(sb + DS_LO + at, lo);
+                            stsm4t(sb + DS_LO + at + 2048, lo + 4);
+                        }
+                    }
+                }
+                wait_st();
+                fence_before();
+                fence_async_smem();
+                arrive(B_SPLIT + i);
+            }
+            arrive(B_GFREE + st);
+            // ---- the state before this chunk, under the products
+            if (p.flags & kFirst) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e) S[e] = 0.f;
                 decay = 1.f;
                 if (full && !(p.flags & kJoins)) {
                     const int src = a.init_slot ? a.init_slot[p.n] : -1;
                     if (src >= 0) {
-                        const size_t from = state_elem(src, a.H, p.h) + v * kD + 64 * half;
+                        const size_t at = elems(src, p.h);
+                        if (a.st == kStateF32)
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const float4 x = state_load4(a.pool, from + e, a.st);
-                            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
-                        }
+                            for (int e = 0; e < 64; ++e) S[e] = static_cast<const float*>(a.pool)[at + (size_t)e * kD];
+                        else if (a.st == kStateBF16)
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) S[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool)[at + (size_t)e * kD]);
+                        else
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) S[e] = __half2float(static_cast<const __half*>(a.pool)[at + (size_t)e * kD]);
                     }
                     if (p.h == 0 && t == 0)
                         for (int x = 0; x < a.M; ++x) {
@@ -733,105 +802,69 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         dead = dead || !set;
                         if (dead) break;
                         const float f = *(volatile float*)(a.decays + j);
-                        const float4* from = a.states + (size_t)j * 4096 + t;
+                        const float* from = a.states + (size_t)j * (kD * kD) + t;
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const float4 x = __ldcg(from + e * 64);
-                            S[e] = fmaf(f, S[e], x.x), S[e + 1] = fmaf(f, S[e + 1], x.y);
-                            S[e + 2] = fmaf(f, S[e + 2], x.z), S[e + 3] = fmaf(f, S[e + 3], x.w);
-                        }
+                        for (int e = 0; e < 64; ++e) S[e] = fmaf(f, S[e], __ldcg(from + e * 256));
                     }
                 }
             }
-            if (full) convert();
-            if (goes_on) {
-                wait(B_GF + st, (it >> 1) & 1);
-                if (__any_sync(~0u, dead)) break;
-                p = info_of(st);
-            }
-            const int left = p.left;
-            const float ac = lds_f1(g_tot + st * 80 + 16);
-            wait(B_KF + st, (it >> 1) & 1);
-            if (full) wait(B_QK + (m & 1), (m >> 1) & 1);  // the scores have read the keys
-            if (left < kDecayChunk) {
-                // rows past the sequence have a weight of zero, and so has to be the value
-                wait(B_VF + st, (it >> 1) & 1);
-                for (int x = max(left, 0) * 8 + t; x < 1024 && !dead; x += 256) {
-                    sts128(sb + DS_V + st * kTile + 16 * x, make_uint4(0, 0, 0, 0));
-                    sts128(sb + DS_V + st * kTile + kTile / 2 + 16 * x, make_uint4(0, 0, 0, 0));
-                }
-            }
-            float f[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) f[b] = lds_f1(g_d + st * 1024 + 512 + 4 * (32 * b + (t >> 3))) * lds_f1(g_tot + st * 80 + 64 + 4 * b);
-            arrive(B_GFREE + st);
-            // half of the tokens at a time, so that the second's split runs under the first's products
-#pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t k0 = sb + DS_K + st * kTile, at = 16 * (512 * i + t);
-                uint4 k[4], lo[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) k[x] = lds128(k0 + at + 4096 * (x & 1) + 16384 * (x >> 1));
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const bool there = 64 * i + 32 * (x & 1) + (t >> 3) < left;
-                    const float f1 = x & 1 ? (i ? f[3] : f[1]) : (i ? f[2] : f[0]);
-                    const float2 ff = make_float2(f1, f1), minus = make_float2(-1.f, -1.f);
-                    uint4 mid;
-                    auto part = [&](uint32_t& hi, uint32_t& md, uint32_t& l) {
-                        float2 y = __fmul2_rn(E::get2(hi), ff);
-                        if (!there) y = make_float2(0.f, 0.f);  // whatever lies there
-                        hi = E::put2(y.x, y.y);
-                        y = __ffma2_rn(E::get2(hi), minus, y);
-                        md = E::put2(y.x, y.y);
-                        if constexpr (!kF16) {
-                            y = __ffma2_rn(E::get2(md), minus, y);
-                            l = E::put2(y.x, y.y);
-                        }
-                    };
-                    part(k[x].x, mid.x, lo[x].x);
-                    part(k[x].y, mid.y, lo[x].y);
-                    part(k[x].z, mid.z, lo[x].z);
-                    part(k[x].w, mid.w, lo[x].w);
-                    if (!dead) {
-                        sts128(k0 + at + 4096 * (x & 1) + 16384 * (x >> 1), k[x]);
-                        sts128(sb + DS_X2 + at + 4096 * (x & 1) + 16384 * (x >> 1), mid);
+            if (full) {
+                if (a.M > 0 && p.rows > 0) {
+                    for (int base = 0; base < a.M; base += 32) {
+                        const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
+                        for (uint32_t hit = __ballot_sync(~0u, x == p.c); hit; hit &= hit - 1)
+                            if (!__any_sync(~0u, dead)) store_state(a.track, elems((int64_t)p.n * a.M + base + __ffs(hit) - 1, p.h));
                     }
                 }
-                if constexpr (!kF16) {
-                    if (full && i == 0) wait(B_QS, m & 1);  // the state's operand, whose place these take, has been read
-                    if (!dead)
+                float ss = 1.f;
+                if constexpr (kF16) {
+                    float mx = 0.f;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) sts128(sb + DS_X1 + at + 4096 * (x & 1) + 16384 * (x >> 1), lo[x]);
+                    for (int e = 0; e < 64; ++e) mx = fmaxf(mx, fabsf(S[e]));
+                    const uint32_t wm = __reduce_max_sync(~0u, __float_as_uint(mx));
+                    float* maxima = reinterpret_cast<float*>(sm + DS_MAX) + 8 * (m & 1);  // the other eight may still be read
+                    if (lane == 0) maxima[warp - 8] = __uint_as_float(wm);
+                    meet();
+                    mx = maxima[0];
+#pragma unroll
+                    for (int x = 1; x < 8; ++x) mx = fmaxf(mx, maxima[x]);
+                    ss = range_scale(mx);
+                    if (t == 0) *reinterpret_cast<float*>(sm + DS_SCALE + 4 * (m & 1)) = ss;
                 }
+                if (m > 0) wait(B_QS, (m - 1) & 1);  // the last operand has been read
+                if (!dead)
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8) {
+                        uint4 x;
+                        x.x = E::put2(S[e] * ss, S[e + 1] * ss);
+                        x.y = E::put2(S[e + 2] * ss, S[e + 3] * ss);
+                        x.z = E::put2(S[e + 4] * ss, S[e + 5] * ss);
+                        x.w = E::put2(S[e + 6] * ss, S[e + 7] * ss);
+                        sts128(sb + DS_S + half * (kTile / 2) + key * 128 + (((e >> 3) ^ (key & 7)) << 4), x);
+                    }
                 fence_async_smem();
-                arrive(B_SPLIT + i);
+                arrive(B_S);
+                ++m;
             }
-            if (full) ++m;
-            wait(B_VK + st, (it >> 1) & 1);
+            wait(B_KV, it & 1);
             fence_after();
             decay *= ac;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float x[32];
-                ld32(tl + 32 * b, x);
+                ld32(tl + DT_KV + 64 * half + 32 * b, x);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(ac, S[32 * b + e], x[e]);
             }
             fence_before();
-            goes_on = !(p.flags & kLast);
-            if (goes_on) continue;
+            if (!(p.flags & kLast)) continue;
             if (p.flags & kFinalState) {
                 const int dst = a.final_slot ? a.final_slot[p.n] : -1;
-                if (dst >= 0 && !__any_sync(~0u, dead)) {
-                    const size_t to = state_elem(dst, a.H, p.h) + v * kD + 64 * half;
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) state_store4(a.pool, to + e, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]), a.st);
-                }
+                if (dst >= 0 && !__any_sync(~0u, dead)) store_state(a.pool, elems(dst, p.h));
             } else if (p.flags & kLeaves) {
-                float4* to = a.states + (size_t)blockIdx.x * 4096 + t;
+                float* to = a.states + (size_t)blockIdx.x * (kD * kD) + t;
 #pragma unroll
-                for (int e = 0; e < 64; e += 4) __stcg(to + e * 64, make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]));
+                for (int e = 0; e < 64; ++e) __stcg(to + e * 256, S[e]);
                 if (t == 0) a.decays[blockIdx.x] = decay;
                 __threadfence();
                 meet();
@@ -955,7 +988,7 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
         cfg.gridDim.x = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
         a.flags = static_cast<uint32_t*>(workspace);
         a.decays = reinterpret_cast<float*>(a.flags + kDecayCtas);
-        a.states = reinterpret_cast<float4*>(a.decays + kDecayCtas);
+        a.states = a.decays + kDecayCtas;
         if (cudaMemsetAsync(a.flags, 0, 4 * kDecayCtas, s) != cudaSuccess) return runtime_failed();
         at[0].id = cudaLaunchAttributeCooperative;
         at[0].val.cooperative = 1;
