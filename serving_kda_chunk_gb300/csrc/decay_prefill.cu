@@ -56,8 +56,9 @@ struct DecayPrefillArgs {
     void *pool, *track;
     int32_t* dev_status;
     int64_t P;
-    int32_t N, T, H, group, M, hq, hk, hv, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
+    int32_t N, T, H, group, M, hq, hk, hv, ho, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
     bool sectors;  // output rows start on 32-byte boundaries
+    bool boxes;    // 16-bit output: whole chunks are stored through maps.out
     float scale;
     // of a cut launch: a flag and a decay a CTA, then its state
     uint32_t* flags;
@@ -66,17 +67,17 @@ struct DecayPrefillArgs {
 };
 
 struct DecayMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 // shared memory
 constexpr uint32_t DS_K = 0, DS_V = 2 * kTile, DS_Q = 4 * kTile, DS_S = 5 * kTile, DS_LO = 6 * kTile, DS_G = 7 * kTile,
-                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 160, DS_CTRL = DS_BAR + 8 * 26, DS_SCAN = DS_CTRL + 64,
+                   DS_TOT = DS_G + 2048, DS_BAR = DS_TOT + 160, DS_CTRL = DS_BAR + 8 * 28, DS_SCAN = DS_CTRL + 64,
                    DS_MAX = DS_SCAN + 136, DS_SCALE = DS_MAX + 64, DS_SMEM = DS_SCALE + 8;
 static_assert(DS_SMEM <= 232448 && DS_SCAN % 8 == 0 && DS_BAR % 8 == 0, "shared memory plan");
 constexpr int B_KF = 0, B_VF = 2, B_QF = 4, B_QK = 5, B_P = 6, B_SPLIT = 7, B_KV = 9, B_S = 11, B_QS = 12, B_SCALED = 13,
               B_O = 14, B_OFREE = 15, B_GF = 16, B_GFREE = 18, B_MEET = 20, B_FREE = 21, B_DRAIN = 23,
-              B_NEVER = 24, B_COUNT = 25;
+              B_NEVER = 24, B_TAKEN = 25, B_COUNT = 27;
 // tensor memory: scores (their weights in the first half), results, K~ V, K~'s first two parts
 constexpr uint32_t DT_SC = 0, DT_O = 128, DT_KV = 256, DT_K1 = 384, DT_K2 = 448;
 
@@ -212,6 +213,18 @@ __device__ __forceinline__ float lds_f1(uint32_t addr) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
+// One box of a 3-D tensor map at (x, y, z) into L2, and one from shared memory (bulk group of the thread).
+__device__ __forceinline__ void prefetch_3d(const void* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void store_3d(const void* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
 // Four 8 x 8 blocks of 16-bit elements, transposed on the way to or from registers.
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -230,6 +243,13 @@ __device__ __forceinline__ void st16x128(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Eight results from o[e] as one 16-byte word.
+template <int DT>
+__device__ __forceinline__ uint4 pack16(const float (&o)[32], int e) {
+    return make_uint4(Elem<DT>::put2(o[e], o[e + 1]), Elem<DT>::put2(o[e + 2], o[e + 3]), Elem<DT>::put2(o[e + 4], o[e + 5]),
+                      Elem<DT>::put2(o[e + 6], o[e + 7]));
 }
 
 // A row's 32 results from column c on, in whole 32-byte sectors where the rows allow it: a warp's lanes write 32
@@ -350,6 +370,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         if (tid == B_P || tid == B_SCALED || tid == B_OFREE) count = 4;      // warps
         if (tid == B_SPLIT || tid == B_SPLIT + 1 || tid == B_S || tid == B_MEET) count = 8;
         if (tid == B_GFREE || tid == B_GFREE + 1) count = 13;
+        if (tid == B_FREE || tid == B_FREE + 1) count = 5;  // four warps and a commit
+        if (tid == B_TAKEN || tid == B_TAKEN + 1) count = 8;
         mbar_init(bar(tid), count);
     }
     if (warp == 1) tmem_alloc(sb + DS_CTRL, 512);
@@ -397,6 +419,12 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 if (m > 0) wait(B_QS, (m - 1) & 1);
                 load(DS_Q, &maps.q, hk * a.hq, B_QF);
                 ++m;
+            }
+            // the next chunk into L2: its loads wait for their buffers (Q's for this chunk's Q S), and from HBM they
+            // took 4400 cycles then
+            if (ch.c + 1 < ch.p.c1 && lane < (ch.p.state_only ? 4 : 6)) {
+                const int which = lane >> 1, head = which == 0 ? hk * a.hk : which == 1 ? h * a.hv : hk * a.hq;
+                prefetch_3d(which == 0 ? &maps.k : which == 1 ? &maps.v : &maps.q, 64 * (lane & 1), head, row + kDecayChunk);
             }
         }
     } else if (warp == 1) {
@@ -488,22 +516,37 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         }
         commit_by(lead, bar(B_DRAIN));
         dead = !wait_for(bar(B_DRAIN), 0) || dead;
-    } else if (warp == 2) {
+    } else if (warp < 4) {
         // ================================================================ decays: lane l has tokens 4l .. 4l + 3
-        uint32_t it = 0;
-        for (Chunks ch(a, rg); !__any_sync(~0u, dead); ch.next(a), ++it) {
+        // two warps in turns, each with the next log decays it needs in flight
+        Chunks ch(a, rg);
+        if (warp == 3 && ch.any) ch.next(a);
+        float ahead[4];
+        auto ask = [&] {
+            const int first = ch.c * kDecayChunk + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ahead[e] = ch.any && first + e < ch.p.rows
+                               ? log_decay_of(a.head_decay, a.log_decay, (int64_t)ch.p.row0 + first + e, a.H, ch.p.h)
+                               : 0.f;
+        };
+        ask();
+        for (uint32_t it = warp & 1; !__any_sync(~0u, dead); it += 2) {
             const uint32_t st = it & 1;
-            double g[4] = {0, 0, 0, 0};
-            if (ch.any) {
-                const int first = ch.c * kDecayChunk + 4 * lane;
-                float x[4];
+            const bool any = ch.any;
+            const int before = ch.c * kDecayChunk;
+            const Piece& p = ch.p;
+            const int flags = !any ? kStop
+                                   : (p.state_only ? 0 : kFull) | (ch.c == p.c0 ? kFirst : 0) | (ch.c + 1 == p.c1 ? kLast : 0) |
+                                         (p.start == kFromOthers ? kJoins : 0) | (p.end == kFinal ? kFinalState : 0) |
+                                         (p.end == kPublish ? kLeaves : 0) | (p.rows - before < kDecayChunk ? kPartial : 0);
+            const int4 info1 = make_int4(p.n, p.h, ch.c, p.row0 + before), info2 = make_int4(p.rows - before, p.rows, flags, 0);
+            double g[4], y0 = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = first + e < ch.p.rows ? log_decay_of(a.head_decay, a.log_decay, (int64_t)ch.p.row0 + first + e, a.H, ch.p.h) : 0.f;
-                double y = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[e] = y += (double)x[e] * 1.4426950408889634;
-            }
+            for (int e = 0; e < 4; ++e) g[e] = y0 += (double)ahead[e] * 1.4426950408889634;
+            if (any) ch.next(a);
+            if (ch.any) ch.next(a);
+            ask();
             double x = g[3];
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
@@ -533,18 +576,12 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 }
                 if (lane == 0) {
                     tot[4] = isnan(all) ? (float)all : chunk;
-                    const Piece& p = ch.p;
-                    const int before = ch.c * kDecayChunk;
-                    const int flags = !ch.any ? kStop
-                                              : (p.state_only ? 0 : kFull) | (ch.c == p.c0 ? kFirst : 0) | (ch.c + 1 == p.c1 ? kLast : 0) |
-                                                    (p.start == kFromOthers ? kJoins : 0) | (p.end == kFinal ? kFinalState : 0) |
-                                                    (p.end == kPublish ? kLeaves : 0) | (p.rows - before < kDecayChunk ? kPartial : 0);
-                    *reinterpret_cast<int4*>(tot + 8) = make_int4(p.n, p.h, ch.c, p.row0 + before);
-                    *reinterpret_cast<int4*>(tot + 12) = make_int4(p.rows - before, p.rows, flags, 0);
+                    *reinterpret_cast<int4*>(tot + 8) = info1;
+                    *reinterpret_cast<int4*>(tot + 12) = info2;
                 }
             }
             arrive(B_GF + st);
-            if (!ch.any) break;
+            if (!any) break;
         }
     } else if (warp >= 4 && warp < 8) {
         // ================================================================ weights and results: a thread has a row
@@ -560,6 +597,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             if (ch.flags & kStop) break;
             if (!(ch.flags & kFull)) {
                 arrive(B_GFREE + st);
+                // not before the stage's last chunk has had its products: an early arrival would count for that one
+                if (it >= 2) wait(B_FREE + st, ((it >> 1) - 1) & 1);
+                arrive(B_FREE + st);
                 continue;
             }
             const uint32_t gd = g_d + st * 1024;
@@ -646,6 +686,11 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             wait(B_O, m & 1);
             if (__any_sync(~0u, dead)) break;
             fence_after();
+            const bool boxes = a.boxes && !(ch.flags & kPartial);
+            const uint32_t stage = sb + DS_K + st * kTile;  // of these keys, for whole chunks' results
+            if (boxes) wait(B_TAKEN + st, (it >> 1) & 1);
+            else arrive(B_FREE + st);
+            if (__any_sync(~0u, dead)) break;
             const int64_t o_at = ((int64_t)ch.row0 + row) * a.out.rs + ch.h * a.out.hs;
             uint8_t* o_row = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base)) + o_at * dtype_bytes(a.out_dt);
 #pragma unroll 1
@@ -659,14 +704,32 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 if constexpr (kF16)
 #pragma unroll
                     for (int z = 0; z < 32; ++z) o[z] *= fp;
-                if (row < ch.left) {
+                if (boxes) {
+                    const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4),
+                               a.out_dt == KDA_BF16 ? pack16<KDA_BF16>(o, 8 * z) : pack16<KDA_F16>(o, 8 * z));
+                } else if (row < ch.left) {
                     if (a.out_dt == KDA_BF16) store_row32<KDA_BF16>(o_row, 32 * b, o, a.sectors);
                     else if (a.out_dt == KDA_F16) store_row32<KDA_F16>(o_row, 32 * b, o, a.sectors);
                     else store_row32<KDA_F32>(o_row, 32 * b, o, a.sectors);
                 }
             }
+            if (boxes) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int x = 0; x < 2; ++x)
+                        store_3d(&maps.out, 64 * x, ch.h * a.ho, ch.row0 + 32 * w, stage + x * (kTile / 2) + 32 * w * 128);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                arrive(B_FREE + st);
+            }
             ++m;
         }
+        if (lane == 0) bulk_wait_all();
     } else if (warp >= 8) {
         // ================================================================ keys and state
         // A thread has key channel `key` of the state, value channels 64 half .. 64 half + 63; of the keys' split its
@@ -765,6 +828,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 fence_async_smem();
                 arrive(B_SPLIT + i);
             }
+            arrive(B_TAKEN + st);
             arrive(B_GFREE + st);
             // ---- the state before this chunk, under the products
             if (p.flags & kFirst) {
@@ -890,12 +954,12 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head and 128 rows.
-bool chunk_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int H, int T) {
+// Tensor map over rows of heads: (channel, head, row), one box 64 channels of one head.
+bool chunk_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int H, int T, int rows) {
     // a dimension that is not stepped along (one head or row, or heads that share a row) has size 1 and any legal stride
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)(r.hs ? H : 1), (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)(r.hs ? r.hs : kD) * 2, (cuuint64_t)(r.rs ? r.rs : kD) * 2};
-    const cuuint32_t box[3] = {64, 1, kDecayChunk};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     return encode_16bit(map, dt, 3, r.base, dims, strides, box);
 }
 
@@ -941,11 +1005,15 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
     DecayPrefillArgs a{};
     if (T_tot > 0) {
         const LatentRows rq = as_rows(q), rk = as_rows(k), rv = as_rows(v);
-        KDA_REQUIRE(chunk_map(&maps.q, in_dtype, rq, Hk, T_tot) && chunk_map(&maps.k, in_dtype, rk, Hk, T_tot) &&
-                        chunk_map(&maps.v, in_dtype, rv, H, T_tot),
+        KDA_REQUIRE(chunk_map(&maps.q, in_dtype, rq, Hk, T_tot, kDecayChunk) &&
+                        chunk_map(&maps.k, in_dtype, rk, Hk, T_tot, kDecayChunk) &&
+                        chunk_map(&maps.v, in_dtype, rv, H, T_tot, kDecayChunk),
                     KDA_ERR_CUDA);
         a.hq = rq.hs != 0, a.hk = rk.hs != 0, a.hv = rv.hs != 0;
         a.out = as_rows(out);
+        a.ho = a.out.hs != 0;
+        a.boxes = out_dtype != KDA_F32 && (a.out.hs != 0 || H == 1) && (a.out.rs > 0 || T_tot == 1) && a.out.hs >= 0;
+        if (a.boxes) KDA_REQUIRE(chunk_map(&maps.out, out_dtype, a.out, H, T_tot, 32), KDA_ERR_CUDA);
         const int per = 32 / dtype_bytes(out_dtype);
         a.sectors = reinterpret_cast<uintptr_t>(out->base) % 32 == 0 && out->row_stride % per == 0 && out->head_stride % per == 0;
     }
