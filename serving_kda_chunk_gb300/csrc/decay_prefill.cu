@@ -47,7 +47,6 @@ constexpr int kPreDecayThreads = 512;
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
 constexpr uint32_t kWaitLimit = 1u << 18;
 constexpr uint32_t kFlagLimit = 1u << 21;
-constexpr uint32_t kPollLimit = 1u << 25;  // of barrier tests, some 40 cycles each
 
 struct DecayPrefillArgs {
     LatentRows out;
@@ -57,7 +56,6 @@ struct DecayPrefillArgs {
     int32_t* dev_status;
     int64_t P;
     int32_t N, T, H, group, M, hq, hk, hv, ho, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
-    bool sectors;  // output rows start on 32-byte boundaries
     bool boxes;    // 16-bit output: whole chunks are stored through maps.out
     float scale;
     // of a cut launch: a flag and a decay a CTA, then its state
@@ -124,7 +122,8 @@ struct Pieces {
         do ++n;
         while (n <= r.ln && seq_chunks(a, n, bad) == 0);
     }
-    __device__ bool next(const DecayPrefillArgs& a, Piece& p) {
+    // (not inlined: its five copies were a fourth of the kernel)
+    __device__ __noinline__ bool next(const DecayPrefillArgs& a, Piece& p) {
         int bad;
         const bool same = r.fn == r.ln && r.fh == r.lh;
         const bool cut = r.lo + 1 < seq_chunks(a, r.ln, bad);  // the last unit goes on in the next range
@@ -185,17 +184,40 @@ struct ChunkInfo {
     int left, rows, flags, pad;  // left: rows of the sequence from this chunk on
 };
 
-// mbar_wait with the usual limit, its loop not unrolled (there are thirty of it).
-__device__ __forceinline__ bool wait_for(uint32_t mbar, uint32_t parity) {
-    uint32_t done = 0;
-#pragma unroll 1
-    for (uint32_t it = 0; it < kWaitLimit && !done; ++it)
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(done)
-            : "r"(mbar), "r"(parity)
-            : "memory");
+// ld32 without the wait: the registers are valid after the next wait_ld().
+__device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ bool try_wait(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
     return done;
+}
+__device__ __forceinline__ int gone_of(uint32_t gone) {  // the block's mark of a wait that ran out
+    int x;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(x) : "r"(gone) : "memory");
+    return x;
+}
+// The rest of a wait whose first try did not do.  When the limit is reached, or another wait of the block has run
+// out, it returns all the same, with the mark set.
+__device__ __noinline__ void wait_on(uint32_t mbar, uint32_t parity, uint32_t gone) {
+#pragma unroll 1
+    for (uint32_t it = 0; it < kWaitLimit; ++it)
+        if (try_wait(mbar, parity) || gone_of(gone)) return;
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(gone), "r"(1) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -225,6 +247,11 @@ __device__ __forceinline__ void store_3d(const void* map, int x, int y, int z, u
                  "r"(x), "r"(y), "r"(z), "r"(src)
                  : "memory");
 }
+// The upper halves of two fp32 values: packed, and as values.
+__device__ __forceinline__ uint32_t upper(float2 x) { return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632); }
+__device__ __forceinline__ float2 upper_of(float2 x) {
+    return make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+}
 // Four 8 x 8 blocks of 16-bit elements, transposed on the way to or from registers.
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -252,28 +279,66 @@ __device__ __forceinline__ uint4 pack16(const float (&o)[32], int e) {
                       Elem<DT>::put2(o[e + 6], o[e + 7]));
 }
 
-// A row's 32 results from column c on, in whole 32-byte sectors where the rows allow it: a warp's lanes write 32
-// rows, so each store is 32 accesses whatever its width (8 bytes a store took 4100 of a chunk's 14000 cycles).
-template <int ODT>
-__device__ __forceinline__ void store_row32(void* row, int c, const float (&o)[32], bool sectors) {
-    constexpr int kWords = ODT == KDA_F32 ? 32 : 16;
-    uint32_t w[kWords];
+// A row of results from tensor memory to its place: outputs of 32 bits, and chunks that a sequence ends in.
+__device__ __noinline__ void store_rows(uint32_t taddr, float f, const uint8_t* to, int dt, bool there) {
+    uint8_t* p = const_cast<uint8_t*>(to);
+#pragma unroll 1
+    for (int c = 0; c < kD; c += 16) {
+        float o[16];
+        ld16(taddr + c, o);
+        if (there)
 #pragma unroll
-    for (int e = 0; e < kWords; ++e)
-        if constexpr (ODT == KDA_F32) w[e] = __float_as_uint(o[e]);
-        else w[e] = Elem<ODT>::put2(o[2 * e], o[2 * e + 1]);
-    uint8_t* p = static_cast<uint8_t*>(row) + c * dtype_bytes(ODT);
-    if (sectors) {
-#pragma unroll
-        for (int e = 0; e < kWords; e += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 4 * e), "r"(w[e]), "r"(w[e + 1]),
-                         "r"(w[e + 2]), "r"(w[e + 3]), "r"(w[e + 4]), "r"(w[e + 5]), "r"(w[e + 6]), "r"(w[e + 7])
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int e = 0; e < kWords; e += 4)
-            *reinterpret_cast<uint4*>(p + 4 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            for (int z = 0; z < 16; z += 4) store4_as(p, c + z, make_float4(o[z] * f, o[z + 1] * f, o[z + 2] * f, o[z + 3] * f), dt);
     }
+    fence_before();
+}
+
+// 64 elements of a state, `stride` elements apart, from and to memory (all in flight together); and joined to those
+// that another CTA left.
+template <class T>
+__device__ __forceinline__ void get_as(float* S, const T* p, size_t stride) {
+    T x[64];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) x[e] = p[e * stride];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) S[e] = (float)x[e];
+}
+template <class T>
+__device__ __forceinline__ void put_as(const float* S, T* p, size_t stride) {
+#pragma unroll
+    for (int e = 0; e < 64; ++e) p[e * stride] = (T)S[e];
+}
+__device__ __noinline__ void get_state(float* S, const void* from, size_t at, size_t stride, int st) {
+    if (st == kStateF32) get_as(S, static_cast<const float*>(from) + at, stride);
+    else if (st == kStateBF16) get_as(S, static_cast<const __nv_bfloat16*>(from) + at, stride);
+    else get_as(S, static_cast<const __half*>(from) + at, stride);
+}
+__device__ __noinline__ void put_state(const float* S, void* to, size_t at, size_t stride, int st) {
+    if (st == kStateF32) put_as(S, static_cast<float*>(to) + at, stride);
+    else if (st == kStateBF16) put_as(S, static_cast<__nv_bfloat16*>(to) + at, stride);
+    else put_as(S, static_cast<__half*>(to) + at, stride);
+}
+__device__ __noinline__ void join_state(float* S, float f, const float* from) {
+    float x[64];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) x[e] = __ldcg(from + e * 256);
+#pragma unroll
+    for (int e = 0; e < 64; ++e) S[e] = fmaf(f, S[e], x[e]);
+}
+
+// Q S_0's rows to the scale of the weights, as the sum that P V goes on: `cols` columns of this thread's lane.
+__device__ __forceinline__ void scale_rows(uint32_t taddr, int cols, float f) {
+    fence_after();
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        float x[32];
+        ld32(taddr + c, x);
+#pragma unroll
+        for (int z = 0; z < 32; ++z) x[z] *= f;
+        st32(taddr + c, x);
+    }
+    wait_st();
+    fence_before();
 }
 
 // The power of two, at most 2^60, that takes x into [2^13, 2^14); 1 for zero, infinities and NaN.
@@ -380,15 +445,16 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     fence_after();
     const uint32_t tmem = ctrl[0];
 
-    // A wait that runs out ends its role: it arrives nowhere and writes nothing from then on, so the other roles'
-    // waits run out too.
-    bool dead = false;
+    // A wait that runs out marks the block: its roles then end with the chunk they are at, and nothing is stored any
+    // more.  (That, and what is rare, stays out of line: the roles share an instruction cache.)
+    const uint32_t gone = sb + DS_CTRL + 4;
     auto wait = [&](int b, uint32_t parity) {
-        if (!dead) dead = !wait_for(bar(b), parity);
+        if (!try_wait(bar(b), parity)) wait_on(bar(b), parity, gone);
     };
+    auto dead = [&] { return __any_sync(~0u, gone_of(gone)); };
     auto arrive = [&](int b) {  // of a warp
         __syncwarp();
-        if (lane == 0 && !dead) mbar_arrive(bar(b));
+        if (lane == 0) mbar_arrive(bar(b));
     };
     const uint32_t g_d = sb + DS_G, g_tot = sb + DS_TOT;  // a stage: D [128], e^-D [128]; totals [4], the chunk's decay, its ChunkInfo, e^ of the totals behind each block [4]
     auto info_of = [&](uint32_t st) {
@@ -399,12 +465,12 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     if (warp == 0) {
         // ================================================================ loads
         uint32_t it = 0, m = 0;
-        for (Chunks ch(a, rg); ch.any && !__any_sync(~0u, dead); ch.next(a), ++it) {
+        for (Chunks ch(a, rg); ch.any && !dead(); ch.next(a), ++it) {
             const uint32_t st = it & 1;
             const int row = ch.p.row0 + ch.c * kDecayChunk, h = ch.p.h, hk = h / a.group;
             if (it >= 2) wait(B_FREE + st, ((it >> 1) - 1) & 1);
             auto load = [&](uint32_t dst, const CUtensorMap* map, int head, int b) {
-                if (lane != 0 || dead) return;
+                if (lane != 0) return;
                 if (ch.p.rows == 0) {  // an empty sequence's one chunk: its keys and values are cleared, its scores not used
                     mbar_arrive(bar(b));
                     return;
@@ -443,79 +509,69 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         int flags = 0;  // of chunk it
         uint32_t m = 0;
         for (uint32_t it = ~0u;; ++it) {
-            // Chunk `it`, each product as soon as its operands are there, and the next chunk's scores (over this one's
-            // weights, so behind P V).
+            // Chunk `it` in the order in which operands come, and the next chunk's scores (over this one's weights, so
+            // behind P V).  The waits suspend the warp: a loop that tested all barriers in turn took so many issue slots
+            // from the three warps beside it that every role waited for those.
             const uint32_t st = it & 1, sn = st ^ 1;
             const bool full = flags & kFull;
-            const uint32_t v4 = sb4 + DS_V / 16 + st * t4, par = m & 1;
-            int next = 0;
-            bool qs = full, pv = full, told = false, ask = false;
-            int halves = it == ~0u ? 2 : 0;  // of each 64 tokens, in K~ V
-            auto have = [&](int b, uint32_t parity) { return __all_sync(~0u, mbar_test(bar(b), parity)); };
-            for (uint32_t polls = 0; (qs || pv || halves < 2 || !told || ask) && !dead; ++polls) {
-                if (halves < 2 && have(B_SPLIT + halves, it & 1) && have(B_VF + st, (it >> 1) & 1)) {
+            const uint32_t v4 = sb4 + DS_V / 16 + st * t4;
+            if (it != ~0u) {
+                wait(B_VF + st, (it >> 1) & 1);
+#pragma unroll 1
+                for (uint32_t i = 0; i < 2; ++i) {  // 32 of each 64 tokens
+                    wait(B_SPLIT + i, it & 1);
                     fence_after();
-                    const uint32_t fresh = halves == 0;
                     // the smallest part first: what a sum of products loses goes by its size so far
                     if constexpr (!kF16) {
 #pragma unroll
                         for (uint32_t x = 0; x < 4; ++x) {
-                            const uint32_t s = 2 * halves + (x & 1) + 4 * (x >> 1);
-                            mma_by(lead, tm + DT_KV, along_mn(lo4, s), along_mn(v4, s), i_tt, x > 0 || !fresh);
+                            const uint32_t s = 2 * i + (x & 1) + 4 * (x >> 1);
+                            mma_by(lead, tm + DT_KV, along_mn(lo4, s), along_mn(v4, s), i_tt, i | x);
                         }
                     }
 #pragma unroll 1
                     for (uint32_t part = 0; part < 2; ++part)
 #pragma unroll
                         for (uint32_t x = 0; x < 4; ++x) {
-                            const uint32_t s = 2 * halves + (x & 1) + 4 * (x >> 1);
+                            const uint32_t s = 2 * i + (x & 1) + 4 * (x >> 1);
                             mma_ta_by(lead, tm + DT_KV, tm + (part ? DT_K1 : DT_K2) + 8 * s, along_mn(v4, s), i_tv,
-                                      !kF16 || part > 0 || x > 0 || !fresh);
+                                      !kF16 || part > 0 || (i | x));
                         }
-                    if (++halves == 2) {
-                        commit_by(lead, bar(B_KV));
-                        if (!pv) commit_by(lead, bar(B_FREE + st));
-                    }
                 }
-                if (qs && have(B_S, par) && (m == 0 || have(B_OFREE, par ^ 1))) {
-                    fence_after();
-#pragma unroll
-                    for (uint32_t s = 0; s < 8; ++s) mma_by(lead, tm + DT_O, along_k(q4, s), along_mn(s4, s), i_tv, s);
-                    commit_by(lead, bar(B_QS));
-                    qs = false;
-                }
-                // rows past the sequence are cleared by those who split the keys
-                if (pv && !qs && have(B_P, par) && have(B_SCALED, par) && have(B_VF + st, (it >> 1) & 1) &&
-                    (!(flags & kPartial) || halves > 0)) {
-                    fence_after();
-#pragma unroll
-                    for (uint32_t s = 0; s < 8; ++s)
-                        mma_ta_by(lead, tm + DT_O, tm + DT_SC + 8 * s, along_mn(v4, s), i_tv, 1);
-                    commit_by(lead, bar(B_O));
-                    pv = false;
-                    if (halves == 2) commit_by(lead, bar(B_FREE + st));  // keys and values have had all their products
-                }
-                if (!told && have(B_GF + sn, ((it + 1) >> 1) & 1)) {
-                    next = __shfl_sync(~0u, info_of(sn).flags, 0);
-                    if (!(next & kStop)) arrive(B_GFREE + sn);
-                    told = true;
-                    ask = (next & (kFull | kStop)) == kFull;
-                }
-                if (ask && !pv && have(B_QF, full ? par ^ 1 : par) && have(B_KF + sn, ((it + 1) >> 1) & 1)) {
-#pragma unroll
-                    for (uint32_t s = 0; s < 8; ++s)
-                        mma_by(lead, tm + DT_SC, along_k(q4, s), along_k(sb4 + DS_K / 16 + sn * t4, s), i_qk, s);
-                    commit_by(lead, bar(B_QK));
-                    ask = false;
-                }
-                dead = polls >= kPollLimit;
+                commit_by(lead, bar(B_KV));
             }
-            m += full;
-            flags = next;
-            if ((flags & kStop) || __any_sync(~0u, dead)) break;
+            if (full) {
+                wait(B_S, m & 1);
+                if (m > 0) wait(B_OFREE, (m - 1) & 1);
+                fence_after();
+#pragma unroll
+                for (uint32_t s = 0; s < 8; ++s) mma_by(lead, tm + DT_O, along_k(q4, s), along_mn(s4, s), i_tv, s);
+                commit_by(lead, bar(B_QS));
+                wait(B_P, m & 1);
+                wait(B_SCALED, m & 1);
+                fence_after();
+#pragma unroll
+                for (uint32_t s = 0; s < 8; ++s) mma_ta_by(lead, tm + DT_O, tm + DT_SC + 8 * s, along_mn(v4, s), i_tv, 1);
+                commit_by(lead, bar(B_O));
+                ++m;
+            }
+            if (it != ~0u) commit_by(lead, bar(B_FREE + st));  // keys and values have had all their products
+            wait(B_GF + sn, ((it + 1) >> 1) & 1);
+            flags = __shfl_sync(~0u, info_of(sn).flags, 0);
+            if ((flags & kStop) || dead()) break;
+            arrive(B_GFREE + sn);
+            if (flags & kFull) {
+                wait(B_QF, m & 1);
+                wait(B_KF + sn, ((it + 1) >> 1) & 1);
+#pragma unroll
+                for (uint32_t s = 0; s < 8; ++s)
+                    mma_by(lead, tm + DT_SC, along_k(q4, s), along_k(sb4 + DS_K / 16 + sn * t4, s), i_qk, s);
+                commit_by(lead, bar(B_QK));
+            }
         }
         commit_by(lead, bar(B_DRAIN));
-        dead = !wait_for(bar(B_DRAIN), 0) || dead;
+        for (uint32_t polls = 0; polls < kWaitLimit && !try_wait(bar(B_DRAIN), 0); ++polls) {
+        }
     } else if (warp < 4) {
         // ================================================================ decays: lane l has tokens 4l .. 4l + 3
         // two warps in turns, each with the next log decays it needs in flight
@@ -531,7 +587,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                                : 0.f;
         };
         ask();
-        for (uint32_t it = warp & 1; !__any_sync(~0u, dead); it += 2) {
+        for (uint32_t it = warp & 1; !dead(); it += 2) {
             const uint32_t st = it & 1;
             const bool any = ch.any;
             const int before = ch.c * kDecayChunk;
@@ -565,7 +621,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             for (int k = 10; k > 0; --k) z = fma(z * y, 1.0 / k, 1.0);
             const float chunk = n < -126.0 ? 0.f : (float)z * __int_as_float(((int)n + 127) << 23);
             if (it >= 2) wait(B_GFREE + st, ((it >> 1) - 1) & 1);
-            if (!dead) {
+            {
                 const uint32_t at = DS_G + st * 1024 + 16 * lane;
                 *reinterpret_cast<float4*>(sm + at) = d;
                 *reinterpret_cast<float4*>(sm + at + 512) = make_float4(ex2(-d.x), ex2(-d.y), ex2(-d.z), ex2(-d.w));
@@ -589,14 +645,21 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         const uint32_t tl = tmem + ((uint32_t)(w * 32) << 16);
         const float scale = a.scale;
         uint32_t m = 0;
+        int owed = -1;  // the stage whose stored results have not been waited for
+        auto give_back = [&] {
+            if (owed < 0) return;
+            if (lane == 0) bulk_wait_read_all();
+            arrive(B_FREE + owed);
+            owed = -1;
+        };
         for (uint32_t it = 0;; ++it) {
             const uint32_t st = it & 1;
             wait(B_GF + st, (it >> 1) & 1);
-            if (__any_sync(~0u, dead)) break;
             const ChunkInfo ch = info_of(st);
-            if (ch.flags & kStop) break;
+            if ((ch.flags & kStop) || dead()) break;
             if (!(ch.flags & kFull)) {
                 arrive(B_GFREE + st);
+                give_back();
                 // not before the stage's last chunk has had its products: an early arrival would count for that one
                 if (it >= 2) wait(B_FREE + st, ((it >> 1) - 1) & 1);
                 arrive(B_FREE + st);
@@ -607,7 +670,6 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             const float tot[4] = {tot4.x, tot4.y, tot4.z, tot4.w};
             const float d = lds_f1(gd + 4 * row);
             wait(B_QK, m & 1);
-            if (__any_sync(~0u, dead)) break;
             fence_after();
             float ps = 1.f;  // fp16: the row's scale
             if constexpr (kF16) {
@@ -621,16 +683,22 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 ps = range_scale(mx * fabsf(scale));
             }
             const float sp = kF16 ? scale * ps : scale;
+            // blocks before the diagonal one, that one, then zeros; a block's scores are asked for ahead of its turn
+            uint32_t ahead[32];
+            ld32_issue(tl + DT_SC, ahead);
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b <= w; ++b) {
+                float s[32];
+                wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(ahead[x]);
+                if (b < w) ld32_issue(tl + DT_SC + 32 * (b + 1), ahead);
                 uint32_t p[16];
                 if (b < w) {
                     float e = d;
 #pragma unroll
                     for (int x = 1; x < 4; ++x) e += x > b && x <= w ? tot[x] : 0.f;
                     const float f = sp * ex2(e);
-                    float s[32];
-                    ld32(tl + DT_SC + 32 * b, s);
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const float4 c = lds_f4(gd + 512 + 4 * (32 * b + x));
@@ -638,9 +706,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         p[x / 2] = E::put2(y.x, y.y);
                         p[x / 2 + 1] = E::put2(y.z, y.w);
                     }
-                } else if (b == w) {
-                    float s[32];
-                    ld32(tl + DT_SC + 32 * b, s);
+                } else {
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const float4 c = lds_f4(gd + 4 * (32 * b + x));
@@ -650,82 +716,69 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         p[x / 2] = E::put2(s[x], s[x + 1]);
                         p[x / 2 + 1] = E::put2(s[x + 2], s[x + 3]);
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) p[x] = 0;
                 }
+                // (over scores of this block and, for the second, the first: both have been read)
+                st16u(tl + DT_SC + 16 * b, p);
+            }
+            for (int b = w + 1; b < 4; ++b) {
+                uint32_t p[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) p[x] = 0;
                 st16u(tl + DT_SC + 16 * b, p);
             }
             wait_st();
             fence_before();
             arrive(B_P);
-            float e = d;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) e += x <= w ? tot[x] : 0.f;
+            give_back();
             arrive(B_GFREE + st);
-            // Q S_0 to the scale of the weights, as the sum that P V goes on
-            float fs = scale * ex2(e), fp = 1.f;
+            float fs = d, fp = 1.f;  // fs: G_i, then Q S_0's factor
+#pragma unroll
+            for (int x = 0; x < 4; ++x) fs += x <= w ? tot[x] : 0.f;
+            fs = sp * ex2(fs);
             wait(B_QS, m & 1);
-            if (__any_sync(~0u, dead)) break;
-            fence_after();
             if constexpr (kF16) {
-                fs *= ps * pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
+                fs *= pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
                 fp = pow2_inverse(ps);
             }
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                float x[32];
-                ld32(tl + DT_O + 32 * b, x);
-#pragma unroll
-                for (int z = 0; z < 32; ++z) x[z] *= fs;
-                st32(tl + DT_O + 32 * b, x);
-            }
-            wait_st();
-            fence_before();
+            scale_rows(tl + DT_O, 128, fs);
             arrive(B_SCALED);
             wait(B_O, m & 1);
-            if (__any_sync(~0u, dead)) break;
             fence_after();
             const bool boxes = a.boxes && !(ch.flags & kPartial);
-            const uint32_t stage = sb + DS_K + st * kTile;  // of these keys, for whole chunks' results
-            if (boxes) wait(B_TAKEN + st, (it >> 1) & 1);
-            else arrive(B_FREE + st);
-            if (__any_sync(~0u, dead)) break;
-            const int64_t o_at = ((int64_t)ch.row0 + row) * a.out.rs + ch.h * a.out.hs;
-            uint8_t* o_row = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(a.out.base)) + o_at * dtype_bytes(a.out_dt);
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                float o[32];
-                ld32(tl + DT_O + 32 * b, o);
-                if (b == 3) {
-                    fence_before();
-                    arrive(B_OFREE);
-                }
-                if constexpr (kF16)
-#pragma unroll
-                    for (int z = 0; z < 32; ++z) o[z] *= fp;
-                if (boxes) {
-                    const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4),
-                               a.out_dt == KDA_BF16 ? pack16<KDA_BF16>(o, 8 * z) : pack16<KDA_F16>(o, 8 * z));
-                } else if (row < ch.left) {
-                    if (a.out_dt == KDA_BF16) store_row32<KDA_BF16>(o_row, 32 * b, o, a.sectors);
-                    else if (a.out_dt == KDA_F16) store_row32<KDA_F16>(o_row, 32 * b, o, a.sectors);
-                    else store_row32<KDA_F32>(o_row, 32 * b, o, a.sectors);
-                }
-            }
             if (boxes) {
+                wait(B_TAKEN + st, (it >> 1) & 1);
+                const uint32_t stage = sb + DS_K + st * kTile;  // of these keys
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    ld32(tl + DT_O + 32 * b, o);
+                    if constexpr (kF16)
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) o[z] *= fp;
+                    const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128;
+                    if (a.out_dt == KDA_BF16) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4), pack16<KDA_BF16>(o, 8 * z));
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4), pack16<KDA_F16>(o, 8 * z));
+                    }
+                }
+                fence_before();
                 fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
+                arrive(B_OFREE);
+                if (!dead() && lane == 0) {
                     for (int x = 0; x < 2; ++x)
                         store_3d(&maps.out, 64 * x, ch.h * a.ho, ch.row0 + 32 * w, stage + x * (kTile / 2) + 32 * w * 128);
                     bulk_commit();
-                    bulk_wait_read_all();
                 }
+                owed = (int)st;
+            } else {
                 arrive(B_FREE + st);
+                const int64_t o_at = ((int64_t)ch.row0 + row) * a.out.rs + ch.h * a.out.hs;
+                store_rows(tl + DT_O, fp, reinterpret_cast<const uint8_t*>(a.out.base) + o_at * dtype_bytes(a.out_dt), a.out_dt,
+                           !dead() && row < ch.left);
+                arrive(B_OFREE);
             }
             ++m;
         }
@@ -745,16 +798,11 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         };
         // this thread's elements of a state in memory, whose rows are value channels
         auto elems = [&](int64_t slot, int h) { return state_elem(slot, a.H, h) + (size_t)(64 * half) * kD + key; };
-        auto store_state = [&](void* to, size_t at) {
-            if (a.st == kStateF32)
+        auto store_state = [&](void* to, size_t at, size_t stride, int st) {
+            float x[64];  // (the registers themselves have no address)
 #pragma unroll
-                for (int e = 0; e < 64; ++e) static_cast<float*>(to)[at + (size_t)e * kD] = S[e];
-            else if (a.st == kStateBF16)
-#pragma unroll
-                for (int e = 0; e < 64; ++e) static_cast<__nv_bfloat16*>(to)[at + (size_t)e * kD] = __float2bfloat16_rn(S[e]);
-            else
-#pragma unroll
-                for (int e = 0; e < 64; ++e) static_cast<__half*>(to)[at + (size_t)e * kD] = __float2half_rn(S[e]);
+            for (int e = 0; e < 64; ++e) x[e] = S[e];
+            if (!dead()) put_state(x, to, at, stride, st);
         };
         // ldmatrix of 8 x 8 blocks, transposed: block j of four has channels 8 (j & 1) .. and tokens 8 (j >> 1) .., its
         // row r lies at token r; the other block of 64 channels 16 KiB on
@@ -763,16 +811,15 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         for (;; ++it) {
             const uint32_t st = it & 1;
             wait(B_GF + st, (it >> 1) & 1);
-            if (__any_sync(~0u, dead)) break;
             const ChunkInfo p = info_of(st);
-            if (p.flags & kStop) break;
+            if ((p.flags & kStop) || dead()) break;
             const bool full = p.flags & kFull;
             const float ac = lds_f1(g_tot + st * 80 + 16);
             wait(B_KF + st, (it >> 1) & 1);
             if (p.left < kDecayChunk) {
                 // rows past the sequence have a weight of zero, and so has to be the value
                 wait(B_VF + st, (it >> 1) & 1);
-                for (int x = max(p.left, 0) * 8 + t; x < 1024 && !dead; x += 256) {
+                for (int x = max(p.left, 0) * 8 + t; x < 1024; x += 256) {
                     sts128(sb + DS_V + st * kTile + 16 * x, make_uint4(0, 0, 0, 0));
                     sts128(sb + DS_V + st * kTile + kTile / 2 + 16 * x, make_uint4(0, 0, 0, 0));
                 }
@@ -790,10 +837,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                                  : "r"(g_d + st * 1024 + 512 + 4 * (token + 8 * g)));
                     f[g] = __fmul2_rn(f[g], make_float2(after, after));
                 }
-                const uint32_t row_at = k_row + 4096 * i;
-#pragma unroll
+#pragma unroll 1
                 for (int lh = 0; lh < 2; ++lh) {  // 16 channels
-                    const uint32_t at = row_at + (((chunk16 + 2 * lh) ^ (lane & 7)) << 4);
+                    const uint32_t at = k_row + 4096 * i + (((chunk16 + 2 * lh) ^ (lane & 7)) << 4);
                     uint32_t k[8], mid[8], lo[8];
                     ldsm4t(sb + DS_K + st * kTile + at, k);
                     ldsm4t(sb + DS_K + st * kTile + at + 2048, k + 4);
@@ -805,22 +851,24 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                             if (token + 8 * (x >> 1) >= p.left) y.x = 0.f;
                             if (token + 8 * (x >> 1) + 1 >= p.left) y.y = 0.f;
                         }
-                        k[x] = E::put2(y.x, y.y);
-                        y = __ffma2_rn(E::get2(k[x]), minus, y);
-                        mid[x] = E::put2(y.x, y.y);
-                        if constexpr (!kF16) {
-                            y = __ffma2_rn(E::get2(mid[x]), minus, y);
-                            lo[x] = E::put2(y.x, y.y);
+                        if constexpr (kF16) {
+                            k[x] = E::put2(y.x, y.y);
+                            y = __ffma2_rn(E::get2(k[x]), minus, y);
+                            mid[x] = E::put2(y.x, y.y);
+                        } else {  // three times the upper 8 bits of what is left: nothing is
+                            k[x] = upper(y);
+                            y = __ffma2_rn(upper_of(y), minus, y);
+                            mid[x] = upper(y);
+                            y = __ffma2_rn(upper_of(y), minus, y);
+                            lo[x] = upper(y);
                         }
                     }
-                    if (!__any_sync(~0u, dead)) {
-                        const uint32_t to = tl + ((uint32_t)(16 * lh) << 16) + 32 * half + 16 * i;
-                        st16x128(to + DT_K1, k);
-                        st16x128(to + DT_K2, mid);
-                        if constexpr (!kF16) {
-                            stsm4t(sb + DS_LO + at, lo);
-                            stsm4t(sb + DS_LO + at + 2048, lo + 4);
-                        }
+                    const uint32_t to = tl + ((uint32_t)(16 * lh) << 16) + 32 * half + 16 * i;
+                    st16x128(to + DT_K1, k);
+                    st16x128(to + DT_K2, mid);
+                    if constexpr (!kF16) {
+                        stsm4t(sb + DS_LO + at, lo);
+                        stsm4t(sb + DS_LO + at + 2048, lo + 4);
                     }
                 }
                 wait_st();
@@ -832,52 +880,43 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             arrive(B_GFREE + st);
             // ---- the state before this chunk, under the products
             if (p.flags & kFirst) {
+                float x[64];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) S[e] = 0.f;
+                for (int e = 0; e < 64; ++e) x[e] = 0.f;
                 decay = 1.f;
                 if (full && !(p.flags & kJoins)) {
                     const int src = a.init_slot ? a.init_slot[p.n] : -1;
-                    if (src >= 0) {
-                        const size_t at = elems(src, p.h);
-                        if (a.st == kStateF32)
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) S[e] = static_cast<const float*>(a.pool)[at + (size_t)e * kD];
-                        else if (a.st == kStateBF16)
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) S[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool)[at + (size_t)e * kD]);
-                        else
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) S[e] = __half2float(static_cast<const __half*>(a.pool)[at + (size_t)e * kD]);
-                    }
+                    if (src >= 0) get_state(x, a.pool, elems(src, p.h), kD, a.st);
                     if (p.h == 0 && t == 0)
-                        for (int x = 0; x < a.M; ++x) {
-                            const int c = a.track_idx[(int64_t)p.n * a.M + x];
+                        for (int y = 0; y < a.M; ++y) {
+                            const int c = a.track_idx[(int64_t)p.n * a.M + y];
                             if (c < -1 || c >= (p.rows + kDecayChunk - 1) / kDecayChunk) report(a.dev_status, KDA_DEV_BAD_TRACK);
                         }
                 } else if (full) {
                     // the CTA with the unit's beginning left a state, those after it their ranges' own
-                    const int j0 = (int)(((x0 - rg.fo + 1) * ctas - 1) / total);
-                    for (int j = j0; j < (int)blockIdx.x; ++j) {
+                    for (int j = (int)(((x0 - rg.fo + 1) * ctas - 1) / total); j < (int)blockIdx.x; ++j) {
                         uint32_t set = 0;
-                        for (uint32_t polls = 0; polls < kFlagLimit && !set && !dead; ++polls) {
+#pragma unroll 1
+                        for (uint32_t polls = 0; polls < kFlagLimit && !set && !gone_of(gone); ++polls) {
                             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(set) : "l"(a.flags + j) : "memory");
                             if (!set) __nanosleep(64);
                         }
-                        dead = dead || !set;
-                        if (dead) break;
-                        const float f = *(volatile float*)(a.decays + j);
-                        const float* from = a.states + (size_t)j * (kD * kD) + t;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) S[e] = fmaf(f, S[e], __ldcg(from + e * 256));
+                        if (!set) {
+                            ctrl[1] = 1;
+                            break;
+                        }
+                        join_state(x, *(volatile float*)(a.decays + j), a.states + (size_t)j * (kD * kD) + t);
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 64; ++e) S[e] = x[e];
             }
             if (full) {
                 if (a.M > 0 && p.rows > 0) {
                     for (int base = 0; base < a.M; base += 32) {
                         const int x = base + lane < a.M ? a.track_idx[(int64_t)p.n * a.M + base + lane] : -1;
                         for (uint32_t hit = __ballot_sync(~0u, x == p.c); hit; hit &= hit - 1)
-                            if (!__any_sync(~0u, dead)) store_state(a.track, elems((int64_t)p.n * a.M + base + __ffs(hit) - 1, p.h));
+                            store_state(a.track, elems((int64_t)p.n * a.M + base + __ffs(hit) - 1, p.h), kD, a.st);
                     }
                 }
                 float ss = 1.f;
@@ -896,7 +935,6 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     if (t == 0) *reinterpret_cast<float*>(sm + DS_SCALE + 4 * (m & 1)) = ss;
                 }
                 if (m > 0) wait(B_QS, (m - 1) & 1);  // the last operand has been read
-                if (!dead)
 #pragma unroll
                     for (int e = 0; e < 64; e += 8) {
                         uint4 x;
@@ -924,29 +962,25 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             if (!(p.flags & kLast)) continue;
             if (p.flags & kFinalState) {
                 const int dst = a.final_slot ? a.final_slot[p.n] : -1;
-                if (dst >= 0 && !__any_sync(~0u, dead)) store_state(a.pool, elems(dst, p.h));
+                if (dst >= 0) store_state(a.pool, elems(dst, p.h), kD, a.st);
             } else if (p.flags & kLeaves) {
-                float* to = a.states + (size_t)blockIdx.x * (kD * kD) + t;
-#pragma unroll
-                for (int e = 0; e < 64; ++e) __stcg(to + e * 256, S[e]);
+                store_state(a.states, (size_t)blockIdx.x * (kD * kD) + t, 256, kStateF32);
                 if (t == 0) a.decays[blockIdx.x] = decay;
                 __threadfence();
                 meet();
-                if (t == 0 && !dead)
+                if (t == 0 && !gone_of(gone))
                     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + blockIdx.x), "r"(1u) : "memory");
             }
         }
-    }
-    if (dead) {
-        ctrl[1] = 1;
-        report(a.dev_status, KDA_DEV_TIMEOUT);
     }
     fence_before();
     __syncthreads();
     // Every load was waited for by a role that is done.  After a wait that ran out that does not hold: a bounded
     // wait on a barrier that nothing arrives on (about a second) lets them land.
     if (ctrl[1] && warp == 0) {
-        wait_for(bar(B_NEVER), 0);
+        for (uint32_t polls = 0; polls < kWaitLimit && !try_wait(bar(B_NEVER), 0); ++polls) {
+        }
+        if (lane == 0) report(a.dev_status, KDA_DEV_TIMEOUT);
         __syncwarp();
     }
     __syncthreads();
@@ -1014,8 +1048,6 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
         a.ho = a.out.hs != 0;
         a.boxes = out_dtype != KDA_F32 && (a.out.hs != 0 || H == 1) && (a.out.rs > 0 || T_tot == 1) && a.out.hs >= 0;
         if (a.boxes) KDA_REQUIRE(chunk_map(&maps.out, out_dtype, a.out, H, T_tot, 32), KDA_ERR_CUDA);
-        const int per = 32 / dtype_bytes(out_dtype);
-        a.sectors = reinterpret_cast<uintptr_t>(out->base) % 32 == 0 && out->row_stride % per == 0 && out->head_stride % per == 0;
     }
     a.head_decay = head_decay;
     a.log_decay = log_decay;
