@@ -56,7 +56,7 @@ struct DecayPrefillArgs {
     int32_t* dev_status;
     int64_t P;
     int32_t N, T, H, group, M, hq, hk, hv, ho, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
-    bool boxes;    // 16-bit output: whole chunks are stored through maps.out
+    bool boxes;  // output of the input's type: whole chunks are stored through maps.out
     float scale;
     // of a cut launch: a flag and a decay a CTA, then its state
     uint32_t* flags;
@@ -334,7 +334,10 @@ __device__ __forceinline__ void scale_rows(uint32_t taddr, int cols, float f) {
         float x[32];
         ld32(taddr + c, x);
 #pragma unroll
-        for (int z = 0; z < 32; ++z) x[z] *= f;
+        for (int z = 0; z < 32; z += 2) {
+            const float2 y = __fmul2_rn(make_float2(x[z], x[z + 1]), make_float2(f, f));
+            x[z] = y.x, x[z + 1] = y.y;
+        }
         st32(taddr + c, x);
     }
     wait_st();
@@ -755,14 +758,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     if constexpr (kF16)
 #pragma unroll
                         for (int z = 0; z < 32; ++z) o[z] *= fp;
-                    const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128;
-                    if (a.out_dt == KDA_BF16) {
+                    const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128, c = 4 * (b & 1);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4), pack16<KDA_BF16>(o, 8 * z));
-                    } else {
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) sts128(to + (((4 * (b & 1) + z) ^ (row & 7)) << 4), pack16<KDA_F16>(o, 8 * z));
-                    }
+                    for (int z = 0; z < 4; ++z) sts128(to + (((c + z) ^ (row & 7)) << 4), pack16<DT>(o, 8 * z));
                 }
                 fence_before();
                 fence_async_smem();
@@ -956,7 +954,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 float x[32];
                 ld32(tl + DT_KV + 64 * half + 32 * b, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(ac, S[32 * b + e], x[e]);
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y = __ffma2_rn(make_float2(ac, ac), make_float2(S[32 * b + e], S[32 * b + e + 1]), make_float2(x[e], x[e + 1]));
+                    S[32 * b + e] = y.x, S[32 * b + e + 1] = y.y;
+                }
             }
             fence_before();
             if (!(p.flags & kLast)) continue;
@@ -1046,7 +1047,7 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
         a.hq = rq.hs != 0, a.hk = rk.hs != 0, a.hv = rv.hs != 0;
         a.out = as_rows(out);
         a.ho = a.out.hs != 0;
-        a.boxes = out_dtype != KDA_F32 && (a.out.hs != 0 || H == 1) && (a.out.rs > 0 || T_tot == 1) && a.out.hs >= 0;
+        a.boxes = out_dtype == in_dtype && (a.out.hs != 0 || H == 1) && (a.out.rs > 0 || T_tot == 1) && a.out.hs >= 0;
         if (a.boxes) KDA_REQUIRE(chunk_map(&maps.out, out_dtype, a.out, H, T_tot, 32), KDA_ERR_CUDA);
     }
     a.head_decay = head_decay;
