@@ -489,6 +489,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 load(DS_Q, &maps.q, hk * a.hq, B_QF);
                 ++m;
             }
+            if (ch.c == ch.p.c0 && ch.p.start == kFromInit && a.init_slot && lane == 0) {
+                const int src = a.init_slot[ch.p.n];
+                if (src >= 0) bulk_prefetch_l2(static_cast<const uint8_t*>(a.pool) + state_elem(src, a.H, h) * state_bytes(a.st), kD * kD * state_bytes(a.st));
+            }
             // the next chunk into L2: its loads wait for their buffers (Q's for this chunk's Q S), and from HBM they
             // took 4400 cycles then
             if (ch.c + 1 < ch.p.c1 && lane < (ch.p.state_only ? 4 : 6)) {
