@@ -8,10 +8,8 @@
 // So the state is read once and, for n >= 1 committed positions, written once, however many positions
 // there are: a position costs one product with the state (and one more if it is committed).
 //
-// Bound by HBM: the state's bytes.  A warp holds whole rows of S^T in registers (a row = one value channel,
-// 128 key channels; lane l owns key channels 4l .. 4l+3), asked for at the start, so that the bytes in
-// flight are the registers of all resident warps.  The row sums of a group of rows (and positions) are
-// reduced together, half of them moving at each step: 31 shuffles for 32 sums in place of 160.
+// Bound by HBM: the state's bytes.  A warp holds whole rows of S^T in registers (a row = one value channel, 128 key
+// channels), asked for at the start, so that the bytes in flight are the registers of all resident warps.
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
@@ -20,6 +18,7 @@ namespace kda {
 namespace {
 
 constexpr int kDecayThreads = 128;
+constexpr int kStepsThreads = 256;  // of several positions
 constexpr int kDecayMaxK = 16;
 
 struct DecayDecodeArgs {
@@ -131,111 +130,156 @@ __global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const DecayDe
     }
 }
 
-// Several positions: 64 rows a block, sixteen a warp.  The block first leaves in shared memory the positions'
-// rows, the products q_t . k_j with their decays, and each committed value with its decay.
-template <int ST>
-__global__ void __launch_bounds__(kDecayThreads) decay_steps_kernel(const DecayDecodeArgs a) {
+// D += A B of 16 x 8 x 8 in tf32 (fp32 bits whose lower 13 are not looked at), fp32 sums.  Lane 4 g + c has rows g and
+// g + 8 of A and D; columns (of A: the k index) c and c + 4 of A, and c, c + 4 by n = g of B; columns 2c, 2c + 1 of D.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+__device__ __forceinline__ float tf32_of(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
+// Sixteen rows times eight, over 4 + 4 of their 128 channels a step pair: x and y (rows g and g + 8) are the lane's
+// channels 4c .. 4c + 3 of a group of 16, q those of row g of the other side, whose order the products may choose.
+// The rows go in two parts of 11 bits each, 2^-21 of them left out; q is exact in one (bf16, fp16) or in two, too.
+__device__ __forceinline__ void rows_times(float (&d)[4], float4 x, float4 y, float4 q, bool wide) {
+    const float4 xh = make_float4(tf32_of(x.x), tf32_of(x.y), tf32_of(x.z), tf32_of(x.w));
+    const float4 yh = make_float4(tf32_of(y.x), tf32_of(y.y), tf32_of(y.z), tf32_of(y.w));
+    mma_tf32(d, xh.x, yh.x, xh.y, yh.y, q.x, q.y);
+    mma_tf32(d, xh.z, yh.z, xh.w, yh.w, q.z, q.w);
+    mma_tf32(d, x.x - xh.x, y.x - yh.x, x.y - xh.y, y.y - yh.y, q.x, q.y);
+    mma_tf32(d, x.z - xh.z, y.z - yh.z, x.w - xh.w, y.w - yh.w, q.z, q.w);
+    if (wide) {
+        mma_tf32(d, xh.x, yh.x, xh.y, yh.y, q.x - tf32_of(q.x), q.y - tf32_of(q.y));
+        mma_tf32(d, xh.z, yh.z, xh.w, yh.w, q.z - tf32_of(q.z), q.w - tf32_of(q.w));
+    }
+}
+
+// Several positions: a block a (request, head), sixteen value channels a warp.  Lane 4 g + c has rows g and g + 8 of
+// its warp's, and of them channels 4c .. 4c + 3 of each group of 16 key channels: the operand layout of the warp's
+// tensor-core products with the positions' queries, which take the place of a sum over the warp for each (row,
+// position) (with those, seven positions of 64 requests took 104 us, most of it instructions).  Those products are
+// HBM's shadow at 8 or 16 columns.  The state itself is updated by fp32 FMAs, each rounded to nearest.  In shared
+// memory: the positions' rows, their products q_t . k_j with the decays between, each committed value with its decay.
+template <int ST, int NT>  // NT: groups of eight positions
+__global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const DecayDecodeArgs a) {
     using SIO = State<ST>;
-    constexpr int RW = 16, RB = 64, parts = kD / RB, K16 = kDecayMaxK;
-    __shared__ __align__(16) float sq[K16][kD], sk[K16][kD], sv[K16][RB], fv[K16][RB];
-    __shared__ float w[K16][K16], lead[K16], dec[K16];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / parts, part = blockIdx.x % parts;
-    const int r = unit / a.H, h = unit - r * a.H, hk = h / a.group;
-    const Plan p = plan_of(a, r, threadIdx.x == 0 && part == 0 && h == 0);
-    const int ql = p.ql, nc = p.commit, row0 = warp * RW;
-    const bool answer = a.out.base != nullptr;
+    constexpr int KT = 8 * NT, QS = 144, KS = 136;  // row lengths in shared memory that spread the lanes' reads over all banks
+    __shared__ __align__(16) float sq[KT][QS], sk[16][KS], sv[KT][kD], fv[KT][kD];
+    __shared__ float w[KT][KT + 1], lead[KT], dec[KT];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H, hk = h / a.group;
+    const Plan p = plan_of(a, r, tid == 0 && h == 0);
+    const int ql = p.ql, nc = p.commit, row = 16 * warp + g;
+    const bool answer = a.out.base != nullptr, wide = a.in_dt == KDA_F32;
     const bool moved = p.live && p.dst >= 0 && p.dst != p.src;
-    float4 s[RW];
+    float4 s[2][8];
     if ((ql && answer) || nc || moved) {
-        const size_t S = state_elem(p.src, a.H, h) + (size_t)(part * RB + row0) * kD + 4 * lane;
+        const size_t S = state_elem(p.src, a.H, h) + (size_t)row * kD + 4 * c;
 #pragma unroll
-        for (int i = 0; i < RW; ++i) s[i] = SIO::load4_cs(a.pool, S + (size_t)i * kD);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) s[i][x] = SIO::load4_cs(a.pool, S + (size_t)(8 * i) * kD + 16 * x);
     }
     const int64_t first = (int64_t)r * a.K;
-    for (int t = ql + warp; answer && t < a.K; t += 4)  // positions that there are not
-        for (int i = lane; i < RB; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), part * RB + i, 0.f, a.out_dt);
+    for (int t = ql + warp; answer && t < a.K; t += kStepsThreads / 32)  // positions that there are not
+        for (int i = lane; i < kD; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), i, 0.f, a.out_dt);
     if (ql) {
-        if (threadIdx.x < ql) dec[threadIdx.x] = __expf(log_decay_of(a.head_decay, a.log_decay, first + threadIdx.x, a.H, h));
-        for (int t = warp; t < ql; t += 4) {
-            if (answer) {
-                const float4 q = load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt);
-                *reinterpret_cast<float4*>(&sq[t][4 * lane]) = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
+        if (tid < ql) dec[tid] = __expf(log_decay_of(a.head_decay, a.log_decay, first + tid, a.H, h));
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int t = warp; t < 16; t += kStepsThreads / 32) {
+            const bool there = t < ql;
+            if (answer && t < KT) {
+                const float4 q = there ? load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
+                *reinterpret_cast<float4*>(&sq[t][4 * lane]) = q;
             }
-            *reinterpret_cast<float4*>(&sk[t][4 * lane]) = load4_as(row_of(a.k, first + t, hk, a.in_dt), 4 * lane, a.in_dt);
-            if (lane < RB / 4)
-                *reinterpret_cast<float4*>(&sv[t][4 * lane]) =
-                    load4_as(row_of(a.v, first + t, h, a.in_dt), part * RB + 4 * lane, a.in_dt);
+            *reinterpret_cast<float4*>(&sk[t][4 * lane]) = there ? load4_as(row_of(a.k, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
+            if (t < KT) *reinterpret_cast<float4*>(&sv[t][4 * lane]) = there ? load4_as(row_of(a.v, first + t, h, a.in_dt), 4 * lane, a.in_dt) : zero;
         }
         __syncthreads();
-        // thread j: prod_{j<s<=t} a_s for t >= j, and of the committed ones the factor of v_j
-        if (threadIdx.x < ql) {
-            const int j = threadIdx.x;
-            float f = 1.f;
-            w[j][j] = 1.f;
-            for (int t = j + 1; t < ql; ++t) w[t][j] = f *= dec[t];
+        // thread j: prod_{j<s<=t} a_s for t >= j; the decays from the state; 0 for t < j
+        if (tid < KT) {
+            const int j = tid;
+            float f = j < ql ? 1.f : 0.f;
+            for (int t = 0; t < KT; ++t) {
+                if (t > j) f *= t < ql ? dec[t] : 0.f;
+                w[t][j] = t < j ? 0.f : f;
+            }
             f = 1.f;
-            for (int t = 0; t <= j; ++t) f *= dec[t];
+            for (int t = 0; t <= j && t < ql; ++t) f *= dec[t];
             lead[j] = f;
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < nc * RB; e += kDecayThreads) {
-            const int j = e / RB, i = e % RB;
-            fv[j][i] = w[nc - 1][j] * sv[j][i];
+        for (int e = tid; e < nc * kD; e += kStepsThreads) fv[e / kD][e % kD] = w[nc - 1][e / kD] * sv[e / kD][e % kD];
+        float d[NT][4];
+        if (answer) {
+            float kq[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0 .. 15 times eight queries, of warps 0 .. NT - 1
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int at = 16 * x + 4 * c;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) rows_times(d[n], s[0][x], s[1][x], *reinterpret_cast<const float4*>(&sq[8 * n + g][at]), wide);
+                if (warp < NT)
+                    rows_times(kq, *reinterpret_cast<const float4*>(&sk[g][at]), *reinterpret_cast<const float4*>(&sk[g + 8][at]),
+                               *reinterpret_cast<const float4*>(&sq[8 * warp + g][at]), wide);
+            }
+            __syncthreads();  // every product of decays has been used
+            if (warp < NT) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = g + 8 * (e >> 1), t = 8 * warp + 2 * c + (e & 1);
+                    if (j < KT) w[t][j] *= kq[e];
+                }
+            }
         }
         __syncthreads();
         if (answer) {
-            // products with the keys, 32 pairs (t, j) of a warp together
-            for (int base = warp * 32; base < ql * ql; base += 128) {
-                float d[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int pair = min(base + e, ql * ql - 1), t = pair / ql, j = pair - t * ql;
-                    d[e] = f4_dot(*reinterpret_cast<const float4*>(&sq[t][4 * lane]), *reinterpret_cast<const float4*>(&sk[j][4 * lane]));
-                }
-                const float x = reduce_scatter<32>(d, lane);
-                const int pair = base + lane, t = pair / ql, j = pair - t * ql;
-                if (pair < ql * ql && j <= t) w[t][j] *= x;
-            }
-            __syncthreads();
-            for (int t0 = 0; t0 < ql; t0 += 2) {  // two positions of sixteen rows: 32 sums
-                float d[32];
+            for (int n = 0; n < NT; ++n) {
+                const int t = 8 * n + 2 * c;
+                float o[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float4 q = *reinterpret_cast<const float4*>(&sq[min(t0 + u, ql - 1)][4 * lane]);
+                for (int e = 0; e < 4; ++e) o[e] = lead[t + (e & 1)] * d[n][e];
+                for (int j = 0; j < ql; ++j) {
+                    const float w0 = w[t][j], w1 = w[t + 1][j], v0 = sv[j][row], v1 = sv[j][row + 8];
+                    if (j <= t) o[0] = fmaf(w0, v0, o[0]), o[2] = fmaf(w0, v1, o[2]);
+                    if (j <= t + 1) o[1] = fmaf(w1, v0, o[1]), o[3] = fmaf(w1, v1, o[3]);
+                }
 #pragma unroll
-                    for (int i = 0; i < RW; ++i) d[16 * u + i] = f4_dot(s[i], q);
-                }
-                const float x = reduce_scatter<32>(d, lane);
-                const int t = t0 + (lane >> 4), i = row0 + (lane & 15);
-                if (t < ql) {
-                    float o = lead[t] * x;
-                    for (int j = 0; j <= t; ++j) o = fmaf(w[t][j], sv[j][i], o);
-                    store1_as(out_row(a.out, first + t, h, a.out_dt), part * RB + i, o, a.out_dt);
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (t + (e & 1) < ql)
+                        store1_as(out_row(a.out, first + t + (e & 1), h, a.out_dt), row + 8 * (e >> 1), a.scale * o[e], a.out_dt);
             }
         }
         if (nc) {
             const float f = lead[nc - 1];
 #pragma unroll
-            for (int i = 0; i < RW; ++i) s[i] = f4_mul(s[i], make_float4(f, f, f, f));
-            for (int j = 0; j < nc; ++j) {
-                const float4 k = *reinterpret_cast<const float4*>(&sk[j][4 * lane]);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < RW; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(&fv[j][row0 + i]);
-                    s[i] = f4_fma(v.x, k, s[i]);
-                    s[i + 1] = f4_fma(v.y, k, s[i + 1]);
-                    s[i + 2] = f4_fma(v.z, k, s[i + 2]);
-                    s[i + 3] = f4_fma(v.w, k, s[i + 3]);
+                for (int x = 0; x < 8; ++x) s[i][x] = f4_mul(s[i][x], make_float4(f, f, f, f));
+            for (int j = 0; j < nc; ++j) {
+                const float v0 = fv[j][row], v1 = fv[j][row + 8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float4 k = *reinterpret_cast<const float4*>(&sk[j][16 * x + 4 * c]);
+                    s[0][x] = f4_fma(v0, k, s[0][x]);
+                    s[1][x] = f4_fma(v1, k, s[1][x]);
                 }
             }
         }
     }
     if (p.live && p.dst >= 0 && (nc || moved)) {
-        const size_t S = state_elem(p.dst, a.H, h) + (size_t)(part * RB + row0) * kD + 4 * lane;
+        const size_t S = state_elem(p.dst, a.H, h) + (size_t)row * kD + 4 * c;
 #pragma unroll
-        for (int i = 0; i < RW; ++i) SIO::store4_cs(a.pool, S + (size_t)i * kD, s[i]);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) SIO::store4_cs(a.pool, S + (size_t)(8 * i) * kD + 16 * x, s[i][x]);
     }
 }
 
@@ -244,8 +288,10 @@ void launch(const DecayDecodeArgs& a, cudaStream_t s) {
     const unsigned units = (unsigned)a.R * (unsigned)a.H;
     if (a.K == 1)
         decay_step_kernel<ST><<<units * 4, kDecayThreads, 0, s>>>(a);
+    else if (a.K <= 8)
+        decay_steps_kernel<ST, 1><<<units, kStepsThreads, 0, s>>>(a);
     else
-        decay_steps_kernel<ST><<<units * 2, kDecayThreads, 0, s>>>(a);
+        decay_steps_kernel<ST, 2><<<units, kStepsThreads, 0, s>>>(a);
 }
 
 }  // namespace

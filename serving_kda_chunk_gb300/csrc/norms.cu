@@ -145,7 +145,7 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
 __device__ __forceinline__ float act_of(float z, int act) {
     if (act == KDA_ACT_NONE) return z;
     // e^-z = inf gives 0; z = -inf gives silu NaN as -inf * 0 does
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
     return act == KDA_ACT_SILU ? z * s : s;
 }
 
