@@ -12,11 +12,15 @@
 // unrounded h, and each output is rounded once on its store.
 #include "kda_host.h"
 #include "latent_common.cuh"
+#include "umma.cuh"
+
+#include <initializer_list>
 
 namespace kda {
 namespace {
 
 constexpr int kNormMaxDim = 16384;
+constexpr int kStreamStages = 8, kStreamBytes = 210 * 1024;  // most rows in a block's ring; bytes of a SM's rings
 
 struct NormRows {
     const void* base;
@@ -142,21 +146,36 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
     return x;
 }
 
-__device__ __forceinline__ float act_of(float z, int act) {
-    if (act == KDA_ACT_NONE) return z;
-    // e^-z = inf gives 0; z = -inf gives silu NaN as -inf * 0 does
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
-    return act == KDA_ACT_SILU ? z * s : s;
+// act(z) of two values; e^-z = inf gives 0 (z = -inf gives silu NaN, as -inf * 0 does).  One exponential and one
+// reciprocal a value, both the fast ones (2^-22).
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 z) {
+    if constexpr (ACT == KDA_ACT_NONE) return z;
+    const float2 e = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
+    const float2 s = make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+    return ACT == KDA_ACT_SILU ? __fmul2_rn(z, s) : s;
 }
+// Runs body(ACT) with the activation fixed at compile time: tested at each element it cost a branch there.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& body) {
+    if (act == KDA_ACT_SILU) body(std::integral_constant<int, KDA_ACT_SILU>{});
+    else if (act == KDA_ACT_SIGMOID) body(std::integral_constant<int, KDA_ACT_SIGMOID>{});
+    else body(std::integral_constant<int, KDA_ACT_NONE>{});
+}
+
+// Pairs of a vector of eight.
+__device__ __forceinline__ float2 pair(const float (&v)[8], int e) { return make_float2(v[2 * e], v[2 * e + 1]); }
+__device__ __forceinline__ void set_pair(float (&v)[8], int e, float2 x) { v[2 * e] = x.x, v[2 * e + 1] = x.y; }
 
 template <int NV>
 __device__ __forceinline__ float sum_sq(const float (&v)[NV][8]) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e & 3] = fmaf(v[i][e], v[i][e], s[e & 3]);
-    return (s[0] + s[1]) + (s[2] + s[3]);
+        for (int e = 0; e < 4; ++e) s[e & 1] = __ffma2_rn(pair(v[i], e), pair(v[i], e), s[e & 1]);
+    return (s[0].x + s[0].y) + (s[1].x + s[1].y);
 }
 
 constexpr int norm_threads(int tpr) { return tpr > 256 ? tpr : tpr > 32 ? tpr : 256; }
@@ -170,53 +189,65 @@ __global__ void __launch_bounds__(norm_threads(TPR)) gated_norm_kernel(
     constexpr int G = norm_threads(TPR) / TPR;  // rows a block at a time
     const int t = threadIdx.x % TPR;
     const int64_t first = (int64_t)blockIdx.x * (G * U) + threadIdx.x / TPR;
+    // rows that lie evenly come as heads of one row each (H = 1): no division
+    auto place = [&](const NormRows& at, int64_t row) {
+        if (H == 1) return row * at.rs;
+        const int64_t r = row / H;
+        return r * at.rs + (row - r * H) * at.hs;
+    };
     Raw8<DT> xr[U][NV], gr[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t row = first + u * G;
         const int dd = row < n ? d : 0;  // a row past the end loads and stores nothing
-        const int64_t r = row / H, h = row - r * H;
+        const void* xp = at_elem(x.base, place(x, row), DT);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            xr[u][i] = load_raw<DT, kVec, TPR>(at_elem(x.base, r * x.rs + h * x.hs, DT), i, t, dd);
-            if (gate.base) gr[u][i] = load_raw<DT, kVec, TPR>(at_elem(gate.base, r * gate.rs + h * gate.hs, DT), i, t, dd);
+        for (int i = 0; i < NV; ++i) xr[u][i] = load_raw<DT, kVec, TPR>(xp, i, t, dd);
+        if (gate.base) {
+            const void* gp = at_elem(gate.base, place(gate, row), DT);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) gr[u][i] = load_raw<DT, kVec, TPR>(gp, i, t, dd);
         }
     }
-    Raw8<DT> wr[NV];
-    if (weight)
+    float w[NV][8];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) wr[i] = load_raw<DT, kVec, TPR>(weight, i, t, d);
+    for (int i = 0; i < NV; ++i) {
+        if (weight) widen<DT>(load_raw<DT, kVec, TPR>(weight, i, t, d), w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[i][e] = weight ? w[i][e] + offset : 1.f;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t row = first + u * G;
         const int dd = row < n ? d : 0;
-        const int64_t r = row / H, h = row - r * H;
         float v[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) widen<DT>(xr[u][i], v[i]);
-        if (gate.base && gate_first) {
+        auto times_gate = [&](bool mask) {
+            with_act(act, [&](auto ACT) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float g[8];
-                widen<DT>(gr[u][i], g);
+                for (int i = 0; i < NV; ++i) {
+                    float g[8];
+                    widen<DT>(gr[u][i], g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] *= elem_at<kVec, TPR>(i, e, t) < dd ? act_of(g[e], act) : 0.f;
-            }
-        }
+                    for (int e = 0; e < 4; ++e) set_pair(v[i], e, __fmul2_rn(pair(v[i], e), act2<ACT>(pair(g, e))));
+                    // an absent element counts as zero, whatever act(0) makes of it
+                    if (mask)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (elem_at<kVec, TPR>(i, e, t) >= dd) v[i][e] = 0.f;
+                }
+            });
+        };
+        if (gate.base && gate_first) times_gate(true);
         const float f = rsqrtf(row_sum<TPR>(sum_sq<NV>(v), part) * inv_d + eps);
+        if (gate.base && !gate_first) times_gate(false);
+        void* to = at_elem(const_cast<void*>(out.base), place(out, row), out_dt);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float w[8], g[8];
-            if (weight) widen<DT>(wr[i], w);
-            if (gate.base && !gate_first) widen<DT>(gr[u][i], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float y = v[i][e] * f;
-                if (weight) y *= w[e] + offset;
-                if (gate.base && !gate_first) y *= act_of(g[e], act);
-                v[i][e] = y;
-            }
-            store8_as<kVec, TPR>(at_elem(const_cast<void*>(out.base), r * out.rs + h * out.hs, out_dt), i, t, dd, v[i], out_dt);
+            for (int e = 0; e < 4; ++e) set_pair(v[i], e, __fmul2_rn(__fmul2_rn(pair(v[i], e), make_float2(f, f)), pair(w[i], e)));
+            store8_as<kVec, TPR>(to, i, t, dd, v[i], out_dt);
         }
         if (TPR > 32 && U > 1) __syncthreads();  // part is written again
     }
@@ -264,12 +295,18 @@ __global__ void __launch_bounds__(norm_threads(TPR)) residual_norm_kernel(const 
     for (int i = 0; i < NV; ++i) {
         float p[8], g[8];
         if (a.post) widen<DT>(pr[i], p);
-        if (a.gate) widen<DT>(gr[i], g);
+        if (a.gate) {
+            widen<DT>(gr[i], g);
+            with_act(a.act, [&](auto ACT) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) set_pair(g, e, act2<ACT>(pair(g, e)));
+            });
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float y = z[i][e] * f;
             if (a.post) y *= p[e] + a.offset;
-            if (a.gate) y *= act_of(g[e], a.act);
+            if (a.gate) y *= g[e];
             z[i][e] = fmaf(a.rscale, r[i][e], y);
             // an absent element counts as zero, whatever act(0) and the offset make of it
             if (elem_at<kVec, TPR>(i, e, t) >= d) z[i][e] = 0.f;
@@ -294,6 +331,112 @@ __global__ void __launch_bounds__(norm_threads(TPR)) residual_norm_kernel(const 
         for (int e = 0; e < 8; ++e) z[i][e] *= a.weight ? f * (w[e] + a.offset) : f;
         store8_as<kVec, TPR>(p, i, t, d, z[i], a.out_dt);
     }
+}
+
+// Many long rows: a block walks rows gridDim.x apart, and a ring of rows in shared memory, filled by bulk copies,
+// keeps HBM busy under the two reductions and the stores.  (Rows in registers alone, 128 threads of four vectors:
+// 140 registers, 17 % of the warps and 4.5 of 6.7 TB/s at 41460 x 4096.)  Weights come from L1 / L2 where they are used.
+constexpr int kStreamThreads = 256;
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(kStreamThreads, NV <= 2 ? 3 : 2) residual_stream_kernel(const ResidualArgs a, int stages) {
+    using namespace umma;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[kStreamStages];
+    __shared__ float part[2][2][kStreamThreads / 32];  // two sums, of even and odd rows: one barrier lies between two uses
+    __shared__ int gone;
+    const int t = threadIdx.x, d = a.d, xb = d * dtype_bytes(DT), rb = d * dtype_bytes(a.res_dt);
+    const bool gates = a.gate && a.gs != 0;  // a gate row a row
+    const int stage_bytes = xb + rb + (gates ? xb : 0);
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+        gone = 0;
+    }
+    __syncthreads();
+    auto ask = [&](int64_t row, int st) {  // by thread 0
+        const uint32_t bar = smem_u32(&full[st]), to = smem_u32(ring) + st * stage_bytes;
+        mbar_expect_tx(bar, stage_bytes);
+        bulk_load(to, at_elem(a.x, row * a.xs, DT), xb, bar);
+        bulk_load(to + xb, at_elem(a.residual, row * a.rs, a.res_dt), rb, bar);
+        if (gates) bulk_load(to + xb + rb, at_elem(a.gate, row * a.gs, DT), xb, bar);
+    };
+    if (t == 0)
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < a.n) ask(blockIdx.x + (int64_t)i * gridDim.x, i);
+    uint32_t it = 0;
+    bool lost = false;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++it) {
+        const int st = it % stages;
+        // (a copy that does not come within about a second: NaN for the block's rows from there on)
+        if (!lost && !mbar_wait(smem_u32(&full[st]), (it / stages) & 1, 1u << 18)) gone = 1;
+        const uint8_t* xs = ring + st * stage_bytes;
+        float z[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) widen<DT>(load_raw<DT, true, kStreamThreads>(xs, i, t, d), z[i]);
+        float f = a.bscale;
+        if (a.post) f *= rsqrtf(row_sum<kStreamThreads>(sum_sq<NV>(z), part[0][it & 1]) * a.inv_d + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (elem_at<true, kStreamThreads>(i, 0, t) >= d) continue;  // (zeros, which add nothing)
+            float y[8];
+            if (a.post) {
+                widen<DT>(load_raw<DT, true, kStreamThreads>(a.post, i, t, d), y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 p = __fadd2_rn(pair(y, e), make_float2(a.offset, a.offset));
+                    set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), p));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) set_pair(z[i], e, __fmul2_rn(pair(z[i], e), make_float2(f, f)));
+            }
+            if (a.gate) {
+                widen<DT>(load_raw<DT, true, kStreamThreads>(gates ? xs + xb + rb : a.gate, i, t, d), y);
+                with_act(a.act, [&](auto ACT) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) set_pair(z[i], e, __fmul2_rn(pair(z[i], e), act2<ACT>(pair(y, e))));
+                });
+            }
+            if (a.res_dt == KDA_F32) widen<KDA_F32>(load_raw<KDA_F32, true, kStreamThreads>(xs + xb, i, t, d), y);
+            else widen<DT>(load_raw<DT, true, kStreamThreads>(xs + xb, i, t, d), y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) set_pair(z[i], e, __ffma2_rn(make_float2(a.rscale, a.rscale), pair(y, e), pair(z[i], e)));
+        }
+        float sum = row_sum<kStreamThreads>(sum_sq<NV>(z), part[1][it & 1]);
+        // all have read the row (and the mark): the next one may come over it
+        lost = gone;
+        if (lost) {
+            sum = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[i][e] = sum;
+        } else if (t == 0 && row + (int64_t)stages * gridDim.x < a.n) {
+            ask(row + (int64_t)stages * gridDim.x, st);
+        }
+        if (a.hidden) {
+            void* p = at_elem(a.hidden, row * a.hs, a.res_dt);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (a.res_dt == KDA_F32) store8<KDA_F32, true, kStreamThreads>(p, i, t, d, z[i]);
+                else store8<DT, true, kStreamThreads>(p, i, t, d, z[i]);
+            }
+        }
+        if (a.out) {
+            f = rsqrtf(sum * a.inv_d + a.eps);
+            void* p = at_elem(a.out, row * a.os, a.out_dt);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float w[8];
+                if (a.weight) widen<DT>(load_raw<DT, true, kStreamThreads>(a.weight, i, t, d), w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[i][e] *= a.weight ? f * (w[e] + a.offset) : f;
+                store8_as<true, kStreamThreads>(p, i, t, d, z[i], a.out_dt);
+            }
+        }
+    }
+    if (lost && t == 0)  // copies in flight land before the block's memory goes
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000000);
 }
 
 inline bool dtype_known(kda_dtype d) { return d == KDA_BF16 || d == KDA_F16 || d == KDA_F32; }
@@ -349,6 +492,14 @@ extern "C" kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc
     const bool vec = d % 8 == 0 && vec_ok(xd.base, xd.rs, xd.hs) && vec_ok(od.base, od.rs, od.hs) &&
                      vec_ok(gd.base, gd.rs, gd.hs) && vec_ok(weight, 0, 0);
     const int64_t n = (int64_t)R * H;
+    // rows and heads that lie evenly are rows alone
+    auto even = [&](NormRows& t) { return t.base == nullptr || H == 1 || R == 1 || t.rs == H * t.hs; };
+    NormRows xe = xd, ge = gd, oe = od;
+    const bool flat = even(xe) && even(ge) && even(oe);
+    if (flat)
+        for (NormRows* t : {&xe, &ge, &oe})
+            if (H > 1) t->rs = t->hs;
+    const int heads = flat ? 1 : H;
     const int nvec = (d + 7) / 8;
     cudaStream_t s = as_stream(stream);
     bool fits = true;
@@ -360,8 +511,8 @@ extern "C" kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc
                 fits = blocks < (1ll << 31);
                 if (fits)
                     gated_norm_kernel<DT, V, TPR, NV, U><<<(unsigned)blocks, norm_threads(TPR), 0, s>>>(
-                        xd, gd, weight, n, H, d, 1.f / (float)d, eps, weight_offset, act,
-                        (flags & KDA_NORM_AFTER_GATE) != 0, od, out_dtype);
+                        xe, ge, weight, n, heads, d, 1.f / (float)d, eps, weight_offset, act,
+                        (flags & KDA_NORM_AFTER_GATE) != 0, oe, out_dtype);
             };
             // rows of one vector a thread go four at a time when there are many
             if constexpr (NV == 1 && TPR <= 32) {
@@ -400,6 +551,31 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
                          hidden_stride, out_stride, R, d, act, residual_dtype, out_dtype, 1.f / (float)d, residual_scale,
                          branch_scale, eps, weight_offset};
     cudaStream_t s = as_stream(stream);
+    const int stage = d * (dtype_bytes(in_dtype) * (gate && gate_stride != 0 ? 2 : 1) + dtype_bytes(residual_dtype));
+    if (vec && d >= 1024 && R >= 1024 && 2 * stage <= kStreamBytes) {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return runtime_failed();
+        cudaError_t err = cudaSuccess;
+        auto run = [&](auto DT, auto NV) {
+            const int most = NV <= 2 ? 3 : 2;  // blocks a SM, by registers
+            const int ctas = most * 2 * stage <= kStreamBytes ? most : kStreamBytes / (2 * stage);
+            const int fit = kStreamBytes / (ctas * stage), stages = fit < kStreamStages ? fit : kStreamStages;
+            auto* f = residual_stream_kernel<DT, NV>;
+            err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+            if (err == cudaSuccess) f<<<(unsigned)(sms * ctas < R ? sms * ctas : R), kStreamThreads, stages * stage, s>>>(a, stages);
+        };
+        auto by_len = [&](auto DT) {
+            if (d <= 8 * kStreamThreads) run(DT, std::integral_constant<int, 1>{});
+            else if (d <= 16 * kStreamThreads) run(DT, std::integral_constant<int, 2>{});
+            else if (d <= 32 * kStreamThreads) run(DT, std::integral_constant<int, 4>{});
+            else run(DT, std::integral_constant<int, 8>{});
+        };
+        if (in_dtype == KDA_BF16) by_len(std::integral_constant<int, KDA_BF16>{});
+        else if (in_dtype == KDA_F16) by_len(std::integral_constant<int, KDA_F16>{});
+        else by_len(std::integral_constant<int, KDA_F32>{});
+        return err == cudaSuccess ? launch_status() : runtime_failed();
+    }
     with_types(in_dtype, vec, [&](auto DT, auto V) {
         with_row_form((d + 7) / 8, R < 1024, [&](auto TPR, auto NV) {
             constexpr int rows = norm_threads(TPR) / TPR;

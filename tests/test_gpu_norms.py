@@ -201,3 +201,27 @@ def test_a_layer_of_decayed_attention():
             # some ten bf16 roundings a side, products of other row counts among them: sqrt(20) 2^-9 < 0.01
             assert (a.float() - b[at].float()).norm() <= 0.015 * b[at].float().norm(), t
     assert (pool[slots.long()] - other[slots.long()]).norm() <= 0.015 * other.norm()
+
+
+@pytest.mark.parametrize("rows,d", [(1024, 1024), (1100, 2056), (1500, 4096), (1024, 8200), (1030, 16384)])
+@pytest.mark.parametrize("dt,rdt,out_dt", [(BF16, BF16, BF16), (BF16, F32, BF16), (F16, F16, F32), (F32, F32, F32)])
+def test_residual_many_long_rows(rows, d, dt, rdt, out_dt):
+    """Rows through the ring in shared memory, with and without the norm after the block, gates a row, in place."""
+    g = gen(rows + d)
+    for post, gate, kind in ((True, None, 0), (False, 1, 0), (False, rows, 1), (True, rows, 2)):
+        x, r = randn(g, rows, d, dt=dt, std=0.5), randn(g, rows, d, dt=rdt, std=2.0)
+        pw, w = (randn(g, d, dt=dt) if post else None), randn(g, d, dt=dt)
+        z = None if gate is None else randn(g, gate, d, dt=dt)
+        br = -0.5 * (norm(x.double(), pw, 0) if post else x.double()) * (1.0 if z is None else act(z, kind))
+        h = r.double() + br
+        out = torch.empty(rows, d, dtype=out_dt, device="cuda")
+        size = r.double().abs() + br.abs()
+        kda.kda_residual_norm(x, r, hidden=r, out=out, post_weight=pw, gate=z, act=kind, weight=w, branch_scale=-0.5)
+        close(r, h, rdt, size)
+        f = (h.square().mean(-1, keepdim=True) + EPS).rsqrt()
+        close(out, norm(h, w, 0), out_dt, (size + h.abs()) * f * w.double().abs() * 2)
+    only = torch.empty_like(out)
+    kda.kda_residual_norm(x, r, out=only)
+    h = r.double() + x.double()
+    f = (h.square().mean(-1, keepdim=True) + EPS).rsqrt()
+    close(only, h * f, out_dt, 2 * (r.double().abs() + x.double().abs()) * f)
