@@ -335,17 +335,17 @@ __global__ void __launch_bounds__(norm_threads(TPR)) residual_norm_kernel(const 
 
 // Many long rows: a block walks rows gridDim.x apart, and a ring of rows in shared memory, filled by bulk copies,
 // keeps HBM busy under the two reductions and the stores.  (Rows in registers alone, 128 threads of four vectors:
-// 140 registers, 17 % of the warps and 4.5 of 6.7 TB/s at 41460 x 4096.)  Weights come from L1 / L2 where they are used.
+// 140 registers, 17 % of the warps and 4.5 of 6.7 TB/s at 41460 x 4096.)
 constexpr int kStreamThreads = 256;
 
-template <int DT, int NV>
-__global__ void __launch_bounds__(kStreamThreads, NV <= 2 ? 3 : 2) residual_stream_kernel(const ResidualArgs a, int stages) {
+template <int DT, int RDT, int NV>
+__global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stream_kernel(const ResidualArgs a, int stages) {
     using namespace umma;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[kStreamStages];
     __shared__ float part[2][2][kStreamThreads / 32];  // two sums, of even and odd rows: one barrier lies between two uses
     __shared__ int gone;
-    const int t = threadIdx.x, d = a.d, xb = d * dtype_bytes(DT), rb = d * dtype_bytes(a.res_dt);
+    const int t = threadIdx.x, d = a.d, xb = d * dtype_bytes(DT), rb = d * dtype_bytes(RDT);
     const bool gates = a.gate && a.gs != 0;  // a gate row a row
     const int stage_bytes = xb + rb + (gates ? xb : 0);
     if (t == 0) {
@@ -357,12 +357,40 @@ __global__ void __launch_bounds__(kStreamThreads, NV <= 2 ? 3 : 2) residual_stre
         const uint32_t bar = smem_u32(&full[st]), to = smem_u32(ring) + st * stage_bytes;
         mbar_expect_tx(bar, stage_bytes);
         bulk_load(to, at_elem(a.x, row * a.xs, DT), xb, bar);
-        bulk_load(to + xb, at_elem(a.residual, row * a.rs, a.res_dt), rb, bar);
+        bulk_load(to + xb, at_elem(a.residual, row * a.rs, RDT), rb, bar);
         if (gates) bulk_load(to + xb + rb, at_elem(a.gate, row * a.gs, DT), xb, bar);
     };
     if (t == 0)
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + (int64_t)i * gridDim.x < a.n) ask(blockIdx.x + (int64_t)i * gridDim.x, i);
+    // What multiplies each channel of the branch (post weight, a gate shared by the rows, the branch's scale) and of
+    // the output, made once: in registers, or where a thread has more than two vectors anew for each row.
+    auto factors = [&](int i, float (&before)[8], float (&after)[8]) {
+        float y[8];
+        if (a.post) {
+            widen<DT>(load_raw<DT, true, kStreamThreads>(a.post, i, t, d), before);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) before[e] = (before[e] + a.offset) * a.bscale;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) before[e] = a.bscale;
+        }
+        if (a.gate && !gates) {
+            widen<DT>(load_raw<DT, true, kStreamThreads>(a.gate, i, t, d), y);
+            with_act(a.act, [&](auto ACT) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) set_pair(before, e, __fmul2_rn(pair(before, e), act2<ACT>(pair(y, e))));
+            });
+        }
+        if (a.weight) widen<DT>(load_raw<DT, true, kStreamThreads>(a.weight, i, t, d), after);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) after[e] = a.weight ? after[e] + a.offset : 1.f;
+    };
+    constexpr bool kKeep = NV <= 2;
+    float before[kKeep ? NV : 1][8], after[kKeep ? NV : 1][8];
+    if constexpr (kKeep)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) factors(i, before[i], after[i]);
     uint32_t it = 0;
     bool lost = false;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++it) {
@@ -373,32 +401,24 @@ __global__ void __launch_bounds__(kStreamThreads, NV <= 2 ? 3 : 2) residual_stre
         float z[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) widen<DT>(load_raw<DT, true, kStreamThreads>(xs, i, t, d), z[i]);
-        float f = a.bscale;
-        if (a.post) f *= rsqrtf(row_sum<kStreamThreads>(sum_sq<NV>(z), part[0][it & 1]) * a.inv_d + a.eps);
+        float f = 1.f;
+        if (a.post) f = rsqrtf(row_sum<kStreamThreads>(sum_sq<NV>(z), part[0][it & 1]) * a.inv_d + a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (elem_at<true, kStreamThreads>(i, 0, t) >= d) continue;  // (zeros, which add nothing)
             float y[8];
-            if (a.post) {
-                widen<DT>(load_raw<DT, true, kStreamThreads>(a.post, i, t, d), y);
+            if constexpr (!kKeep) factors(i, before[0], after[0]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 p = __fadd2_rn(pair(y, e), make_float2(a.offset, a.offset));
-                    set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), p));
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) set_pair(z[i], e, __fmul2_rn(pair(z[i], e), make_float2(f, f)));
-            }
-            if (a.gate) {
-                widen<DT>(load_raw<DT, true, kStreamThreads>(gates ? xs + xb + rb : a.gate, i, t, d), y);
+            for (int e = 0; e < 4; ++e)
+                set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), pair(before[kKeep ? i : 0], e)));
+            if (gates) {
+                widen<DT>(load_raw<DT, true, kStreamThreads>(xs + xb + rb, i, t, d), y);
                 with_act(a.act, [&](auto ACT) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) set_pair(z[i], e, __fmul2_rn(pair(z[i], e), act2<ACT>(pair(y, e))));
                 });
             }
-            if (a.res_dt == KDA_F32) widen<KDA_F32>(load_raw<KDA_F32, true, kStreamThreads>(xs + xb, i, t, d), y);
-            else widen<DT>(load_raw<DT, true, kStreamThreads>(xs + xb, i, t, d), y);
+            widen<RDT>(load_raw<RDT, true, kStreamThreads>(xs + xb, i, t, d), y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) set_pair(z[i], e, __ffma2_rn(make_float2(a.rscale, a.rscale), pair(y, e), pair(z[i], e)));
         }
@@ -415,22 +435,19 @@ __global__ void __launch_bounds__(kStreamThreads, NV <= 2 ? 3 : 2) residual_stre
             ask(row + (int64_t)stages * gridDim.x, st);
         }
         if (a.hidden) {
-            void* p = at_elem(a.hidden, row * a.hs, a.res_dt);
+            void* p = at_elem(a.hidden, row * a.hs, RDT);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (a.res_dt == KDA_F32) store8<KDA_F32, true, kStreamThreads>(p, i, t, d, z[i]);
-                else store8<DT, true, kStreamThreads>(p, i, t, d, z[i]);
-            }
+            for (int i = 0; i < NV; ++i) store8<RDT, true, kStreamThreads>(p, i, t, d, z[i]);
         }
         if (a.out) {
             f = rsqrtf(sum * a.inv_d + a.eps);
             void* p = at_elem(a.out, row * a.os, a.out_dt);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float w[8];
-                if (a.weight) widen<DT>(load_raw<DT, true, kStreamThreads>(a.weight, i, t, d), w);
+                if constexpr (!kKeep) factors(i, before[0], after[0]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[i][e] *= a.weight ? f * (w[e] + a.offset) : f;
+                for (int e = 0; e < 4; ++e)
+                    set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), pair(after[kKeep ? i : 0], e)));
                 store8_as<true, kStreamThreads>(p, i, t, d, z[i], a.out_dt);
             }
         }
@@ -557,23 +574,26 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return runtime_failed();
         cudaError_t err = cudaSuccess;
-        auto run = [&](auto DT, auto NV) {
-            const int most = NV <= 2 ? 3 : 2;  // blocks a SM, by registers
+        auto run = [&](auto DT, auto RDT, auto NV) {
+            const int most = NV == 1 ? 3 : 2;  // blocks a SM, by registers
             const int ctas = most * 2 * stage <= kStreamBytes ? most : kStreamBytes / (2 * stage);
             const int fit = kStreamBytes / (ctas * stage), stages = fit < kStreamStages ? fit : kStreamStages;
-            auto* f = residual_stream_kernel<DT, NV>;
+            auto* f = residual_stream_kernel<DT, RDT, NV>;
             err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
             if (err == cudaSuccess) f<<<(unsigned)(sms * ctas < R ? sms * ctas : R), kStreamThreads, stages * stage, s>>>(a, stages);
         };
-        auto by_len = [&](auto DT) {
-            if (d <= 8 * kStreamThreads) run(DT, std::integral_constant<int, 1>{});
-            else if (d <= 16 * kStreamThreads) run(DT, std::integral_constant<int, 2>{});
-            else if (d <= 32 * kStreamThreads) run(DT, std::integral_constant<int, 4>{});
-            else run(DT, std::integral_constant<int, 8>{});
+        auto by_len = [&](auto DT, auto RDT) {
+            if (d <= 8 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 1>{});
+            else if (d <= 16 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 2>{});
+            else if (d <= 32 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 4>{});
+            else run(DT, RDT, std::integral_constant<int, 8>{});
         };
-        if (in_dtype == KDA_BF16) by_len(std::integral_constant<int, KDA_BF16>{});
-        else if (in_dtype == KDA_F16) by_len(std::integral_constant<int, KDA_F16>{});
-        else by_len(std::integral_constant<int, KDA_F32>{});
+        using BF = std::integral_constant<int, KDA_BF16>;
+        using HF = std::integral_constant<int, KDA_F16>;
+        using F = std::integral_constant<int, KDA_F32>;
+        if (in_dtype == KDA_F32) by_len(F{}, F{});
+        else if (in_dtype == KDA_BF16) residual_dtype == KDA_F32 ? by_len(BF{}, F{}) : by_len(BF{}, BF{});
+        else residual_dtype == KDA_F32 ? by_len(HF{}, F{}) : by_len(HF{}, HF{});
         return err == cudaSuccess ? launch_status() : runtime_failed();
     }
     with_types(in_dtype, vec, [&](auto DT, auto V) {
