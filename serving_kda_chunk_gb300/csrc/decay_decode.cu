@@ -175,6 +175,26 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
     const int ql = p.ql, nc = p.commit, row = 16 * warp + g;
     const bool answer = a.out.base != nullptr, wide = a.in_dt == KDA_F32;
     const bool moved = p.live && p.dst >= 0 && p.dst != p.src;
+    const int64_t first = (int64_t)r * a.K;
+    // the positions' rows are asked for ahead of the state, whose 64 KiB they would else queue behind: what is made of
+    // them alone is then done while the state comes
+    constexpr int kWarps = kStepsThreads / 32;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 qr[NT], kr[2], vr[NT];
+    float log_a = 0.f;
+    if (ql) {
+        if (tid < ql) log_a = log_decay_of(a.head_decay, a.log_decay, first + tid, a.H, h);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = warp + kWarps * i;
+            const bool there = t < ql;
+            kr[i] = there ? load4_as(row_of(a.k, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
+            if (i < NT) {
+                vr[i] = there ? load4_as(row_of(a.v, first + t, h, a.in_dt), 4 * lane, a.in_dt) : zero;
+                qr[i] = there && answer ? load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
+            }
+        }
+    }
     float4 s[2][8];
     if ((ql && answer) || nc || moved) {
         const size_t S = state_elem(p.src, a.H, h) + (size_t)row * kD + 4 * c;
@@ -183,20 +203,18 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
 #pragma unroll
             for (int x = 0; x < 8; ++x) s[i][x] = SIO::load4_cs(a.pool, S + (size_t)(8 * i) * kD + 16 * x);
     }
-    const int64_t first = (int64_t)r * a.K;
-    for (int t = ql + warp; answer && t < a.K; t += kStepsThreads / 32)  // positions that there are not
+    for (int t = ql + warp; answer && t < a.K; t += kWarps)  // positions that there are not
         for (int i = lane; i < kD; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), i, 0.f, a.out_dt);
     if (ql) {
-        if (tid < ql) dec[tid] = __expf(log_decay_of(a.head_decay, a.log_decay, first + tid, a.H, h));
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int t = warp; t < 16; t += kStepsThreads / 32) {
-            const bool there = t < ql;
-            if (answer && t < KT) {
-                const float4 q = there ? load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
-                *reinterpret_cast<float4*>(&sq[t][4 * lane]) = q;
+        if (tid < ql) dec[tid] = __expf(log_a);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = warp + kWarps * i;
+            *reinterpret_cast<float4*>(&sk[t][4 * lane]) = kr[i];
+            if (i < NT) {
+                *reinterpret_cast<float4*>(&sv[t][4 * lane]) = vr[i];
+                *reinterpret_cast<float4*>(&sq[t][4 * lane]) = qr[i];
             }
-            *reinterpret_cast<float4*>(&sk[t][4 * lane]) = there ? load4_as(row_of(a.k, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
-            if (t < KT) *reinterpret_cast<float4*>(&sv[t][4 * lane]) = there ? load4_as(row_of(a.v, first + t, h, a.in_dt), 4 * lane, a.in_dt) : zero;
         }
         __syncthreads();
         // thread j: prod_{j<s<=t} a_s for t >= j; the decays from the state; 0 for t < j
