@@ -24,10 +24,11 @@
 // carry the state.  K and V are double-buffered, Q single (its load runs under the products that need no Q).
 //
 // Balance: the (sequence, head) pairs' chunks lie in one row, cut into equal ranges, one a CTA.  A pair cut
-// once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its
-// end last.  A pair over more CTAs: those in the middle first sum up their range's own state (K and V only, read
-// twice), leave it, and then start from the states before theirs joined in order.  CTAs wait for one another, so
-// this is a cooperative launch; every wait has a limit.
+// once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
+// last.  A pair over more CTAs: each but the last first sums up its range's own state (K and V only, read twice) and
+// leaves it, then starts from the states before its own joined in order (with the pair's
+// beginning in one pass the others waited for its state: 131072 tokens, 16 heads 686 us).  CTAs wait for one another, so this is a
+// cooperative launch; every wait has a limit.
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
@@ -98,12 +99,13 @@ struct Piece {
     int start, end;
 };
 
-// A CTA's range of chunks: where it begins (a unit and the chunks of it that lie before) and where its last chunk lies.
+// A CTA's range of chunks: from chunk fo of the first unit (a sequence and head) up to, but without, chunk lx of the last.
 struct Range {
-    int fn, fh, fo, ln, lh, lo;
+    int fn, fh, fo, ln, lh, lx;
+    bool twice;  // the last unit goes on beyond the next CTA
 };
 
-// The pieces of a range in the order they are taken (see the top).  All roles walk them alike.
+// The pieces of a range in the order they are taken (see the top).
 struct Pieces {
     Range r;
     int phase = 0, n, h;
@@ -120,41 +122,43 @@ struct Pieces {
         if (++h < a.H) return;
         h = 0;
         do ++n;
-        while (n <= r.ln && seq_chunks(a, n, bad) == 0);
+        while (n < a.N && n <= r.ln && seq_chunks(a, n, bad) == 0);
     }
-    // (not inlined: its five copies were a fourth of the kernel)
+    // (not inlined: its copies were a fourth of the kernel)
     __device__ __noinline__ bool next(const DecayPrefillArgs& a, Piece& p) {
         int bad;
         const bool same = r.fn == r.ln && r.fh == r.lh;
-        const bool cut = r.lo + 1 < seq_chunks(a, r.ln, bad);  // the last unit goes on in the next range
+        // what goes on beyond this range and the next is gone through twice, for its state first (1 and 2; 3: a range within
+        // a unit)
         if (phase == 0) {
-            if (same && r.fo > 0 && cut) {
+            if (same && r.fo > 0) {
                 phase = 3;
-                return emit(a, p, r.fn, r.fh, r.fo, r.lo + 1, true, kFromZero, kPublish);
+                return emit(a, p, r.fn, r.fh, r.fo, r.lx, true, kFromZero, kPublish);
             }
             phase = 1;
-            if (r.fo > 0) step(a);
-            if (cut) {
-                if (same) phase = 4;
-                return emit(a, p, r.ln, r.lh, 0, r.lo + 1, false, kFromInit, kPublish);
+            if (!same && r.fo > 0) step(a);
+            if (r.lx > 0) {
+                if (r.twice) phase = 2;
+                else if (same) phase = 4;
+                return emit(a, p, r.ln, r.lh, 0, r.lx, r.twice, kFromInit, kPublish);
             }
         }
+        if (phase == 2) {
+            phase = same ? 4 : 1;
+            return emit(a, p, r.ln, r.lh, 0, r.lx, false, kFromInit, kNothing);
+        }
         if (phase == 1) {
-            const bool before = n < r.ln || (n == r.ln && h < r.lh), at = n == r.ln && h == r.lh;
-            if (before || (at && !cut)) {
+            if (n < r.ln || (n == r.ln && h < r.lh)) {
                 const int un = n, uh = h;
                 step(a);
                 return emit(a, p, un, uh, 0, seq_chunks(a, un, bad), false, kFromInit, kFinal);
             }
-            phase = 2;
-        }
-        if (phase == 2) {
             phase = 4;
             if (r.fo > 0) return emit(a, p, r.fn, r.fh, r.fo, seq_chunks(a, r.fn, bad), false, kFromOthers, kFinal);
         }
         if (phase == 3) {
             phase = 4;
-            return emit(a, p, r.fn, r.fh, r.fo, r.lo + 1, false, kFromOthers, kNothing);
+            return emit(a, p, r.fn, r.fh, r.fo, r.lx, false, kFromOthers, kNothing);
         }
         return false;
     }
@@ -178,7 +182,7 @@ struct Chunks {
 };
 
 // What the other roles know of a chunk.
-enum ChunkFlags { kFull = 1, kFirst = 2, kLast = 4, kJoins = 8, kFinalState = 16, kLeaves = 32, kPartial = 64, kStop = 128 };
+enum ChunkFlags { kFull = 1, kFirst = 2, kLast = 4, kJoins = 8, kFinalState = 16, kLeaves = 32, kPartial = 64, kStop = 128, kInit = 256 };
 struct ChunkInfo {
     int n, h, c, row0;  // row0: the chunk's first row
     int left, rows, flags, pad;  // left: rows of the sequence from this chunk on
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int* ctrl = reinterpret_cast<int*>(sm + DS_CTRL);  // 0 tensor memory, 1 waits that ran out, 2.. the range, 8 CTAs, 10 all chunks
+    volatile int* ctrl = reinterpret_cast<int*>(sm + DS_CTRL);  // 0 tensor memory, 1 waits that ran out, 2.. the range, 8 the first unit's place
     volatile long long* scan = reinterpret_cast<long long*>(sm + DS_SCAN);
     auto bar = [&](int i) { return sb + DS_BAR + 8 * i; };
     const bool cut = a.flags != nullptr;
@@ -374,21 +378,26 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     }
     // ---- this CTA's range of chunks
     Range rg;
-    int64_t x0 = 0, total = 0;
+    int64_t total = 0, unit_at = 0;  // all chunks; the first one of the first unit
     int ctas = 1;
     if (!cut) {
         int bad;
-        const int n = blockIdx.x / a.H, c = seq_chunks(a, n, bad);
-        rg = Range{n, (int)blockIdx.x - n * a.H, 0, n, (int)blockIdx.x - n * a.H, c - 1};
-        if (tid == 0 && rg.fh == 0 && bad) report(a.dev_status, bad);
+        const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, c = seq_chunks(a, n, bad);
+        rg = Range{n, h, 0, h + 1 < a.H ? n : n + 1, h + 1 < a.H ? h + 1 : 0, 0, false};
+        if (tid == 0 && h == 0 && bad) report(a.dev_status, bad);
         if (c == 0) return;
     } else {
-        auto block_scan = [&](int64_t x, int64_t& sum) {  // inclusive
-#pragma unroll
+        // Inclusive sums over 512 values, or over 32 that every warp has alike.
+        const bool few = a.N <= 32;
+        const int me = few ? lane : tid, width = few ? 32 : kPreDecayThreads;
+        auto sums = [&](int64_t x, int64_t& sum) {
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o) x += y;
             }
+            sum = __shfl_sync(~0u, x, 31);
+            if (few) return x;
             __syncthreads();
             if (lane == 31) scan[warp] = x;
             __syncthreads();
@@ -402,36 +411,43 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             return x + off;
         };
         int64_t mine = 0;
-        for (int n = tid; n < a.N; n += kPreDecayThreads) {
+        for (int n = me; n < a.N; n += width) {
             int bad;
             mine += seq_chunks(a, n, bad);
-            if (bad && blockIdx.x == 0) report(a.dev_status, bad);
+            if (bad && blockIdx.x == 0 && tid < width) report(a.dev_status, bad);
         }
-        block_scan(mine, total);
+        sums(mine, total);
         total *= a.H;
         ctas = (int)min((int64_t)gridDim.x, (total + kCutChunks - 1) / kCutChunks);
         if ((int)blockIdx.x >= ctas) return;
-        x0 = total * blockIdx.x / ctas;
-        const int64_t x1 = total * (blockIdx.x + 1) / ctas - 1;
+        if (tid == 0) {
+            ctrl[5] = a.N;  // the last CTA's end
+            ctrl[6] = ctrl[7] = ctrl[10] = 0;
+        }
+        __syncthreads();
         int64_t before = 0;
-        for (int base = 0; base < a.N; base += kPreDecayThreads) {
-            const int n = base + tid;
+        for (int base = 0; base < a.N; base += width) {
+            const int n = base + me;
             int bad;
             const int c = n < a.N ? seq_chunks(a, n, bad) : 0;
             int64_t sum;
-            const int64_t end = (before + block_scan(c, sum)) * a.H, begin = end - (int64_t)c * a.H;
+            const int64_t end = (before + sums(c, sum)) * a.H, begin = end - (int64_t)c * a.H;
             before += sum;
             for (int e = 0; e < 2; ++e) {
-                const int64_t x = e ? x1 : x0;
-                if (c && x >= begin && x < end) {
+                const int64_t x = total * (blockIdx.x + e) / ctas;
+                if (c && x >= begin && x < end && tid < width) {
+                    const int64_t h = (x - begin) / c, unit = begin + h * c;
                     ctrl[2 + 3 * e] = n;
-                    ctrl[3 + 3 * e] = (int)((x - begin) / c);
-                    ctrl[4 + 3 * e] = (int)((x - begin) % c);
+                    ctrl[3 + 3 * e] = (int)h;
+                    ctrl[4 + 3 * e] = (int)(x - unit);
+                    if (e == 0) *reinterpret_cast<volatile long long*>(sm + DS_CTRL + 32) = unit;
+                    else ctrl[10] = total * (blockIdx.x + 2) / ctas < unit + c;
                 }
             }
         }
         __syncthreads();
-        rg = Range{ctrl[2], ctrl[3], ctrl[4], ctrl[5], ctrl[6], ctrl[7]};
+        rg = Range{ctrl[2], ctrl[3], ctrl[4], ctrl[5], ctrl[6], ctrl[7], ctrl[10] != 0};
+        unit_at = *reinterpret_cast<volatile long long*>(sm + DS_CTRL + 32);
     }
     if (tid < B_COUNT) {
         int count = 1;
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             const Piece& p = ch.p;
             const int flags = !any ? kStop
                                    : (p.state_only ? 0 : kFull) | (ch.c == p.c0 ? kFirst : 0) | (ch.c + 1 == p.c1 ? kLast : 0) |
-                                         (p.start == kFromOthers ? kJoins : 0) | (p.end == kFinal ? kFinalState : 0) |
+                                         (p.start == kFromOthers ? kJoins : 0) | (p.start == kFromInit ? kInit : 0) | (p.end == kFinal ? kFinalState : 0) |
                                          (p.end == kPublish ? kLeaves : 0) | (p.rows - before < kDecayChunk ? kPartial : 0);
             const int4 info1 = make_int4(p.n, p.h, ch.c, p.row0 + before), info2 = make_int4(p.rows - before, p.rows, flags, 0);
             double g[4], y0 = 0;
@@ -886,17 +902,25 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 64; ++e) x[e] = 0.f;
                 decay = 1.f;
-                if (full && !(p.flags & kJoins)) {
+                if (p.flags & kInit) {
                     const int src = a.init_slot ? a.init_slot[p.n] : -1;
-                    if (src >= 0) get_state(x, a.pool, elems(src, p.h), kD, a.st);
-                    if (p.h == 0 && t == 0)
+                    // The second pass over a unit's beginning comes after its state was left: its last CTA may be done by
+                    // then and have written the very slot.  So that pass starts from a copy.
+                    const size_t copy = (size_t)(kDecayCtas + blockIdx.x) * (kD * kD) + t;
+                    const bool second = full && !(p.flags & (kFinalState | kLeaves));
+                    if (src >= 0) {
+                        if (second) get_state(x, a.states, copy, 256, kStateF32);
+                        else get_state(x, a.pool, elems(src, p.h), kD, a.st);
+                        if (!full) put_state(x, a.states, copy, 256, kStateF32);
+                    }
+                    if (p.h == 0 && t == 0 && full)
                         for (int y = 0; y < a.M; ++y) {
                             const int c = a.track_idx[(int64_t)p.n * a.M + y];
                             if (c < -1 || c >= (p.rows + kDecayChunk - 1) / kDecayChunk) report(a.dev_status, KDA_DEV_BAD_TRACK);
                         }
-                } else if (full) {
+                } else if (p.flags & kJoins) {
                     // the CTA with the unit's beginning left a state, those after it their ranges' own
-                    for (int j = (int)(((x0 - rg.fo + 1) * ctas - 1) / total); j < (int)blockIdx.x; ++j) {
+                    for (int j = (int)(((unit_at + 1) * ctas - 1) / total); j < (int)blockIdx.x; ++j) {
                         uint32_t set = 0;
 #pragma unroll 1
                         for (uint32_t polls = 0; polls < kFlagLimit && !set && !gone_of(gone); ++polls) {
@@ -1002,9 +1026,9 @@ bool chunk_map(CUtensorMap* map, kda_dtype dt, const LatentRows& r, int H, int T
     return encode_16bit(map, dt, 3, r.base, dims, strides, box);
 }
 
-// Bytes of a cut launch's workspace: flags, decays, states; none for prompts that no cut helps.
+// Bytes of a cut launch's workspace: flags, decays, states left and initial states kept; none for prompts that no cut helps.
 bool may_cut(int32_t T_tot) { return T_tot > kDecayChunk * kCutChunks; }
-constexpr size_t kCutBytes = 2 * 4 * kDecayCtas + (size_t)kDecayCtas * kD * kD * 4;
+constexpr size_t kCutBytes = 2 * 4 * kDecayCtas + (size_t)2 * kDecayCtas * kD * kD * 4;
 
 }  // namespace
 }  // namespace kda
