@@ -43,7 +43,7 @@ using namespace umma;
 
 constexpr int kDecayChunk = 128;
 constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
-constexpr int kCutChunks = 2;          // a CTA's least range: below it one CTA walks the pair
+constexpr int kCutChunks = 6;          // a CTA's least range: with 2 to 16, 16384 tokens of one head took 158, 106 (4), 95 (8), 115 us
 constexpr int kPreDecayThreads = 512;
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
 constexpr uint32_t kWaitLimit = 1u << 18;
@@ -817,6 +817,13 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         // this thread's elements of a state in memory, whose rows are value channels
         auto elems = [&](int64_t slot, int h) { return state_elem(slot, a.H, h) + (size_t)(64 * half) * kD + key; };
         auto store_state = [&](void* to, size_t at, size_t stride, int st) {
+            if (st == kStateF32) {
+                float* p = static_cast<float*>(to) + at;
+                if (!dead())
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) p[e * stride] = S[e];
+                return;
+            }
             float x[64];  // (the registers themselves have no address)
 #pragma unroll
             for (int e = 0; e < 64; ++e) x[e] = S[e];
@@ -898,9 +905,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             arrive(B_GFREE + st);
             // ---- the state before this chunk, under the products
             if (p.flags & kFirst) {
-                float x[64];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = 0.f;
+                for (int e = 0; e < 64; ++e) S[e] = 0.f;
                 decay = 1.f;
                 if (p.flags & kInit) {
                     const int src = a.init_slot ? a.init_slot[p.n] : -1;
@@ -908,17 +914,27 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     // then and have written the very slot.  So that pass starts from a copy.
                     const size_t copy = (size_t)(kDecayCtas + blockIdx.x) * (kD * kD) + t;
                     const bool second = full && !(p.flags & (kFinalState | kLeaves));
-                    if (src >= 0) {
-                        if (second) get_state(x, a.states, copy, 256, kStateF32);
-                        else get_state(x, a.pool, elems(src, p.h), kD, a.st);
-                        if (!full) put_state(x, a.states, copy, 256, kStateF32);
+                    if (src >= 0 && (second || a.st == kStateF32)) {
+                        const float* from = second ? a.states + copy : static_cast<const float*>(a.pool) + elems(src, p.h);
+                        const size_t stride = second ? 256 : kD;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) S[e] = from[e * stride];
+                    } else if (src >= 0) {
+                        float x[64];  // (the registers themselves have no address)
+                        get_state(x, a.pool, elems(src, p.h), kD, a.st);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) S[e] = x[e];
                     }
+                    if (src >= 0 && !full) store_state(a.states, copy, 256, kStateF32);
                     if (p.h == 0 && t == 0 && full)
                         for (int y = 0; y < a.M; ++y) {
                             const int c = a.track_idx[(int64_t)p.n * a.M + y];
                             if (c < -1 || c >= (p.rows + kDecayChunk - 1) / kDecayChunk) report(a.dev_status, KDA_DEV_BAD_TRACK);
                         }
                 } else if (p.flags & kJoins) {
+                    float x[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) x[e] = 0.f;
                     // the CTA with the unit's beginning left a state, those after it their ranges' own
                     for (int j = (int)(((unit_at + 1) * ctas - 1) / total); j < (int)blockIdx.x; ++j) {
                         uint32_t set = 0;
@@ -933,9 +949,9 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         }
                         join_state(x, *(volatile float*)(a.decays + j), a.states + (size_t)j * (kD * kD) + t);
                     }
-                }
 #pragma unroll
-                for (int e = 0; e < 64; ++e) S[e] = x[e];
+                    for (int e = 0; e < 64; ++e) S[e] = x[e];
+                }
             }
             if (full) {
                 if (a.M > 0 && p.rows > 0) {
