@@ -552,8 +552,8 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
  * delta rule.  Per value head h (its key head is h / (H / Hk), Hk divides H):
  *   g_t = min(head_decay[h] + log_decay[t][h], 0)
  *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = S_t^T (scale q_t).
- * Either source of the log decay (natural logarithm, fp32) may be NULL, not
- * both.  Values below -104, -inf included, forget the state: e^-104 is 0 in
+ * Either source of the log decay (natural logarithm, fp32; 4-byte aligned) may
+ * be NULL, not both.  Values below -104, -inf included, forget the state: e^-104 is 0 in
  * fp32 (a state that holds an infinity gives NaN there, as 0 times it does).
  * NaN stays NaN.
  *
@@ -591,8 +591,12 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
  *   workspace      : NULL, or >= kda_decay_prefill_workspace_size(T_tot, N, H)
  *                    bytes.  With it long (sequence, head) pairs are cut between
  *                    SMs; what an earlier call left there reaches no result.
- * A value or key that is not finite reaches, beside the rows behind it, rows of
- * its own chunk of 128 before it.  T_tot < 2^30, N * H < 2^27.
+ * A value, key or decay that is not finite makes the rows behind it (and the state)
+ * NaN or infinite, and may make rows of its own chunk of 128 before it NaN.
+ * fp16 calls: scores and states below 2^-28 of the largest of their row and state
+ * lose bits, and a decayed key is 2^-25 off at most (bf16 has fp32's exponents).
+ * With KDA_DEV_TIMEOUT, rows and states that the call did not finish are not
+ * written.  T_tot < 2^30, N * H < 2^27.
  */
 kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_desc* k,
                              const kda_rows_desc* v, kda_dtype in_dtype, const float* head_decay,
@@ -748,6 +752,22 @@ kda_status kda_selftest_latent_prefill_give_up(
     int32_t N, int32_t Tq, int32_t Tk, int32_t H, int32_t d_nope, int32_t d_rope, int32_t dv,
     float scale, uint32_t flags, const kda_rows_desc* out, kda_dtype out_dtype, float* lse,
     int32_t* dev_status, void* stream, int32_t block, int32_t tile);
+
+/*
+ * kda_selftest_decay_prefill_give_up -- diagnostic: kda_decay_prefill in which one
+ * wait counts as run out: block `block` of the grid stops before it loads its chunk
+ * number `load`.  Its other roles and the blocks that wait for its state end by
+ * themselves (within some seconds), and KDA_DEV_TIMEOUT is set.  A block or chunk
+ * that the call does not reach leaves it as it is.
+ */
+kda_status kda_selftest_decay_prefill_give_up(
+    const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v, kda_dtype in_dtype,
+    const float* head_decay, const float* log_decay, const int32_t* cu_seqlens, int32_t N,
+    int32_t T_tot, int32_t H, int32_t Hk, int32_t dk, int32_t dv, float scale, uint32_t flags,
+    void* state_pool, int64_t P, const int32_t* init_slot, const int32_t* final_slot,
+    const int32_t* track_chunk_idx, int32_t M, void* track_state, const kda_rows_desc* out,
+    kda_dtype out_dtype, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream,
+    int32_t block, int32_t load);
 
 const char* kda_status_string(kda_status s);
 

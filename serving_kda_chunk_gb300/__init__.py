@@ -141,6 +141,8 @@ def lib():
         L.kda_decay_prefill.argtypes = [rows, rows, rows, ctypes.c_int, vp, vp, vp, i32, i32, i32,
                                         i32, i32, i32, f32, u32, vp, i64, vp, vp, vp, i32, vp, rows,
                                         ctypes.c_int, vp, sz, vp, vp]
+        L.kda_selftest_decay_prefill_give_up.argtypes = L.kda_decay_prefill.argtypes + [i32, i32]
+        L.kda_selftest_decay_prefill_give_up.restype = ctypes.c_int
         L.kda_decay_prefill_workspace_size.argtypes = [i32, i32, i32]
         L.kda_decay_prefill_workspace_size.restype = sz
         L.kda_decay_decode.argtypes = [rows, rows, rows, ctypes.c_int, vp, vp, i32, i32, vp, vp, i32,

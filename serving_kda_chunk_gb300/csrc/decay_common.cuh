@@ -7,6 +7,11 @@
 
 namespace kda {
 
+// One of the two at least, of whole floats (read one at a time, so that rows of log_decay may start anywhere).
+inline bool decays_ok(const float* head_decay, const float* log_decay) {
+    return (head_decay || log_decay) && reinterpret_cast<uintptr_t>(head_decay) % 4 == 0 && reinterpret_cast<uintptr_t>(log_decay) % 4 == 0;
+}
+
 // Log decay of row t and head h (either source may be missing).  Above 0 counts as 0, and below
 // -104 (whose exponential is 0 in fp32), -inf included, as -104, so that differences of sums stay
 // numbers; NaN stays NaN.

@@ -331,10 +331,10 @@ extern "C" kda_status kda_decay_decode(const kda_rows_desc* q, const kda_rows_de
     KDA_REQUIRE((int64_t)R * H * 4 < (1ll << 31) && (int64_t)R * K < (1ll << 31), KDA_ERR_UNSUPPORTED);
     if (R == 0 || K == 0) return KDA_OK;
     KDA_REQUIRE(rows_ok(k) && rows_ok(v) && (!out || (rows_ok(out) && rows_ok(q))), KDA_ERR_INVALID_ARG);
-    KDA_REQUIRE(head_decay || log_decay, KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(decays_ok(head_decay, log_decay), KDA_ERR_INVALID_ARG);
     const void* need[] = {state_pool, slot};
     for (const void* p : need) KDA_REQUIRE(p != nullptr, KDA_ERR_INVALID_ARG);
-    const void* ptrs[] = {state_pool, slot, dst_slot, q_len, n_commit, head_decay, log_decay};
+    const void* ptrs[] = {state_pool, slot, dst_slot, q_len, n_commit};
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
     DecayDecodeArgs a{};
     a.k = as_rows(k);

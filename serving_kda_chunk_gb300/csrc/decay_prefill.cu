@@ -59,7 +59,8 @@ struct DecayPrefillArgs {
     int32_t N, T, H, group, M, hq, hk, hv, ho, out_dt, st;  // hq ..: 1, or 0 where all heads share a row
     bool boxes;  // output of the input's type: whole chunks are stored through maps.out
     float scale;
-    // of a cut launch: a flag and a decay a CTA, then its state
+    int32_t give_up_cta, give_up_load;  // of the self-test: this CTA's loads stop before this chunk
+    // of a cut launch: a flag and a decay a CTA, then the state it leaves
     uint32_t* flags;
     float* decays;
     float* states;
@@ -486,6 +487,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         uint32_t it = 0, m = 0;
         for (Chunks ch(a, rg); ch.any && !dead(); ch.next(a), ++it) {
             const uint32_t st = it & 1;
+            if ((int)blockIdx.x == a.give_up_cta && (int)it == a.give_up_load) {
+                ctrl[1] = 1;
+                break;
+            }
             const int row = ch.p.row0 + ch.c * kDecayChunk, h = ch.p.h, hk = h / a.group;
             if (it >= 2) wait(B_FREE + st, ((it >> 1) - 1) & 1);
             auto load = [&](uint32_t dst, const CUtensorMap* map, int head, int b) {
@@ -1055,14 +1060,17 @@ extern "C" size_t kda_decay_prefill_workspace_size(int32_t T_tot, int32_t N, int
     return may_cut(T_tot) && N > 0 && H > 0 ? kCutBytes : 16;
 }
 
-extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
-                                        kda_dtype in_dtype, const float* head_decay, const float* log_decay,
-                                        const int32_t* cu_seqlens, int32_t N, int32_t T_tot, int32_t H, int32_t Hk,
-                                        int32_t dk, int32_t dv, float scale, uint32_t flags, void* state_pool, int64_t P,
-                                        const int32_t* init_slot, const int32_t* final_slot,
-                                        const int32_t* track_chunk_idx, int32_t M, void* track_state,
-                                        const kda_rows_desc* out, kda_dtype out_dtype, void* workspace, size_t ws_bytes,
-                                        int32_t* dev_status, void* stream) {
+namespace kda {
+namespace {
+
+// Both entry points; give_up_cta < 0 for the call itself.
+kda_status prefill_call(
+    const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
+    kda_dtype in_dtype, const float* head_decay, const float* log_decay, const int32_t* cu_seqlens, int32_t N, int32_t T_tot,
+    int32_t H, int32_t Hk, int32_t dk, int32_t dv, float scale, uint32_t flags, void* state_pool, int64_t P,
+    const int32_t* init_slot, const int32_t* final_slot, const int32_t* track_chunk_idx, int32_t M, void* track_state,
+    const kda_rows_desc* out, kda_dtype out_dtype, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream, int32_t give_up_cta,
+    int32_t give_up_load) {
     KDA_REQUIRE(N >= 0 && T_tot >= 0 && H > 0 && Hk > 0 && P >= 0 && M >= 0, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(H % Hk == 0 && isfinite(scale), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(dk == kD && dv == kD, KDA_ERR_UNSUPPORTED);
@@ -1075,10 +1083,11 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
     if (T_tot > 0)
         for (const kda_rows_desc* d : {q, k, v})
             KDA_REQUIRE((d->row_stride > 0 || T_tot == 1) && d->row_stride >= 0 && d->head_stride >= 0, KDA_ERR_INVALID_ARG);
-    KDA_REQUIRE(cu_seqlens && (head_decay || log_decay), KDA_ERR_INVALID_ARG);
+    KDA_REQUIRE(cu_seqlens, KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(state_pool || (!init_slot && !final_slot), KDA_ERR_INVALID_ARG);
     KDA_REQUIRE(M == 0 || (track_chunk_idx && track_state), KDA_ERR_INVALID_ARG);
-    const void* ptrs[] = {cu_seqlens, head_decay, log_decay, state_pool, init_slot, final_slot, track_chunk_idx, track_state, workspace};
+    KDA_REQUIRE(decays_ok(head_decay, log_decay), KDA_ERR_INVALID_ARG);
+    const void* ptrs[] = {cu_seqlens, state_pool, init_slot, final_slot, track_chunk_idx, track_state, workspace};
     for (const void* p : ptrs) KDA_REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG);
     DecayMaps maps;
     DecayPrefillArgs a{};
@@ -1112,6 +1121,8 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
     a.out_dt = out_dtype;
     a.st = state_type(flags);
     a.scale = scale;
+    a.give_up_cta = give_up_cta;
+    a.give_up_load = give_up_load;
     auto* f = in_dtype == KDA_BF16 ? decay_prefill_kernel<KDA_BF16> : decay_prefill_kernel<KDA_F16>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DS_SMEM) != cudaSuccess)
         return runtime_failed();
@@ -1142,4 +1153,29 @@ extern "C" kda_status kda_decay_prefill(const kda_rows_desc* q, const kda_rows_d
     }
     if (cudaLaunchKernelEx(&cfg, f, maps, a) != cudaSuccess) return runtime_failed();
     return launch_status();
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_decay_prefill(
+    const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
+    kda_dtype in_dtype, const float* head_decay, const float* log_decay, const int32_t* cu_seqlens, int32_t N, int32_t T_tot,
+    int32_t H, int32_t Hk, int32_t dk, int32_t dv, float scale, uint32_t flags, void* state_pool, int64_t P,
+    const int32_t* init_slot, const int32_t* final_slot, const int32_t* track_chunk_idx, int32_t M, void* track_state,
+    const kda_rows_desc* out, kda_dtype out_dtype, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    return prefill_call(q, k, v, in_dtype, head_decay, log_decay, cu_seqlens, N, T_tot, H, Hk, dk, dv, scale, flags, state_pool, P, init_slot,
+                        final_slot, track_chunk_idx, M, track_state, out, out_dtype, workspace, ws_bytes, dev_status, stream, -1, 0);
+}
+
+extern "C" kda_status kda_selftest_decay_prefill_give_up(
+    const kda_rows_desc* q, const kda_rows_desc* k, const kda_rows_desc* v,
+    kda_dtype in_dtype, const float* head_decay, const float* log_decay, const int32_t* cu_seqlens, int32_t N, int32_t T_tot,
+    int32_t H, int32_t Hk, int32_t dk, int32_t dv, float scale, uint32_t flags, void* state_pool, int64_t P,
+    const int32_t* init_slot, const int32_t* final_slot, const int32_t* track_chunk_idx, int32_t M, void* track_state,
+    const kda_rows_desc* out, kda_dtype out_dtype, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream,
+    int32_t block, int32_t load) {
+    KDA_REQUIRE(block >= 0 && load >= 0, KDA_ERR_INVALID_ARG);
+    return prefill_call(q, k, v, in_dtype, head_decay, log_decay, cu_seqlens, N, T_tot, H, Hk, dk, dv, scale, flags, state_pool, P, init_slot,
+                        final_slot, track_chunk_idx, M, track_state, out, out_dtype, workspace, ws_bytes, dev_status, stream, block, load);
 }

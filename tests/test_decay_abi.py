@@ -36,7 +36,7 @@ def test_prefill_refusals(kda):
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(hd=None), dict(cu=None), dict(N=-1),
                 dict(T=-1), dict(H=0), dict(Hk=0), dict(Hk=3), dict(P=-1), dict(M=-1), dict(M=1), dict(M=1, track=FAKE),
                 dict(pool=None), dict(pool=FAKE + 8), dict(cu=FAKE + 4), dict(init=FAKE + 4), dict(final=FAKE + 2),
-                dict(hd=FAKE + 4), dict(ld=FAKE + 4), dict(q=rows(kda, None)), dict(k=rows(kda, FAKE + 8)),
+                dict(hd=FAKE + 2), dict(ld=FAKE + 1), dict(q=rows(kda, None)), dict(k=rows(kda, FAKE + 8)),
                 dict(v=rows(kda, rs=516)), dict(out=rows(kda, hs=4)), dict(scale=NAN), dict(scale=INF),
                 dict(ws=FAKE + 4, wb=1 << 30), dict(q=rows(kda, rs=-512)), dict(k=rows(kda, rs=0))):
         assert call(**bad) == INVALID, bad
@@ -64,7 +64,7 @@ def test_decode_refusals(kda):
     assert call(R=0, **none) == OK and call(K=0, **none) == OK
     for bad in (dict(k=None), dict(v=None), dict(q=None), dict(hd=None), dict(pool=None), dict(slot=None), dict(R=-1),
                 dict(K=-1), dict(H=0), dict(Hk=0), dict(Hk=3), dict(P=-1), dict(pool=FAKE + 8), dict(slot=FAKE + 4),
-                dict(dst=FAKE + 4), dict(ql=FAKE + 4), dict(nc=FAKE + 8), dict(hd=FAKE + 4), dict(ld=FAKE + 2),
+                dict(dst=FAKE + 4), dict(ql=FAKE + 4), dict(nc=FAKE + 8), dict(hd=FAKE + 1), dict(ld=FAKE + 2),
                 dict(k=rows(kda, FAKE + 2)), dict(q=rows(kda, rs=100)), dict(out=rows(kda, hs=9)), dict(scale=-INF),
                 dict(scale=NAN)):
         assert call(**bad) == INVALID, bad
@@ -135,3 +135,14 @@ def test_binding_refuses_shapes_and_types(kda):
         kda.kda_residual_norm(x, x.float(), hidden=x)
     with pytest.raises(ValueError, match="gate must have"):
         kda.kda_residual_norm(x, x, out=x, gate=z(2, 64, dtype=h))
+
+
+def test_prefill_self_test_refusals(kda):
+    ok = rows(kda)
+
+    def call(block=0, load=0, hd=FAKE):
+        return kda.lib().kda_selftest_decay_prefill_give_up(ok, ok, ok, BF16, hd, None, FAKE, 2, 10, 4, 2, 128, 128, 1.0, 0,
+                                                            FAKE, 8, FAKE, FAKE, None, 0, None, ok, BF16, None, 0, None,
+                                                            None, block, load)
+
+    assert call(block=-1) == INVALID and call(load=-1) == INVALID and call(hd=None) == INVALID
