@@ -593,6 +593,8 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
  *                    SMs; what an earlier call left there reaches no result.
  * A value, key or decay that is not finite makes the rows behind it (and the state)
  * NaN or infinite, and may make rows of its own chunk of 128 before it NaN.
+ * Sums are formed at up to 2^60 times a row's scale where its chunk's decays are
+ * that strong: scores times values stay below 2^60.
  * fp16 calls: scores and states below 2^-28 of the largest of their row and state
  * lose bits, and a decayed key is 2^-25 off at most (bf16 has fp32's exponents).
  * With KDA_DEV_TIMEOUT, rows and states that the call did not finish are not

@@ -708,10 +708,16 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * b + e <= row ? fabsf(s[e]) : 0.f);
                 }
-                ps = range_scale(mx * fabsf(scale));
+                ps = range_scale(mx);
             }
-            const float sp = kF16 ? scale * ps : scale;
+            float gi = d;  // G_i
+#pragma unroll
+            for (int x = 0; x < 4; ++x) gi += x <= w ? tot[x] : 0.f;
+            // Weights and Q S_0 are summed at the scale 2^-ref, ref = max(G_i, -60) (bf16: weights are 2^60 at most), so
+            // that Q S_0 is taken as it is unless the row's decay is below 2^-60.  fp16 weights take the row's own scale.
+            const float ref = kF16 ? 0.f : fmaxf(gi, -60.f);
             // blocks before the diagonal one, that one, then zeros; a block's scores are asked for ahead of its turn
+            const float dr = d - ref;
             uint32_t ahead[32];
             ld32_issue(tl + DT_SC, ahead);
 #pragma unroll 1
@@ -723,10 +729,10 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 if (b < w) ld32_issue(tl + DT_SC + 32 * (b + 1), ahead);
                 uint32_t p[16];
                 if (b < w) {
-                    float e = d;
+                    float e = d - ref;
 #pragma unroll
                     for (int x = 1; x < 4; ++x) e += x > b && x <= w ? tot[x] : 0.f;
-                    const float f = sp * ex2(e);
+                    const float f = kF16 ? ps * ex2(e) : ex2(e);
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const float4 c = lds_f4(gd + 512 + 4 * (32 * b + x));
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         const float4 c = lds_f4(gd + 4 * (32 * b + x));
                         const float cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) s[x + y] = x + y <= lane ? s[x + y] * sp * ex2(d - cc[y]) : 0.f;
+                        for (int y = 0; y < 4; ++y) s[x + y] = x + y <= lane ? (kF16 ? s[x + y] * ps : s[x + y]) * ex2(dr - cc[y]) : 0.f;
                         p[x / 2] = E::put2(s[x], s[x + 1]);
                         p[x / 2 + 1] = E::put2(s[x + 2], s[x + 3]);
                     }
@@ -759,16 +765,18 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             arrive(B_P);
             give_back();
             arrive(B_GFREE + st);
-            float fs = d, fp = 1.f;  // fs: G_i, then Q S_0's factor
-#pragma unroll
-            for (int x = 0; x < 4; ++x) fs += x <= w ? tot[x] : 0.f;
-            fs = sp * ex2(fs);
-            wait(B_QS, m & 1);
+            float fp = scale;  // the sum's factor
             if constexpr (kF16) {
-                fs *= pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1)));
-                fp = pow2_inverse(ps);
+                wait(B_QS, m & 1);
+                scale_rows(tl + DT_O, 128, ps * ex2(gi) * pow2_inverse(lds_f1(sb + DS_SCALE + 4 * (m & 1))));
+                fp *= pow2_inverse(ps);
+            } else {
+                if (__any_sync(~0u, !(gi >= -60.f))) {
+                    wait(B_QS, m & 1);
+                    scale_rows(tl + DT_O, 128, ex2(gi - ref));
+                }
+                fp *= ex2(ref);
             }
-            scale_rows(tl + DT_O, 128, fs);
             arrive(B_SCALED);
             wait(B_O, m & 1);
             fence_after();
@@ -780,9 +788,11 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 for (int b = 0; b < 4; ++b) {
                     float o[32];
                     ld32(tl + DT_O + 32 * b, o);
-                    if constexpr (kF16)
 #pragma unroll
-                        for (int z = 0; z < 32; ++z) o[z] *= fp;
+                    for (int z = 0; z < 32; z += 2) {
+                        const float2 y = __fmul2_rn(make_float2(o[z], o[z + 1]), make_float2(fp, fp));
+                        o[z] = y.x, o[z + 1] = y.y;
+                    }
                     const uint32_t to = stage + (b >> 1) * (kTile / 2) + row * 128, c = 4 * (b & 1);
 #pragma unroll
                     for (int z = 0; z < 4; ++z) sts128(to + (((c + z) ^ (row & 7)) << 4), pack16<DT>(o, 8 * z));
