@@ -144,17 +144,23 @@ __device__ __forceinline__ float tf32_of(float x) { return __uint_as_float(__flo
 // Sixteen rows times eight, over 4 + 4 of their 128 channels a step pair: x and y (rows g and g + 8) are the lane's
 // channels 4c .. 4c + 3 of a group of 16, q those of row g of the other side, whose order the products may choose.
 // The rows go in two parts of 11 bits each, 2^-21 of them left out; q is exact in one (bf16, fp16) or in two, too.
-__device__ __forceinline__ void rows_times(float (&d)[4], float4 x, float4 y, float4 q, bool wide) {
+// N sums take the products in turns: on one sum 32 of them waited for one another, some 35 cycles each.
+template <int N>
+__device__ __forceinline__ void rows_times(float (&d)[N][4], float4 x, float4 y, float4 q, bool wide) {
     const float4 xh = make_float4(tf32_of(x.x), tf32_of(x.y), tf32_of(x.z), tf32_of(x.w));
     const float4 yh = make_float4(tf32_of(y.x), tf32_of(y.y), tf32_of(y.z), tf32_of(y.w));
-    mma_tf32(d, xh.x, yh.x, xh.y, yh.y, q.x, q.y);
-    mma_tf32(d, xh.z, yh.z, xh.w, yh.w, q.z, q.w);
-    mma_tf32(d, x.x - xh.x, y.x - yh.x, x.y - xh.y, y.y - yh.y, q.x, q.y);
-    mma_tf32(d, x.z - xh.z, y.z - yh.z, x.w - xh.w, y.w - yh.w, q.z, q.w);
+    mma_tf32(d[0], xh.x, yh.x, xh.y, yh.y, q.x, q.y);
+    mma_tf32(d[1 % N], xh.z, yh.z, xh.w, yh.w, q.z, q.w);
+    mma_tf32(d[2 % N], x.x - xh.x, y.x - yh.x, x.y - xh.y, y.y - yh.y, q.x, q.y);
+    mma_tf32(d[3 % N], x.z - xh.z, y.z - yh.z, x.w - xh.w, y.w - yh.w, q.z, q.w);
     if (wide) {
-        mma_tf32(d, xh.x, yh.x, xh.y, yh.y, q.x - tf32_of(q.x), q.y - tf32_of(q.y));
-        mma_tf32(d, xh.z, yh.z, xh.w, yh.w, q.z - tf32_of(q.z), q.w - tf32_of(q.w));
+        mma_tf32(d[2 % N], xh.x, yh.x, xh.y, yh.y, q.x - tf32_of(q.x), q.y - tf32_of(q.y));
+        mma_tf32(d[3 % N], xh.z, yh.z, xh.w, yh.w, q.z - tf32_of(q.z), q.w - tf32_of(q.w));
     }
+}
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&d)[N][4], int e) {
+    return N == 4 ? (d[0][e] + d[1 % N][e]) + (d[2 % N][e] + d[3 % N][e]) : d[0][e] + d[1 % N][e];
 }
 
 // Several positions: a block a (request, head), sixteen value channels a warp.  Lane 4 g + c has rows g and g + 8 of
@@ -220,41 +226,53 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
         // thread j: prod_{j<s<=t} a_s for t >= j; the decays from the state; 0 for t < j
         if (tid < KT) {
             const int j = tid;
-            float f = j < ql ? 1.f : 0.f;
+            float de[KT];
+#pragma unroll
+            for (int t = 0; t < KT; ++t) de[t] = t < ql ? dec[t] : 0.f;
+            float f = j < ql ? 1.f : 0.f, l = 1.f;
+#pragma unroll
             for (int t = 0; t < KT; ++t) {
-                if (t > j) f *= t < ql ? dec[t] : 0.f;
+                if (t > j) f *= de[t];
+                if (t <= j) l *= de[t];
                 w[t][j] = t < j ? 0.f : f;
             }
-            f = 1.f;
-            for (int t = 0; t <= j && t < ql; ++t) f *= dec[t];
-            lead[j] = f;
+            lead[j] = l;
+        }
+        // keys 0 .. 15 times eight queries a warp, of the last warps, while the state is on its way
+        constexpr int kSums = NT == 1 ? 4 : 2;
+        const int kn = warp - (kWarps - NT);
+        float kq[kSums][4];
+        if (answer && kn >= 0) {
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) kq[i][0] = kq[i][1] = kq[i][2] = kq[i][3] = 0.f;
+#pragma unroll 2
+            for (int x = 0; x < 8; ++x) {
+                const int at = 16 * x + 4 * c;
+                rows_times<kSums>(kq, *reinterpret_cast<const float4*>(&sk[g][at]), *reinterpret_cast<const float4*>(&sk[g + 8][at]),
+                                  *reinterpret_cast<const float4*>(&sq[8 * kn + g][at]), wide);
+            }
         }
         __syncthreads();
         for (int e = tid; e < nc * kD; e += kStepsThreads) fv[e / kD][e % kD] = w[nc - 1][e / kD] * sv[e / kD][e % kD];
-        float d[NT][4];
+        float d[NT][kSums][4];
         if (answer) {
-            float kq[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0 .. 15 times eight queries, of warps 0 .. NT - 1
+            __syncthreads();  // every product of decays has been used
+            if (kn >= 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = g + 8 * (e >> 1), t = 8 * kn + 2 * c + (e & 1);
+                    if (j < KT) w[t][j] *= sum_of<kSums>(kq, e);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
+                for (int e = 0; e < 4 * kSums; ++e) d[n][e >> 2][e & 3] = 0.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int at = 16 * x + 4 * c;
+            for (int x = 0; x < 8; ++x)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) rows_times(d[n], s[0][x], s[1][x], *reinterpret_cast<const float4*>(&sq[8 * n + g][at]), wide);
-                if (warp < NT)
-                    rows_times(kq, *reinterpret_cast<const float4*>(&sk[g][at]), *reinterpret_cast<const float4*>(&sk[g + 8][at]),
-                               *reinterpret_cast<const float4*>(&sq[8 * warp + g][at]), wide);
-            }
-            __syncthreads();  // every product of decays has been used
-            if (warp < NT) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = g + 8 * (e >> 1), t = 8 * warp + 2 * c + (e & 1);
-                    if (j < KT) w[t][j] *= kq[e];
-                }
-            }
+                for (int n = 0; n < NT; ++n)
+                    rows_times<kSums>(d[n], s[0][x], s[1][x], *reinterpret_cast<const float4*>(&sq[8 * n + g][16 * x + 4 * c]), wide);
         }
         __syncthreads();
         if (answer) {
@@ -263,7 +281,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
                 const int t = 8 * n + 2 * c;
                 float o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = lead[t + (e & 1)] * d[n][e];
+                for (int e = 0; e < 4; ++e) o[e] = lead[t + (e & 1)] * sum_of<kSums>(d[n], e);
                 for (int j = 0; j < ql; ++j) {
                     const float w0 = w[t][j], w1 = w[t + 1][j], v0 = sv[j][row], v1 = sv[j][row + 8];
                     if (j <= t) o[0] = fmaf(w0, v0, o[0]), o[2] = fmaf(w0, v1, o[2]);
