@@ -168,13 +168,13 @@ __device__ __forceinline__ float sum_of(const float (&d)[N][4], int e) {
 // tensor-core products with the positions' queries, which take the place of a sum over the warp for each (row,
 // position) (with those, seven positions of 64 requests took 104 us, most of it instructions).  Those products are
 // HBM's shadow at 8 or 16 columns.  The state itself is updated by fp32 FMAs, each rounded to nearest.  In shared
-// memory: the positions' rows, their products q_t . k_j with the decays between, each committed value with its decay.
+// memory: the positions' rows, their products q_t . k_j with the decays between.
 template <int ST, int NT>  // NT: groups of eight positions
 __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const DecayDecodeArgs a) {
     using SIO = State<ST>;
     constexpr int KT = 8 * NT, QS = 144, KS = 136;  // row lengths in shared memory that spread the lanes' reads over all banks
-    __shared__ __align__(16) float sq[KT][QS], sk[16][KS], sv[KT][kD], fv[KT][kD];
-    __shared__ float w[KT][KT + 1], lead[KT], dec[KT];
+    __shared__ __align__(16) float sq[KT][QS], sk[16][KS], sv[KT][kD];
+    __shared__ float w[KT][KT + 1], lead[KT], dec[KT], kept[KT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H, hk = h / a.group;
     const Plan p = plan_of(a, r, tid == 0 && h == 0);
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
                 w[t][j] = t < j ? 0.f : f;
             }
             lead[j] = l;
+            kept[j] = nc ? w[nc - 1][j] : 0.f;  // of v_j in the committed state
         }
         // keys 0 .. 15 times eight queries a warp, of the last warps, while the state is on its way
         constexpr int kSums = NT == 1 ? 4 : 2;
@@ -253,10 +254,8 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
             }
         }
         __syncthreads();
-        for (int e = tid; e < nc * kD; e += kStepsThreads) fv[e / kD][e % kD] = w[nc - 1][e / kD] * sv[e / kD][e % kD];
         float d[NT][kSums][4];
         if (answer) {
-            __syncthreads();  // every product of decays has been used
             if (kn >= 0) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -274,8 +273,8 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
                 for (int n = 0; n < NT; ++n)
                     rows_times<kSums>(d[n], s[0][x], s[1][x], *reinterpret_cast<const float4*>(&sq[8 * n + g][16 * x + 4 * c]), wide);
         }
-        __syncthreads();
         if (answer) {
+            __syncthreads();
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int t = 8 * n + 2 * c;
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s[i][x] = f4_mul(s[i][x], make_float4(f, f, f, f));
             for (int j = 0; j < nc; ++j) {
-                const float v0 = fv[j][row], v1 = fv[j][row + 8];
+                const float v0 = kept[j] * sv[j][row], v1 = kept[j] * sv[j][row + 8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const float4 k = *reinterpret_cast<const float4*>(&sk[j][16 * x + 4 * c]);
