@@ -625,38 +625,82 @@ def kda_token_logprobs(logits, tokens, logprob, *, entropy=None, top_ids=None, t
 # linear attention with a decay a head, and the norms around a block
 
 
-def _here(first, *rest):
-    """All tensors on the device that is current: the calls launch there."""
-    dev = first.get_device()
+# Here every tensor has to lie on the device that is current, where the calls launch: one query of its device
+# (about 0.07 us) stands for the checks that it is a CUDA tensor at all.
+
+
+def _device(t):
+    """The device of a call's first tensor, which has to be the current one."""
+    dev = t.get_device()
     if dev < 0:
         raise ValueError("libkda takes CUDA tensors")
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
     if dev != _current_device():
-        raise ValueError(f"tensors on {first.device}, but device {_current_device()} is current")
+        raise ValueError(f"tensors on {t.device}, but device {_current_device()} is current")
+    return dev
+
+
+def _elsewhere(t):
+    raise ValueError("libkda takes CUDA tensors" if t.get_device() < 0 else f"tensors on different devices: {t.device} among them")
+
+
+def _on(t, dev, dtype, name, shape=None):
+    """Device pointer of a contiguous tensor of the given device, dtype and shape, or of none."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be a tensor of {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        _elsewhere(t)
+    if not t.is_contiguous():
+        raise ValueError("libkda takes contiguous CUDA tensors")
+    return t.data_ptr()
+
+
+def _placed(t, dev, name, n, h):
+    """Descriptor of a tensor [n rows, h heads, channels] of the given device with contiguous channels, or of none."""
+    if t is None:
+        return None
+    rs, hs, cs = t.stride()
+    if cs != 1 and n and h and t.shape[2] > 1:
+        raise ValueError(f"{name} needs contiguous channels")
+    if t.get_device() != dev:
+        _elsewhere(t)
+    # a dimension of one element is never stepped along: torch may give it any stride
+    return RowsDesc(t.data_ptr(), rs if n > 1 else 0, hs if h > 1 else 0)
 
 
 def _decay_args(q, k, v, out, head_decay, log_decay):
-    """(rows, H, Hk, dk, dv, in_dtype) and the checked decay pointers of the decayed-attention calls."""
+    """(device, rows, H, Hk, dk, dv, in_dtype, q, k, v, out, decays) of the decayed-attention calls, checked."""
     n, H, dv = v.shape
-    _, Hk, dk = k.shape
-    if k.shape[0] != n or (q is not None and q.shape != k.shape) or (out is not None and out.shape != v.shape):
+    ks = k.shape
+    _, Hk, dk = ks
+    if ks[0] != n or (q is not None and q.shape != ks) or (out is not None and out.shape != v.shape):
         for name, t, shape in (("q", q, (n, Hk, dk)), ("k", k, (n, Hk, dk)), ("out", out, (n, H, dv))):
             if t is not None and t.shape != shape:
                 raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if head_decay is None and log_decay is None:
         raise ValueError("head_decay or log_decay is needed")
-    dt = _one_dtype("q, k and v", k, v, k if q is None else q)
-    return (n, H, Hk, dk, dv, dt,
-            None if head_decay is None else _arr(head_decay, _f32t, "head_decay", (H,)),
-            None if log_decay is None else _arr(log_decay, _f32t, "log_decay", (n, H)))
+    dt = v.dtype
+    if k.dtype is not dt or (q is not None and q.dtype is not dt):
+        raise ValueError("q, k and v must share one dtype")
+    for name, t, shape in (("head_decay", head_decay, (H,)), ("log_decay", log_decay, (n, H))):
+        if t is not None and (t.dtype is not _f32t or t.shape != shape):
+            raise ValueError(f"{name} must be an fp32 tensor of shape {shape}, got {tuple(t.shape)} of {t.dtype}")
+    dev = _device(v)
+    return (dev, n, H, Hk, dk, dv, _dt3(v), _placed(q, dev, "q", n, Hk), _placed(k, dev, "k", n, Hk), _placed(v, dev, "v", n, H),
+            _placed(out, dev, "out", n, H), _on(head_decay, dev, _f32t, "head_decay"), _on(log_decay, dev, _f32t, "log_decay"))
 
 
-def _pool(state_pool, H, dk, dv):
-    if state_pool.shape[1:] != (H, dv, dk):
+def _pool(state_pool, dev, H, dk, dv):
+    """(pointer, slots, state flag) of a state pool, or of none."""
+    if state_pool is None:
+        return None, 0, 0
+    P, h, a, b = state_pool.shape
+    if h != H or a != dv or b != dk:
         raise ValueError(f"state_pool must be [slots, {H}, {dv}, {dk}], got {tuple(state_pool.shape)}")
-    return _p(state_pool)
+    return _on(state_pool, dev, state_pool.dtype, "state_pool"), P, _state_flag(state_pool)
 
 
 def kda_decay_prefill_workspace_size(T_tot, N, H) -> int:
@@ -669,24 +713,22 @@ def kda_decay_prefill(q, k, v, cu_seqlens, out, *, head_decay=None, log_decay=No
     """Linear attention with a decay a head over packed sequences (see include/kda.h).  q and k
     [T, Hk, 128], v and out [T, H, 128] may be strided over rows and heads; head_decay [H] and
     log_decay [T, H] are natural logarithms in fp32."""
-    T, H, Hk, dk, dv, dt, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
-    _here(v, q, k, out, cu_seqlens, head_decay, log_decay, state_pool, init_slot, final_slot, track_chunk_idx,
-          track_state, workspace, dev_status)
+    dev, T, H, Hk, dk, dv, dt, qd, kd, vd, od, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
     N = cu_seqlens.shape[0] - 1
+    pool, P, state = _pool(state_pool, dev, H, dk, dv)
     M = 0
     if track_chunk_idx is not None:
         M = track_chunk_idx.shape[1]
         if track_state is None or track_state.shape != (N, M, H, dv, dk):
             raise ValueError(f"track_state must have shape {(N, M, H, dv, dk)}")
+        state = _state_flag(state_pool, track_state)
     st = (_lib or lib()).kda_decay_prefill(
-        _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), dt, hd, ld, _arr(cu_seqlens, _i32, "cu_seqlens"), N, T, H, Hk,
-        dk, dv, scale, flags | _state_flag(state_pool, track_state),
-        None if state_pool is None else _pool(state_pool, H, dk, dv), 0 if state_pool is None else state_pool.shape[0],
-        None if init_slot is None else _arr(init_slot, _i32, "init_slot", (N,)),
-        None if final_slot is None else _arr(final_slot, _i32, "final_slot", (N,)),
-        None if track_chunk_idx is None else _arr(track_chunk_idx, _i32, "track_chunk_idx", (N, M)), M,
-        _p(track_state), _rows(out, "out"), _dt3(out), _p(workspace), 0 if workspace is None else workspace.nbytes,
-        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+        qd, kd, vd, dt, hd, ld, _on(cu_seqlens, dev, _i32, "cu_seqlens"), N, T, H, Hk, dk, dv, scale, flags | state, pool, P,
+        _on(init_slot, dev, _i32, "init_slot", (N,)), _on(final_slot, dev, _i32, "final_slot", (N,)),
+        _on(track_chunk_idx, dev, _i32, "track_chunk_idx", (N, M)), M,
+        None if track_state is None else _on(track_state, dev, track_state.dtype, "track_state"), od, _dt3(out),
+        None if workspace is None else _on(workspace, dev, workspace.dtype, "workspace"),
+        0 if workspace is None else workspace.nbytes, _on(dev_status, dev, _i32, "dev_status"), _stream(stream))
     if st:
         _check(st, "kda_decay_prefill")
 
@@ -697,19 +739,15 @@ def kda_decay_decode(q, k, v, state_pool, slot, out, *, K=1, q_len=None, n_commi
     and out [R*K, H, 128] may be strided over rows and heads; q and out may be None for a commit."""
     if q is None and out is not None:
         raise ValueError("an output needs q")
-    n, H, Hk, dk, dv, dt, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
-    _here(v, q, k, out, state_pool, slot, dst_slot, q_len, n_commit, head_decay, log_decay, dev_status)
+    dev, n, H, Hk, dk, dv, dt, qd, kd, vd, od, hd, ld = _decay_args(q, k, v, out, head_decay, log_decay)
     R = slot.shape[0]
     if K < 0 or n != R * K:
         raise ValueError(f"v has {n} rows, not {R} requests x K = {K}")
+    pool, P, state = _pool(state_pool, dev, H, dk, dv)
     st = (_lib or lib()).kda_decay_decode(
-        None if q is None else _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), dt, hd, ld, R, K,
-        None if q_len is None else _arr(q_len, _i32, "q_len", (R,)),
-        None if n_commit is None else _arr(n_commit, _i32, "n_commit", (R,)), H, Hk, dk, dv, scale,
-        flags | _state_flag(state_pool), _pool(state_pool, H, dk, dv), state_pool.shape[0],
-        _arr(slot, _i32, "slot", (R,)), None if dst_slot is None else _arr(dst_slot, _i32, "dst_slot", (R,)),
-        None if out is None else _rows(out, "out"), dt if out is None else _dt3(out),
-        None if dev_status is None else _arr(dev_status, _i32, "dev_status"), _stream(stream))
+        qd, kd, vd, dt, hd, ld, R, K, _on(q_len, dev, _i32, "q_len", (R,)), _on(n_commit, dev, _i32, "n_commit", (R,)), H,
+        Hk, dk, dv, scale, flags | state, pool, P, _on(slot, dev, _i32, "slot"), _on(dst_slot, dev, _i32, "dst_slot", (R,)), od,
+        dt if out is None else _dt3(out), _on(dev_status, dev, _i32, "dev_status"), _stream(stream))
     if st:
         _check(st, "kda_decay_decode")
 
@@ -718,28 +756,31 @@ def kda_gated_norm(x, out, *, gate=None, weight=None, eps=1e-6, weight_offset=0.
                    stream=None):
     """Each head's row normalised and multiplied by its activated gate (see include/kda.h).  x, gate and
     out: [R, H, d], strided over rows and heads; weight: [d]."""
-    R, H, d = x.shape
-    if out.shape != x.shape or (gate is not None and gate.shape != x.shape):
-        raise ValueError(f"gate and out must have the shape of x, {tuple(x.shape)}")
-    dt = _one_dtype("x, gate and weight", x, x if gate is None else gate, x if weight is None else weight)
-    _here(x, out, gate, weight)
+    shape = R, H, d = x.shape
+    dt = x.dtype
+    if out.shape != shape or (gate is not None and gate.shape != shape):
+        raise ValueError(f"gate and out must have the shape of x, {tuple(shape)}")
+    if (gate is not None and gate.dtype is not dt) or (weight is not None and weight.dtype is not dt):
+        raise ValueError("x, gate and weight must share one dtype")
+    dev = _device(x)
     st = (_lib or lib()).kda_gated_norm(
-        _rows(x, "x"), None if gate is None else _rows(gate, "gate"),
-        None if weight is None else _arr(weight, weight.dtype, "weight", (d,)), dt, R, H, d, eps, weight_offset, act,
-        flags, _rows(out, "out"), _dt3(out), _stream(stream))
+        _placed(x, dev, "x", R, H), _placed(gate, dev, "gate", R, H), _on(weight, dev, dt, "weight", (d,)), _dt3(x), R, H, d,
+        eps, weight_offset, act, flags, _placed(out, dev, "out", R, H), _dt3(out), _stream(stream))
     if st:
         _check(st, "kda_gated_norm")
 
 
-def _row_stride(t, name, shape):
+def _row_stride(t, dev, name, shape):
     """(pointer, row stride) of a tensor of rows, or of none."""
     if t is None:
         return None, 0
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     rs, cs = t.stride()
     if cs != 1 and shape[0] and shape[1] > 1:
         raise ValueError(f"{name} needs contiguous rows")
+    if t.get_device() != dev:
+        _elsewhere(t)
     return t.data_ptr(), rs if shape[0] > 1 else 0
 
 
@@ -747,21 +788,25 @@ def kda_residual_norm(x, residual, *, hidden=None, out=None, post_weight=None, g
                       weight=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6, weight_offset=0.0, stream=None):
     """Norm after a block, gate, residual sum and norm before the next block (see include/kda.h).  x [R, d];
     residual and hidden [R, d] of x's type or fp32; gate [R, d] or [1, d]; out [R, d]; weights [d]."""
-    shape = R, d = tuple(x.shape)
+    shape = R, d = x.shape
+    dt = x.dtype
     if hidden is None and out is None:
         raise ValueError("hidden or out is needed")
-    dt = _one_dtype("x, gate and weights", x, *(t for t in (gate, post_weight, weight) if t is not None))
     if hidden is not None and hidden.dtype is not residual.dtype:
         raise ValueError(f"hidden must have residual's dtype {residual.dtype}, got {hidden.dtype}")
-    gp, gs = _row_stride(gate, "gate", (1, d) if gate is not None and gate.shape[0] == 1 else shape)
-    xp, xs = _row_stride(x, "x", shape)
-    rp, rs = _row_stride(residual, "residual", shape)
-    hp, hs = _row_stride(hidden, "hidden", shape)
-    op, os_ = _row_stride(out, "out", shape)
-    _here(x, residual, hidden, out, post_weight, gate, weight)
+    if gate is not None and gate.dtype is not dt:
+        raise ValueError("x, gate and weights must share one dtype")
+    if gate is not None and gate.shape != shape and gate.shape != (1, d):
+        raise ValueError(f"gate must have shape {tuple(shape)} or {(1, d)}, got {tuple(gate.shape)}")
+    dev = _device(x)
+    gp, gs = _row_stride(gate, dev, "gate", shape if gate is None else gate.shape)
+    xp, xs = _row_stride(x, dev, "x", shape)
+    rp, rs = _row_stride(residual, dev, "residual", shape)
+    hp, hs = _row_stride(hidden, dev, "hidden", shape)
+    op, os_ = _row_stride(out, dev, "out", shape)
     st = (_lib or lib()).kda_residual_norm(
-        xp, xs, rp, rs, _dt3(residual), None if post_weight is None else _arr(post_weight, x.dtype, "post_weight", (d,)),
-        gp, gs, act, None if weight is None else _arr(weight, x.dtype, "weight", (d,)), dt, R, d, residual_scale,
-        branch_scale, eps, weight_offset, hp, hs, op, os_, dt if out is None else _dt3(out), _stream(stream))
+        xp, xs, rp, rs, _dt3(residual), _on(post_weight, dev, dt, "post_weight", (d,)), gp, gs, act,
+        _on(weight, dev, dt, "weight", (d,)), _dt3(x), R, d, residual_scale, branch_scale, eps, weight_offset, hp, hs, op, os_,
+        _dt3(x if out is None else out), _stream(stream))
     if st:
         _check(st, "kda_residual_norm")
