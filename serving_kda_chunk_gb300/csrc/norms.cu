@@ -9,7 +9,8 @@
 // One pass: a row lives in the registers of the TPR threads that share it (NV vectors of eight elements
 // each), so every input is read once and every output written once, and the second norm of the residual
 // form costs a reduction and no traffic.  Bound by HBM.  All arithmetic is fp32; y comes from the
-// unrounded h, and each output is rounded once on its store.
+// unrounded h, and each output is rounded once on its store.  41460 rows, bf16: gated, 32 heads of 128, 148 us (the
+// measured copy rate); residual of 4096 channels, fp32 residual, 240 us (85 % of it).
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "umma.cuh"
@@ -461,18 +462,21 @@ inline bool elem_aligned(const void* p, kda_dtype dt) { return reinterpret_cast<
 // Whole 16-byte vectors of eight elements: the row length, and each tensor's start and strides.
 inline bool vec_ok(const void* p, int64_t rs, int64_t hs) { return p == nullptr || (aligned16(p) && rs % 8 == 0 && hs % 8 == 0); }
 
-// Calls launch(TPR, NV) for the form that holds a row of nvec vectors.  A row goes to as many threads as it
-// has vectors while there are fewer rows than fill the device (`few`): one vector a thread is the shortest
-// path.  With many rows four vectors a thread keep more bytes in flight and share the reductions.
+// Calls launch(TPR, NV) for the form that holds a row of nvec vectors: one vector a thread as long as a block of 256
+// takes the row, at any number of rows (residual, bf16, 16384 rows of 1024: 29 us, and 40 with four vectors a thread of a
+// warp; 512: 16 and 36).  Up to 512 vectors it is 512 threads while there are fewer rows than fill the device (`few`;
+// 4096 channels, gated: 64 rows 2.4 and 2.8 us, 1024 rows 8.9 and 9.2), else four vectors a thread, which keep more
+// bytes in flight and share the reductions (16384 rows 85 and 71).
 template <class F>
 void with_row_form(int nvec, bool few, F&& launch) {
     if (nvec <= 8) launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 16) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 32) launch(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-    else if (nvec <= 128 && !few) launch(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+    else if (nvec <= 64) launch(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 128) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
-    else if (nvec <= 512 && !few) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 4>{});
-    else if (nvec <= 512) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 256) launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 512 && few) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 512) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 4>{});
     else launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
 
@@ -531,9 +535,10 @@ extern "C" kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc
                         xe, ge, weight, n, heads, d, 1.f / (float)d, eps, weight_offset, act,
                         (flags & KDA_NORM_AFTER_GATE) != 0, oe, out_dtype);
             };
-            // rows of one vector a thread go four at a time when there are many
+            // rows of one vector a thread of a warp go four at a time when there are many (128 channels: 131072 rows 20.2 and
+            // 21.1 us, 524288 rows 62 and 74; 65536 rows 12.6 and 12.3, 8192 rows 3.5 and 2.6)
             if constexpr (NV == 1 && TPR <= 32) {
-                if (n >= 65536) run(std::integral_constant<int, 4>{});
+                if (n >= 131072) run(std::integral_constant<int, 4>{});
                 else run(std::integral_constant<int, 1>{});
             } else {
                 run(std::integral_constant<int, 1>{});
@@ -569,7 +574,10 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
                          branch_scale, eps, weight_offset};
     cudaStream_t s = as_stream(stream);
     const int stage = d * (dtype_bytes(in_dtype) * (gate && gate_stride != 0 ? 2 : 1) + dtype_bytes(residual_dtype));
-    if (vec && d >= 1024 && R >= 1024 && 2 * stage <= kStreamBytes) {
+    // The ring from 1280 channels and 1024 rows on (against rows in registers: bf16, 1280 channels 15 and 17 us at 4096
+    // rows, 5.0 and 4.5 at 1024; 4096 channels 25 and 33, 10.3 and 11.9; fp32 residual 37 and 41, 13.9 and 14.6; but 1024
+    // channels 14 and 10), and above 4096 channels from 256 rows on (8192 channels: 7.5 and 8.6, 12.9 and 16.8 at 512).
+    if (vec && d > 1024 && R >= (d > 4096 ? 256 : 1024) && 2 * stage <= kStreamBytes) {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return runtime_failed();
