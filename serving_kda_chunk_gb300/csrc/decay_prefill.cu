@@ -4,31 +4,37 @@
 //     o_i = scale ( sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j + e^{G_i} S_0^T q_i ),
 //     S_C = e^{G_C} S_0 + sum_j e^{G_C - G_j} k_j v_j^T.
 // Four products of 128 x 128 x 128 a chunk and head on the tensor cores (tcgen05, accumulators in tensor memory):
-//     scores Q K^T;  P V with the weighted, masked scores P;  Q S_0;  V^T K~ with the decayed keys K~.
-// The last does not depend on the state, so the chain from chunk to chunk is S <- a S + V^T K~ in registers, 64
-// elements a thread, and the state never collects the products' own rounding.
+//     scores Q K^T;  Q S_0;  P V with the weighted, masked scores P, onto the last;  K~ V with the decayed keys K~.
+// The last does not depend on the state, so the chain from chunk to chunk is S <- a S + K~ V in registers (a thread
+// has a key channel and 64 value channels), and the state never collects the products' own rounding.
 //
 // What is rounded to the input type, and why that is enough: P and S_0, once each, for a product that is then
 // rounded to a 16-bit output (their errors lie on the two summands of o, so together they weigh as much as the
-// output's own rounding).  The decayed keys enter the fp32 state: they are split into parts of the input type,
-// three for bf16 (2^-25 left), two for fp16 (2^-22 left), and V^T K~ is as many products.  fp16 scores and states
-// are scaled by a power of two (a row's, a chunk's) to the upper end of fp16's range first.
+// output's own rounding).  The decayed keys enter the fp32 state: they are split into parts of the input type, three
+// for bf16 (by truncation, nothing left), two for fp16 (2^-22 left), and K~ V is as many products: part 1 and 2 as
+// operand from tensor memory, part 3 from shared memory.  fp16 scores and states are scaled by a power of two (a
+// row's, a chunk's) to the upper end of fp16's range first.
 //
 // Decays are kept per block of 32 tokens: D_i = G_i - G_end(block) >= 0 and the blocks' totals, from a sum in
 // 64 bits.  A weight of an earlier block is then e^{G_i - G_end} (a row's factor) times e^{G_end - G_j} (a
 // column's), both at most 1, and only the diagonal blocks take an exponential an element.  A forgotten state
 // (-104 a token) inside a chunk leaves the differences exact enough: |D| is 150 a forgetting, in log2 units.
 //
-// Bound by HBM on paper: 128 KiB a chunk and head, 5700 cycles of an SM's share.  One CTA a SM: a warp loads
-// (TMA), one issues products, one sums decays, four warps weigh scores and write results, eight split keys and
-// carry the state.  K and V are double-buffered, Q single (its load runs under the products that need no Q).
+// Bound by HBM on paper: 128 KiB a chunk and head, 5700 cycles of an SM's share.  One CTA a SM, 16 warps: one loads
+// (TMA; the next chunk into L2), one issues products, two sum decays in turns, four weigh scores and write results,
+// eight split keys and carry the state.  Of shared memory K and V have two stages, Q and the state's operand one, the
+// third part of K~ one (32 KiB each, 227 KB in all, so no second CTA); whole chunks of the input's type go out by TMA
+// through the stage of their keys.  What bounds it now is instruction issue and fetch: the roles run different code on
+// four schedulers, so what is rare is kept out of line, loops over halves stay loops, waits suspend their warp.  Each
+// of the steps that made the code smaller gave more than one that took arithmetic away.  8 sequences of ~5182 tokens,
+// 32 heads, bf16, states read and written: 281 us, 5.1 of 6.7 TB/s (535 us in the first form that used tensor cores).
 //
 // Balance: the (sequence, head) pairs' chunks lie in one row, cut into equal ranges, one a CTA.  A pair cut
 // once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
 // last.  A pair over more CTAs: each but the last first sums up its range's own state (K and V only, read twice) and
-// leaves it, then starts from the states before its own joined in order (with the pair's
-// beginning in one pass the others waited for its state: 131072 tokens, 16 heads 686 us).  CTAs wait for one another, so this is a
-// cooperative launch; every wait has a limit.
+// leaves it, then starts from the states before its own joined in order (131072 tokens, 16 heads: 614 us; with the
+// pair's beginning in one pass the others waited for its state, 685; ranges weighted by their passes were slower
+// too).  CTAs wait for one another, so this is a cooperative launch; every wait has a limit.
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
@@ -699,23 +705,35 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             const float d = lds_f1(gd + 4 * row);
             wait(B_QK, m & 1);
             fence_after();
-            float ps = 1.f;  // fp16: the row's scale
+            float ps = 1.f, lps = 0.f;  // fp16: the row's scale
             if constexpr (kF16) {
-                float mx = 0.f;
-                for (int b = 0; b <= w; ++b) {
+                float mx = 0.f, my = 0.f;
+#pragma unroll 1
+                for (int b = 0; b < w; ++b) {
                     float s[32];
                     ld32(tl + DT_SC + 32 * b, s);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * b + e <= row ? fabsf(s[e]) : 0.f);
+                    for (int e = 0; e < 32; e += 4) {
+                        mx = fmaxf(fmaxf(mx, fabsf(s[e])), fabsf(s[e + 1]));
+                        my = fmaxf(fmaxf(my, fabsf(s[e + 2])), fabsf(s[e + 3]));
+                    }
                 }
-                ps = range_scale(mx);
+                float s[32];
+                ld32(tl + DT_SC + 32 * w, s);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    mx = e <= lane ? fmaxf(mx, fabsf(s[e])) : mx;
+                    my = e + 1 <= lane ? fmaxf(my, fabsf(s[e + 1])) : my;
+                }
+                ps = range_scale(fmaxf(mx, my));
+                lps = (float)((int)(__float_as_uint(ps) >> 23) - 127);
             }
             float gi = d;  // G_i
 #pragma unroll
             for (int x = 0; x < 4; ++x) gi += x <= w ? tot[x] : 0.f;
             // Weights and Q S_0 are summed at the scale 2^-ref, ref = max(G_i, -60) (bf16: weights are 2^60 at most), so
             // that Q S_0 is taken as it is unless the row's decay is below 2^-60.  fp16 weights take the row's own scale.
-            const float ref = kF16 ? 0.f : fmaxf(gi, -60.f);
+            const float ref = kF16 ? -lps : fmaxf(gi, -60.f);
             // blocks before the diagonal one, that one, then zeros; a block's scores are asked for ahead of its turn
             const float dr = d - ref;
             uint32_t ahead[32];
@@ -732,7 +750,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     float e = d - ref;
 #pragma unroll
                     for (int x = 1; x < 4; ++x) e += x > b && x <= w ? tot[x] : 0.f;
-                    const float f = kF16 ? ps * ex2(e) : ex2(e);
+                    const float f = ex2(e);
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const float4 c = lds_f4(gd + 512 + 4 * (32 * b + x));
@@ -746,7 +764,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                         const float4 c = lds_f4(gd + 4 * (32 * b + x));
                         const float cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) s[x + y] = x + y <= lane ? (kF16 ? s[x + y] * ps : s[x + y]) * ex2(dr - cc[y]) : 0.f;
+                        for (int y = 0; y < 4; ++y) s[x + y] = x + y <= lane ? s[x + y] * ex2(dr - cc[y]) : 0.f;
                         p[x / 2] = E::put2(s[x], s[x + 1]);
                         p[x / 2 + 1] = E::put2(s[x + 2], s[x + 3]);
                     }
@@ -950,19 +968,23 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                     float x[64];
 #pragma unroll
                     for (int e = 0; e < 64; ++e) x[e] = 0.f;
-                    // the CTA with the unit's beginning left a state, those after it their ranges' own
-                    for (int j = (int)(((unit_at + 1) * ctas - 1) / total); j < (int)blockIdx.x; ++j) {
+                    // the CTA with the unit's beginning left a state, those after it their ranges' own; a lane waits for each
+                    for (int j0 = (int)(((unit_at + 1) * ctas - 1) / total); j0 < (int)blockIdx.x; j0 += 32) {
+                        const int j = min(j0 + lane, (int)blockIdx.x - 1);
                         uint32_t set = 0;
 #pragma unroll 1
                         for (uint32_t polls = 0; polls < kFlagLimit && !set && !gone_of(gone); ++polls) {
                             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(set) : "l"(a.flags + j) : "memory");
                             if (!set) __nanosleep(64);
                         }
-                        if (!set) {
+                        const float f = set ? *(volatile float*)(a.decays + j) : 0.f;
+                        if (!__all_sync(~0u, set)) {
                             ctrl[1] = 1;
                             break;
                         }
-                        join_state(x, *(volatile float*)(a.decays + j), a.states + (size_t)j * (kD * kD) + t);
+                        const int n = min((int)blockIdx.x - j0, 32);
+                        for (int y = 0; y < n; ++y)
+                            join_state(x, __shfl_sync(~0u, f, y), a.states + (size_t)(j0 + y) * (kD * kD) + t);
                     }
 #pragma unroll
                     for (int e = 0; e < 64; ++e) S[e] = x[e];
