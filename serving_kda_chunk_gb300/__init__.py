@@ -723,7 +723,7 @@ def kda_decay_prefill(q, k, v, cu_seqlens, out, *, head_decay=None, log_decay=No
             raise ValueError(f"track_state must have shape {(N, M, H, dv, dk)}")
         state = _state_flag(state_pool, track_state)
     st = (_lib or lib()).kda_decay_prefill(
-        qd, kd, vd, dt, hd, ld, _on(cu_seqlens, dev, _i32, "cu_seqlens"), N, T, H, Hk, dk, dv, scale, flags | state, pool, P,
+        qd, kd, vd, dt, hd, ld, _on(cu_seqlens, dev, _i32, "cu_seqlens", (N + 1,)), N, T, H, Hk, dk, dv, scale, flags | state, pool, P,
         _on(init_slot, dev, _i32, "init_slot", (N,)), _on(final_slot, dev, _i32, "final_slot", (N,)),
         _on(track_chunk_idx, dev, _i32, "track_chunk_idx", (N, M)), M,
         None if track_state is None else _on(track_state, dev, track_state.dtype, "track_state"), od, _dt3(out),
@@ -746,7 +746,7 @@ def kda_decay_decode(q, k, v, state_pool, slot, out, *, K=1, q_len=None, n_commi
     pool, P, state = _pool(state_pool, dev, H, dk, dv)
     st = (_lib or lib()).kda_decay_decode(
         qd, kd, vd, dt, hd, ld, R, K, _on(q_len, dev, _i32, "q_len", (R,)), _on(n_commit, dev, _i32, "n_commit", (R,)), H,
-        Hk, dk, dv, scale, flags | state, pool, P, _on(slot, dev, _i32, "slot"), _on(dst_slot, dev, _i32, "dst_slot", (R,)), od,
+        Hk, dk, dv, scale, flags | state, pool, P, _on(slot, dev, _i32, "slot", (R,)), _on(dst_slot, dev, _i32, "dst_slot", (R,)), od,
         dt if out is None else _dt3(out), _on(dev_status, dev, _i32, "dev_status"), _stream(stream))
     if st:
         _check(st, "kda_decay_decode")

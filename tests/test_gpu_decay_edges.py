@@ -210,3 +210,13 @@ def test_a_refused_launch_leaves_no_error(name):
     assert left == 0
     call(s)
     torch.cuda.synchronize()
+
+
+def test_indexes_of_another_shape_are_refused():
+    z = lambda *n, dt=BF16: torch.zeros(*n, dtype=dt, device="cuda")  # noqa: E731
+    x, pool, hd = z(4, 2, D), z(3, 2, D, D, dt=F32), z(2, dt=F32)
+    for slot in (z(4, 2, dt=torch.int32), z(4, 1, dt=torch.int32)):
+        with pytest.raises(ValueError, match="slot must have shape"):
+            kda.kda_decay_decode(x, x, x, pool, slot, torch.empty_like(x), head_decay=hd)
+    with pytest.raises(ValueError, match="cu_seqlens must have shape"):
+        kda.kda_decay_prefill(x, x, x, z(2, 2, dt=torch.int32), torch.empty_like(x), head_decay=hd)
