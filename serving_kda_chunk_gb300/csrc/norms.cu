@@ -10,7 +10,7 @@
 // each), so every input is read once and every output written once, and the second norm of the residual
 // form costs a reduction and no traffic.  Bound by HBM.  All arithmetic is fp32; y comes from the
 // unrounded h, and each output is rounded once on its store.  41460 rows, bf16: gated, 32 heads of 128, 148 us (the
-// measured copy rate); residual of 4096 channels, fp32 residual, 240 us (85 % of it).
+// measured copy rate); residual of 4096 channels 213 us (95 % of it).
 #include "kda_host.h"
 #include "latent_common.cuh"
 #include "umma.cuh"
@@ -337,14 +337,15 @@ __global__ void __launch_bounds__(norm_threads(TPR)) residual_norm_kernel(const 
 // Many long rows: a block walks rows gridDim.x apart, and a ring of rows in shared memory, filled by bulk copies,
 // keeps HBM busy under the two reductions and the stores.  (Rows in registers alone, 128 threads of four vectors:
 // 140 registers, 17 % of the warps and 4.5 of 6.7 TB/s at 41460 x 4096.)
-constexpr int kStreamThreads = 256;
+template <int T, int NV>
+constexpr int stream_ctas = T == 128 ? 4 : T == 256 ? (NV == 1 ? 3 : 2) : (NV <= 2 ? 2 : 1);  // blocks a SM, by registers
 
-template <int DT, int RDT, int NV>
-__global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stream_kernel(const ResidualArgs a, int stages) {
+template <int DT, int RDT, int T, int NV>
+__global__ void __launch_bounds__(T, stream_ctas<T, NV>) residual_stream_kernel(const ResidualArgs a, int stages) {
     using namespace umma;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[kStreamStages];
-    __shared__ float part[2][2][kStreamThreads / 32];  // two sums, of even and odd rows: one barrier lies between two uses
+    __shared__ float part[2][2][T / 32];  // two sums, of even and odd rows: one barrier lies between two uses
     __shared__ int gone;
     const int t = threadIdx.x, d = a.d, xb = d * dtype_bytes(DT), rb = d * dtype_bytes(RDT);
     const bool gates = a.gate && a.gs != 0;  // a gate row a row
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stre
     auto factors = [&](int i, float (&before)[8], float (&after)[8]) {
         float y[8];
         if (a.post) {
-            widen<DT>(load_raw<DT, true, kStreamThreads>(a.post, i, t, d), before);
+            widen<DT>(load_raw<DT, true, T>(a.post, i, t, d), before);
 #pragma unroll
             for (int e = 0; e < 8; ++e) before[e] = (before[e] + a.offset) * a.bscale;
         } else {
@@ -377,13 +378,13 @@ __global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stre
             for (int e = 0; e < 8; ++e) before[e] = a.bscale;
         }
         if (a.gate && !gates) {
-            widen<DT>(load_raw<DT, true, kStreamThreads>(a.gate, i, t, d), y);
+            widen<DT>(load_raw<DT, true, T>(a.gate, i, t, d), y);
             with_act(a.act, [&](auto ACT) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) set_pair(before, e, __fmul2_rn(pair(before, e), act2<ACT>(pair(y, e))));
             });
         }
-        if (a.weight) widen<DT>(load_raw<DT, true, kStreamThreads>(a.weight, i, t, d), after);
+        if (a.weight) widen<DT>(load_raw<DT, true, T>(a.weight, i, t, d), after);
 #pragma unroll
         for (int e = 0; e < 8; ++e) after[e] = a.weight ? after[e] + a.offset : 1.f;
     };
@@ -401,29 +402,29 @@ __global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stre
         const uint8_t* xs = ring + st * stage_bytes;
         float z[NV][8];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) widen<DT>(load_raw<DT, true, kStreamThreads>(xs, i, t, d), z[i]);
+        for (int i = 0; i < NV; ++i) widen<DT>(load_raw<DT, true, T>(xs, i, t, d), z[i]);
         float f = 1.f;
-        if (a.post) f = rsqrtf(row_sum<kStreamThreads>(sum_sq<NV>(z), part[0][it & 1]) * a.inv_d + a.eps);
+        if (a.post) f = rsqrtf(row_sum<T>(sum_sq<NV>(z), part[0][it & 1]) * a.inv_d + a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (elem_at<true, kStreamThreads>(i, 0, t) >= d) continue;  // (zeros, which add nothing)
+            if (elem_at<true, T>(i, 0, t) >= d) continue;  // (zeros, which add nothing)
             float y[8];
             if constexpr (!kKeep) factors(i, before[0], after[0]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), pair(before[kKeep ? i : 0], e)));
             if (gates) {
-                widen<DT>(load_raw<DT, true, kStreamThreads>(xs + xb + rb, i, t, d), y);
+                widen<DT>(load_raw<DT, true, T>(xs + xb + rb, i, t, d), y);
                 with_act(a.act, [&](auto ACT) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) set_pair(z[i], e, __fmul2_rn(pair(z[i], e), act2<ACT>(pair(y, e))));
                 });
             }
-            widen<RDT>(load_raw<RDT, true, kStreamThreads>(xs + xb, i, t, d), y);
+            widen<RDT>(load_raw<RDT, true, T>(xs + xb, i, t, d), y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) set_pair(z[i], e, __ffma2_rn(make_float2(a.rscale, a.rscale), pair(y, e), pair(z[i], e)));
         }
-        float sum = row_sum<kStreamThreads>(sum_sq<NV>(z), part[1][it & 1]);
+        float sum = row_sum<T>(sum_sq<NV>(z), part[1][it & 1]);
         // all have read the row (and the mark): the next one may come over it
         lost = gone;
         if (lost) {
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stre
         if (a.hidden) {
             void* p = at_elem(a.hidden, row * a.hs, RDT);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) store8<RDT, true, kStreamThreads>(p, i, t, d, z[i]);
+            for (int i = 0; i < NV; ++i) store8<RDT, true, T>(p, i, t, d, z[i]);
         }
         if (a.out) {
             f = rsqrtf(sum * a.inv_d + a.eps);
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kStreamThreads, NV == 1 ? 3 : 2) residual_stre
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     set_pair(z[i], e, __fmul2_rn(__fmul2_rn(pair(z[i], e), make_float2(f, f)), pair(after[kKeep ? i : 0], e)));
-                store8_as<true, kStreamThreads>(p, i, t, d, z[i], a.out_dt);
+                store8_as<true, T>(p, i, t, d, z[i], a.out_dt);
             }
         }
     }
@@ -574,27 +575,36 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
                          branch_scale, eps, weight_offset};
     cudaStream_t s = as_stream(stream);
     const int stage = d * (dtype_bytes(in_dtype) * (gate && gate_stride != 0 ? 2 : 1) + dtype_bytes(residual_dtype));
-    // The ring from 1280 channels and 1024 rows on (against rows in registers: bf16, 1280 channels 15 and 17 us at 4096
-    // rows, 5.0 and 4.5 at 1024; 4096 channels 25 and 33, 10.3 and 11.9; fp32 residual 37 and 41, 13.9 and 14.6; but 1024
-    // channels 14 and 10), and above 4096 channels from 256 rows on (8192 channels: 7.5 and 8.6, 12.9 and 16.8 at 512).
+    // The ring from 1280 channels and 1024 rows on (against rows in registers: bf16, 1280 channels 14 and 17 us at 4096
+    // rows, 4.5 and 4.5 at 1024; 4096 channels 25 and 33, 10.3 and 11.9; fp32 residual 37 and 41, 13.9 and 14.6; but 1024
+    // channels 14 and 10), and above 4096 channels from 256 rows on (8192 channels: 6.1 and 8.6, 15.8 and 28 at 1024).
     if (vec && d > 1024 && R >= (d > 4096 ? 256 : 1024) && 2 * stage <= kStreamBytes) {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return runtime_failed();
         cudaError_t err = cudaSuccess;
-        auto run = [&](auto DT, auto RDT, auto NV) {
-            const int most = NV == 1 ? 3 : 2;  // blocks a SM, by registers
+        auto run = [&](auto DT, auto RDT, auto T, auto NV) {
+            constexpr int most = stream_ctas<T, NV>;
             const int ctas = most * 2 * stage <= kStreamBytes ? most : kStreamBytes / (2 * stage);
             const int fit = kStreamBytes / (ctas * stage), stages = fit < kStreamStages ? fit : kStreamStages;
-            auto* f = residual_stream_kernel<DT, RDT, NV>;
+            auto* f = residual_stream_kernel<DT, RDT, T, NV>;
             err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
-            if (err == cudaSuccess) f<<<(unsigned)(sms * ctas < R ? sms * ctas : R), kStreamThreads, stages * stage, s>>>(a, stages);
+            if (err == cudaSuccess) f<<<(unsigned)(sms * ctas < R ? sms * ctas : R), T(), stages * stage, s>>>(a, stages);
         };
         auto by_len = [&](auto DT, auto RDT) {
-            if (d <= 8 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 1>{});
-            else if (d <= 16 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 2>{});
-            else if (d <= 32 * kStreamThreads) run(DT, RDT, std::integral_constant<int, 4>{});
-            else run(DT, RDT, std::integral_constant<int, 8>{});
+            // Threads and vectors of each: by how many threads a row leaves idle, and how many rows a SM then has.  bf16: 1280
+            // channels, 41460 rows 84 us (256 x 1: 105), but with an fp32 residual 118 and 109; 3584 channels, 16384 rows 74
+            // (512 x 1: 88); 4096, 41460 rows 237 (512 x 1: 211, but of 8192 rows 45 and 48, and with an fp32 residual 346 and
+            // 348); 5120, 16384 rows 127 (256 x 4: 168); 16384 channels 429 (256 x 8: 847).
+            using T128 = std::integral_constant<int, 128>;
+            using T256 = std::integral_constant<int, 256>;
+            using T512 = std::integral_constant<int, 512>;
+            if (d <= 1536 && RDT != KDA_F32) run(DT, RDT, T128{}, std::integral_constant<int, 2>{});
+            else if (d <= 2048) run(DT, RDT, T256{}, std::integral_constant<int, 1>{});
+            else if (d <= 4096 && d > 3968 && R >= 16384 && RDT != KDA_F32) run(DT, RDT, T512{}, std::integral_constant<int, 1>{});
+            else if (d <= 4096) run(DT, RDT, T256{}, std::integral_constant<int, 2>{});
+            else if (d <= 8192) run(DT, RDT, T512{}, std::integral_constant<int, 2>{});
+            else run(DT, RDT, T512{}, std::integral_constant<int, 4>{});
         };
         using BF = std::integral_constant<int, KDA_BF16>;
         using HF = std::integral_constant<int, KDA_F16>;

@@ -203,7 +203,8 @@ def test_a_layer_of_decayed_attention():
     assert (pool[slots.long()] - other[slots.long()]).norm() <= 0.015 * other.norm()
 
 
-@pytest.mark.parametrize("rows,d", [(1024, 1024), (1100, 2056), (1500, 4096), (1024, 8200), (1030, 16384)])
+@pytest.mark.parametrize("rows,d", [(1024, 1024), (1030, 1280), (1025, 2048), (1100, 2056), (1500, 4096), (16384, 4096),
+                                    (300, 5120), (256, 8192), (1024, 8200), (1030, 16384)])
 @pytest.mark.parametrize("dt,rdt,out_dt", [(BF16, BF16, BF16), (BF16, F32, BF16), (F16, F16, F32), (F32, F32, F32)])
 def test_residual_many_long_rows(rows, d, dt, rdt, out_dt):
     """Rows through the ring in shared memory, with and without the norm after the block, gates a row, in place."""
