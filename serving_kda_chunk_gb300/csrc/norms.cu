@@ -465,10 +465,13 @@ inline bool vec_ok(const void* p, int64_t rs, int64_t hs) { return p == nullptr 
 
 // Calls launch(TPR, NV) for the form that holds a row of nvec vectors: one vector a thread as long as a block of 256
 // takes the row, at any number of rows (residual, bf16, 16384 rows of 1024: 29 us, and 40 with four vectors a thread of a
-// warp; 512: 16 and 36).  Up to 512 vectors it is 512 threads while there are fewer rows than fill the device (`few`;
+// warp; 512: 16 and 36).  Longer rows of whole vectors: 512 threads while there are fewer rows than fill the device (`few`;
 // 4096 channels, gated: 64 rows 2.4 and 2.8 us, 1024 rows 8.9 and 9.2), else four vectors a thread, which keep more
-// bytes in flight and share the reductions (16384 rows 85 and 71).
-template <class F>
+// bytes in flight and share the reductions (8192 rows 39 and 45); above 512 vectors two a thread (8192 channels, residual,
+// 200 rows: 5.6 us, 1024 x 1 6.3, 512 x 4 7.4), above 1024 four (11.0; 1024 x 2 12.6).  Rows of single elements, whose
+// accesses are eight times as many, want every thread (8192 rows, residual: 4095 channels 102 us, 128 x 4 110; 4097
+// 211, 512 x 4 329).
+template <bool kVec, class F>
 void with_row_form(int nvec, bool few, F&& launch) {
     if (nvec <= 8) launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 16) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
@@ -476,8 +479,12 @@ void with_row_form(int nvec, bool few, F&& launch) {
     else if (nvec <= 64) launch(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 128) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
     else if (nvec <= 256) launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    else if (nvec <= 512 && few) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
-    else if (nvec <= 512) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 4>{});
+    else if (nvec <= 512 && (few || !kVec)) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+    else if constexpr (!kVec) {
+        if (nvec <= 1024) launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+        else launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+    } else if (nvec <= 512) launch(std::integral_constant<int, 128>{}, std::integral_constant<int, 4>{});
+    else if (nvec <= 1024) launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
     else launch(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
 
@@ -526,7 +533,7 @@ extern "C" kda_status kda_gated_norm(const kda_rows_desc* x, const kda_rows_desc
     cudaStream_t s = as_stream(stream);
     bool fits = true;
     with_types(in_dtype, vec, [&](auto DT, auto V) {
-        with_row_form(nvec, n < 1024, [&](auto TPR, auto NV) {
+        with_row_form<V>(nvec, n < 1024, [&](auto TPR, auto NV) {
             auto run = [&](auto U) {
                 constexpr int rows = norm_threads(TPR) / TPR * U;
                 const int64_t blocks = (n + rows - 1) / rows;
@@ -615,7 +622,7 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
         return err == cudaSuccess ? launch_status() : runtime_failed();
     }
     with_types(in_dtype, vec, [&](auto DT, auto V) {
-        with_row_form((d + 7) / 8, R < 1024, [&](auto TPR, auto NV) {
+        with_row_form<V>((d + 7) / 8, R < 1024, [&](auto TPR, auto NV) {
             constexpr int rows = norm_threads(TPR) / TPR;
             residual_norm_kernel<DT, V, TPR, NV><<<(unsigned)(((int64_t)R + rows - 1) / rows), norm_threads(TPR), 0, s>>>(a);
         });
