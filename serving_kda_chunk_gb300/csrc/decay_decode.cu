@@ -11,7 +11,7 @@
 // Bound by HBM: the state's bytes.  A warp holds whole rows of S^T in registers (a row = one value channel, 128 key
 // channels), asked for at the start, so that the bytes in flight are the registers of all resident warps.
 // 256 requests, 32 heads, fp32 states: one position 168 us (96 % of the measured copy rate); 64 requests of seven
-// positions: verify 39 us (57 %), commit 54 us (76 %).
+// positions: verify 39 us (57 %), commit 53 us (77 %).
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
@@ -20,7 +20,6 @@ namespace kda {
 namespace {
 
 constexpr int kDecayThreads = 128;
-constexpr int kStepsThreads = 256;  // of several positions
 constexpr int kDecayMaxK = 16;
 
 struct DecayDecodeArgs {
@@ -165,43 +164,43 @@ __device__ __forceinline__ float sum_of(const float (&d)[N][4], int e) {
     return N == 4 ? (d[0][e] + d[1 % N][e]) + (d[2 % N][e] + d[3 % N][e]) : d[0][e] + d[1 % N][e];
 }
 
-// Several positions: a block a (request, head), sixteen value channels a warp.  Lane 4 g + c has rows g and g + 8 of
+// Several positions: a block or two a (request, head), sixteen value channels a warp.  Lane 4 g + c has rows g and g + 8 of
 // its warp's, and of them channels 4c .. 4c + 3 of each group of 16 key channels: the operand layout of the warp's
 // tensor-core products with the positions' queries, which take the place of a sum over the warp for each (row,
 // position): with those, the verify of seven positions of 64 requests, 32 heads, took 104 us, most of it instructions;
 // now 39, and what is left is a block's own chain (rows, then state, then products, then rows out) at two blocks a SM,
 // which their registers allow.  The state itself is updated by fp32 FMAs, each rounded to nearest.  In shared
 // memory: the positions' rows, their products q_t . k_j with the decays between.
-template <int ST, int NT>  // NT: groups of eight positions
-__global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const DecayDecodeArgs a) {
+template <int ST, int NT, int PARTS>  // NT: groups of eight positions; PARTS: blocks a (request, head)
+__global__ void __launch_bounds__(256 / PARTS, 2 * PARTS) decay_steps_kernel(const DecayDecodeArgs a) {
     using SIO = State<ST>;
+    constexpr int kWarps = 8 / PARTS, kRows = 16 * kWarps;  // of a block: warps, value channels
     constexpr int KT = 8 * NT, QS = 144, KS = 136;  // row lengths in shared memory that spread the lanes' reads over all banks
-    __shared__ __align__(16) float sq[KT][QS], sk[16][KS], sv[KT][kD];
+    __shared__ __align__(16) float sq[KT][QS], sk[KT][KS], sv[KT][kRows];
     __shared__ float w[KT][KT + 1], lead[KT], dec[KT], kept[KT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H, hk = h / a.group;
-    const Plan p = plan_of(a, r, tid == 0 && h == 0);
-    const int ql = p.ql, nc = p.commit, row = 16 * warp + g;
+    const int unit = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
+    const int r = unit / a.H, h = unit - r * a.H, hk = h / a.group;
+    const Plan p = plan_of(a, r, tid == 0 && part == 0 && h == 0);
+    const int ql = p.ql, nc = p.commit, col = 16 * warp + g, row = part * kRows + col;
     const bool answer = a.out.base != nullptr, wide = a.in_dt == KDA_F32;
     const bool moved = p.live && p.dst >= 0 && p.dst != p.src;
     const int64_t first = (int64_t)r * a.K;
     // the positions' rows are asked for ahead of the state, whose 64 KiB they would else queue behind: what is made of
     // them alone is then done while the state comes
-    constexpr int kWarps = kStepsThreads / 32;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 qr[NT], kr[2], vr[NT];
+    constexpr int kTurns = KT / kWarps;  // rows t of a warp: warp, warp + kWarps, ..
+    float4 qr[kTurns], kr[kTurns], vr[kTurns];
     float log_a = 0.f;
     if (ql) {
         if (tid < ql) log_a = log_decay_of(a.head_decay, a.log_decay, first + tid, a.H, h);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kTurns; ++i) {
             const int t = warp + kWarps * i;
             const bool there = t < ql;
             kr[i] = there ? load4_as(row_of(a.k, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
-            if (i < NT) {
-                vr[i] = there ? load4_as(row_of(a.v, first + t, h, a.in_dt), 4 * lane, a.in_dt) : zero;
-                qr[i] = there && answer ? load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
-            }
+            vr[i] = there && 4 * lane < kRows ? load4_as(row_of(a.v, first + t, h, a.in_dt), part * kRows + 4 * lane, a.in_dt) : zero;
+            qr[i] = there && answer ? load4_as(row_of(a.q, first + t, hk, a.in_dt), 4 * lane, a.in_dt) : zero;
         }
     }
     float4 s[2][8];
@@ -213,17 +212,15 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
             for (int x = 0; x < 8; ++x) s[i][x] = SIO::load4_cs(a.pool, S + (size_t)(8 * i) * kD + 16 * x);
     }
     for (int t = ql + warp; answer && t < a.K; t += kWarps)  // positions that there are not
-        for (int i = lane; i < kD; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), i, 0.f, a.out_dt);
+        for (int i = lane; i < kRows; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), part * kRows + i, 0.f, a.out_dt);
     if (ql) {
         if (tid < ql) dec[tid] = __expf(log_a);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kTurns; ++i) {
             const int t = warp + kWarps * i;
             *reinterpret_cast<float4*>(&sk[t][4 * lane]) = kr[i];
-            if (i < NT) {
-                *reinterpret_cast<float4*>(&sv[t][4 * lane]) = vr[i];
-                *reinterpret_cast<float4*>(&sq[t][4 * lane]) = qr[i];
-            }
+            if (4 * lane < kRows) *reinterpret_cast<float4*>(&sv[t][4 * lane]) = vr[i];
+            *reinterpret_cast<float4*>(&sq[t][4 * lane]) = qr[i];
         }
         __syncthreads();
         // thread j: prod_{j<s<=t} a_s for t >= j; the decays from the state; 0 for t < j
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
 #pragma unroll 2
             for (int x = 0; x < 8; ++x) {
                 const int at = 16 * x + 4 * c;
-                rows_times<kSums>(kq, *reinterpret_cast<const float4*>(&sk[g][at]), *reinterpret_cast<const float4*>(&sk[g + 8][at]),
+                rows_times<kSums>(kq, *reinterpret_cast<const float4*>(&sk[g][at]), NT == 1 ? zero : *reinterpret_cast<const float4*>(&sk[(g + 8) % KT][at]),
                                   *reinterpret_cast<const float4*>(&sq[8 * kn + g][at]), wide);
             }
         }
@@ -285,7 +282,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = lead[t + (e & 1)] * sum_of<kSums>(d[n], e);
                 for (int j = 0; j < ql; ++j) {
-                    const float w0 = w[t][j], w1 = w[t + 1][j], v0 = sv[j][row], v1 = sv[j][row + 8];
+                    const float w0 = w[t][j], w1 = w[t + 1][j], v0 = sv[j][col], v1 = sv[j][col + 8];
                     if (j <= t) o[0] = fmaf(w0, v0, o[0]), o[2] = fmaf(w0, v1, o[2]);
                     if (j <= t + 1) o[1] = fmaf(w1, v0, o[1]), o[3] = fmaf(w1, v1, o[3]);
                 }
@@ -302,7 +299,7 @@ __global__ void __launch_bounds__(kStepsThreads, 2) decay_steps_kernel(const Dec
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s[i][x] = f4_mul(s[i][x], make_float4(f, f, f, f));
             for (int j = 0; j < nc; ++j) {
-                const float v0 = kept[j] * sv[j][row], v1 = kept[j] * sv[j][row + 8];
+                const float v0 = kept[j] * sv[j][col], v1 = kept[j] * sv[j][col + 8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const float4 k = *reinterpret_cast<const float4*>(&sk[j][16 * x + 4 * c]);
@@ -326,10 +323,15 @@ void launch(const DecayDecodeArgs& a, cudaStream_t s) {
     const unsigned units = (unsigned)a.R * (unsigned)a.H;
     if (a.K == 1)
         decay_step_kernel<ST><<<units * 4, kDecayThreads, 0, s>>>(a);
+    // A state in two blocks of 64 value channels: four chains a SM for two, and the positions' rows read twice.  64 requests
+    // of 32 heads, fp32 states, two blocks and one: step of 2 positions 56 and 62 us, 4 58 and 63, 7 67 and 68; verify 4
+    // 35.2 and 36.9, 5 41.3 and 36.9; commit 4 45 and 48.5, 7 48.7 and 49.8.  bf16 states, 256 requests, 7: commit 176 and 164.
+    else if (a.K <= 4 || (a.K <= 8 && !a.out.base && ST == kStateF32))
+        decay_steps_kernel<ST, 1, 2><<<units * 2, 128, 0, s>>>(a);
     else if (a.K <= 8)
-        decay_steps_kernel<ST, 1><<<units, kStepsThreads, 0, s>>>(a);
+        decay_steps_kernel<ST, 1, 1><<<units, 256, 0, s>>>(a);
     else
-        decay_steps_kernel<ST, 2><<<units, kStepsThreads, 0, s>>>(a);
+        decay_steps_kernel<ST, 2, 1><<<units, 256, 0, s>>>(a);
 }
 
 }  // namespace
