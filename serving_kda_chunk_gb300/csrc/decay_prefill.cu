@@ -29,7 +29,7 @@
 // of the steps that made the code smaller gave more than one that took arithmetic away.  8 sequences of ~5182 tokens,
 // 32 heads, bf16, states read and written: 281 us, 5.1 of 6.7 TB/s (535 us in the first form that used tensor cores).
 //
-// Balance: the (sequence, head) pairs' chunks lie in one row, cut into equal ranges, one a CTA.  A pair cut
+// Balance: the (sequence, head) pairs' chunks lie in one row, some places between pairs, cut into equal ranges, one a CTA.  A pair cut
 // once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
 // last.  A pair over more CTAs: each but the last first sums up its range's own state (K and V only, read twice) and
 // leaves it, then starts from the states before its own joined in order (131072 tokens, 16 heads: 614 us; with the
@@ -51,6 +51,8 @@ constexpr int kDecayChunk = 128;
 constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
 constexpr int kCutChunks = 6;          // a CTA's least range: with 2 to 16, 16384 tokens of one head took 158, 106 (4), 95 (8), 115 us
 constexpr int kPreDecayThreads = 512;
+constexpr int kUnitChunks = 2;         // what a pair's states, join and first chunk cost beside its chunks, for equal ranges: with 0, 1, 2,
+                                       // 3 one prompt of 4096 tokens, 32 heads took 80, 76, 70, 72 us, 16 of 700, 16 heads 83, 73, 73, 74
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
 constexpr uint32_t kWaitLimit = 1u << 18;
 constexpr uint32_t kFlagLimit = 1u << 21;
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
     }
     // ---- this CTA's range of chunks
     Range rg;
-    int64_t total = 0, unit_at = 0;  // all chunks; the first one of the first unit
+    int64_t total = 0, unit_at = 0;  // the places of all units (a place a chunk, then kUnitChunks); the first unit's first place
     int ctas = 1;
     if (!cut) {
         int bad;
@@ -420,7 +422,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         int64_t mine = 0;
         for (int n = me; n < a.N; n += width) {
             int bad;
-            mine += seq_chunks(a, n, bad);
+            const int c = seq_chunks(a, n, bad);
+            mine += c ? c + kUnitChunks : 0;
             if (bad && blockIdx.x == 0 && tid < width) report(a.dev_status, bad);
         }
         sums(mine, total);
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
         for (int base = 0; base < a.N; base += width) {
             const int n = base + me;
             int bad;
-            const int c = n < a.N ? seq_chunks(a, n, bad) : 0;
+            const int chunks = n < a.N ? seq_chunks(a, n, bad) : 0, c = chunks ? chunks + kUnitChunks : 0;
             int64_t sum;
             const int64_t end = (before + sums(c, sum)) * a.H, begin = end - (int64_t)c * a.H;
             before += sum;
@@ -444,16 +447,26 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                 const int64_t x = total * (blockIdx.x + e) / ctas;
                 if (c && x >= begin && x < end && tid < width) {
                     const int64_t h = (x - begin) / c, unit = begin + h * c;
+                    const bool past = x - unit >= chunks;  // the next unit
                     ctrl[2 + 3 * e] = n;
-                    ctrl[3 + 3 * e] = (int)h;
-                    ctrl[4 + 3 * e] = (int)(x - unit);
+                    ctrl[3 + 3 * e] = (int)h + past;
+                    ctrl[4 + 3 * e] = past ? 0 : (int)(x - unit);
                     if (e == 0) *reinterpret_cast<volatile long long*>(sm + DS_CTRL + 32) = unit;
-                    else ctrl[10] = total * (blockIdx.x + 2) / ctas < unit + c;
+                    else ctrl[10] = !past && total * (blockIdx.x + 2) / ctas < unit + chunks;
                 }
             }
         }
         __syncthreads();
         rg = Range{ctrl[2], ctrl[3], ctrl[4], ctrl[5], ctrl[6], ctrl[7], ctrl[10] != 0};
+        auto carry = [&](int& n, int& h) {  // from behind the last head to the next sequence
+            int bad;
+            if (h < a.H) return;
+            h = 0;
+            do ++n;
+            while (n < a.N && seq_chunks(a, n, bad) == 0);
+        };
+        carry(rg.fn, rg.fh);
+        carry(rg.ln, rg.lh);
         unit_at = *reinterpret_cast<volatile long long*>(sm + DS_CTRL + 32);
     }
     if (tid < B_COUNT) {
@@ -1170,7 +1183,7 @@ kda_status prefill_call(
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return runtime_failed();
-        const int64_t most = ((int64_t)T_tot / kDecayChunk + N) * H;  // chunks
+        const int64_t most = ((int64_t)T_tot / kDecayChunk + (1 + kUnitChunks) * (int64_t)N) * H;  // places
         const int64_t ctas = (most + kCutChunks - 1) / kCutChunks;
         const int most_ctas = sms < kDecayCtas ? sms : kDecayCtas;
         cfg.gridDim.x = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
