@@ -51,6 +51,8 @@ constexpr int kDecayChunk = 128;
 constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
 constexpr int kCutChunks = 6;          // a CTA's least range: with 2 to 16, 16384 tokens of one head took 158, 106 (4), 95 (8), 115 us
 constexpr int kPreDecayThreads = 512;
+constexpr int kShortUnit = 14;         // pairs of fewer places on average are not worth cutting while SMs are left: 1000 tokens of 16 heads
+                                       // took 50 us cut, 39 not, 800 of 64 heads 46 and 41; 1500 of 8 heads (14 places) 52 and 53
 constexpr int kUnitChunks = 2;         // what a pair's states, join and first chunk cost beside its chunks, for equal ranges: with 0, 1, 2,
                                        // 3 one prompt of 4096 tokens, 32 heads took 80, 76, 70, 72 us, 16 of 700, 16 heads 83, 73, 73, 74
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels
@@ -419,16 +421,19 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
             }
             return x + off;
         };
+        const int64_t one = a.N <= 65536 ? 1ll << 40 : 0;  // the units' number, in the upper bits (places stay below 2^39 then)
         int64_t mine = 0;
         for (int n = me; n < a.N; n += width) {
             int bad;
             const int c = seq_chunks(a, n, bad);
-            mine += c ? c + kUnitChunks : 0;
+            mine += c ? c + kUnitChunks + one : 0;
             if (bad && blockIdx.x == 0 && tid < width) report(a.dev_status, bad);
         }
         sums(mine, total);
-        total *= a.H;
-        ctas = (int)min((int64_t)gridDim.x, (total + kCutChunks - 1) / kCutChunks);
+        const int64_t units = one ? (total >> 40) * a.H : 0;
+        total = (one ? total & (one - 1) : total) * a.H;
+        const int64_t least = total < kShortUnit * units ? units : (total + kCutChunks - 1) / kCutChunks;
+        ctas = (int)min((int64_t)gridDim.x, least);
         if ((int)blockIdx.x >= ctas) return;
         if (tid == 0) {
             ctrl[5] = a.N;  // the last CTA's end
