@@ -29,8 +29,8 @@
 // of the steps that made the code smaller gave more than one that took arithmetic away.  8 sequences of ~5182 tokens,
 // 32 heads, bf16, states read and written: 281 us, 5.1 of 6.7 TB/s (535 us in the first form that used tensor cores).
 //
-// Balance: the (sequence, head) pairs' chunks lie in one row, some places between pairs, cut into equal ranges, one a CTA.  A pair cut
-// once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
+// Balance: the (sequence, head) pairs' chunks lie in one row, with places for what a pair costs besides, cut into equal
+// ranges, one a CTA.  A pair cut once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
 // last.  A pair over more CTAs: each but the last first sums up its range's own state (K and V only, read twice) and
 // leaves it, then starts from the states before its own joined in order (131072 tokens, 16 heads: 614 us; with the
 // pair's beginning in one pass the others waited for its state, 685; ranges weighted by their passes were slower
@@ -49,7 +49,8 @@ using namespace umma;
 
 constexpr int kDecayChunk = 128;
 constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
-constexpr int kCutChunks = 6;          // a CTA's least range: with 2 to 16, 16384 tokens of one head took 158, 106 (4), 95 (8), 115 us
+constexpr int kCutChunks = 6;          // a CTA's least range, in places: with 5, 6, 8, 10 one prompt of 16384 tokens, one head took 85, 81, 82,
+                                       // 85 us, 6000 tokens of 16 heads 68, 66, 71, 78, two of 8192, 4 heads 70, 68, 72, 80
 constexpr int kPreDecayThreads = 512;
 constexpr int kShortUnit = 14;         // pairs of fewer places on average are not worth cutting while SMs are left: 1000 tokens of 16 heads
                                        // took 50 us cut, 39 not, 800 of 64 heads 46 and 41; 1500 of 8 heads (14 places) 52 and 53

@@ -93,6 +93,41 @@ def test_prefill_of_many_sequences(n):
     assert torch.equal(alone, out) and torch.equal(other, pool)
 
 
+@pytest.mark.parametrize("seed", range(10))
+def test_prefill_cut_anywhere(seed):
+    """Pairs cut between blocks, wherever that falls, against one block a pair: states in place, empty and refused
+    sequences among them.  Outputs are within 1.5 half steps each (as elsewhere); states add up to 40 chunks and the
+    ranges' states in fp32, each addition 2^-24 off."""
+    g = torch.Generator().manual_seed(seed)
+    pick = lambda n: int(torch.randint(0, n, (1,), generator=g))  # noqa: E731
+    n, H = (1, 2, 3, 7, 33, 50)[pick(6)], (1, 2, 3, 5, 16)[pick(5)]
+    most = min(5000, 120000 // (n * H))
+    lens = [(0, 128, 129, pick(most) + 1, pick(most) + 1)[pick(5)] for _ in range(n)] + [1000]
+    n += 1
+    c = prefill_case(lens, H, H, BF16, "both", extra=0)
+    pool = torch.randn(n, H, D, D, generator=gen(seed), device="cuda")
+    slots = list(range(n))
+    if seed % 2 and n > 2:
+        slots[n // 2] = n + 5  # there is none
+    slot = i32(slots)
+    got = []
+    for size in (kda.kda_decay_prefill_workspace_size(c["T"], n, H), 0):
+        p, out = pool.clone(), torch.full((c["T"], H, D), 7.0, dtype=BF16, device="cuda")
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda") if size else None
+        st = raw_prefill(c, out, p, slot, slot, ws)
+        assert st == (kda.KDA_DEV_BAD_SLOT if max(slots) >= n else 0)
+        got.append((out, p))
+    (a, p), (b, q) = got
+    at = 0
+    for length, s in zip(lens, slots):
+        if s >= n:
+            assert (a[at:at + length] == 7.0).all()
+        elif length:
+            assert rel(a[at:at + length].transpose(0, 1), b[at:at + length].transpose(0, 1)) <= 2 * 1.5 * half_step(BF16)
+        at += length
+    assert rel(p, q) <= 1e-5
+
+
 def test_offsets_past_32_bits():
     """Rows that lie 2^23 elements apart, a pool of more than 2^32 bytes."""
     g, n, step = gen(6), 300, 1 << 23
