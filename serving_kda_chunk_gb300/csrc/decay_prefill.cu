@@ -1001,6 +1001,8 @@ __global__ void __launch_bounds__(kPreDecayThreads, 1)
                             ctrl[1] = 1;
                             break;
                         }
+                        // a lane reads states whose flags others acquired: the vote and the shuffles order no memory
+                        __syncwarp();
                         const int n = min((int)blockIdx.x - j0, 32);
                         for (int y = 0; y < n; ++y)
                             join_state(x, __shfl_sync(~0u, f, y), a.states + (size_t)(j0 + y) * (kD * kD) + t);
