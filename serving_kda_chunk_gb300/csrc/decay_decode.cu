@@ -10,8 +10,8 @@
 //
 // Bound by HBM: the state's bytes.  A warp holds whole rows of S^T in registers (a row = one value channel, 128 key
 // channels), asked for at the start, so that the bytes in flight are the registers of all resident warps.
-// 256 requests, 32 heads, fp32 states: one position 168 us (96 % of the measured copy rate); 64 requests of seven
-// positions: verify 39 us (57 %), commit 53 us (77 %).
+// 256 requests, 32 heads, fp32 states: one position 169 us (95 % of the measured copy rate); 64 requests of seven
+// positions: verify 39 us (57 %), commit 54 us (76 %).
 #include "decay_common.cuh"
 #include "kda_host.h"
 #include "latent_host.h"
@@ -83,9 +83,32 @@ __device__ __forceinline__ void* out_row(const LatentRows& d, int64_t row, int h
     return const_cast<void*>(row_of(d, row, h, dt));
 }
 
-// One position: 32 rows a block, eight a warp.  Nothing is shared between warps.
+// e^g for what is not summed up over calls; a forgotten state leaves exactly nothing.
+__device__ __forceinline__ float exp_of(float g) { return g <= -104.f ? 0.f : expf(g); }
+
+// What a state is multiplied by.  The nearest fp32 value to e^g is up to 2^-25 off, for a fixed slope alike at every token:
+// 9e-5 of the state after 4096 tokens at g = -1e-4.  So from e^g = 1/2 on it is taken less one, whose rounding goes by
+// 1 - e^g, and an fp32 state s becomes s + s (e^g - 1), rounded once.  (16-bit states lose more at each store.)  256 requests,
+// 32 heads: 159.7 us, with the product alone 158.9; 64 x 7 commit 49.6 and 48.7.
+struct Fade {
+    float m;    // e^g - 1 if near, else e^g
+    bool near;
+};
+constexpr float kNear = -0.69f;
 template <int ST>
-__global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const DecayDecodeArgs a) {
+__device__ __forceinline__ Fade fade_of(float g) { return ST == kStateF32 && g > kNear ? Fade{expm1f(g), true} : Fade{exp_of(g), false}; }
+__device__ __forceinline__ float faded(float s, Fade f) {
+    // an infinite s stays what it is: only a finite one is taken times e^g - 1
+    return f.near ? fmaf(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f), f.m, s) : s * f.m;
+}
+__device__ __forceinline__ float4 faded(float4 s, Fade f) {
+    return make_float4(faded(s.x, f), faded(s.y, f), faded(s.z, f), faded(s.w, f));
+}
+
+// One position: 32 rows a block, eight a warp.  Nothing is shared between warps.  Seven blocks a SM by registers (64 of them):
+// 16-bit states, 256 requests, 94.7 us, with the 72 that the compiler takes otherwise 99.5.
+template <int ST>
+__global__ void __launch_bounds__(kDecayThreads, 7) decay_step_kernel(const DecayDecodeArgs a) {
     using SIO = State<ST>;
     constexpr int RW = 8, parts = kD / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,7 +126,7 @@ __global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const DecayDe
         const int hk = h / a.group;
         const float4 k = load4_as(row_of(a.k, r, hk, a.in_dt), 4 * lane, a.in_dt);
         const float vm = load1_as(row_of(a.v, r, h, a.in_dt), row0 + (lane >> 2), a.in_dt);  // of the row lane / 4
-        const float decay = __expf(log_decay_of(a.head_decay, a.log_decay, r, a.H, h));
+        const Fade fade = fade_of<ST>(log_decay_of(a.head_decay, a.log_decay, r, a.H, h));
         if (a.out.base) {
             float4 q = load4_as(row_of(a.q, r, hk, a.in_dt), 4 * lane, a.in_dt);
             q = make_float4(q.x * a.scale, q.y * a.scale, q.z * a.scale, q.w * a.scale);
@@ -111,14 +134,19 @@ __global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const DecayDe
             float d[RW];
 #pragma unroll
             for (int i = 0; i < RW; ++i) d[i] = f4_dot(s[i], q);
-            const float o = fmaf(decay, reduce_scatter<RW>(d, lane), kq * vm);
+            const float o = fmaf(fade.near ? 1.f + fade.m : fade.m, reduce_scatter<RW>(d, lane), kq * vm);
             if ((lane & 3) == 0) store1_as(out_row(a.out, r, h, a.out_dt), row0 + (lane >> 2), o, a.out_dt);
         }
         if (p.commit) {
+            if (fade.near) {
 #pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                const float4 x = f4_mul(s[i], make_float4(decay, decay, decay, decay));
-                s[i] = f4_fma(__shfl_sync(0xffffffffu, vm, 4 * i), k, x);
+                for (int i = 0; i < RW; ++i) s[i] = f4_fma(__shfl_sync(0xffffffffu, vm, 4 * i), k, faded(s[i], fade));
+            } else {
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float4 x = f4_mul(s[i], make_float4(fade.m, fade.m, fade.m, fade.m));
+                    s[i] = f4_fma(__shfl_sync(0xffffffffu, vm, 4 * i), k, x);
+                }
             }
         }
     } else if (a.out.base) {
@@ -177,7 +205,7 @@ __global__ void __launch_bounds__(256 / PARTS, 2 * PARTS) decay_steps_kernel(con
     constexpr int kWarps = 8 / PARTS, kRows = 16 * kWarps;  // of a block: warps, value channels
     constexpr int KT = 8 * NT, QS = 144, KS = 136;  // row lengths in shared memory that spread the lanes' reads over all banks
     __shared__ __align__(16) float sq[KT][QS], sk[KT][KS], sv[KT][kRows];
-    __shared__ float w[KT][KT + 1], lead[KT], dec[KT], kept[KT];
+    __shared__ float w[KT][KT + 1], lead[KT], dec[KT], logs[KT], kept[KT], sum_log;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int unit = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
     const int r = unit / a.H, h = unit - r * a.H, hk = h / a.group;
@@ -214,7 +242,7 @@ __global__ void __launch_bounds__(256 / PARTS, 2 * PARTS) decay_steps_kernel(con
     for (int t = ql + warp; answer && t < a.K; t += kWarps)  // positions that there are not
         for (int i = lane; i < kRows; i += 32) store1_as(out_row(a.out, first + t, h, a.out_dt), part * kRows + i, 0.f, a.out_dt);
     if (ql) {
-        if (tid < ql) dec[tid] = __expf(log_a);
+        if (tid < ql) dec[tid] = exp_of(log_a), logs[tid] = log_a;
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
             const int t = warp + kWarps * i;
@@ -238,6 +266,11 @@ __global__ void __launch_bounds__(256 / PARTS, 2 * PARTS) decay_steps_kernel(con
             }
             lead[j] = l;
             kept[j] = nc ? w[nc - 1][j] : 0.f;  // of v_j in the committed state
+            if (j == nc - 1) {
+                float g = 0.f;
+                for (int t = 0; t < nc; ++t) g += logs[t];
+                sum_log = g;
+            }
         }
         // keys 0 .. 15 times eight queries a warp, of the last warps, while the state is on its way
         constexpr int kSums = NT == 1 ? 4 : 2;
@@ -293,11 +326,13 @@ __global__ void __launch_bounds__(256 / PARTS, 2 * PARTS) decay_steps_kernel(con
             }
         }
         if (nc) {
-            const float f = lead[nc - 1];
+            // (far from one, the product of the positions' decays: it is as exact, and needs no sum)
+            const float g = sum_log;
+            const Fade f = ST == kStateF32 && g > kNear ? Fade{expm1f(g), true} : Fade{lead[nc - 1], false};
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) s[i][x] = f4_mul(s[i][x], make_float4(f, f, f, f));
+                for (int x = 0; x < 8; ++x) s[i][x] = faded(s[i][x], f);
             for (int j = 0; j < nc; ++j) {
                 const float v0 = kept[j] * sv[j][col], v1 = kept[j] * sv[j][col + 8];
 #pragma unroll
