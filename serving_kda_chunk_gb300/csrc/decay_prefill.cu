@@ -40,6 +40,7 @@
 #include "latent_host.h"
 #include "umma.cuh"
 
+#include <algorithm>
 #include <initializer_list>
 
 namespace kda {
@@ -1192,9 +1193,11 @@ kda_status prefill_call(
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return runtime_failed();
         const int64_t most = ((int64_t)T_tot / kDecayChunk + (1 + kUnitChunks) * (int64_t)N) * H;  // places
-        const int64_t ctas = (most + kCutChunks - 1) / kCutChunks;
-        const int most_ctas = sms < kDecayCtas ? sms : kDecayCtas;
-        cfg.gridDim.x = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
+        // The kernel, which sees the lengths, takes one for each kCutChunks places, or one for each pair where those are short,
+        // and leaves the rest.  (Without the second: 16 prompts of 70 tokens, 4 heads 24.7 us for 18.6, 16 of 100, 8 heads 30.3
+        // for 26.7.)
+        const int64_t pairs = (int64_t)N * H, ctas = std::max((most + kCutChunks - 1) / kCutChunks, pairs);
+        cfg.gridDim.x = (unsigned)std::min(ctas, (int64_t)(sms < kDecayCtas ? sms : kDecayCtas));
         a.flags = static_cast<uint32_t*>(workspace);
         a.decays = reinterpret_cast<float*>(a.flags + kDecayCtas);
         a.states = a.decays + kDecayCtas;
