@@ -595,8 +595,19 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
  * NaN or infinite, and may make rows of its own chunk of 128 before it NaN.
  * Sums are formed at up to 2^60 times a row's scale where its chunk's decays are
  * that strong: scores times values stay below 2^60.
+ * What is rounded: a chunk's weighted scores and the state are rounded once each to
+ * in_dtype for the products that make `out`, whatever out_dtype is.  Together that
+ * weighs about as much as one rounding of `out` to in_dtype: an fp32 `out` saves its
+ * own rounding, and is not good to fp32.  States and snapshots are: fp32 sums over
+ * keys that are decayed in fp32 and enter whole (bf16).
  * fp16 calls: scores and states below 2^-28 of the largest of their row and state
- * lose bits, and a decayed key is 2^-25 off at most (bf16 has fp32's exponents).
+ * lose bits, and a decayed key is off by 2^-22 of itself or by 2^-25, whichever is
+ * more, 2^-25 being half a step of fp16's smallest numbers (bf16 has fp32's exponents).
+ * fp32 q, k and v are not taken (kda_decay_decode takes them): the chunk form's
+ * products have 16-bit operands, and those of fp32 rows in parts would not fit
+ * beside one another in shared memory.
+ * A workspace is for prompts that a cut helps.  Where all are shorter than some 1500
+ * tokens and N * H is below the number of SMs, a call without one is 5 to 10 us faster.
  * With KDA_DEV_TIMEOUT, rows and states that the call did not finish are not
  * written.  T_tot < 2^30, N * H < 2^27.
  */
