@@ -590,7 +590,9 @@ kda_status kda_latent_prefill(const kda_rows_desc* q, const kda_rows_desc* k_nop
  *                    sequence are left as they were.
  *   workspace      : NULL, or >= kda_decay_prefill_workspace_size(T_tot, N, H)
  *                    bytes.  With it long (sequence, head) pairs are cut between
- *                    SMs; what an earlier call left there reaches no result.
+ *                    SMs; what an earlier call left there reaches no result.  Calls
+ *                    that may run at once (on two streams, in two captured graphs)
+ *                    need one each.
  * A value, key or decay that is not finite makes the rows behind it (and the state)
  * NaN or infinite, and may make rows of its own chunk of 128 before it NaN.
  * Sums are formed at up to 2^60 times a row's scale where its chunk's decays are

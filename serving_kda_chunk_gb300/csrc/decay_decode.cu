@@ -359,8 +359,10 @@ void launch(const DecayDecodeArgs& a, cudaStream_t s) {
     if (a.K == 1)
         decay_step_kernel<ST><<<units * 4, kDecayThreads, 0, s>>>(a);
     // A state in two blocks of 64 value channels: four chains a SM for two, and the positions' rows read twice.  64 requests
-    // of 32 heads, fp32 states, two blocks and one: step of 2 positions 56 and 62 us, 4 58 and 63, 7 67 and 68; verify 4
-    // 35.2 and 36.9, 5 41.3 and 36.9; commit 4 45 and 48.5, 7 48.7 and 49.8.  bf16 states, 256 requests, 7: commit 176 and 164.
+    // of 32 heads, fp32 states, two blocks and one: step of 2 positions 56 and 62 us, 4 58 and 63; verify 4 35.2 and 36.9,
+    // 5 41.3 and 36.9, 7 40.4 and 36.6; commit 4 45 and 48.5, 7 50.5 and 51.5.  bf16 states, 7: commit 38.5 and 37.1.
+    // Steps of 5 to 8 positions go with the verify, which the host does not tell from them: of 7, 66.5 and 66.8 (256
+    // requests 273.7 and 275), bf16 states 58.2 and 56.4 (246 and 231), but fp32 rows 63.9 and 68.1 (227 and 249).
     else if (a.K <= 4 || (a.K <= 8 && !a.out.base && ST == kStateF32))
         decay_steps_kernel<ST, 1, 2><<<units * 2, 128, 0, s>>>(a);
     else if (a.K <= 8)

@@ -27,13 +27,14 @@
 // through the stage of their keys.  What bounds it now is instruction issue and fetch: the roles run different code on
 // four schedulers, so what is rare is kept out of line, loops over halves stay loops, waits suspend their warp.  Each
 // of the steps that made the code smaller gave more than one that took arithmetic away.  8 sequences of ~5182 tokens,
-// 32 heads, bf16, states read and written: 281 us, 5.1 of 6.7 TB/s (535 us in the first form that used tensor cores).
+// 32 heads, bf16, states read and written: 281 to 290 us by the GPU, 4.9 to 5.1 of 6.7 TB/s (535 us in the first form that
+// used tensor cores).
 //
 // Balance: the (sequence, head) pairs' chunks lie in one row, with places for what a pair costs besides, cut into equal
 // ranges, one a CTA.  A pair cut once: the CTA that has its beginning takes that first and leaves the state for the next CTA, which takes its end
 // last.  A pair over more CTAs: each but the last first sums up its range's own state (K and V only, read twice) and
-// leaves it, then starts from the states before its own joined in order (131072 tokens, 16 heads: 614 us; with the
-// pair's beginning in one pass the others waited for its state, 685; ranges weighted by their passes were slower
+// leaves it, then starts from the states before its own joined in order (131072 tokens, 16 heads: 612 to 639 us;
+// with the pair's beginning in one pass the others waited for its state, 685 where this took 614; ranges weighted by their passes were slower
 // too).  CTAs wait for one another, so this is a cooperative launch; every wait has a limit.
 #include "decay_common.cuh"
 #include "kda_host.h"
@@ -51,10 +52,13 @@ using namespace umma;
 constexpr int kDecayChunk = 128;
 constexpr int kDecayCtas = 160;        // most CTAs of a cut launch (states that a workspace holds)
 constexpr int kCutChunks = 6;          // a CTA's least range, in places: with 5, 6, 8, 10 one prompt of 16384 tokens, one head took 85, 81, 82,
-                                       // 85 us, 6000 tokens of 16 heads 68, 66, 71, 78, two of 8192, 4 heads 70, 68, 72, 80
+                                       // 85 us, 6000 tokens of 16 heads 68, 66, 71, 78, two of 8192, 4 heads 70, 68, 72, 80.  5 is better
+                                       // where 6 leaves SMs idle: 1500 tokens of 8 heads 45.2 and 50.5, 2500 of 4 47.2 and 50.4, four of
+                                       // 2000, 2 heads 47.5 and 50.7, two of 2048, 8 heads 47.8 and 51.4, 4096 of 8 53.6 and 55.4
 constexpr int kPreDecayThreads = 512;
 constexpr int kShortUnit = 14;         // pairs of fewer places on average are not worth cutting while SMs are left: 1000 tokens of 16 heads
-                                       // took 50 us cut, 39 not, 800 of 64 heads 46 and 41; 1500 of 8 heads (14 places) 52 and 53
+                                       // took 50 us cut, 39 not, 800 of 64 heads 46 and 41; 1500 of 8 heads (14 places) 52 and 53.  (A call
+                                       // without a workspace, so without sums over lengths and a cooperative launch, takes 33, 34 and 43.)
 constexpr int kUnitChunks = 2;         // what a pair's states, join and first chunk cost beside its chunks, for equal ranges: with 0, 1, 2,
                                        // 3 one prompt of 4096 tokens, 32 heads took 80, 76, 70, 72 us, 16 of 700, 16 heads 83, 73, 73, 74
 constexpr uint32_t kTile = 32768;      // 128 rows of 128 16-bit channels

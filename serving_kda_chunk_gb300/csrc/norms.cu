@@ -582,9 +582,10 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
                          branch_scale, eps, weight_offset};
     cudaStream_t s = as_stream(stream);
     const int stage = d * (dtype_bytes(in_dtype) * (gate && gate_stride != 0 ? 2 : 1) + dtype_bytes(residual_dtype));
-    // The ring from 1280 channels and 1024 rows on (against rows in registers: bf16, 1280 channels 14 and 17 us at 4096
-    // rows, 4.5 and 4.5 at 1024; 4096 channels 25 and 33, 10.3 and 11.9; fp32 residual 37 and 41, 13.9 and 14.6; but 1024
-    // channels 14 and 10), and above 4096 channels from 256 rows on (8192 channels: 6.1 and 8.6, 15.8 and 28 at 1024).
+    // The ring above 1024 channels, from 1024 rows on (against rows in registers: bf16, 1032 channels 84 and 137 us at 41460
+    // rows, 10.2 and 13.4 at 4096, 4.4 and 4.5 at 1024, with an fp32 residual 107 and 140, 13.4 and 15.4, but 5.1 and 4.4; 4096
+    // channels 25 and 33 at 4096 rows, 10.3 and 11.9 at 1024; fp32 residual 37 and 41, 13.9 and 14.6; but 1024 channels 14 and
+    // 10 at 4096 rows), and above 4096 channels from 256 rows on (8192 channels: 6.1 and 8.6, 15.8 and 28 at 1024).
     if (vec && d > 1024 && R >= (d > 4096 ? 256 : 1024) && 2 * stage <= kStreamBytes) {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -601,8 +602,10 @@ extern "C" kda_status kda_residual_norm(const void* x, int64_t x_stride, const v
         auto by_len = [&](auto DT, auto RDT) {
             // Threads and vectors of each: by how many threads a row leaves idle, and how many rows a SM then has.  bf16: 1280
             // channels, 41460 rows 84 us (256 x 1: 105), but with an fp32 residual 118 and 109; 3584 channels, 16384 rows 74
-            // (512 x 1: 88); 4096, 41460 rows 237 (512 x 1: 211, but of 8192 rows 45 and 48, and with an fp32 residual 346 and
-            // 348); 5120, 16384 rows 127 (256 x 4: 168); 16384 channels 429 (256 x 8: 847).
+            // (512 x 1: 88); 5120, 16384 rows 127 (256 x 4: 168); 16384 channels 429 (256 x 8: 847).  512 x 1 against 256 x 2 at
+            // 4096 channels: 8192 rows 47.5 and 45.8, 16384 rows 88 and 94, 24000 126 and 139, 41460 211 and 237; 3976 channels
+            // 47 and 44, 88 and 85, 125 and 129, 212 and 223; with an fp32 residual 144 and 137 at 16384 x 4096, 351 and 348 at
+            // 41460, though 124 and 134 at 16384 x 3976: there it is left.
             using T128 = std::integral_constant<int, 128>;
             using T256 = std::integral_constant<int, 256>;
             using T512 = std::integral_constant<int, 512>;
