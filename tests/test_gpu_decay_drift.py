@@ -62,3 +62,19 @@ def test_decode_of_one_decay(K, g):
     # decay is 2^-149 off (-103.9: 7.5e-46 counts as 1.4e-45), times the state before it, and the result 2^-149 more
     least = 2.0 ** -149 * (1 + (S / rate).abs().amax((1, 2)))
     assert ((got - S).abs().amax((1, 2)) <= (2 + 2 * K) * 2.0 ** -24 * S.abs().amax((1, 2)) + least).all()
+
+
+@pytest.mark.parametrize("K", [1, 4, 7, 16])
+@pytest.mark.parametrize("g", [0.0, -1e-3, -0.5, -2.0])
+def test_infinities_in_a_state_stay_what_they_are(K, g):
+    """inf e^g is inf; the other elements of the state are those of a call without them."""
+    x = gen(23)
+    k, v = randn(x, K, 2, D, dt=BF16, std=D ** -0.5), randn(x, K, 2, D, dt=BF16)
+    pool = randn(x, 1, 2, D, D)
+    head, inf = torch.full((2,), g, device="cuda"), float("inf")
+    want = pool.clone()
+    kda.kda_decay_decode(None, k, v, want, i32([0]), None, K=K, head_decay=head)
+    pool[0, 0, 3, 5], pool[0, 1, 127, 0] = inf, -inf
+    want[0, 0, 3, 5], want[0, 1, 127, 0] = inf, -inf
+    kda.kda_decay_decode(None, k, v, pool, i32([0]), None, K=K, head_decay=head)
+    assert torch.equal(pool, want)
